@@ -382,6 +382,53 @@ moe_status moe_unpermute_combine_backward(const void *dout, moe_dtype dout_dt, c
 moe_status moe_route_topk_backward(const int32_t *topk_idx, const float *topk_w, const float *d_topk_w, int64_t T,
                                    int32_t E, int32_t K, float *d_logits, hipStream_t stream);
 
+/* Residual addition and RMS norm, the step before an MoE layer's router and dispatch:
+ *   h[t,j] = x[t,j] + residual[t,j]   (residual NULL: h = x)
+ *   s[t]   = 1 / sqrt(mean_j h[t,j]^2 + eps)
+ *   out[t,j] = h[t,j] * s[t] * weight[j]
+ * in float32 from the loads to the one rounding of each output: the norm is that of the unrounded
+ * float32 sum, also where sum_out stores it as bf16.
+ *   x [T, H] (x_dt), residual [T, H] (sum_dt) or NULL, weight [H] (weight_dt); each float32 or bf16;
+ *   eps finite, >= 0 (with eps 0 a row of zeros gives NaN; a row whose sum of squares passes float32's
+ *   range gives zeros);
+ *   sum_out [T, H] (sum_dt) or NULL: h, the new residual; out [T, H] (out_dt); rstd [T] float32 or
+ *   NULL: s, for the backward.
+ * sum_out may be x or residual, and out may be x or residual, where the types are the same (each
+ * element is read before it is written); otherwise outputs overlap nothing.
+ * T <= 2^31 - 1 (else MOE_ERR_UNSUPPORTED). */
+moe_status moe_add_rmsnorm(const void *x, moe_dtype x_dt, const void *residual, moe_dtype sum_dt,
+                           const void *weight, moe_dtype weight_dt, int64_t T, int64_t H, float eps,
+                           void *sum_out, void *out, moe_dtype out_dt, float *rstd, hipStream_t stream);
+
+/* moe_add_rmsnorm with its output as the rows of the FP8 dispatch: per block of `block` consecutive
+ * elements the scale and codes of moe_quantize_fp8, taken from the float32 values of out (one rounding,
+ * not that of out's type first).
+ *   q [T, H] E4M3 codes, scales [T, H/block] float32; out [T, H] (out_dt) or NULL: the rows themselves
+ *   too (the router's input). block >= 1 must divide H (else MOE_ERR_INVALID). A block that holds a NaN
+ *   or an infinity has unspecified codes. The other arguments as in moe_add_rmsnorm; q and scales overlap
+ *   no input. */
+moe_status moe_add_rmsnorm_fp8(const void *x, moe_dtype x_dt, const void *residual, moe_dtype sum_dt,
+                               const void *weight, moe_dtype weight_dt, int64_t T, int64_t H, float eps,
+                               int32_t block, void *sum_out, void *out, moe_dtype out_dt, uint8_t *q,
+                               float *scales, float *rstd, hipStream_t stream);
+
+/* Backward of moe_add_rmsnorm, given its h (sum_out, or x without a residual) and s (rstd): with
+ * a = dout * weight and m[t] = s[t]^2 * mean_j a[t,j] h[t,j],
+ *   dx[t,j]    = s[t] * (a[t,j] - h[t,j] * m[t]) + d_sum[t,j]   (the gradient of x and of residual alike)
+ *   dweight[j] = sum_t dout[t,j] * h[t,j] * s[t]
+ * in float32, summed in an order that depends on the sizes alone (no atomics).
+ *   dout [T, H] (dout_dt), h [T, H] (h_dt), d_sum [T, H] (dx_dt) or NULL: the gradient that reaches
+ *   sum_out by other ways; dx [T, H] (dx_dt), which may be d_sum and overlaps no other input;
+ *   dweight [H] float32 or NULL (not computed). T = 0 writes zeros to dweight.
+ * The workspace (16-byte aligned, contents need no initialisation; needed with dweight only) must hold
+ * moe_add_rmsnorm_backward_workspace_size bytes. */
+moe_status moe_add_rmsnorm_backward_workspace_size(int64_t T, int64_t H, size_t *bytes);
+moe_status moe_add_rmsnorm_backward(const void *dout, moe_dtype dout_dt, const void *h, moe_dtype h_dt,
+                                    const void *weight, moe_dtype weight_dt, const float *rstd,
+                                    const void *d_sum, int64_t T, int64_t H, void *dx, moe_dtype dx_dt,
+                                    float *dweight, void *workspace, size_t workspace_bytes,
+                                    hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,6 +12,9 @@ MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
 _P = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
+_f32 = ctypes.c_float
+_dt = ctypes.c_int
+_size = ctypes.c_size_t
 
 
 class MoeIndexStruct(ctypes.Structure):
@@ -48,6 +51,12 @@ SIGNATURES = {
                                              ctypes.c_int, _P]),
     "moe_group_precombine": (ctypes.c_int, [_P, ctypes.c_int, _i64, _i64, _P, _P, _P, _i64, _i32, _i32,
                                             _i32, _P, _i64, _P, ctypes.c_int, _P]),
+    "moe_add_rmsnorm": (ctypes.c_int, [_P, _dt, _P, _dt, _P, _dt, _i64, _i64, _f32, _P, _P, _dt, _P, _P]),
+    "moe_add_rmsnorm_fp8": (ctypes.c_int, [_P, _dt, _P, _dt, _P, _dt, _i64, _i64, _f32, _i32, _P, _P, _dt, _P, _P, _P,
+                                           _P]),
+    "moe_add_rmsnorm_backward_workspace_size": (ctypes.c_int, [_i64, _i64, ctypes.POINTER(_size)]),
+    "moe_add_rmsnorm_backward": (ctypes.c_int, [_P, _dt, _P, _dt, _P, _dt, _P, _P, _i64, _i64, _P, _dt, _P, _P, _size,
+                                                _P]),
 }
 
 

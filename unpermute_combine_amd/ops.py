@@ -553,3 +553,139 @@ def route_topk_backward(topk_idx: torch.Tensor, topk_w: torch.Tensor, d_topk_w: 
     check("moe_route_topk_backward", lib().moe_route_topk_backward(
         _p(topk_idx), _p(topk_w), _p(d_topk_w), T, num_experts, K, _p(out), _stream()))
     return out
+
+
+# ---------------------------------------------------------------- residual addition and RMS norm
+
+
+def _norm_inputs(x, weight, residual, sum_out):
+    """Checks shared by the two forward norms; returns (T, H, dtype of the sum)."""
+    _need(x, "x", None, 2)
+    T, H = x.shape
+    _need(weight, "weight", None, 1)
+    if weight.shape[0] != H:
+        raise ValueError(f"weight must have {H} elements")
+    for t, name in ((residual, "residual"), (sum_out, "sum_out")):
+        if t is not None:
+            _need(t, name, None, 2)
+            if tuple(t.shape) != (T, H):
+                raise ValueError(f"{name} must be [{T}, {H}]")
+    sum_dtype = residual.dtype if residual is not None else (sum_out.dtype if sum_out is not None else x.dtype)
+    if sum_out is not None and sum_out.dtype != sum_dtype:
+        raise TypeError(f"sum_out must be {sum_dtype}, got {sum_out.dtype}")
+    return T, H, sum_dtype
+
+
+def _row_dt(dtype: torch.dtype, name: str) -> int:
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return _DT[dtype]
+
+
+def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                out_dtype: Optional[torch.dtype] = None, want_rstd: bool = False,
+                out: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None):
+    """h = x + residual; out = h / sqrt(mean(h^2) + eps) * weight, in float32 with one rounding per output.
+
+    Returns (out, sum, rstd): sum is h in the residual's dtype (None without a residual, unless sum_out
+    is given), rstd float32 [T] (None unless want_rstd), both for add_rmsnorm_backward. sum_out may be
+    the residual or x itself, out likewise (same dtype)."""
+    T, H, sum_dtype = _norm_inputs(x, weight, residual, sum_out)
+    x_dt, s_dt, w_dt = _row_dt(x.dtype, "x"), _row_dt(sum_dtype, "residual"), _row_dt(weight.dtype, "weight")
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype or x.dtype, device=x.device)
+    _need(out, "out", out_dtype, 2)
+    if tuple(out.shape) != (T, H):
+        raise ValueError(f"out must be [{T}, {H}]")
+    if sum_out is None and residual is not None:
+        sum_out = torch.empty((T, H), dtype=sum_dtype, device=x.device)
+    rstd = torch.empty(T, dtype=torch.float32, device=x.device) if want_rstd else None
+    check("moe_add_rmsnorm", lib().moe_add_rmsnorm(
+        _p(x), x_dt, _p(residual), s_dt, _p(weight), w_dt, T, H, eps, _p(sum_out), _p(out),
+        _row_dt(out.dtype, "out"), _p(rstd), _stream()))
+    return out, sum_out, rstd
+
+
+def add_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                    block: int = 128, want_rows: bool = False, out_dtype: Optional[torch.dtype] = None,
+                    want_rstd: bool = False, out=None, sum_out: Optional[torch.Tensor] = None):
+    """add_rmsnorm with its output quantized per (token, block) as quantize_fp8 does, from the float32
+    values: the FP8 dispatch's rows. Returns (q [T, H] uint8, scales [T, H/block] float32, sum, rows, rstd);
+    rows (the norm's output itself, for the router) only with want_rows; out = (q, scales)."""
+    T, H, sum_dtype = _norm_inputs(x, weight, residual, sum_out)
+    x_dt, s_dt, w_dt = _row_dt(x.dtype, "x"), _row_dt(sum_dtype, "residual"), _row_dt(weight.dtype, "weight")
+    if block < 1 or H % block:
+        raise ValueError("block must divide H")
+    q, sc = (None, None) if out is None else out
+    q = torch.empty((T, H), dtype=torch.uint8, device=x.device) if q is None else q
+    sc = torch.empty((T, H // block), dtype=torch.float32, device=x.device) if sc is None else sc
+    _need(q, "q", torch.uint8, 2)
+    _need(sc, "scales", torch.float32, 2)
+    if tuple(q.shape) != (T, H) or tuple(sc.shape) != (T, H // block):
+        raise ValueError(f"output shapes must be [{T}, {H}] and [{T}, {H // block}]")
+    if sum_out is None and residual is not None:
+        sum_out = torch.empty((T, H), dtype=sum_dtype, device=x.device)
+    o_dtype = out_dtype or x.dtype
+    o_dt = _row_dt(o_dtype, "out_dtype")
+    rows = torch.empty((T, H), dtype=o_dtype, device=x.device) if want_rows else None
+    rstd = torch.empty(T, dtype=torch.float32, device=x.device) if want_rstd else None
+    check("moe_add_rmsnorm_fp8", lib().moe_add_rmsnorm_fp8(
+        _p(x), x_dt, _p(residual), s_dt, _p(weight), w_dt, T, H, eps, block, _p(sum_out), _p(rows), o_dt, _p(q),
+        _p(sc), _p(rstd), _stream()))
+    return q, sc, sum_out, rows, rstd
+
+
+def add_rmsnorm_backward(dout: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                         d_sum: Optional[torch.Tensor] = None, want_dw: bool = True,
+                         dx_dtype: Optional[torch.dtype] = None, out=None,
+                         workspace: Optional[torch.Tensor] = None):
+    """Backward of add_rmsnorm from its sum h (x itself without a residual) and rstd: (dx, dweight | None).
+    dx is the gradient of x and of the residual alike; d_sum, the gradient that reaches the sum by other
+    ways, is added to it (its dtype is dx's). dweight is float32 [H]. out = (dx, dweight), either of which may be
+    None; dx may be d_sum."""
+    _need(dout, "dout", None, 2)
+    T, H = dout.shape
+    _need(h, "h", None, 2)
+    if tuple(h.shape) != (T, H):
+        raise ValueError("h must have the shape of dout")
+    _need(weight, "weight", None, 1)
+    _need(rstd, "rstd", torch.float32, 1)
+    if weight.shape[0] != H or rstd.shape[0] != T:
+        raise ValueError(f"weight must have {H} elements and rstd {T}")
+    g_dt, h_dt, w_dt = _row_dt(dout.dtype, "dout"), _row_dt(h.dtype, "h"), _row_dt(weight.dtype, "weight")
+    dx, dw = (None, None) if out is None else out
+    ddt = dx_dtype or (d_sum.dtype if d_sum is not None else (dx.dtype if dx is not None else dout.dtype))
+    d_dt = _row_dt(ddt, "dx")
+    if d_sum is not None:
+        _need(d_sum, "d_sum", ddt, 2)
+        if tuple(d_sum.shape) != (T, H):
+            raise ValueError("d_sum must have the shape of dout")
+    if dx is None:
+        dx = torch.empty((T, H), dtype=ddt, device=dout.device)
+    _need(dx, "dx", ddt, 2)
+    if tuple(dx.shape) != (T, H):
+        raise ValueError("dx must have the shape of dout")
+    if not want_dw:
+        dw, workspace, nbytes = None, None, 0
+    else:
+        if dw is None:
+            dw = torch.empty(H, dtype=torch.float32, device=dout.device)
+        _need(dw, "dweight", torch.float32, 1)
+        if dw.shape[0] != H:
+            raise ValueError(f"dweight must have {H} elements")
+        if workspace is None:
+            workspace = torch.empty(rmsnorm_workspace_bytes(T, H), dtype=torch.uint8, device=dout.device)
+        _need(workspace, "workspace", torch.uint8, 1)
+        nbytes = workspace.numel()
+    check("moe_add_rmsnorm_backward", lib().moe_add_rmsnorm_backward(
+        _p(dout), g_dt, _p(h), h_dt, _p(weight), w_dt, _p(rstd), _p(d_sum), T, H, _p(dx), d_dt, _p(dw),
+        _p(workspace), nbytes, _stream()))
+    return dx, dw
+
+
+def rmsnorm_workspace_bytes(T: int, H: int) -> int:
+    """Workspace bytes of add_rmsnorm_backward for these sizes (needed with the weight's gradient only)."""
+    n = ctypes.c_size_t(0)
+    check("moe_add_rmsnorm_backward_workspace_size",
+          lib().moe_add_rmsnorm_backward_workspace_size(T, H, ctypes.byref(n)))
+    return int(n.value)
