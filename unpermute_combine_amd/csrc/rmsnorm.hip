@@ -146,6 +146,226 @@ __global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(NormArgs a)
         norm_row<X, S>(a, t);
 }
 
+// ---------------------------------------------------------------- rows in registers
+// 8 consecutive elements of a row; the address need not be aligned beyond its element (gfx950's global
+// memory instructions take any), so odd lengths and offsets use the same wide accesses. Elements past
+// the row's end read as 0 and are not written.
+template <typename X>
+struct Raw8 {
+    u32x4 v[sizeof(X) / 2];
+};
+
+template <typename X>
+__device__ __forceinline__ Raw8<X> load_raw(const X *row, int64_t e, int64_t H)
+{
+    Raw8<X> q{};
+    if (e + 8 <= H) {
+        __builtin_memcpy(&q, row + e, sizeof(q));
+    } else if (e < H) {
+        X t[8] = {};
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (e + i < H)
+                t[i] = row[e + i];
+        __builtin_memcpy(&q, t, sizeof(q));
+    }
+    return q;
+}
+
+__device__ __forceinline__ void widen(const Raw8<uint16_t> &q, float (&f)[8])
+{
+    const uint32_t u[4] = {q.v[0].x, q.v[0].y, q.v[0].z, q.v[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(u[i]);
+        f[2 * i + 1] = bf16_hi(u[i]);
+    }
+}
+
+__device__ __forceinline__ void widen(const Raw8<float> &q, float (&f)[8]) { __builtin_memcpy(f, &q, sizeof(q)); }
+
+__device__ __forceinline__ void store8(uint16_t *row, int64_t e, int64_t H, const float (&f)[8])
+{
+    const u32x4 q{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+    if (e + 8 <= H) {
+        __builtin_memcpy(row + e, &q, sizeof(q));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (e + i < H)
+                store_f(row + e + i, f[i]);
+    }
+}
+
+__device__ __forceinline__ void store8(float *row, int64_t e, int64_t H, const float (&f)[8])
+{
+    if (e + 8 <= H) {
+        __builtin_memcpy(row + e, f, sizeof(f));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (e + i < H)
+                row[e + i] = f[i];
+    }
+}
+
+__device__ __forceinline__ void load_weight8(const Row &w, int64_t e, int64_t H, float (&f)[8])
+{
+    if (w.bf16)
+        widen(load_raw(static_cast<const uint16_t *>(w.p), e, H), f);
+    else
+        widen(load_raw(static_cast<const float *>(w.p), e, H), f);
+}
+
+// Sum over the workgroup in every thread, in a fixed order, with one barrier: consecutive calls alternate
+// between two places (`turn`), so that a wavefront still reading the last one's is not overtaken.
+__device__ __forceinline__ float block_sum1(float v, int turn)
+{
+    __shared__ float sh[2][16];
+    v = wave_sum(v);
+    if ((threadIdx.x & (kWave - 1)) == 0)
+        sh[turn][threadIdx.x / kWave] = v;
+    __syncthreads();
+    float s = 0.0f;
+    for (int w = 0; w < static_cast<int>(blockDim.x) / kWave; ++w)
+        s += sh[turn][w];
+    return s;
+}
+
+__device__ __forceinline__ float block_max1(float v, int turn)
+{
+    __shared__ float sh[2][16];
+    v = wave_max(v);
+    if ((threadIdx.x & (kWave - 1)) == 0)
+        sh[turn][threadIdx.x / kWave] = v;
+    __syncthreads();
+    float s = 0.0f;
+    for (int w = 0; w < static_cast<int>(blockDim.x) / kWave; ++w)
+        s = fmaxf(s, sh[turn][w]);
+    return s;
+}
+
+// One workgroup per row at a time, the row in registers: thread i holds the 8-element vectors i, i + blockDim,
+// ... (NV of them), so that each row is read once, the next row's loads are in flight while this one is reduced and
+// written, and the weights are read once per workgroup. FP8 (kBlocks): a block of 8 << n elements lies in 1 << n
+// neighbouring lanes, whose largest value a few xor shuffles find; (kWholeRow): one scale for the row, through LDS.
+enum NormOut { kRows, kBlocks, kWholeRow };
+
+template <typename X, typename S, int NV, NormOut OUT>
+__global__ __launch_bounds__(1024) void add_rmsnorm_regs_kernel(NormArgs a)
+{
+    const int64_t H = a.H;
+    const int64_t e0 = 8 * static_cast<int64_t>(threadIdx.x), step = 8 * static_cast<int64_t>(blockDim.x);
+    const X *xs = static_cast<const X *>(a.x);
+    const S *rs = static_cast<const S *>(a.residual);
+    Raw8<X> x[NV];
+    Raw8<S> r[NV];
+    float w[NV][8];
+    int64_t t = blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        x[i] = load_raw(xs + t * H, e0 + i * step, H);
+        if (rs)
+            r[i] = load_raw(rs + t * H, e0 + i * step, H);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        load_weight8(a.weight, e0 + i * step, H, w[i]);
+    for (int turn = 0; t < a.T; turn ^= 1) {
+        float h[NV][8];
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            widen(x[i], h[i]);
+            if (rs) {
+                float f[8];
+                widen(r[i], f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    h[i][j] += f[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                ss = fmaf(h[i][j], h[i][j], ss);
+        }
+        const int64_t now = t;
+        t += gridDim.x;
+        if (t < a.T) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                x[i] = load_raw(xs + t * H, e0 + i * step, H);
+                if (rs)
+                    r[i] = load_raw(rs + t * H, e0 + i * step, H);
+            }
+        }
+        const float s = 1.0f / sqrtf(block_sum1(ss, turn) / static_cast<float>(H) + a.eps);
+        if (a.rstd && threadIdx.x == 0)
+            a.rstd[now] = s;
+        float row_scale = 1.0f;
+        if (a.sum_out) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                store8(static_cast<S *>(a.sum_out) + now * H, e0 + i * step, H, h[i]);
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                h[i][j] = h[i][j] * s * w[i][j];
+                if (OUT == kWholeRow)
+                    top = fmaxf(top, fabsf(h[i][j]));
+            }
+        if (OUT == kWholeRow) {
+            top = block_max1(top, turn);
+            row_scale = top > 0.0f ? top / kE4M3Max : 1.0f;
+            if (threadIdx.x == 0)
+                a.scales[now] = row_scale;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int64_t e = e0 + i * step;
+            if (OUT != kRows) {
+                float scale = row_scale;
+                if (OUT == kBlocks) {  // H is a multiple of 8 here: no partial vectors
+                    float amax = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        amax = fmaxf(amax, fabsf(h[i][j]));
+                    for (int off = 1; off < a.block / 8; off <<= 1)
+                        amax = fmaxf(amax, __shfl_xor(amax, off));
+                    scale = amax > 0.0f ? amax / kE4M3Max : 1.0f;
+                    if (e < H && e % a.block == 0)
+                        a.scales[now * (H / a.block) + e / a.block] = scale;
+                }
+                float c[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    c[j] = h[i][j] / scale;
+                uint2 q;
+                int lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+                q.x = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
+                lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
+                q.y = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], lo, true);
+                if (e + 8 <= H) {
+                    __builtin_memcpy(a.q + now * H + e, &q, sizeof(q));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 7; ++j)
+                        if (e + j < H)
+                            a.q[now * H + e + j] = static_cast<uint8_t>((j < 4 ? q.x >> (8 * j) : q.y >> (8 * (j - 4))) & 0xffu);
+                }
+            }
+            if (OUT == kRows || a.out.p) {
+                if (a.out.bf16)
+                    store8(static_cast<uint16_t *>(a.out.p) + now * H, e, H, h[i]);
+                else
+                    store8(static_cast<float *>(a.out.p) + now * H, e, H, h[i]);
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------- backward, any length
 // dx: one workgroup per row. dweight: columns by thread over ranges of rows, the ranges' sums put
 // together in order by a second kernel.
@@ -219,18 +439,47 @@ moe_status check_norm(const void *x, moe_dtype x_dt, const void *residual, moe_d
     return MOE_OK;
 }
 
+template <typename X, typename S, NormOut OUT>
+void launch_norm_regs(const NormArgs &a, int nv, dim3 grid, dim3 block, hipStream_t stream)
+{
+    if (nv == 1)
+        hipLaunchKernelGGL((add_rmsnorm_regs_kernel<X, S, 1, OUT>), grid, block, 0, stream, a);
+    else if (nv == 2)
+        hipLaunchKernelGGL((add_rmsnorm_regs_kernel<X, S, 2, OUT>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((add_rmsnorm_regs_kernel<X, S, 4, OUT>), grid, block, 0, stream, a);
+}
+
+bool pow2(int64_t n) { return (n & (n - 1)) == 0; }
+
+template <typename X, typename S>
+moe_status launch_norm_xs(const NormArgs &a, hipStream_t stream)
+{
+    const int64_t vecs = ceil_div(a.H, 8);
+    const bool blocks = a.q && pow2(a.block) && a.block >= 8 && a.block <= 8 * kWave;
+    if (vecs > 4 * 1024 || (a.q && !blocks && a.block != a.H)) {
+        hipLaunchKernelGGL((add_rmsnorm_kernel<X, S>), dim3(row_blocks(a.T)), dim3(kNormThreads), 0, stream, a);
+        return launch_status();
+    }
+    const int nv = vecs <= (a.T <= 1024 ? 1024 : 256) ? 1 : vecs <= 2 * 1024 ? 2 : 4;
+    const dim3 block(static_cast<unsigned>(ceil_div(ceil_div(vecs, nv), kWave) * kWave));
+    const int64_t resident = 256 * (2048 / block.x);
+    const dim3 grid(static_cast<unsigned>(a.T < resident ? a.T : resident));
+    if (!a.q)
+        launch_norm_regs<X, S, kRows>(a, nv, grid, block, stream);
+    else if (blocks)
+        launch_norm_regs<X, S, kBlocks>(a, nv, grid, block, stream);
+    else
+        launch_norm_regs<X, S, kWholeRow>(a, nv, grid, block, stream);
+    return launch_status();
+}
+
 moe_status launch_norm(const NormArgs &a, moe_dtype x_dt, moe_dtype sum_dt, hipStream_t stream)
 {
-    const dim3 grid(row_blocks(a.T)), block(kNormThreads);
-    if (x_dt == MOE_BF16 && sum_dt == MOE_BF16)
-        hipLaunchKernelGGL((add_rmsnorm_kernel<uint16_t, uint16_t>), grid, block, 0, stream, a);
-    else if (x_dt == MOE_BF16)
-        hipLaunchKernelGGL((add_rmsnorm_kernel<uint16_t, float>), grid, block, 0, stream, a);
-    else if (sum_dt == MOE_BF16)
-        hipLaunchKernelGGL((add_rmsnorm_kernel<float, uint16_t>), grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL((add_rmsnorm_kernel<float, float>), grid, block, 0, stream, a);
-    return launch_status();
+    if (x_dt == MOE_BF16)
+        return sum_dt == MOE_BF16 ? launch_norm_xs<uint16_t, uint16_t>(a, stream)
+                                  : launch_norm_xs<uint16_t, float>(a, stream);
+    return sum_dt == MOE_BF16 ? launch_norm_xs<float, uint16_t>(a, stream) : launch_norm_xs<float, float>(a, stream);
 }
 
 template <typename G, typename S, typename D>
