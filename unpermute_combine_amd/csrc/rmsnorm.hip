@@ -389,8 +389,6 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_dx_kernel(const G *dout,
     }
 }
 
-constexpr int kDwMaxRanges = 256;
-
 template <typename G, typename S>
 __global__ __launch_bounds__(kNormThreads) void rmsnorm_dweight_kernel(const G *dout, const S *h, const float *rstd,
                                                                        int64_t T, int64_t H, int64_t rows, float *part)
@@ -405,22 +403,118 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_dweight_kernel(const G *
     part[blockIdx.y * H + j] = v;
 }
 
-__global__ __launch_bounds__(kNormThreads) void rmsnorm_dweight_sum_kernel(const float *part, int64_t ranges, int64_t H,
-                                                                           float *dweight)
+// dweight = the ranges' sums put together: a workgroup takes 32 columns, its 32 rows of threads every 32nd range
+// each, and the 32 partial sums meet in order.
+constexpr int kSumCols = 32, kSumRows = 32;
+
+__global__ __launch_bounds__(kSumCols *kSumRows) void rmsnorm_dweight_sum_kernel(const float *part, int64_t ranges,
+                                                                                  int64_t H, float *dweight)
 {
-    const int64_t j = static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x;
-    if (j >= H)
-        return;
+    __shared__ float sh[kSumRows][kSumCols];
+    const int c = threadIdx.x % kSumCols, g = threadIdx.x / kSumCols;
+    const int64_t j = static_cast<int64_t>(blockIdx.x) * kSumCols + c;
     float v = 0.0f;
-    for (int64_t p = 0; p < ranges; ++p)
-        v += part[p * H + j];
-    dweight[j] = v;
+    if (j < H) {
+#pragma unroll 4
+        for (int64_t p = g; p < ranges; p += kSumRows)
+            v += part[p * H + j];
+    }
+    sh[g][c] = v;
+    __syncthreads();
+    if (g == 0 && j < H) {
+        for (int k = 1; k < kSumRows; ++k)
+            v += sh[k][c];
+        dweight[j] = v;
+    }
 }
 
 // One workgroup per row up to 2^20 of them (a grid holds fewer than 2^32 threads), then several rows each.
 unsigned row_blocks(int64_t T) { return static_cast<unsigned>(T < (1 << 20) ? T : (1 << 20)); }
 
+// Ranges of rows whose dweight sums are formed apart.
+constexpr int64_t kDwMaxRanges = 512;
 int64_t dw_ranges(int64_t T) { return T < kDwMaxRanges ? T : kDwMaxRanges; }
+
+// Rows in registers as in the forward: thread i keeps its columns' weights and their gradient's sums while its
+// workgroup takes rows blockIdx, blockIdx + gridDim, ...; the sums of the gridDim workgroups are put together in
+// order by rmsnorm_dweight_sum_kernel. Each of dout, h and d_sum is read once.
+template <typename G, typename S, typename D, int NV>
+__global__ __launch_bounds__(1024) void rmsnorm_backward_regs_kernel(const G *dout, const S *h, Row weight,
+                                                                     const float *rstd, const D *d_sum, int64_t T,
+                                                                     int64_t H, D *dx, float *part)
+{
+    const int64_t e0 = 8 * static_cast<int64_t>(threadIdx.x), step = 8 * static_cast<int64_t>(blockDim.x);
+    Raw8<G> gq[NV];
+    Raw8<S> hq[NV];
+    Raw8<D> dq[NV];
+    float w[NV][8], dw[NV][8];
+    int64_t t = blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        gq[i] = load_raw(dout + t * H, e0 + i * step, H);
+        hq[i] = load_raw(h + t * H, e0 + i * step, H);
+    }
+    float s = rstd[t];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        load_weight8(weight, e0 + i * step, H, w[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            dw[i][j] = 0.0f;
+    }
+    for (int turn = 0; t < T; turn ^= 1) {
+        if (d_sum) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                dq[i] = load_raw(d_sum + t * H, e0 + i * step, H);
+        }
+        float a[NV][8], x[NV][8];
+        float ah = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            widen(gq[i], a[i]);
+            widen(hq[i], x[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dw[i][j] = fmaf(a[i][j] * s, x[i][j], dw[i][j]);
+                a[i][j] *= w[i][j];
+                ah = fmaf(a[i][j], x[i][j], ah);
+            }
+        }
+        const int64_t now = t;
+        const float s1 = s;
+        t += gridDim.x;
+        if (t < T) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                gq[i] = load_raw(dout + t * H, e0 + i * step, H);
+                hq[i] = load_raw(h + t * H, e0 + i * step, H);
+            }
+            s = rstd[t];
+        }
+        const float m = s1 * s1 * (block_sum1(ah, turn) / static_cast<float>(H));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = s1 * fmaf(-x[i][j], m, a[i][j]);
+            if (d_sum) {
+                float f[8];
+                widen(dq[i], f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] += f[j];
+            }
+            store8(dx + now * H, e0 + i * step, H, v);
+        }
+    }
+    if (part) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            store8(part + blockIdx.x * H, e0 + i * step, H, dw[i]);
+    }
+}
 
 bool row_type(moe_dtype d) { return d == MOE_F32 || d == MOE_BF16; }
 
@@ -482,20 +576,39 @@ moe_status launch_norm(const NormArgs &a, moe_dtype x_dt, moe_dtype sum_dt, hipS
     return sum_dt == MOE_BF16 ? launch_norm_xs<float, uint16_t>(a, stream) : launch_norm_xs<float, float>(a, stream);
 }
 
+void launch_dweight_sum(const float *part, int64_t ranges, int64_t H, float *dweight, hipStream_t stream)
+{
+    hipLaunchKernelGGL(rmsnorm_dweight_sum_kernel, dim3(static_cast<unsigned>(ceil_div(H, kSumCols))),
+                       dim3(kSumCols * kSumRows), 0, stream, part, ranges, H, dweight);
+}
+
 template <typename G, typename S, typename D>
 moe_status launch_backward(const void *dout, const void *h, Row weight, const float *rstd, const void *d_sum,
                            int64_t T, int64_t H, void *dx, float *dweight, float *part, hipStream_t stream)
 {
-    hipLaunchKernelGGL((rmsnorm_dx_kernel<G, S, D>), dim3(row_blocks(T)), dim3(kNormThreads), 0, stream,
-                       static_cast<const G *>(dout), static_cast<const S *>(h), weight, rstd,
-                       static_cast<const D *>(d_sum), T, H, static_cast<D *>(dx));
-    if (!dweight)
-        return launch_status();
-    const int64_t ranges = dw_ranges(T), rows = ceil_div(T, ranges);
-    const unsigned cols = static_cast<unsigned>(ceil_div(H, kNormThreads));
-    hipLaunchKernelGGL((rmsnorm_dweight_kernel<G, S>), dim3(cols, static_cast<unsigned>(ranges)), dim3(kNormThreads), 0,
-                       stream, static_cast<const G *>(dout), static_cast<const S *>(h), rstd, T, H, rows, part);
-    hipLaunchKernelGGL(rmsnorm_dweight_sum_kernel, dim3(cols), dim3(kNormThreads), 0, stream, part, ranges, H, dweight);
+    const G *g = static_cast<const G *>(dout);
+    const S *hs = static_cast<const S *>(h);
+    const D *ds = static_cast<const D *>(d_sum);
+    const int64_t vecs = ceil_div(H, 8), ranges = dw_ranges(T);
+    if (vecs <= 2 * 1024) {
+        const int nv = vecs <= 256 ? 1 : 2;
+        const dim3 grid(static_cast<unsigned>(ranges)), block(static_cast<unsigned>(ceil_div(ceil_div(vecs, nv), kWave) * kWave));
+        if (nv == 1)
+            hipLaunchKernelGGL((rmsnorm_backward_regs_kernel<G, S, D, 1>), grid, block, 0, stream, g, hs, weight, rstd, ds, T,
+                               H, static_cast<D *>(dx), dweight ? part : nullptr);
+        else
+            hipLaunchKernelGGL((rmsnorm_backward_regs_kernel<G, S, D, 2>), grid, block, 0, stream, g, hs, weight, rstd, ds, T,
+                               H, static_cast<D *>(dx), dweight ? part : nullptr);
+    } else {
+        hipLaunchKernelGGL((rmsnorm_dx_kernel<G, S, D>), dim3(row_blocks(T)), dim3(kNormThreads), 0, stream, g, hs, weight,
+                           rstd, ds, T, H, static_cast<D *>(dx));
+        if (dweight)
+            hipLaunchKernelGGL((rmsnorm_dweight_kernel<G, S>),
+                               dim3(static_cast<unsigned>(ceil_div(H, kNormThreads)), static_cast<unsigned>(ranges)),
+                               dim3(kNormThreads), 0, stream, g, hs, rstd, T, H, ceil_div(T, ranges), part);
+    }
+    if (dweight)
+        launch_dweight_sum(part, ranges, H, dweight, stream);
     return launch_status();
 }
 
@@ -583,9 +696,7 @@ extern "C" moe_status moe_add_rmsnorm_backward(const void *dout, moe_dtype dout_
     if (T == 0) {  // no rows: the weight's gradient is an empty sum
         if (!dweight)
             return MOE_OK;
-        const unsigned cols = static_cast<unsigned>(ceil_div(H, kNormThreads));
-        hipLaunchKernelGGL(rmsnorm_dweight_sum_kernel, dim3(cols), dim3(kNormThreads), 0, stream,
-                           static_cast<const float *>(nullptr), int64_t{0}, H, dweight);
+        launch_dweight_sum(nullptr, 0, H, dweight, stream);
         return launch_status();
     }
     size_t need = 0;
