@@ -46,18 +46,63 @@ struct RowOut {
     }
 };
 
+// Reductions over 2 << n neighbouring lanes: within 16 lanes by DPP moves (lane xor 1, xor 2, then mirrors, which
+// find the other half once its lanes agree), beyond by shuffles through LDS.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
+
+constexpr int kDppQuadXor1 = 0xb1, kDppQuadXor2 = 0x4e, kDppRowHalfMirror = 0x141, kDppRowMirror = 0x140;
+
 __device__ __forceinline__ float wave_sum(float v)
 {
-    for (int off = kWave / 2; off >= 1; off >>= 1)
-        v += __shfl_xor(v, off);
+    v += dpp<kDppQuadXor1>(v);
+    v += dpp<kDppQuadXor2>(v);
+    v += dpp<kDppRowHalfMirror>(v);
+    v += dpp<kDppRowMirror>(v);
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
     return v;
 }
 
-__device__ __forceinline__ float wave_max(float v)
+__device__ __forceinline__ float lanes_max(float v, int lanes)
 {
-    for (int off = kWave / 2; off >= 1; off >>= 1)
-        v = fmaxf(v, __shfl_xor(v, off));
+    if (lanes > 1)
+        v = fmaxf(v, dpp<kDppQuadXor1>(v));
+    if (lanes > 2)
+        v = fmaxf(v, dpp<kDppQuadXor2>(v));
+    if (lanes > 4)
+        v = fmaxf(v, dpp<kDppRowHalfMirror>(v));
+    if (lanes > 8)
+        v = fmaxf(v, dpp<kDppRowMirror>(v));
+    if (lanes > 16)
+        v = fmaxf(v, __shfl_xor(v, 16));
+    if (lanes > 32)
+        v = fmaxf(v, __shfl_xor(v, 32));
     return v;
+}
+
+__device__ __forceinline__ float wave_max(float v) { return lanes_max(v, kWave); }
+
+// v[i] / scale for eight values, each the correctly rounded quotient, with one division: with y the correctly
+// rounded reciprocal, q = v y corrected by its exact remainder, q + (v - q scale) y, is v / scale rounded once
+// (Markstein's theorem; the range keeps the reciprocal, and every remainder that can decide a code, normal).
+__device__ __forceinline__ void divide8(const float (&v)[8], float scale, float (&c)[8])
+{
+    if (scale >= 0x1p-90f && scale <= 0x1p+90f) {
+        const float y = 1.0f / scale;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float q = v[j] * y;
+            c[j] = copysignf(fmaf(fmaf(-q, scale, v[j]), y, q), v[j]);  // the sums above lose a -0
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            c[j] = v[j] / scale;
+    }
 }
 
 // Sum over the workgroup in every thread, in a fixed order.
@@ -245,10 +290,9 @@ __device__ __forceinline__ float block_max1(float v, int turn)
     return s;
 }
 
-// One workgroup per row at a time, the row in registers: thread i holds the 8-element vectors i, i + blockDim,
-// ... (NV of them), so that each row is read once, the next row's loads are in flight while this one is reduced and
-// written, and the weights are read once per workgroup. FP8 (kBlocks): a block of 8 << n elements lies in 1 << n
-// neighbouring lanes, whose largest value a few xor shuffles find; (kWholeRow): one scale for the row, through LDS.
+// One workgroup per row, the row in registers: thread i holds the 8-element vectors i, i + blockDim, ... (NV of
+// them), so that each row is read once. FP8 (kBlocks): a block of 8 << n elements lies in 1 << n neighbouring
+// lanes; (kWholeRow): one scale for the row, through LDS.
 enum NormOut { kRows, kBlocks, kWholeRow };
 
 template <typename X, typename S, int NV, NormOut OUT>
@@ -261,17 +305,17 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_regs_kernel(NormArgs a)
     Raw8<X> x[NV];
     Raw8<S> r[NV];
     float w[NV][8];
-    int64_t t = blockIdx.x;
+    int turn = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        x[i] = load_raw(xs + t * H, e0 + i * step, H);
-        if (rs)
-            r[i] = load_raw(rs + t * H, e0 + i * step, H);
-    }
+        for (int i = 0; i < NV; ++i) {
+            x[i] = load_raw(xs + t * H, e0 + i * step, H);
+            if (rs)
+                r[i] = load_raw(rs + t * H, e0 + i * step, H);
+        }
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        load_weight8(a.weight, e0 + i * step, H, w[i]);
-    for (int turn = 0; t < a.T; turn ^= 1) {
+        for (int i = 0; i < NV; ++i)
+            load_weight8(a.weight, e0 + i * step, H, w[i]);
         float h[NV][8];
         float ss = 0.0f;
 #pragma unroll
@@ -288,24 +332,14 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_regs_kernel(NormArgs a)
             for (int j = 0; j < 8; ++j)
                 ss = fmaf(h[i][j], h[i][j], ss);
         }
-        const int64_t now = t;
-        t += gridDim.x;
-        if (t < a.T) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                x[i] = load_raw(xs + t * H, e0 + i * step, H);
-                if (rs)
-                    r[i] = load_raw(rs + t * H, e0 + i * step, H);
-            }
-        }
         const float s = 1.0f / sqrtf(block_sum1(ss, turn) / static_cast<float>(H) + a.eps);
         if (a.rstd && threadIdx.x == 0)
-            a.rstd[now] = s;
+            a.rstd[t] = s;
         float row_scale = 1.0f;
         if (a.sum_out) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                store8(static_cast<S *>(a.sum_out) + now * H, e0 + i * step, H, h[i]);
+                store8(static_cast<S *>(a.sum_out) + t * H, e0 + i * step, H, h[i]);
         }
         float top = 0.0f;
 #pragma unroll
@@ -320,7 +354,7 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_regs_kernel(NormArgs a)
             top = block_max1(top, turn);
             row_scale = top > 0.0f ? top / kE4M3Max : 1.0f;
             if (threadIdx.x == 0)
-                a.scales[now] = row_scale;
+                a.scales[t] = row_scale;
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -332,35 +366,32 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_regs_kernel(NormArgs a)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         amax = fmaxf(amax, fabsf(h[i][j]));
-                    for (int off = 1; off < a.block / 8; off <<= 1)
-                        amax = fmaxf(amax, __shfl_xor(amax, off));
+                    amax = lanes_max(amax, static_cast<int>(a.block / 8));
                     scale = amax > 0.0f ? amax / kE4M3Max : 1.0f;
                     if (e < H && e % a.block == 0)
-                        a.scales[now * (H / a.block) + e / a.block] = scale;
+                        a.scales[t * (H / a.block) + e / a.block] = scale;
                 }
                 float c[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    c[j] = h[i][j] / scale;
+                divide8(h[i], scale, c);
                 uint2 q;
                 int lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
                 q.x = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
                 lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
                 q.y = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], lo, true);
                 if (e + 8 <= H) {
-                    __builtin_memcpy(a.q + now * H + e, &q, sizeof(q));
+                    __builtin_memcpy(a.q + t * H + e, &q, sizeof(q));
                 } else {
 #pragma unroll
                     for (int j = 0; j < 7; ++j)
                         if (e + j < H)
-                            a.q[now * H + e + j] = static_cast<uint8_t>((j < 4 ? q.x >> (8 * j) : q.y >> (8 * (j - 4))) & 0xffu);
+                            a.q[t * H + e + j] = static_cast<uint8_t>((j < 4 ? q.x >> (8 * j) : q.y >> (8 * (j - 4))) & 0xffu);
                 }
             }
             if (OUT == kRows || a.out.p) {
                 if (a.out.bf16)
-                    store8(static_cast<uint16_t *>(a.out.p) + now * H, e, H, h[i]);
+                    store8(static_cast<uint16_t *>(a.out.p) + t * H, e, H, h[i]);
                 else
-                    store8(static_cast<float *>(a.out.p) + now * H, e, H, h[i]);
+                    store8(static_cast<float *>(a.out.p) + t * H, e, H, h[i]);
             }
         }
     }
@@ -557,8 +588,7 @@ moe_status launch_norm_xs(const NormArgs &a, hipStream_t stream)
     }
     const int nv = vecs <= (a.T <= 1024 ? 1024 : 256) ? 1 : vecs <= 2 * 1024 ? 2 : 4;
     const dim3 block(static_cast<unsigned>(ceil_div(ceil_div(vecs, nv), kWave) * kWave));
-    const int64_t resident = 256 * (2048 / block.x);
-    const dim3 grid(static_cast<unsigned>(a.T < resident ? a.T : resident));
+    const dim3 grid(row_blocks(a.T));
     if (!a.q)
         launch_norm_regs<X, S, kRows>(a, nv, grid, block, stream);
     else if (blocks)

@@ -23,7 +23,9 @@ _DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.uint8: MOE_FP8_E4
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the current stream of the current device as a hipStream_t (torch.cuda.current_stream() builds a Python
+    # stream object first: 2.9 us a call against 0.3)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -568,7 +570,7 @@ def _norm_inputs(x, weight, residual, sum_out):
     for t, name in ((residual, "residual"), (sum_out, "sum_out")):
         if t is not None:
             _need(t, name, None, 2)
-            if tuple(t.shape) != (T, H):
+            if t.shape != x.shape:
                 raise ValueError(f"{name} must be [{T}, {H}]")
     sum_dtype = residual.dtype if residual is not None else (sum_out.dtype if sum_out is not None else x.dtype)
     if sum_out is not None and sum_out.dtype != sum_dtype:
@@ -593,12 +595,13 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     T, H, sum_dtype = _norm_inputs(x, weight, residual, sum_out)
     x_dt, s_dt, w_dt = _row_dt(x.dtype, "x"), _row_dt(sum_dtype, "residual"), _row_dt(weight.dtype, "weight")
     if out is None:
-        out = torch.empty((T, H), dtype=out_dtype or x.dtype, device=x.device)
-    _need(out, "out", out_dtype, 2)
-    if tuple(out.shape) != (T, H):
-        raise ValueError(f"out must be [{T}, {H}]")
+        out = torch.empty_like(x, dtype=out_dtype)
+    else:
+        _need(out, "out", out_dtype, 2)
+        if out.shape != x.shape:
+            raise ValueError(f"out must be [{T}, {H}]")
     if sum_out is None and residual is not None:
-        sum_out = torch.empty((T, H), dtype=sum_dtype, device=x.device)
+        sum_out = torch.empty_like(residual)
     rstd = torch.empty(T, dtype=torch.float32, device=x.device) if want_rstd else None
     check("moe_add_rmsnorm", lib().moe_add_rmsnorm(
         _p(x), x_dt, _p(residual), s_dt, _p(weight), w_dt, T, H, eps, _p(sum_out), _p(out),
@@ -617,14 +620,18 @@ def add_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[to
     if block < 1 or H % block:
         raise ValueError("block must divide H")
     q, sc = (None, None) if out is None else out
-    q = torch.empty((T, H), dtype=torch.uint8, device=x.device) if q is None else q
-    sc = torch.empty((T, H // block), dtype=torch.float32, device=x.device) if sc is None else sc
-    _need(q, "q", torch.uint8, 2)
-    _need(sc, "scales", torch.float32, 2)
+    if q is None:
+        q = torch.empty_like(x, dtype=torch.uint8)
+    else:
+        _need(q, "q", torch.uint8, 2)
+    if sc is None:
+        sc = torch.empty((T, H // block), dtype=torch.float32, device=x.device)
+    else:
+        _need(sc, "scales", torch.float32, 2)
     if tuple(q.shape) != (T, H) or tuple(sc.shape) != (T, H // block):
         raise ValueError(f"output shapes must be [{T}, {H}] and [{T}, {H // block}]")
     if sum_out is None and residual is not None:
-        sum_out = torch.empty((T, H), dtype=sum_dtype, device=x.device)
+        sum_out = torch.empty_like(residual)
     o_dtype = out_dtype or x.dtype
     o_dt = _row_dt(o_dtype, "out_dtype")
     rows = torch.empty((T, H), dtype=o_dtype, device=x.device) if want_rows else None
@@ -661,21 +668,24 @@ def add_rmsnorm_backward(dout: torch.Tensor, h: torch.Tensor, weight: torch.Tens
         if tuple(d_sum.shape) != (T, H):
             raise ValueError("d_sum must have the shape of dout")
     if dx is None:
-        dx = torch.empty((T, H), dtype=ddt, device=dout.device)
-    _need(dx, "dx", ddt, 2)
-    if tuple(dx.shape) != (T, H):
-        raise ValueError("dx must have the shape of dout")
+        dx = torch.empty_like(dout, dtype=ddt)
+    else:
+        _need(dx, "dx", ddt, 2)
+        if dx.shape != dout.shape:
+            raise ValueError("dx must have the shape of dout")
     if not want_dw:
         dw, workspace, nbytes = None, None, 0
     else:
         if dw is None:
             dw = torch.empty(H, dtype=torch.float32, device=dout.device)
-        _need(dw, "dweight", torch.float32, 1)
-        if dw.shape[0] != H:
-            raise ValueError(f"dweight must have {H} elements")
+        else:
+            _need(dw, "dweight", torch.float32, 1)
+            if dw.shape[0] != H:
+                raise ValueError(f"dweight must have {H} elements")
         if workspace is None:
             workspace = torch.empty(rmsnorm_workspace_bytes(T, H), dtype=torch.uint8, device=dout.device)
-        _need(workspace, "workspace", torch.uint8, 1)
+        else:
+            _need(workspace, "workspace", torch.uint8, 1)
         nbytes = workspace.numel()
     check("moe_add_rmsnorm_backward", lib().moe_add_rmsnorm_backward(
         _p(dout), g_dt, _p(h), h_dt, _p(weight), w_dt, _p(rstd), _p(d_sum), T, H, _p(dx), d_dt, _p(dw),
