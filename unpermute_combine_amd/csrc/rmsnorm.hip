@@ -200,13 +200,14 @@ struct Raw8 {
     u32x4 v[sizeof(X) / 2];
 };
 
-template <typename X>
-__device__ __forceinline__ Raw8<X> load_raw(const X *row, int64_t e, int64_t H)
+// TAIL: the row's last vector may be partial (its length is no multiple of 8).
+template <bool TAIL, typename X>
+__device__ __forceinline__ Raw8<X> load_raw(const X *row, int e, int H)
 {
     Raw8<X> q{};
-    if (e + 8 <= H) {
+    if (TAIL ? e + 8 <= H : e < H) {
         __builtin_memcpy(&q, row + e, sizeof(q));
-    } else if (e < H) {
+    } else if (TAIL && e < H) {
         X t[8] = {};
 #pragma unroll
         for (int i = 0; i < 7; ++i)
@@ -229,12 +230,21 @@ __device__ __forceinline__ void widen(const Raw8<uint16_t> &q, float (&f)[8])
 
 __device__ __forceinline__ void widen(const Raw8<float> &q, float (&f)[8]) { __builtin_memcpy(f, &q, sizeof(q)); }
 
-__device__ __forceinline__ void store8(uint16_t *row, int64_t e, int64_t H, const float (&f)[8])
+__device__ __forceinline__ void narrow(const float (&f)[8], Raw8<uint16_t> &q)
 {
-    const u32x4 q{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
-    if (e + 8 <= H) {
+    q.v[0] = u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+}
+
+__device__ __forceinline__ void narrow(const float (&f)[8], Raw8<float> &q) { __builtin_memcpy(&q, f, sizeof(q)); }
+
+template <bool TAIL, typename X>
+__device__ __forceinline__ void store8(X *row, int e, int H, const float (&f)[8])
+{
+    Raw8<X> q;
+    narrow(f, q);
+    if (TAIL ? e + 8 <= H : e < H) {
         __builtin_memcpy(row + e, &q, sizeof(q));
-    } else {
+    } else if (TAIL) {
 #pragma unroll
         for (int i = 0; i < 7; ++i)
             if (e + i < H)
@@ -242,24 +252,13 @@ __device__ __forceinline__ void store8(uint16_t *row, int64_t e, int64_t H, cons
     }
 }
 
-__device__ __forceinline__ void store8(float *row, int64_t e, int64_t H, const float (&f)[8])
-{
-    if (e + 8 <= H) {
-        __builtin_memcpy(row + e, f, sizeof(f));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (e + i < H)
-                row[e + i] = f[i];
-    }
-}
-
-__device__ __forceinline__ void load_weight8(const Row &w, int64_t e, int64_t H, float (&f)[8])
+template <bool TAIL>
+__device__ __forceinline__ void load_weight8(const Row &w, int e, int H, float (&f)[8])
 {
     if (w.bf16)
-        widen(load_raw(static_cast<const uint16_t *>(w.p), e, H), f);
+        widen(load_raw<TAIL>(static_cast<const uint16_t *>(w.p), e, H), f);
     else
-        widen(load_raw(static_cast<const float *>(w.p), e, H), f);
+        widen(load_raw<TAIL>(static_cast<const float *>(w.p), e, H), f);
 }
 
 // Sum over the workgroup in every thread, in a fixed order, with one barrier: consecutive calls alternate
@@ -295,27 +294,27 @@ __device__ __forceinline__ float block_max1(float v, int turn)
 // lanes; (kWholeRow): one scale for the row, through LDS.
 enum NormOut { kRows, kBlocks, kWholeRow };
 
-template <typename X, typename S, int NV, NormOut OUT>
-__global__ __launch_bounds__(1024) void add_rmsnorm_regs_kernel(NormArgs a)
+template <typename X, typename S, int NV, NormOut OUT, bool TAIL>
+__global__ __launch_bounds__(NV == 2 ? 512 : 1024) void add_rmsnorm_regs_kernel(NormArgs a)
 {
-    const int64_t H = a.H;
-    const int64_t e0 = 8 * static_cast<int64_t>(threadIdx.x), step = 8 * static_cast<int64_t>(blockDim.x);
-    const X *xs = static_cast<const X *>(a.x);
-    const S *rs = static_cast<const S *>(a.residual);
+    const int H = static_cast<int>(a.H), e0 = 8 * threadIdx.x, step = 8 * blockDim.x;
     Raw8<X> x[NV];
     Raw8<S> r[NV];
     float w[NV][8];
+    const int block = static_cast<int>(a.block);
     int turn = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+        const X *xs = static_cast<const X *>(a.x) + t * H;
+        const S *rs = a.residual ? static_cast<const S *>(a.residual) + t * H : nullptr;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            x[i] = load_raw(xs + t * H, e0 + i * step, H);
+            x[i] = load_raw<TAIL>(xs, e0 + i * step, H);
             if (rs)
-                r[i] = load_raw(rs + t * H, e0 + i * step, H);
+                r[i] = load_raw<TAIL>(rs, e0 + i * step, H);
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            load_weight8(a.weight, e0 + i * step, H, w[i]);
+            load_weight8<TAIL>(a.weight, e0 + i * step, H, w[i]);
         float h[NV][8];
         float ss = 0.0f;
 #pragma unroll
@@ -339,7 +338,7 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_regs_kernel(NormArgs a)
         if (a.sum_out) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                store8(static_cast<S *>(a.sum_out) + t * H, e0 + i * step, H, h[i]);
+                store8<TAIL>(static_cast<S *>(a.sum_out) + t * H, e0 + i * step, H, h[i]);
         }
         float top = 0.0f;
 #pragma unroll
@@ -358,7 +357,7 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_regs_kernel(NormArgs a)
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t e = e0 + i * step;
+            const int e = e0 + i * step;
             if (OUT != kRows) {
                 float scale = row_scale;
                 if (OUT == kBlocks) {  // H is a multiple of 8 here: no partial vectors
@@ -366,10 +365,10 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_regs_kernel(NormArgs a)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         amax = fmaxf(amax, fabsf(h[i][j]));
-                    amax = lanes_max(amax, static_cast<int>(a.block / 8));
+                    amax = lanes_max(amax, block / 8);
                     scale = amax > 0.0f ? amax / kE4M3Max : 1.0f;
-                    if (e < H && e % a.block == 0)
-                        a.scales[t * (H / a.block) + e / a.block] = scale;
+                    if (e < H && e % block == 0)
+                        a.scales[t * (H / block) + e / block] = scale;
                 }
                 float c[8];
                 divide8(h[i], scale, c);
@@ -378,9 +377,9 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_regs_kernel(NormArgs a)
                 q.x = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
                 lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
                 q.y = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], lo, true);
-                if (e + 8 <= H) {
+                if (TAIL ? e + 8 <= H : e < H) {
                     __builtin_memcpy(a.q + t * H + e, &q, sizeof(q));
-                } else {
+                } else if (TAIL) {
 #pragma unroll
                     for (int j = 0; j < 7; ++j)
                         if (e + j < H)
@@ -389,9 +388,9 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_regs_kernel(NormArgs a)
             }
             if (OUT == kRows || a.out.p) {
                 if (a.out.bf16)
-                    store8(static_cast<uint16_t *>(a.out.p) + t * H, e, H, h[i]);
+                    store8<TAIL>(static_cast<uint16_t *>(a.out.p) + t * H, e, H, h[i]);
                 else
-                    store8(static_cast<float *>(a.out.p) + t * H, e, H, h[i]);
+                    store8<TAIL>(static_cast<float *>(a.out.p) + t * H, e, H, h[i]);
             }
         }
     }
@@ -469,12 +468,12 @@ int64_t dw_ranges(int64_t T) { return T < kDwMaxRanges ? T : kDwMaxRanges; }
 // Rows in registers as in the forward: thread i keeps its columns' weights and their gradient's sums while its
 // workgroup takes rows blockIdx, blockIdx + gridDim, ...; the sums of the gridDim workgroups are put together in
 // order by rmsnorm_dweight_sum_kernel. Each of dout, h and d_sum is read once.
-template <typename G, typename S, typename D, int NV>
-__global__ __launch_bounds__(1024) void rmsnorm_backward_regs_kernel(const G *dout, const S *h, Row weight,
+template <typename G, typename S, typename D, int NV, bool TAIL>
+__global__ __launch_bounds__(512) void rmsnorm_backward_regs_kernel(const G *dout, const S *h, Row weight,
                                                                      const float *rstd, const D *d_sum, int64_t T,
-                                                                     int64_t H, D *dx, float *part)
+                                                                     int H, D *dx, float *part)
 {
-    const int64_t e0 = 8 * static_cast<int64_t>(threadIdx.x), step = 8 * static_cast<int64_t>(blockDim.x);
+    const int e0 = 8 * threadIdx.x, step = 8 * blockDim.x;
     Raw8<G> gq[NV];
     Raw8<S> hq[NV];
     Raw8<D> dq[NV];
@@ -482,13 +481,13 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_regs_kernel(const G *do
     int64_t t = blockIdx.x;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        gq[i] = load_raw(dout + t * H, e0 + i * step, H);
-        hq[i] = load_raw(h + t * H, e0 + i * step, H);
+        gq[i] = load_raw<TAIL>(dout + t * H, e0 + i * step, H);
+        hq[i] = load_raw<TAIL>(h + t * H, e0 + i * step, H);
     }
     float s = rstd[t];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        load_weight8(weight, e0 + i * step, H, w[i]);
+        load_weight8<TAIL>(weight, e0 + i * step, H, w[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             dw[i][j] = 0.0f;
@@ -497,7 +496,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_regs_kernel(const G *do
         if (d_sum) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                dq[i] = load_raw(d_sum + t * H, e0 + i * step, H);
+                dq[i] = load_raw<TAIL>(d_sum + t * H, e0 + i * step, H);
         }
         float a[NV][8], x[NV][8];
         float ah = 0.0f;
@@ -518,8 +517,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_regs_kernel(const G *do
         if (t < T) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                gq[i] = load_raw(dout + t * H, e0 + i * step, H);
-                hq[i] = load_raw(h + t * H, e0 + i * step, H);
+                gq[i] = load_raw<TAIL>(dout + t * H, e0 + i * step, H);
+                hq[i] = load_raw<TAIL>(h + t * H, e0 + i * step, H);
             }
             s = rstd[t];
         }
@@ -537,13 +536,13 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_regs_kernel(const G *do
                 for (int j = 0; j < 8; ++j)
                     v[j] += f[j];
             }
-            store8(dx + now * H, e0 + i * step, H, v);
+            store8<TAIL>(dx + now * H, e0 + i * step, H, v);
         }
     }
     if (part) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            store8(part + blockIdx.x * H, e0 + i * step, H, dw[i]);
+            store8<TAIL>(part + static_cast<int64_t>(blockIdx.x) * H, e0 + i * step, H, dw[i]);
     }
 }
 
@@ -564,15 +563,19 @@ moe_status check_norm(const void *x, moe_dtype x_dt, const void *residual, moe_d
     return MOE_OK;
 }
 
-template <typename X, typename S, NormOut OUT>
-void launch_norm_regs(const NormArgs &a, int nv, dim3 grid, dim3 block, hipStream_t stream)
+template <typename X, typename S, NormOut OUT, bool TAIL>
+void launch_norm_regs(const NormArgs &a, hipStream_t stream)
 {
+    // few rows: as many threads as vectors (up to 1024), for a row's latency; many rows: two vectors a thread
+    const int64_t vecs = ceil_div(a.H, 8);
+    const int nv = vecs <= (a.T <= 1024 ? 1024 : 256) ? 1 : vecs <= 2 * 512 ? 2 : 4;
+    const dim3 grid(row_blocks(a.T)), block(static_cast<unsigned>(ceil_div(ceil_div(vecs, nv), kWave) * kWave));
     if (nv == 1)
-        hipLaunchKernelGGL((add_rmsnorm_regs_kernel<X, S, 1, OUT>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((add_rmsnorm_regs_kernel<X, S, 1, OUT, TAIL>), grid, block, 0, stream, a);
     else if (nv == 2)
-        hipLaunchKernelGGL((add_rmsnorm_regs_kernel<X, S, 2, OUT>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((add_rmsnorm_regs_kernel<X, S, 2, OUT, TAIL>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((add_rmsnorm_regs_kernel<X, S, 4, OUT>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((add_rmsnorm_regs_kernel<X, S, 4, OUT, TAIL>), grid, block, 0, stream, a);
 }
 
 bool pow2(int64_t n) { return (n & (n - 1)) == 0; }
@@ -580,21 +583,17 @@ bool pow2(int64_t n) { return (n & (n - 1)) == 0; }
 template <typename X, typename S>
 moe_status launch_norm_xs(const NormArgs &a, hipStream_t stream)
 {
-    const int64_t vecs = ceil_div(a.H, 8);
     const bool blocks = a.q && pow2(a.block) && a.block >= 8 && a.block <= 8 * kWave;
-    if (vecs > 4 * 1024 || (a.q && !blocks && a.block != a.H)) {
+    if (a.H > 8 * 4 * 1024 || (a.q && !blocks && a.block != a.H))
         hipLaunchKernelGGL((add_rmsnorm_kernel<X, S>), dim3(row_blocks(a.T)), dim3(kNormThreads), 0, stream, a);
-        return launch_status();
-    }
-    const int nv = vecs <= (a.T <= 1024 ? 1024 : 256) ? 1 : vecs <= 2 * 1024 ? 2 : 4;
-    const dim3 block(static_cast<unsigned>(ceil_div(ceil_div(vecs, nv), kWave) * kWave));
-    const dim3 grid(row_blocks(a.T));
-    if (!a.q)
-        launch_norm_regs<X, S, kRows>(a, nv, grid, block, stream);
     else if (blocks)
-        launch_norm_regs<X, S, kBlocks>(a, nv, grid, block, stream);
+        launch_norm_regs<X, S, kBlocks, false>(a, stream);
+    else if (a.q)
+        launch_norm_regs<X, S, kWholeRow, true>(a, stream);
+    else if (a.H % 8 == 0)
+        launch_norm_regs<X, S, kRows, false>(a, stream);
     else
-        launch_norm_regs<X, S, kWholeRow>(a, nv, grid, block, stream);
+        launch_norm_regs<X, S, kRows, true>(a, stream);
     return launch_status();
 }
 
@@ -620,15 +619,28 @@ moe_status launch_backward(const void *dout, const void *h, Row weight, const fl
     const S *hs = static_cast<const S *>(h);
     const D *ds = static_cast<const D *>(d_sum);
     const int64_t vecs = ceil_div(H, 8), ranges = dw_ranges(T);
-    if (vecs <= 2 * 1024) {
-        const int nv = vecs <= 256 ? 1 : 2;
+    if (vecs <= 4 * 512) {
+        const int nv = vecs <= 256 ? 1 : vecs <= 2 * 512 ? 2 : 4;
         const dim3 grid(static_cast<unsigned>(ranges)), block(static_cast<unsigned>(ceil_div(ceil_div(vecs, nv), kWave) * kWave));
-        if (nv == 1)
-            hipLaunchKernelGGL((rmsnorm_backward_regs_kernel<G, S, D, 1>), grid, block, 0, stream, g, hs, weight, rstd, ds, T,
-                               H, static_cast<D *>(dx), dweight ? part : nullptr);
-        else
-            hipLaunchKernelGGL((rmsnorm_backward_regs_kernel<G, S, D, 2>), grid, block, 0, stream, g, hs, weight, rstd, ds, T,
-                               H, static_cast<D *>(dx), dweight ? part : nullptr);
+#define MOE_BACKWARD_LAUNCH(NV, TAIL)                                                                                  \
+    hipLaunchKernelGGL((rmsnorm_backward_regs_kernel<G, S, D, NV, TAIL>), grid, block, 0, stream, g, hs, weight, rstd, \
+                       ds, T, static_cast<int>(H), static_cast<D *>(dx), dweight ? part : nullptr)
+        if (H % 8 == 0) {
+            if (nv == 1)
+                MOE_BACKWARD_LAUNCH(1, false);
+            else if (nv == 2)
+                MOE_BACKWARD_LAUNCH(2, false);
+            else
+                MOE_BACKWARD_LAUNCH(4, false);
+        } else {
+            if (nv == 1)
+                MOE_BACKWARD_LAUNCH(1, true);
+            else if (nv == 2)
+                MOE_BACKWARD_LAUNCH(2, true);
+            else
+                MOE_BACKWARD_LAUNCH(4, true);
+        }
+#undef MOE_BACKWARD_LAUNCH
     } else {
         hipLaunchKernelGGL((rmsnorm_dx_kernel<G, S, D>), dim3(row_blocks(T)), dim3(kNormThreads), 0, stream, g, hs, weight,
                            rstd, ds, T, H, static_cast<D *>(dx));
