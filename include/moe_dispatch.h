@@ -59,6 +59,7 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype;
 /* Upper limits of the kernels. */
 #define MOE_MAX_EXPERTS 1024
 #define MOE_MAX_TOPK 32
+#define MOE_MAX_FEW_TOKENS 256 /* tokens of moe_few_token_layer and moe_few_token_experts */
 
 /* Markers in gather maps (sorted_indices, esrc): a padding row, written as zeros by the
  * permutes; and an unused row after the last expert segment (buffer slack when the buffer is
@@ -428,6 +429,47 @@ moe_status moe_add_rmsnorm_backward(const void *dout, moe_dtype dout_dt, const v
                                     const void *d_sum, int64_t T, int64_t H, void *dx, moe_dtype dx_dt,
                                     float *dweight, void *workspace, size_t workspace_bytes,
                                     hipStream_t stream);
+
+/* The whole MoE layer for a few tokens (a decode step), from hidden rows to combined rows: the router's
+ * product, moe_route_topk, each chosen expert's gated products and the weighted merge, without the
+ * dispatched and permuted rows in between ([Scratch] §3, §16 for the routing and the merge):
+ *   logits[t,e] = sum_j x[t,j] router[e,j]   summed in double, rounded once to float32
+ *   topk_idx, topk_w as moe_route_topk of them (route_group_size > 0: moe_route_topk_grouped, with its
+ *              limits)
+ *   h[t,k,:] = topk_w[t,k] * silu(G_e x[t]) * (U_e x[t]),   e = topk_idx[t,k], silu(g) = g / (1 + exp(-g))
+ *   out[t,:] = sum_k D_e h[t,k,:] (+ bias[t,:])
+ * where w_gate_up [E, 2I, H] holds G_e in rows [0, I) and U_e in rows [I, 2I) of expert e, and w_down
+ * [E, H, I] holds D_e. Sums are float32 (their order depends on the sizes and the routing alone: no
+ * atomics), h is kept to 16 significant bits or more, and out is rounded once.
+ *   x [T, H] and router [E, H] of dtype dt (float32 or bf16); bias [T, H] of dtype out_dt or NULL, which
+ *   may be out itself; out [T, H] (out_dt); topk_idx [T, K], topk_w [T, K] out.
+ *   weight_dt: dt, or MOE_FP8_E4M3 beside bf16 rows: codes with float32 scales, one per row and block of
+ *   `block` consecutive elements of the row, as moe_quantize_fp8 of the weight rows gives them
+ *   (gate_up_scales [E, 2I, H/block], down_scales [E, H, I/block]); block must divide H and I (else
+ *   MOE_ERR_INVALID) and be a multiple of 64 (else MOE_ERR_UNSUPPORTED). Other types of weights:
+ *   MOE_ERR_UNSUPPORTED; block and scales are ignored without FP8.
+ *   T <= MOE_MAX_FEW_TOKENS, H and I <= 2^24 (else MOE_ERR_UNSUPPORTED): for more tokens dispatch them.
+ * Weights of experts that no token uses are not read. Rows are independent: what is not finite in one token's row
+ * or in an expert's weights reaches only the tokens that use it.
+ * The workspace (16-byte aligned, contents need no initialisation and mean nothing after the call) must
+ * hold moe_few_token_workspace_size bytes; calls that may overlap need one each. */
+moe_status moe_few_token_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t K, size_t *bytes);
+moe_status moe_few_token_layer(const void *x, moe_dtype dt, const void *router, int64_t T, int64_t H, int64_t I,
+                               int32_t E, int32_t K, int32_t route_group_size, int32_t topk_groups,
+                               const void *w_gate_up, const void *w_down, moe_dtype weight_dt,
+                               const float *gate_up_scales, const float *down_scales, int32_t block,
+                               const void *bias, void *out, moe_dtype out_dt, int32_t *topk_idx, float *topk_w,
+                               void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The experts of moe_few_token_layer after a routing that the caller has: topk_idx [T, K] (an id outside
+ * [0, E) routes nowhere, so a rank can name the experts it does not hold -1; an id may repeat within a row, each slot
+ * counting), topk_w [T, K] or NULL (unit weights). A token without experts gets zeros (or its bias).
+ * Arguments, limits and workspace as above. */
+moe_status moe_few_token_experts(const void *x, moe_dtype dt, int64_t T, int64_t H, int64_t I, int32_t E,
+                                 int32_t K, const int32_t *topk_idx, const float *topk_w, const void *w_gate_up,
+                                 const void *w_down, moe_dtype weight_dt, const float *gate_up_scales,
+                                 const float *down_scales, int32_t block, const void *bias, void *out,
+                                 moe_dtype out_dt, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

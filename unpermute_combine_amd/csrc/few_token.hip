@@ -1,0 +1,600 @@
+// The whole MoE layer for a few tokens, where dispatch, grouped products and combine would each be latency:
+//
+//   logits[t,e] = sum_j x[t,j] router[e,j]      (summed in double, rounded once to float32)
+//   topk_idx, topk_w = moe_route_topk(logits)
+//   h[t,k,:] = topk_w[t,k] * silu(G_e x[t]) * (U_e x[t]),  e = topk_idx[t,k],  silu(g) = g / (1 + exp(-g))
+//   out[t,:] = sum_k D_e h[t,k,:] (+ bias[t,:])
+//
+// with expert e's gate rows G_e = w_gate_up[e][0..I), up rows U_e = w_gate_up[e][I..2I) and D_e = w_down[e].
+//
+// The time is that of reading the weights of the experts in use, once each. A wavefront multiplies 16 rows of a
+// weight matrix by up to 16 tokens with MFMA 16x16 tiles (few tokens leave most of a tile's columns empty, which
+// costs nothing while the weights' stream sets the pace): 4 lanes read 64 consecutive bytes of each of the 16 rows,
+// straight from memory into the matrix instruction's operand registers, without LDS.
+#include "moe_common.h"
+
+namespace moe {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kMaxFewTokens = MOE_MAX_FEW_TOKENS;
+constexpr int kTile = 16;  // tokens and weight rows of one matrix tile
+
+// Weight element types. A "load" is 16 bytes in each lane: 64 bytes of each of 16 rows, i.e. kLoadElems consecutive
+// elements of the rows, of which lane group g = lane / 16 holds the g-th quarter.
+enum Weights { kWF32, kWBf16, kWFp8 };
+template <Weights W> constexpr int kLaneElems = W == kWF32 ? 4 : W == kWBf16 ? 8 : 16;
+template <Weights W> constexpr int kLoadElems = 4 * kLaneElems<W>;
+
+// The activations that meet one load of weights: as many elements, bf16 (or float32 with float32 weights).
+template <Weights W>
+struct Acts {
+    u32x4 v[W == kWFp8 ? 2 : 1];
+};
+
+// n <= N consecutive elements of type X at p + e, zeros past the row's end. The address need not be aligned beyond
+// its element.
+template <bool TAIL, int N, typename X, typename R>
+__device__ __forceinline__ void load_elems(const X *p, int e, int len, R &r)
+{
+    static_assert(sizeof(R) == N * sizeof(X), "one register set");
+    __builtin_memset(&r, 0, sizeof(r));
+    if (TAIL ? e + N <= len : e < len) {
+        __builtin_memcpy(&r, p + e, sizeof(r));
+    } else if (TAIL && e < len) {
+        X t[N] = {};
+#pragma unroll
+        for (int i = 0; i < N - 1; ++i)
+            if (e + i < len)
+                t[i] = p[e + i];
+        __builtin_memcpy(&r, t, sizeof(r));
+    }
+}
+
+template <Weights W> struct WeightType { typedef uint16_t type; };
+template <> struct WeightType<kWF32> { typedef float type; };
+template <> struct WeightType<kWFp8> { typedef uint8_t type; };
+template <Weights W> struct ActType { typedef uint16_t type; };
+template <> struct ActType<kWF32> { typedef float type; };
+
+// Eight E4M3 codes as bf16 (exact: three mantissa bits, and the exponents of E4M3 are normal in bf16).
+__device__ __forceinline__ bf16x8 fp8_to_bf16(uint32_t a, uint32_t b)
+{
+    const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+    const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+    const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+    const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+    return bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+// acc[token, weight row] += sum over the load's elements of act * weight. The tile's rows (A operand) are tokens and
+// its columns (B operand) weight rows; both operands hold, in lane l, row or column l % 16, and the same elements in
+// the same lane group and register, so any order of the elements inside a load is right.
+template <Weights W>
+__device__ __forceinline__ f32x4 multiply(f32x4 acc, const Acts<W> &x, const u32x4 &w)
+{
+    if constexpr (W == kWF32) {
+        const f32x4 a = __builtin_bit_cast(f32x4, x.v[0]), b = __builtin_bit_cast(f32x4, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], acc, 0, 0, 0);
+    } else if constexpr (W == kWBf16) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x.v[0]), __builtin_bit_cast(bf16x8, w),
+                                                      acc, 0, 0, 0);
+    } else {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x.v[0]), fp8_to_bf16(w.x, w.y), acc, 0,
+                                                      0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x.v[1]), fp8_to_bf16(w.z, w.w), acc, 0,
+                                                      0, 0);
+    }
+    return acc;
+}
+
+// ---------------------------------------------------------------- router
+// One workgroup per (expert, kRouterTokens tokens). The sums are double so that which experts are picked does not
+// depend on the order of a float32 sum; products of float32 or bf16 values are exact in double or rounded to it.
+constexpr int kRouterThreads = 256, kRouterTokens = 8;
+
+__device__ __forceinline__ float to_f32(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+
+template <typename X>
+__global__ __launch_bounds__(kRouterThreads) void router_logits_kernel(const X *x, const X *router, int T, int H, int E,
+                                                                       float *logits)
+{
+    __shared__ double sh[kRouterThreads / kWave][kRouterTokens];
+    const int e = blockIdx.x, t0 = blockIdx.y * kRouterTokens;
+    const X *r = router + static_cast<int64_t>(e) * H;
+    double acc[kRouterTokens] = {};
+    for (int j = threadIdx.x; j < H; j += kRouterThreads) {
+        const double w = to_f32(r[j]);
+#pragma unroll
+        for (int i = 0; i < kRouterTokens; ++i)
+            if (t0 + i < T)
+                acc[i] = fma(static_cast<double>(to_f32(x[static_cast<int64_t>(t0 + i) * H + j])), w, acc[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kRouterTokens; ++i) {
+        for (int off = kWave / 2; off >= 1; off >>= 1)
+            acc[i] += __shfl_xor(acc[i], off);
+        if ((threadIdx.x & (kWave - 1)) == 0)
+            sh[threadIdx.x / kWave][i] = acc[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < kRouterTokens && t0 + static_cast<int>(threadIdx.x) < T) {
+        double s = 0.0;
+        for (int w = 0; w < kRouterThreads / kWave; ++w)
+            s += sh[w][threadIdx.x];
+        logits[static_cast<int64_t>(t0 + threadIdx.x) * E + e] = static_cast<float>(s);
+    }
+}
+
+// ---------------------------------------------------------------- plan
+// The experts in use in ascending order, and the slots s = t * K + k of each in ascending order: a stable counting
+// sort by one workgroup. Each wavefront ranks its own stretch of the slots 64 at a time (the lanes that hold the same
+// expert found by ballots over its bits), so the positions do not depend on timing.
+struct Plan {
+    int32_t *head;   // [0]: experts in use (n)
+    int32_t *act;    // [n] their ids
+    int32_t *start;  // [n + 1] first position of each in order
+    int32_t *order;  // [start[n]] slots
+};
+
+constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / kWave;
+
+__global__ __launch_bounds__(kPlanThreads) void few_token_plan_kernel(const int32_t *topk_idx, int n, int E, Plan plan)
+{
+    extern __shared__ uint16_t cnt[];  // [kPlanWaves][E]: each wavefront's slots per expert, then its next position
+    __shared__ uint32_t wave_total[kPlanWaves];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    for (int i = threadIdx.x; i < kPlanWaves * E; i += kPlanThreads)
+        cnt[i] = 0;
+    __syncthreads();
+    const int per = (n + kPlanThreads - 1) / kPlanThreads * kWave;
+    const int s0 = wave * per, s1 = min(n, s0 + per);
+    const int bits = 32 - __builtin_clz(E);  // of the ids 0..E, E standing for "no expert"
+    uint16_t *mine = cnt + wave * E;
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int s = s0; s < s1; s += kWave) {
+            int e = s + lane < s1 ? topk_idx[s + lane] : E;
+            if (e < 0 || e > E)
+                e = E;
+            uint64_t peers = ~0ull;
+            for (int b = 0; b < bits; ++b) {
+                const uint64_t m = __ballot((e >> b) & 1);
+                peers &= ((e >> b) & 1) ? m : ~m;
+            }
+            const int rank = __popcll(peers & lanemask_lt());
+            int pos = 0;
+            if (e < E) {
+                pos = mine[e];
+                if (pass == 1)
+                    plan.order[pos + rank] = s + lane;
+            }
+            __builtin_amdgcn_wave_barrier();
+            if (e < E && rank == 0)
+                mine[e] = static_cast<uint16_t>(pos + __popcll(peers));
+            __builtin_amdgcn_wave_barrier();
+        }
+        __syncthreads();
+        if (pass == 1)
+            return;
+        // totals per expert, and over them the positions (low half) and the ranks of those in use (high half)
+        const int e = threadIdx.x;
+        uint32_t total = 0;
+        if (e < E)
+            for (int w = 0; w < kPlanWaves; ++w)
+                total += cnt[w * E + e];
+        uint32_t v = total | (total ? 1u << 16 : 0u);
+        const uint32_t own = v;
+        for (int off = 1; off < kWave; off <<= 1) {
+            const uint32_t o = __shfl_up(v, off);
+            if (lane >= off)
+                v += o;
+        }
+        if (lane == kWave - 1)
+            wave_total[wave] = v;
+        __syncthreads();
+        uint32_t before = 0;
+        for (int w = 0; w < wave; ++w)
+            before += wave_total[w];
+        v += before;
+        uint32_t pos = (v - own) & 0xffffu;
+        if (total) {
+            plan.act[(v - own) >> 16] = e;
+            plan.start[(v - own) >> 16] = pos;
+        }
+        if (threadIdx.x == kPlanThreads - 1) {
+            plan.head[0] = v >> 16;
+            plan.start[v >> 16] = v & 0xffffu;
+        }
+        if (e < E)
+            for (int w = 0; w < kPlanWaves; ++w) {
+                const uint16_t c = cnt[w * E + e];
+                cnt[w * E + e] = static_cast<uint16_t>(pos);
+                pos += c;
+            }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- gate and up products
+// One workgroup per (16 columns of h, expert in use): its wavefronts share the hidden dimension's loads, and their
+// tiles meet in LDS. h goes out in the order of the plan, already multiplied by the slot's weight; beside bf16 or FP8
+// weights as two bf16 rows whose sum it is to 16 bits, so that the down product is one of bf16 operands without
+// bf16's rounding of h.
+constexpr int kExpertThreads = 512, kExpertWaves = kExpertThreads / kWave;
+
+struct ExpertArgs {
+    const void *x;            // [T, H] activations
+    const float *topk_w;      // [T, K] or NULL
+    const void *w;            // gate_up or down
+    const float *scales;      // FP8
+    void *h;                  // [slots][I] float32, or [slots][2][I] bf16
+    const void *bias;
+    void *out;
+    int T, K, H, I, block;
+    bool out_bf16;
+    Plan plan;
+};
+
+template <Weights W>
+__device__ __forceinline__ float block_scale(const float *scales, int64_t row, int e, int nb, int block)
+{
+    return W == kWFp8 ? scales[row * nb + e / block] : 1.0f;
+}
+
+template <Weights W, bool TAIL>
+__global__ __launch_bounds__(kExpertThreads) void gate_up_kernel(ExpertArgs a)
+{
+    typedef typename WeightType<W>::type Wt;
+    typedef typename ActType<W>::type X;
+    __shared__ f32x4 red[kExpertWaves][2][kWave];
+    if (static_cast<int>(blockIdx.y) >= a.plan.head[0])
+        return;
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, m = lane % kTile, g = lane / kTile;
+    const int64_t ex = a.plan.act[blockIdx.y];
+    const int p0 = a.plan.start[blockIdx.y], n = a.plan.start[blockIdx.y + 1] - p0;
+    const int c0 = blockIdx.x * kTile, col = min(c0 + m, a.I - 1);
+    const int64_t grow = ex * 2 * a.I + col, urow = grow + a.I;
+    const Wt *gw = static_cast<const Wt *>(a.w) + grow * a.H, *uw = static_cast<const Wt *>(a.w) + urow * a.H;
+    const int loads = (a.H + kLoadElems<W> - 1) / kLoadElems<W>;
+    const int l0 = loads * wave / kExpertWaves, l1 = loads * (wave + 1) / kExpertWaves;
+    const int nb = W == kWFp8 ? a.H / a.block : 0;
+    for (int r0 = 0; r0 < n; r0 += kTile) {
+        const bool live = r0 + m < n;
+        const X *xr = static_cast<const X *>(a.x) +
+                      static_cast<int64_t>(a.plan.order[p0 + (live ? r0 + m : 0)] / a.K) * a.H;
+        f32x4 ga{}, ua{};
+        for (int l = l0; l < l1; ++l) {
+            const int e = l * kLoadElems<W> + g * kLaneElems<W>;
+            u32x4 wg, wu;
+            Acts<W> xa;
+            load_elems<TAIL, kLaneElems<W>>(gw, e, a.H, wg);
+            load_elems<TAIL, kLaneElems<W>>(uw, e, a.H, wu);
+            load_elems<TAIL, kLaneElems<W>>(xr, e, live ? a.H : 0, xa);
+            if (W == kWFp8) {
+                ga += multiply<W>(f32x4{}, xa, wg) * block_scale<W>(a.scales, grow, l * kLoadElems<W>, nb, a.block);
+                ua += multiply<W>(f32x4{}, xa, wu) * block_scale<W>(a.scales, urow, l * kLoadElems<W>, nb, a.block);
+            } else {
+                ga = multiply<W>(ga, xa, wg);
+                ua = multiply<W>(ua, xa, wu);
+            }
+        }
+        red[wave][0][lane] = ga;
+        red[wave][1][lane] = ua;
+        __syncthreads();
+        // thread = (token row, column): row 4 (lane / 16) + r of the tile is in register r
+        if (threadIdx.x < kTile * kTile) {
+            const int src = threadIdx.x / 4, r = threadIdx.x % 4;
+            const int row = r0 + 4 * (src / kTile) + r, c = c0 + src % kTile;
+            float gate = 0.0f, up = 0.0f;
+            for (int w = 0; w < kExpertWaves; ++w) {
+                gate += red[w][0][src][r];
+                up += red[w][1][src][r];
+            }
+            if (row < n && c < a.I) {
+                const int slot = a.plan.order[p0 + row];
+                const float h = gate / (1.0f + expf(-gate)) * up * (a.topk_w ? a.topk_w[slot] : 1.0f);
+                if (W == kWF32) {
+                    static_cast<float *>(a.h)[static_cast<int64_t>(p0 + row) * a.I + c] = h;
+                } else {
+                    uint16_t *hr = static_cast<uint16_t *>(a.h) + static_cast<int64_t>(p0 + row) * 2 * a.I;
+                    const uint32_t hi = f32_to_bf16_bits(h);
+                    const float rest = h - __uint_as_float(hi << 16);
+                    hr[c] = static_cast<uint16_t>(hi);
+                    // an infinite or NaN h is wholly in the first row
+                    hr[a.I + c] = (hi & 0x7f80u) == 0x7f80u ? 0 : static_cast<uint16_t>(f32_to_bf16_bits(rest));
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- down product and combine
+// One workgroup per 16 columns of out, for all experts in use: the (expert, load) pairs in order are cut into one
+// stretch per wavefront, each wavefront adds its tiles into its own [T][16] sums in LDS when its expert changes, and
+// the wavefronts' sums are put together in order. No atomics: the result does not depend on timing.
+template <Weights W, bool TAIL>
+__global__ __launch_bounds__(kExpertThreads) void down_kernel(ExpertArgs a)
+{
+    typedef typename WeightType<W>::type Wt;
+    typedef typename ActType<W>::type X;
+    extern __shared__ float sums[];  // [kExpertWaves][T][kTile]
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, m = lane % kTile, g = lane / kTile;
+    const int c0 = blockIdx.x * kTile, col = min(c0 + m, a.H - 1);
+    float *mine = sums + wave * a.T * kTile;
+    for (int i = lane; i < a.T * kTile; i += kWave)
+        mine[i] = 0.0f;
+    __builtin_amdgcn_wave_barrier();
+    const int loads = (a.I + kLoadElems<W> - 1) / kLoadElems<W>;
+    const int64_t all = static_cast<int64_t>(a.plan.head[0]) * loads;
+    const int64_t u1 = all * (wave + 1) / kExpertWaves;
+    const int nb = W == kWFp8 ? a.I / a.block : 0;
+    for (int64_t u = all * wave / kExpertWaves; u < u1;) {
+        const int i = static_cast<int>(u / loads), l0 = static_cast<int>(u - static_cast<int64_t>(i) * loads);
+        const int l1 = static_cast<int>(min(static_cast<int64_t>(loads), l0 + (u1 - u)));
+        u += l1 - l0;
+        const int p0 = a.plan.start[i], n = a.plan.start[i + 1] - p0;
+        const int64_t wrow = static_cast<int64_t>(a.plan.act[i]) * a.H + col;
+        const Wt *w = static_cast<const Wt *>(a.w) + wrow * a.I;
+        for (int r0 = 0; r0 < n; r0 += kTile) {
+            const bool live = r0 + m < n;
+            const int p = p0 + (live ? r0 + m : 0);
+            const X *hr = static_cast<const X *>(a.h) + static_cast<int64_t>(p) * (W == kWF32 ? 1 : 2) * a.I;
+            f32x4 acc{};
+            for (int l = l0; l < l1; ++l) {
+                const int e = l * kLoadElems<W> + g * kLaneElems<W>;
+                u32x4 wd;
+                Acts<W> hi, lo;
+                load_elems<TAIL, kLaneElems<W>>(w, e, a.I, wd);
+                load_elems<TAIL, kLaneElems<W>>(hr, e, live ? a.I : 0, hi);
+                f32x4 part = W == kWFp8 ? f32x4{} : acc;
+                part = multiply<W>(part, hi, wd);
+                if (W != kWF32) {
+                    load_elems<TAIL, kLaneElems<W>>(hr + a.I, e, live ? a.I : 0, lo);
+                    part = multiply<W>(part, lo, wd);
+                }
+                if (W == kWFp8)
+                    acc += part * block_scale<W>(a.scales, wrow, l * kLoadElems<W>, nb, a.block);
+                else
+                    acc = part;
+            }
+            // this lane holds column m for the tile's rows 4 g .. 4 g + 3. A token that names the expert twice has two
+            // rows: then the lane groups add one after the other
+            const int tok = a.plan.order[p] / a.K;
+            const bool twice = __ballot(live && m > 0 && tok == __shfl_up(tok, 1)) != 0;
+            for (int turn = 0; turn < (twice ? 4 : 1); ++turn) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = __shfl(tok, 4 * g + r);
+                    if ((!twice || g == turn) && r0 + 4 * g + r < n)
+                        mine[t * kTile + m] += acc[r];
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.T * kTile; i += kExpertThreads) {
+        const int t = i / kTile, c = c0 + i % kTile;
+        if (c >= a.H)
+            continue;
+        float v = 0.0f;
+        for (int k = 0; k < kExpertWaves; ++k)
+            v += sums[k * a.T * kTile + i];
+        const int64_t o = static_cast<int64_t>(t) * a.H + c;
+        if (a.out_bf16) {
+            if (a.bias)
+                v += to_f32(static_cast<const uint16_t *>(a.bias)[o]);
+            static_cast<uint16_t *>(a.out)[o] = static_cast<uint16_t>(f32_to_bf16_bits(v));
+        } else {
+            if (a.bias)
+                v += static_cast<const float *>(a.bias)[o];
+            static_cast<float *>(a.out)[o] = v;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
+
+// The workspace: logits, plan, h.
+struct Layout {
+    size_t logits, head, act, start, order, h, bytes;
+};
+
+Layout layout(int64_t T, int64_t E, int64_t K, int64_t I)
+{
+    Layout l{};
+    const int64_t slots = T * K, used = E < slots ? E : slots;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += round16(n);
+        return here;
+    };
+    l.logits = take(4 * T * E);
+    l.head = take(4);
+    l.act = take(4 * used);
+    l.start = take(4 * (used + 1));
+    l.order = take(4 * slots);
+    l.h = take(4 * slots * I);
+    l.bytes = at;
+    return l;
+}
+
+moe_status check_sizes(int64_t T, int64_t H, int64_t I, int32_t E, int32_t K)
+{
+    if (T < 0 || H < 1 || I < 1 || E < 1 || K < 1 || K > E)
+        return MOE_ERR_INVALID;
+    if (T > kMaxFewTokens || E > MOE_MAX_EXPERTS || K > MOE_MAX_TOPK || H > (1 << 24) || I > (1 << 24))
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+struct ExpertWeights {
+    const void *gate_up, *down;
+    moe_dtype dt;
+    const float *gate_up_scales, *down_scales;
+    int32_t block;
+};
+
+moe_status check_layer(const void *x, moe_dtype dt, int64_t T, int64_t H, int64_t I, int32_t E, int32_t K,
+                       const ExpertWeights &w, const void *out, moe_dtype out_dt, const void *workspace,
+                       size_t workspace_bytes)
+{
+    moe_status st = check_sizes(T, H, I, E, K);
+    if (st != MOE_OK)
+        return st;
+    if ((dt != MOE_F32 && dt != MOE_BF16 && dt != MOE_FP8_E4M3) || (w.dt != MOE_F32 && w.dt != MOE_BF16 && w.dt != MOE_FP8_E4M3) ||
+        (out_dt != MOE_F32 && out_dt != MOE_BF16 && out_dt != MOE_FP8_E4M3))
+        return MOE_ERR_INVALID;
+    if (dt == MOE_FP8_E4M3 || out_dt == MOE_FP8_E4M3 || (w.dt != dt && !(dt == MOE_BF16 && w.dt == MOE_FP8_E4M3)))
+        return MOE_ERR_UNSUPPORTED;
+    if (w.dt == MOE_FP8_E4M3) {
+        if (w.block < 1 || H % w.block || I % w.block)
+            return MOE_ERR_INVALID;
+        if (w.block % 64)
+            return MOE_ERR_UNSUPPORTED;
+    }
+    if (T == 0)
+        return MOE_OK;
+    if (!x || !w.gate_up || !w.down || !out || (w.dt == MOE_FP8_E4M3 && (!w.gate_up_scales || !w.down_scales)))
+        return MOE_ERR_INVALID;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < layout(T, E, K, I).bytes)
+        return MOE_ERR_INVALID;
+    return MOE_OK;
+}
+
+template <Weights W, bool TAIL>
+void launch_gate_up(const ExpertArgs &a, int used, hipStream_t stream)
+{
+    hipLaunchKernelGGL((gate_up_kernel<W, TAIL>), dim3(static_cast<unsigned>(ceil_div(a.I, kTile)), static_cast<unsigned>(used)),
+                       dim3(kExpertThreads), 0, stream, a);
+}
+
+template <Weights W, bool TAIL>
+void launch_down(const ExpertArgs &a, hipStream_t stream)
+{
+    const size_t lds = sizeof(float) * kExpertWaves * kTile * static_cast<size_t>(a.T);
+    hipLaunchKernelGGL((down_kernel<W, TAIL>), dim3(static_cast<unsigned>(ceil_div(a.H, kTile))), dim3(kExpertThreads), lds,
+                       stream, a);
+}
+
+moe_status launch_experts(const void *x, int64_t T, int64_t H, int64_t I, int32_t E, int32_t K, const int32_t *topk_idx,
+                          const float *topk_w, const ExpertWeights &w, const void *bias, void *out, moe_dtype out_dt,
+                          char *ws, hipStream_t stream)
+{
+    const Layout l = layout(T, E, K, I);
+    const int slots = static_cast<int>(T * K), used = E < slots ? E : slots;
+    ExpertArgs a{};
+    a.plan = Plan{reinterpret_cast<int32_t *>(ws + l.head), reinterpret_cast<int32_t *>(ws + l.act),
+                  reinterpret_cast<int32_t *>(ws + l.start), reinterpret_cast<int32_t *>(ws + l.order)};
+    a.x = x;
+    a.topk_w = topk_w;
+    a.h = ws + l.h;
+    a.bias = bias;
+    a.out = out;
+    a.out_bf16 = out_dt == MOE_BF16;
+    a.T = static_cast<int>(T);
+    a.K = K;
+    a.H = static_cast<int>(H);
+    a.I = static_cast<int>(I);
+    a.block = w.block;
+    hipLaunchKernelGGL(few_token_plan_kernel, dim3(1), dim3(kPlanThreads), sizeof(uint16_t) * kPlanWaves * E, stream,
+                       topk_idx, slots, E, a.plan);
+    a.w = w.gate_up;
+    a.scales = w.gate_up_scales;
+    const bool f32 = w.dt == MOE_F32;
+    if (w.dt == MOE_FP8_E4M3)
+        launch_gate_up<kWFp8, false>(a, used, stream);
+    else if (H % (f32 ? 4 : 8) == 0)
+        f32 ? launch_gate_up<kWF32, false>(a, used, stream) : launch_gate_up<kWBf16, false>(a, used, stream);
+    else
+        f32 ? launch_gate_up<kWF32, true>(a, used, stream) : launch_gate_up<kWBf16, true>(a, used, stream);
+    a.w = w.down;
+    a.scales = w.down_scales;
+    if (w.dt == MOE_FP8_E4M3)
+        launch_down<kWFp8, false>(a, stream);
+    else if (I % (f32 ? 4 : 8) == 0)
+        f32 ? launch_down<kWF32, false>(a, stream) : launch_down<kWBf16, false>(a, stream);
+    else
+        f32 ? launch_down<kWF32, true>(a, stream) : launch_down<kWBf16, true>(a, stream);
+    return launch_status();
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status moe_few_token_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t K, size_t *bytes)
+{
+    using namespace moe;
+    if (!bytes)
+        return MOE_ERR_INVALID;
+    const moe_status st = check_sizes(T, H, I, E, K);
+    if (st != MOE_OK)
+        return st;
+    *bytes = T == 0 ? 0 : layout(T, E, K, I).bytes;
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_few_token_experts(const void *x, moe_dtype dt, int64_t T, int64_t H, int64_t I, int32_t E,
+                                            int32_t K, const int32_t *topk_idx, const float *topk_w,
+                                            const void *w_gate_up, const void *w_down, moe_dtype weight_dt,
+                                            const float *gate_up_scales, const float *down_scales, int32_t block,
+                                            const void *bias, void *out, moe_dtype out_dt, void *workspace,
+                                            size_t workspace_bytes, hipStream_t stream)
+{
+    using namespace moe;
+    const ExpertWeights w{w_gate_up, w_down, weight_dt, gate_up_scales, down_scales, block};
+    const moe_status st = check_layer(x, dt, T, H, I, E, K, w, out, out_dt, workspace, workspace_bytes);
+    if (st != MOE_OK || T == 0)
+        return st;
+    if (!topk_idx)
+        return MOE_ERR_INVALID;
+    return launch_experts(x, T, H, I, E, K, topk_idx, topk_w, w, bias, out, out_dt, static_cast<char *>(workspace), stream);
+}
+
+extern "C" moe_status moe_few_token_layer(const void *x, moe_dtype dt, const void *router, int64_t T, int64_t H,
+                                          int64_t I, int32_t E, int32_t K, int32_t route_group_size,
+                                          int32_t topk_groups, const void *w_gate_up, const void *w_down,
+                                          moe_dtype weight_dt, const float *gate_up_scales, const float *down_scales,
+                                          int32_t block, const void *bias, void *out, moe_dtype out_dt,
+                                          int32_t *topk_idx, float *topk_w, void *workspace, size_t workspace_bytes,
+                                          hipStream_t stream)
+{
+    using namespace moe;
+    const ExpertWeights w{w_gate_up, w_down, weight_dt, gate_up_scales, down_scales, block};
+    moe_status st = check_layer(x, dt, T, H, I, E, K, w, out, out_dt, workspace, workspace_bytes);
+    if (st != MOE_OK)
+        return st;
+    // the routing's own argument errors, before anything is launched
+    const int32_t gs = route_group_size > 0 ? route_group_size : 0;
+    st = gs ? moe_route_topk_grouped(nullptr, 0, E, K, gs, topk_groups, nullptr, nullptr, stream) : MOE_OK;
+    if (st != MOE_OK || T == 0)
+        return st;
+    if (!router || !topk_idx || !topk_w)
+        return MOE_ERR_INVALID;
+    char *ws = static_cast<char *>(workspace);
+    float *logits = reinterpret_cast<float *>(ws + layout(T, E, K, I).logits);
+    const dim3 grid(static_cast<unsigned>(E), static_cast<unsigned>(ceil_div(T, kRouterTokens)));
+    if (dt == MOE_F32)
+        hipLaunchKernelGGL(router_logits_kernel<float>, grid, dim3(kRouterThreads), 0, stream, static_cast<const float *>(x),
+                           static_cast<const float *>(router), static_cast<int>(T), static_cast<int>(H), E, logits);
+    else
+        hipLaunchKernelGGL(router_logits_kernel<uint16_t>, grid, dim3(kRouterThreads), 0, stream,
+                           static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(router), static_cast<int>(T),
+                           static_cast<int>(H), E, logits);
+    if ((st = launch_status()) != MOE_OK)
+        return st;
+    st = gs ? moe_route_topk_grouped(logits, T, E, K, gs, topk_groups, topk_idx, topk_w, stream)
+            : moe_route_topk(logits, T, E, K, topk_idx, topk_w, stream);
+    if (st != MOE_OK)
+        return st;
+    return launch_experts(x, T, H, I, E, K, topk_idx, topk_w, w, bias, out, out_dt, ws, stream);
+}

@@ -699,3 +699,112 @@ def rmsnorm_workspace_bytes(T: int, H: int) -> int:
     check("moe_add_rmsnorm_backward_workspace_size",
           lib().moe_add_rmsnorm_backward_workspace_size(T, H, ctypes.byref(n)))
     return int(n.value)
+
+
+# ---------------------------------------------------------------- the whole layer for a few tokens
+
+
+def few_token_workspace_bytes(T: int, H: int, I: int, E: int, K: int) -> int:
+    """Workspace bytes of few_token_layer and few_token_experts for these sizes."""
+    n = ctypes.c_size_t(0)
+    check("moe_few_token_workspace_size", lib().moe_few_token_workspace_size(T, H, I, E, K, ctypes.byref(n)))
+    return int(n.value)
+
+
+def _expert_weights(x, w_gate_up, w_down, gate_up_scales, down_scales):
+    """Checks of the expert weights; returns (T, H, I, E, rows dtype, weights dtype, block)."""
+    _need(x, "x", None, 2)
+    x_dt = _row_dt(x.dtype, "x")
+    T, H = x.shape
+    _need(w_gate_up, "w_gate_up", None, 3)
+    _need(w_down, "w_down", w_gate_up.dtype, 3)
+    w_dt = _hidden_dt(w_gate_up, "w_gate_up")
+    E, _, I = w_down.shape
+    if tuple(w_gate_up.shape) != (E, 2 * I, H) or w_down.shape[1] != H:
+        raise ValueError(f"w_gate_up must be [E, 2I, {H}] and w_down [E, {H}, I], got {tuple(w_gate_up.shape)} and "
+                         f"{tuple(w_down.shape)}")
+    if w_dt != MOE_FP8_E4M3:
+        if w_dt != x_dt:
+            raise TypeError(f"weights must have the type of x or hold FP8 codes (uint8), got {w_gate_up.dtype}")
+        if gate_up_scales is not None or down_scales is not None:
+            raise ValueError("scales belong to FP8 weights")
+        return T, H, I, E, x_dt, w_dt, 0
+    if x_dt != MOE_BF16:
+        raise TypeError("FP8 weights take bfloat16 rows")
+    _need(gate_up_scales, "gate_up_scales", torch.float32, 3)
+    _need(down_scales, "down_scales", torch.float32, 3)
+    nb = gate_up_scales.shape[2]
+    block = H // nb if nb > 0 and H % nb == 0 else 0
+    if block == 0 or I % block or tuple(gate_up_scales.shape) != (E, 2 * I, H // block) or \
+            tuple(down_scales.shape) != (E, H, I // block):
+        raise ValueError("scales must be [E, 2I, H/block] and [E, H, I/block] with one block that divides H and I")
+    return T, H, I, E, x_dt, w_dt, block
+
+
+def _few_token_out(x, bias, out, out_dtype):
+    if out is None:
+        out = torch.empty_like(x, dtype=out_dtype)
+    else:
+        _need(out, "out", out_dtype, 2)
+        if out.shape != x.shape:
+            raise ValueError(f"out must be {list(x.shape)}")
+    if bias is not None:
+        _need(bias, "bias", out.dtype, 2)
+        if bias.shape != x.shape:
+            raise ValueError(f"bias must be {list(x.shape)}")
+    return out, _row_dt(out.dtype, "out")
+
+
+def _few_token_ws(workspace, T, H, I, E, K, device):
+    if workspace is None:
+        return torch.empty(few_token_workspace_bytes(T, H, I, E, K), dtype=torch.uint8, device=device)
+    return _need(workspace, "workspace", torch.uint8, 1)
+
+
+def few_token_layer(x: torch.Tensor, router: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, k: int,
+                    gate_up_scales: Optional[torch.Tensor] = None, down_scales: Optional[torch.Tensor] = None,
+                    bias: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                    group_size: int = 0, topk_groups: int = 0, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None):
+    """The whole MoE layer for a few tokens (at most 256): router product (summed in double), route_topk, each
+    chosen expert's down(silu(gate) * up), the weighted merge and the optional bias (the residual stream, say; it
+    may be out itself). x [T, H] and router [E, H] float32 or bfloat16; w_gate_up [E, 2I, H] (gate rows first) and
+    w_down [E, H, I] of the same type, or FP8 codes with the scales of quantize_fp8 over their rows (blocks of a
+    multiple of 64). Returns (out [T, H], topk_idx, topk_w)."""
+    T, H, I, E, x_dt, w_dt, block = _expert_weights(x, w_gate_up, w_down, gate_up_scales, down_scales)
+    _need(router, "router", x.dtype, 2)
+    if tuple(router.shape) != (E, H):
+        raise ValueError(f"router must be [{E}, {H}]")
+    out, o_dt = _few_token_out(x, bias, out, out_dtype)
+    idx = torch.empty((T, k), dtype=torch.int32, device=x.device)
+    w = torch.empty((T, k), dtype=torch.float32, device=x.device)
+    workspace = _few_token_ws(workspace, T, H, I, E, k, x.device)
+    check("moe_few_token_layer", lib().moe_few_token_layer(
+        _p(x), x_dt, _p(router), T, H, I, E, k, group_size, topk_groups, _p(w_gate_up), _p(w_down), w_dt,
+        _p(gate_up_scales), _p(down_scales), block, _p(bias), _p(out), o_dt, _p(idx), _p(w), _p(workspace),
+        workspace.numel(), _stream()))
+    return out, idx, w
+
+
+def few_token_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: Optional[torch.Tensor], w_gate_up: torch.Tensor,
+                      w_down: torch.Tensor, gate_up_scales: Optional[torch.Tensor] = None,
+                      down_scales: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                      out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """few_token_layer after a routing that the caller has: ids outside [0, E) route nowhere (the experts of other
+    ranks, say), topk_w None means unit weights. Returns out [T, H]."""
+    T, H, I, E, x_dt, w_dt, block = _expert_weights(x, w_gate_up, w_down, gate_up_scales, down_scales)
+    _need(topk_idx, "topk_idx", torch.int32, 2)
+    if topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must have one row per row of x")
+    K = topk_idx.shape[1]
+    if topk_w is not None:
+        _need(topk_w, "topk_w", torch.float32, 2)
+        if topk_w.shape != topk_idx.shape:
+            raise ValueError("topk_w must have the shape of topk_idx")
+    out, o_dt = _few_token_out(x, bias, out, out_dtype)
+    workspace = _few_token_ws(workspace, T, H, I, E, K, x.device)
+    check("moe_few_token_experts", lib().moe_few_token_experts(
+        _p(x), x_dt, T, H, I, E, K, _p(topk_idx), _p(topk_w), _p(w_gate_up), _p(w_down), w_dt, _p(gate_up_scales),
+        _p(down_scales), block, _p(bias), _p(out), o_dt, _p(workspace), workspace.numel(), _stream()))
+    return out
