@@ -448,7 +448,7 @@ moe_status moe_add_rmsnorm_backward(const void *dout, moe_dtype dout_dt, const v
  *   (gate_up_scales [E, 2I, H/block], down_scales [E, H, I/block]); block must divide H and I (else
  *   MOE_ERR_INVALID) and be a multiple of 64 (else MOE_ERR_UNSUPPORTED). Other types of weights:
  *   MOE_ERR_UNSUPPORTED; block and scales are ignored without FP8.
- *   T <= MOE_MAX_FEW_TOKENS, H and I <= 2^24 (else MOE_ERR_UNSUPPORTED): for more tokens dispatch them.
+ *   T <= MOE_MAX_FEW_TOKENS, H and I <= 2^20 (else MOE_ERR_UNSUPPORTED): for more tokens dispatch them.
  * Weights of experts that no token uses are not read. Rows are independent: what is not finite in one token's row
  * or in an expert's weights reaches only the tokens that use it.
  * The workspace (16-byte aligned, contents need no initialisation and mean nothing after the call) must

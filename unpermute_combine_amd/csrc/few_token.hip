@@ -35,23 +35,24 @@ struct Acts {
     u32x4 v[W == kWFp8 ? 2 : 1];
 };
 
-// n <= N consecutive elements of type X at p + e, zeros past the row's end. The address need not be aligned beyond
-// its element.
-template <bool TAIL, int N, typename X, typename R>
-__device__ __forceinline__ void load_elems(const X *p, int e, int len, R &r)
+// A lane's consecutive elements, all of them inside the row. The address need not be aligned beyond its element.
+template <typename X, typename R>
+__device__ __forceinline__ void load_whole(const X *p, R &r)
 {
-    static_assert(sizeof(R) == N * sizeof(X), "one register set");
-    __builtin_memset(&r, 0, sizeof(r));
-    if (TAIL ? e + N <= len : e < len) {
-        __builtin_memcpy(&r, p + e, sizeof(r));
-    } else if (TAIL && e < len) {
-        X t[N] = {};
+    __builtin_memcpy(&r, p, sizeof(r));
+}
+
+// The same where the row ends at `len`: zeros past its end.
+template <typename X, typename R>
+__device__ __forceinline__ void load_tail(const X *row, int e, int len, R &r)
+{
+    constexpr int n = sizeof(R) / sizeof(X);
+    X t[n] = {};
 #pragma unroll
-        for (int i = 0; i < N - 1; ++i)
-            if (e + i < len)
-                t[i] = p[e + i];
-        __builtin_memcpy(&r, t, sizeof(r));
-    }
+    for (int i = 0; i < n; ++i)
+        if (e + i < len)
+            t[i] = row[e + i];
+    __builtin_memcpy(&r, t, sizeof(r));
 }
 
 template <Weights W> struct WeightType { typedef uint16_t type; };
@@ -236,82 +237,186 @@ struct ExpertArgs {
     void *h;                  // [slots][I] float32, or [slots][2][I] bf16
     const void *bias;
     void *out;
-    int T, K, H, I, block;
+    int T, K, H, I;
+    int nb;                   // FP8: scales per row of w,
+    uint32_t per_block;       // and 2^32 over the loads of one, rounded up (0: one load each)
     bool out_bf16;
     Plan plan;
 };
 
-template <Weights W>
-__device__ __forceinline__ float block_scale(const float *scales, int64_t row, int e, int nb, int block)
-{
-    return W == kWFp8 ? scales[row * nb + e / block] : 1.0f;
-}
-
-template <Weights W, bool TAIL>
-__global__ __launch_bounds__(kExpertThreads) void gate_up_kernel(ExpertArgs a)
-{
+// The products of NW rows of weights (one per lane column) with NT tiles of 16 tokens over a range of loads: LO adds
+// the activations' second bf16 row, `lo` elements behind the first. Loads go out U at a time, before the first of
+// them is used, so that each wavefront keeps U * NW KiB of weights in flight.
+template <Weights W, int NW, int NT, bool LO>
+struct Product {
     typedef typename WeightType<W>::type Wt;
     typedef typename ActType<W>::type X;
-    __shared__ f32x4 red[kExpertWaves][2][kWave];
+    const Wt *w[NW];
+    const float *scale[NW];
+    const X *x[NT];
+    int lo;
+    uint32_t per_block;
+    f32x4 acc[NW][NT];
+
+    // rows that lack a tile's token take another's row: what they give is not stored
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                acc[i][t] = f32x4{};
+    }
+
+    __device__ __forceinline__ void add(const u32x4 (&wr)[NW], const Acts<W> (&xa)[NT], const Acts<W> (&xl)[NT],
+                                        const float (&s)[NW])
+    {
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                f32x4 p = W == kWFp8 ? f32x4{} : acc[i][t];
+                p = multiply<W>(p, xa[t], wr[i]);
+                if (LO)
+                    p = multiply<W>(p, xl[t], wr[i]);
+                if (W == kWFp8)  // a load lies in one block of scales
+                    acc[i][t] += p * s[i];
+                else
+                    acc[i][t] = p;
+            }
+    }
+
+    template <int U>
+    __device__ __forceinline__ void batch(int l, int g)
+    {
+        u32x4 wr[U][NW];
+        Acts<W> xa[U][NT], xl[U][NT];
+        float s[U][NW];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = (l + u) * kLoadElems<W> + g * kLaneElems<W>;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+                load_whole(w[i] + e, wr[u][i]);
+                s[u][i] = W == kWFp8 ? scale[i][per_block ? __umulhi(l + u, per_block) : l + u] : 1.0f;
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                load_whole(x[t] + e, xa[u][t]);
+                if (LO)
+                    load_whole(x[t] + lo + e, xl[u][t]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            add(wr[u], xa[u], xl[u], s[u]);
+    }
+
+    __device__ __forceinline__ void run(int l, int l1, int len, int g)
+    {
+        // as many loads in flight as about 80 registers hold
+        constexpr int one = NW + NT * (LO ? 2 : 1) * (W == kWFp8 ? 2 : 1), U = one <= 5 ? 4 : one <= 10 ? 2 : 1;
+        const int whole = min(l1, len / kLoadElems<W>);
+        for (; l + U <= whole; l += U)
+            batch<U>(l, g);
+        if (U > 2 && l + 2 <= whole) {
+            batch<2>(l, g);
+            l += 2;
+        }
+        if (U > 1 && l < whole)
+            batch<1>(l++, g);
+        if (W != kWFp8 && l < l1) {  // the row's last load, partial
+            const int e = l * kLoadElems<W> + g * kLaneElems<W>;
+            u32x4 wr[NW];
+            Acts<W> xa[NT], xl[NT];
+            const float s[NW] = {};
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                load_tail(w[i], e, len, wr[i]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                load_tail(x[t], e, len, xa[t]);
+                if (LO)
+                    load_tail(x[t] + lo, e, len, xl[t]);
+            }
+            add(wr, xa, xl, s);
+        }
+    }
+};
+
+// SwiGLU of up to NT tiles of an expert's tokens, from row r0 of its n on.
+template <Weights W, int NT>
+__device__ __forceinline__ void gate_up_rows(const ExpertArgs &a, int64_t ex, int p0, int r0, int n,
+                                             f32x4 (*red)[kExpertWaves][2][kWave])
+{
+    typedef Product<W, 2, NT, false> P;
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, m = lane % kTile, g = lane / kTile;
+    const int c0 = blockIdx.x * kTile, col = min(c0 + m, a.I - 1);
+    P p;
+    p.clear();
+    p.lo = 0;
+    p.per_block = a.per_block;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // the gate's row, the up's row
+        const int64_t row = (ex * 2 + i) * a.I + col;
+        p.w[i] = static_cast<const typename P::Wt *>(a.w) + row * a.H;
+        p.scale[i] = a.scales + row * a.nb;
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = min(r0 + t * kTile + m, n - 1);
+        p.x[t] = static_cast<const typename P::X *>(a.x) + static_cast<int64_t>(a.plan.order[p0 + r] / a.K) * a.H;
+    }
+    const int loads = (a.H + kLoadElems<W> - 1) / kLoadElems<W>;
+    p.run(loads * wave / kExpertWaves, loads * (wave + 1) / kExpertWaves, a.H, g);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        red[t][wave][0][lane] = p.acc[0][t];
+        red[t][wave][1][lane] = p.acc[1][t];
+    }
+    __syncthreads();
+    // register r of lane l holds the tile's row 4 (l / 16) + r and column l % 16
+    for (int i = threadIdx.x; i < NT * kTile * kTile; i += kExpertThreads) {
+        const int t = i / (kTile * kTile), src = i % (kTile * kTile) / 4, r = i % 4;
+        const int row = r0 + t * kTile + 4 * (src / kTile) + r, c = c0 + src % kTile;
+        float gate = 0.0f, up = 0.0f;
+        for (int w = 0; w < kExpertWaves; ++w) {
+            gate += red[t][w][0][src][r];
+            up += red[t][w][1][src][r];
+        }
+        if (row < n && c < a.I) {
+            const float weight = a.topk_w ? a.topk_w[a.plan.order[p0 + row]] : 1.0f;
+            const float h = gate / (1.0f + expf(-gate)) * up * weight;
+            if (W == kWF32) {
+                static_cast<float *>(a.h)[static_cast<int64_t>(p0 + row) * a.I + c] = h;
+            } else {
+                uint16_t *hr = static_cast<uint16_t *>(a.h) + static_cast<int64_t>(p0 + row) * 2 * a.I;
+                const uint32_t hi = f32_to_bf16_bits(h);
+                const float rest = h - __uint_as_float(hi << 16);
+                hr[c] = static_cast<uint16_t>(hi);
+                // an infinite or NaN h is wholly in the first row
+                hr[a.I + c] = (hi & 0x7f80u) == 0x7f80u ? 0 : static_cast<uint16_t>(f32_to_bf16_bits(rest));
+            }
+        }
+    }
+    __syncthreads();
+}
+
+template <Weights W>
+__global__ __launch_bounds__(kExpertThreads, 4) void gate_up_kernel(ExpertArgs a)
+{
+    __shared__ f32x4 red[4][kExpertWaves][2][kWave];
     if (static_cast<int>(blockIdx.y) >= a.plan.head[0])
         return;
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, m = lane % kTile, g = lane / kTile;
     const int64_t ex = a.plan.act[blockIdx.y];
     const int p0 = a.plan.start[blockIdx.y], n = a.plan.start[blockIdx.y + 1] - p0;
-    const int c0 = blockIdx.x * kTile, col = min(c0 + m, a.I - 1);
-    const int64_t grow = ex * 2 * a.I + col, urow = grow + a.I;
-    const Wt *gw = static_cast<const Wt *>(a.w) + grow * a.H, *uw = static_cast<const Wt *>(a.w) + urow * a.H;
-    const int loads = (a.H + kLoadElems<W> - 1) / kLoadElems<W>;
-    const int l0 = loads * wave / kExpertWaves, l1 = loads * (wave + 1) / kExpertWaves;
-    const int nb = W == kWFp8 ? a.H / a.block : 0;
-    for (int r0 = 0; r0 < n; r0 += kTile) {
-        const bool live = r0 + m < n;
-        const X *xr = static_cast<const X *>(a.x) +
-                      static_cast<int64_t>(a.plan.order[p0 + (live ? r0 + m : 0)] / a.K) * a.H;
-        f32x4 ga{}, ua{};
-        for (int l = l0; l < l1; ++l) {
-            const int e = l * kLoadElems<W> + g * kLaneElems<W>;
-            u32x4 wg, wu;
-            Acts<W> xa;
-            load_elems<TAIL, kLaneElems<W>>(gw, e, a.H, wg);
-            load_elems<TAIL, kLaneElems<W>>(uw, e, a.H, wu);
-            load_elems<TAIL, kLaneElems<W>>(xr, e, live ? a.H : 0, xa);
-            if (W == kWFp8) {
-                ga += multiply<W>(f32x4{}, xa, wg) * block_scale<W>(a.scales, grow, l * kLoadElems<W>, nb, a.block);
-                ua += multiply<W>(f32x4{}, xa, wu) * block_scale<W>(a.scales, urow, l * kLoadElems<W>, nb, a.block);
-            } else {
-                ga = multiply<W>(ga, xa, wg);
-                ua = multiply<W>(ua, xa, wu);
-            }
-        }
-        red[wave][0][lane] = ga;
-        red[wave][1][lane] = ua;
-        __syncthreads();
-        // thread = (token row, column): row 4 (lane / 16) + r of the tile is in register r
-        if (threadIdx.x < kTile * kTile) {
-            const int src = threadIdx.x / 4, r = threadIdx.x % 4;
-            const int row = r0 + 4 * (src / kTile) + r, c = c0 + src % kTile;
-            float gate = 0.0f, up = 0.0f;
-            for (int w = 0; w < kExpertWaves; ++w) {
-                gate += red[w][0][src][r];
-                up += red[w][1][src][r];
-            }
-            if (row < n && c < a.I) {
-                const int slot = a.plan.order[p0 + row];
-                const float h = gate / (1.0f + expf(-gate)) * up * (a.topk_w ? a.topk_w[slot] : 1.0f);
-                if (W == kWF32) {
-                    static_cast<float *>(a.h)[static_cast<int64_t>(p0 + row) * a.I + c] = h;
-                } else {
-                    uint16_t *hr = static_cast<uint16_t *>(a.h) + static_cast<int64_t>(p0 + row) * 2 * a.I;
-                    const uint32_t hi = f32_to_bf16_bits(h);
-                    const float rest = h - __uint_as_float(hi << 16);
-                    hr[c] = static_cast<uint16_t>(hi);
-                    // an infinite or NaN h is wholly in the first row
-                    hr[a.I + c] = (hi & 0x7f80u) == 0x7f80u ? 0 : static_cast<uint16_t>(f32_to_bf16_bits(rest));
-                }
-            }
-        }
-        __syncthreads();
+    for (int r0 = 0; r0 < n; r0 += 4 * kTile) {
+        if (n - r0 <= kTile)
+            gate_up_rows<W, 1>(a, ex, p0, r0, n, red);
+        else if (n - r0 <= 2 * kTile)
+            gate_up_rows<W, 2>(a, ex, p0, r0, n, red);
+        else
+            gate_up_rows<W, 4>(a, ex, p0, r0, n, red);
     }
 }
 
@@ -319,64 +424,69 @@ __global__ __launch_bounds__(kExpertThreads) void gate_up_kernel(ExpertArgs a)
 // One workgroup per 16 columns of out, for all experts in use: the (expert, load) pairs in order are cut into one
 // stretch per wavefront, each wavefront adds its tiles into its own [T][16] sums in LDS when its expert changes, and
 // the wavefronts' sums are put together in order. No atomics: the result does not depend on timing.
-template <Weights W, bool TAIL>
-__global__ __launch_bounds__(kExpertThreads) void down_kernel(ExpertArgs a)
+template <Weights W, int NT>
+__device__ __forceinline__ void down_rows(const ExpertArgs &a, int64_t wrow, int p0, int r0, int n, int l0, int l1,
+                                          float *mine)
 {
-    typedef typename WeightType<W>::type Wt;
-    typedef typename ActType<W>::type X;
+    typedef Product<W, 1, NT, W != kWF32> P;
+    const int lane = threadIdx.x & (kWave - 1), m = lane % kTile, g = lane / kTile;
+    P p;
+    p.clear();
+    p.lo = a.I;
+    p.per_block = a.per_block;
+    p.w[0] = static_cast<const typename P::Wt *>(a.w) + wrow * a.I;
+    p.scale[0] = a.scales + wrow * a.nb;
+    int tok[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int q = p0 + min(r0 + t * kTile + m, n - 1);
+        p.x[t] = static_cast<const typename P::X *>(a.h) + static_cast<int64_t>(q) * (W == kWF32 ? 1 : 2) * a.I;
+        tok[t] = a.plan.order[q] / a.K;
+    }
+    p.run(l0, l1, a.I, g);
+    // this lane holds column m for each tile's rows 4 g .. 4 g + 3. A token that names the expert twice has two rows,
+    // neighbours: then the lane groups add one after the other
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const bool live = r0 + t * kTile + m < n;
+        const bool twice = __ballot(live && m > 0 && tok[t] == __shfl_up(tok[t], 1)) != 0;
+        for (int turn = 0; turn < (twice ? 4 : 1); ++turn) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int to = __shfl(tok[t], 4 * g + r);
+                if ((!twice || g == turn) && r0 + t * kTile + 4 * g + r < n)
+                    mine[to * kTile + m] += p.acc[0][t][r];
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+}
+
+template <Weights W>
+__global__ __launch_bounds__(kExpertThreads, 4) void down_kernel(ExpertArgs a)
+{
     extern __shared__ float sums[];  // [kExpertWaves][T][kTile]
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, m = lane % kTile, g = lane / kTile;
-    const int c0 = blockIdx.x * kTile, col = min(c0 + m, a.H - 1);
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int c0 = blockIdx.x * kTile, col = min(c0 + lane % kTile, a.H - 1);
     float *mine = sums + wave * a.T * kTile;
     for (int i = lane; i < a.T * kTile; i += kWave)
         mine[i] = 0.0f;
     __builtin_amdgcn_wave_barrier();
     const int loads = (a.I + kLoadElems<W> - 1) / kLoadElems<W>;
-    const int64_t all = static_cast<int64_t>(a.plan.head[0]) * loads;
-    const int64_t u1 = all * (wave + 1) / kExpertWaves;
-    const int nb = W == kWFp8 ? a.I / a.block : 0;
-    for (int64_t u = all * wave / kExpertWaves; u < u1;) {
-        const int i = static_cast<int>(u / loads), l0 = static_cast<int>(u - static_cast<int64_t>(i) * loads);
-        const int l1 = static_cast<int>(min(static_cast<int64_t>(loads), l0 + (u1 - u)));
+    const int all = a.plan.head[0] * loads;
+    const int u1 = static_cast<int64_t>(all) * (wave + 1) / kExpertWaves;
+    for (int u = static_cast<int64_t>(all) * wave / kExpertWaves; u < u1;) {
+        const int i = u / loads, l0 = u - i * loads, l1 = min(loads, l0 + (u1 - u));
         u += l1 - l0;
         const int p0 = a.plan.start[i], n = a.plan.start[i + 1] - p0;
         const int64_t wrow = static_cast<int64_t>(a.plan.act[i]) * a.H + col;
-        const Wt *w = static_cast<const Wt *>(a.w) + wrow * a.I;
-        for (int r0 = 0; r0 < n; r0 += kTile) {
-            const bool live = r0 + m < n;
-            const int p = p0 + (live ? r0 + m : 0);
-            const X *hr = static_cast<const X *>(a.h) + static_cast<int64_t>(p) * (W == kWF32 ? 1 : 2) * a.I;
-            f32x4 acc{};
-            for (int l = l0; l < l1; ++l) {
-                const int e = l * kLoadElems<W> + g * kLaneElems<W>;
-                u32x4 wd;
-                Acts<W> hi, lo;
-                load_elems<TAIL, kLaneElems<W>>(w, e, a.I, wd);
-                load_elems<TAIL, kLaneElems<W>>(hr, e, live ? a.I : 0, hi);
-                f32x4 part = W == kWFp8 ? f32x4{} : acc;
-                part = multiply<W>(part, hi, wd);
-                if (W != kWF32) {
-                    load_elems<TAIL, kLaneElems<W>>(hr + a.I, e, live ? a.I : 0, lo);
-                    part = multiply<W>(part, lo, wd);
-                }
-                if (W == kWFp8)
-                    acc += part * block_scale<W>(a.scales, wrow, l * kLoadElems<W>, nb, a.block);
-                else
-                    acc = part;
-            }
-            // this lane holds column m for the tile's rows 4 g .. 4 g + 3. A token that names the expert twice has two
-            // rows: then the lane groups add one after the other
-            const int tok = a.plan.order[p] / a.K;
-            const bool twice = __ballot(live && m > 0 && tok == __shfl_up(tok, 1)) != 0;
-            for (int turn = 0; turn < (twice ? 4 : 1); ++turn) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = __shfl(tok, 4 * g + r);
-                    if ((!twice || g == turn) && r0 + 4 * g + r < n)
-                        mine[t * kTile + m] += acc[r];
-                }
-                __builtin_amdgcn_wave_barrier();
-            }
+        for (int r0 = 0; r0 < n; r0 += 4 * kTile) {
+            if (n - r0 <= kTile)
+                down_rows<W, 1>(a, wrow, p0, r0, n, l0, l1, mine);
+            else if (n - r0 <= 2 * kTile)
+                down_rows<W, 2>(a, wrow, p0, r0, n, l0, l1, mine);
+            else
+                down_rows<W, 4>(a, wrow, p0, r0, n, l0, l1, mine);
         }
     }
     __syncthreads();
@@ -432,7 +542,7 @@ moe_status check_sizes(int64_t T, int64_t H, int64_t I, int32_t E, int32_t K)
 {
     if (T < 0 || H < 1 || I < 1 || E < 1 || K < 1 || K > E)
         return MOE_ERR_INVALID;
-    if (T > kMaxFewTokens || E > MOE_MAX_EXPERTS || K > MOE_MAX_TOPK || H > (1 << 24) || I > (1 << 24))
+    if (T > kMaxFewTokens || E > MOE_MAX_EXPERTS || K > MOE_MAX_TOPK || H > (1 << 20) || I > (1 << 20))
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
@@ -471,18 +581,22 @@ moe_status check_layer(const void *x, moe_dtype dt, int64_t T, int64_t H, int64_
     return MOE_OK;
 }
 
-template <Weights W, bool TAIL>
-void launch_gate_up(const ExpertArgs &a, int used, hipStream_t stream)
+template <Weights W>
+void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t stream)
 {
-    hipLaunchKernelGGL((gate_up_kernel<W, TAIL>), dim3(static_cast<unsigned>(ceil_div(a.I, kTile)), static_cast<unsigned>(used)),
+    // FP8: the scale of load l is l / (loads per block), by a multiplication (exact for l * block / 64 < 2^32)
+    const int lb = W == kWFp8 ? w.block / kLoadElems<kWFp8> : 1;
+    a.per_block = lb == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + lb - 1) / lb);
+    a.w = w.gate_up;
+    a.scales = w.gate_up_scales;
+    a.nb = W == kWFp8 ? a.H / w.block : 0;
+    hipLaunchKernelGGL((gate_up_kernel<W>), dim3(static_cast<unsigned>(ceil_div(a.I, kTile)), static_cast<unsigned>(used)),
                        dim3(kExpertThreads), 0, stream, a);
-}
-
-template <Weights W, bool TAIL>
-void launch_down(const ExpertArgs &a, hipStream_t stream)
-{
+    a.w = w.down;
+    a.scales = w.down_scales;
+    a.nb = W == kWFp8 ? a.I / w.block : 0;
     const size_t lds = sizeof(float) * kExpertWaves * kTile * static_cast<size_t>(a.T);
-    hipLaunchKernelGGL((down_kernel<W, TAIL>), dim3(static_cast<unsigned>(ceil_div(a.H, kTile))), dim3(kExpertThreads), lds,
+    hipLaunchKernelGGL((down_kernel<W>), dim3(static_cast<unsigned>(ceil_div(a.H, kTile))), dim3(kExpertThreads), lds,
                        stream, a);
 }
 
@@ -505,26 +619,14 @@ moe_status launch_experts(const void *x, int64_t T, int64_t H, int64_t I, int32_
     a.K = K;
     a.H = static_cast<int>(H);
     a.I = static_cast<int>(I);
-    a.block = w.block;
     hipLaunchKernelGGL(few_token_plan_kernel, dim3(1), dim3(kPlanThreads), sizeof(uint16_t) * kPlanWaves * E, stream,
                        topk_idx, slots, E, a.plan);
-    a.w = w.gate_up;
-    a.scales = w.gate_up_scales;
-    const bool f32 = w.dt == MOE_F32;
     if (w.dt == MOE_FP8_E4M3)
-        launch_gate_up<kWFp8, false>(a, used, stream);
-    else if (H % (f32 ? 4 : 8) == 0)
-        f32 ? launch_gate_up<kWF32, false>(a, used, stream) : launch_gate_up<kWBf16, false>(a, used, stream);
+        launch_products<kWFp8>(a, w, used, stream);
+    else if (w.dt == MOE_F32)
+        launch_products<kWF32>(a, w, used, stream);
     else
-        f32 ? launch_gate_up<kWF32, true>(a, used, stream) : launch_gate_up<kWBf16, true>(a, used, stream);
-    a.w = w.down;
-    a.scales = w.down_scales;
-    if (w.dt == MOE_FP8_E4M3)
-        launch_down<kWFp8, false>(a, stream);
-    else if (I % (f32 ? 4 : 8) == 0)
-        f32 ? launch_down<kWF32, false>(a, stream) : launch_down<kWBf16, false>(a, stream);
-    else
-        f32 ? launch_down<kWF32, true>(a, stream) : launch_down<kWBf16, true>(a, stream);
+        launch_products<kWBf16>(a, w, used, stream);
     return launch_status();
 }
 
