@@ -35,23 +35,16 @@ struct Acts {
     u32x4 v[W == kWFp8 ? 2 : 1];
 };
 
-// A lane's consecutive elements, all of them inside the row. The address need not be aligned beyond its element.
+// The first `rest` (or none, or all) of a lane's consecutive elements, zeros after them.
 template <typename X, typename R>
-__device__ __forceinline__ void load_whole(const X *p, R &r)
-{
-    __builtin_memcpy(&r, p, sizeof(r));
-}
-
-// The same where the row ends at `len`: zeros past its end.
-template <typename X, typename R>
-__device__ __forceinline__ void load_tail(const X *row, int e, int len, R &r)
+__device__ __forceinline__ void load_tail(const X *p, int rest, R &r)
 {
     constexpr int n = sizeof(R) / sizeof(X);
     X t[n] = {};
 #pragma unroll
     for (int i = 0; i < n; ++i)
-        if (e + i < len)
-            t[i] = row[e + i];
+        if (i < rest)
+            t[i] = p[i];
     __builtin_memcpy(&r, t, sizeof(r));
 }
 
@@ -141,12 +134,13 @@ struct Plan {
     int32_t *head;   // [0]: experts in use (n)
     int32_t *act;    // [n] their ids
     int32_t *start;  // [n + 1] first position of each in order
-    int32_t *order;  // [start[n]] slots
+    int32_t *order;  // [start[n]] slots,
+    int32_t *token;  // and the token of each
 };
 
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / kWave;
 
-__global__ __launch_bounds__(kPlanThreads) void few_token_plan_kernel(const int32_t *topk_idx, int n, int E, Plan plan)
+__global__ __launch_bounds__(kPlanThreads) void few_token_plan_kernel(const int32_t *topk_idx, int n, int E, int K, Plan plan)
 {
     extern __shared__ uint16_t cnt[];  // [kPlanWaves][E]: each wavefront's slots per expert, then its next position
     __shared__ uint32_t wave_total[kPlanWaves];
@@ -172,8 +166,10 @@ __global__ __launch_bounds__(kPlanThreads) void few_token_plan_kernel(const int3
             int pos = 0;
             if (e < E) {
                 pos = mine[e];
-                if (pass == 1)
+                if (pass == 1) {
                     plan.order[pos + rank] = s + lane;
+                    plan.token[pos + rank] = (s + lane) / K;
+                }
             }
             __builtin_amdgcn_wave_barrier();
             if (e < E && rank == 0)
@@ -227,6 +223,14 @@ __global__ __launch_bounds__(kPlanThreads) void few_token_plan_kernel(const int3
 // tiles meet in LDS. h goes out in the order of the plan, already multiplied by the slot's weight; beside bf16 or FP8
 // weights as two bf16 rows whose sum it is to 16 bits, so that the down product is one of bf16 operands without
 // bf16's rounding of h.
+// The wavefront's number as a value known to be the same in its lanes: which loads a wavefront takes decides branches
+// around matrix instructions, and these write every lane whatever the execution mask, so the branches have to be
+// scalar ones.
+__device__ __forceinline__ int wave_id()
+{
+    return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / kWave));
+}
+
 constexpr int kExpertThreads = 512, kExpertWaves = kExpertThreads / kWave;
 
 struct ExpertArgs {
@@ -245,20 +249,30 @@ struct ExpertArgs {
 };
 
 // The products of NW rows of weights (one per lane column) with NT tiles of 16 tokens over a range of loads: LO adds
-// the activations' second bf16 row, `lo` elements behind the first. Loads go out U at a time, before the first of
-// them is used, so that each wavefront keeps U * NW KiB of weights in flight.
+// the activations' second bf16 row, `lo` bytes behind the first. The loads run D ahead of the matrix instructions in
+// a ring of registers, so that each wavefront keeps D * NW KiB of weights in flight all the time. Addresses are a
+// uniform base, which moves, and a 32-bit offset in each lane, which does not.
 template <Weights W, int NW, int NT, bool LO>
 struct Product {
     typedef typename WeightType<W>::type Wt;
     typedef typename ActType<W>::type X;
-    const Wt *w[NW];
+    static constexpr int kSlotRegs = 4 * (NW + NT * (LO ? 2 : 1) * (W == kWFp8 ? 2 : 1)) + (W == kWFp8 ? NW : 0);
+    static constexpr int kRoom = ((W == kWFp8 ? 76 : 88) - 4 * NW * NT) / kSlotRegs;
+    static constexpr int D = kRoom > 6 ? 6 : kRoom < 1 ? 1 : kRoom;
+    static constexpr int kActBytes = kLoadElems<W> * sizeof(X);  // of a token's row per load
+    const char *w[NW], *x;
     const float *scale[NW];
-    const X *x[NT];
-    int lo;
+    uint32_t w_off, x_off[NT], s_off;
+    int64_t lo;
     uint32_t per_block;
     f32x4 acc[NW][NT];
 
-    // rows that lack a tile's token take another's row: what they give is not stored
+    struct Slot {
+        u32x4 w[NW];
+        Acts<W> x[NT], y[NT];
+        float s[NW];
+    };
+
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
@@ -268,78 +282,76 @@ struct Product {
                 acc[i][t] = f32x4{};
     }
 
-    __device__ __forceinline__ void add(const u32x4 (&wr)[NW], const Acts<W> (&xa)[NT], const Acts<W> (&xl)[NT],
-                                        const float (&s)[NW])
+    __device__ __forceinline__ void add(const Slot &q)
     {
 #pragma unroll
         for (int i = 0; i < NW; ++i)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 f32x4 p = W == kWFp8 ? f32x4{} : acc[i][t];
-                p = multiply<W>(p, xa[t], wr[i]);
+                p = multiply<W>(p, q.x[t], q.w[i]);
                 if (LO)
-                    p = multiply<W>(p, xl[t], wr[i]);
+                    p = multiply<W>(p, q.y[t], q.w[i]);
                 if (W == kWFp8)  // a load lies in one block of scales
-                    acc[i][t] += p * s[i];
+                    acc[i][t] += p * q.s[i];
                 else
                     acc[i][t] = p;
             }
     }
 
-    template <int U>
-    __device__ __forceinline__ void batch(int l, int g)
+    __device__ __forceinline__ void issue(Slot &q, int l)
     {
-        u32x4 wr[U][NW];
-        Acts<W> xa[U][NT], xl[U][NT];
-        float s[U][NW];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int e = (l + u) * kLoadElems<W> + g * kLaneElems<W>;
-#pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                load_whole(w[i] + e, wr[u][i]);
-                s[u][i] = W == kWFp8 ? scale[i][per_block ? __umulhi(l + u, per_block) : l + u] : 1.0f;
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                load_whole(x[t] + e, xa[u][t]);
-                if (LO)
-                    load_whole(x[t] + lo + e, xl[u][t]);
-            }
+        for (int i = 0; i < NW; ++i) {
+            __builtin_memcpy(&q.w[i], w[i] + static_cast<int64_t>(l) * 64 + w_off, 16);
+            if (W == kWFp8)
+                q.s[i] = (scale[i] + (per_block ? __umulhi(l, per_block) : l))[s_off];
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            add(wr[u], xa[u], xl[u], s[u]);
+        for (int t = 0; t < NT; ++t) {
+            const char *row = x + static_cast<int64_t>(l) * kActBytes;
+            __builtin_memcpy(&q.x[t], row + x_off[t], sizeof(q.x[t]));
+            if (LO)
+                __builtin_memcpy(&q.y[t], row + lo + x_off[t], sizeof(q.y[t]));
+        }
     }
 
-    __device__ __forceinline__ void run(int l, int l1, int len, int g)
+    // Loads l .. l1 - 1 of rows of len elements.
+    __device__ __forceinline__ void run(int l, int l1, int len)
     {
-        // as many loads in flight as about 80 registers hold
-        constexpr int one = NW + NT * (LO ? 2 : 1) * (W == kWFp8 ? 2 : 1), U = one <= 5 ? 4 : one <= 10 ? 2 : 1;
         const int whole = min(l1, len / kLoadElems<W>);
-        for (; l + U <= whole; l += U)
-            batch<U>(l, g);
-        if (U > 2 && l + 2 <= whole) {
-            batch<2>(l, g);
-            l += 2;
+        if (l < whole) {
+            Slot q[D];
+#pragma unroll
+            for (int u = 0; u < D; ++u)
+                issue(q[u], min(l + u, whole - 1));
+            for (; l + D < whole; l += D) {
+#pragma unroll
+                for (int u = 0; u < D; ++u) {
+                    add(q[u]);
+                    issue(q[u], min(l + D + u, whole - 1));
+                    __builtin_amdgcn_sched_barrier(0);  // left alone, the scheduler gathers the loop's loads at its end
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < D; ++u)
+                if (l + u < whole)
+                    add(q[u]);
         }
-        if (U > 1 && l < whole)
-            batch<1>(l++, g);
-        if (W != kWFp8 && l < l1) {  // the row's last load, partial
-            const int e = l * kLoadElems<W> + g * kLaneElems<W>;
-            u32x4 wr[NW];
-            Acts<W> xa[NT], xl[NT];
-            const float s[NW] = {};
+        if (W != kWFp8 && whole < l1) {  // the row's last load, partial
+            const int rest = len - whole * kLoadElems<W> - static_cast<int>(threadIdx.x % kWave / kTile) * kLaneElems<W>;
+            Slot z;
 #pragma unroll
             for (int i = 0; i < NW; ++i)
-                load_tail(w[i], e, len, wr[i]);
+                load_tail(reinterpret_cast<const Wt *>(w[i] + static_cast<int64_t>(whole) * 64 + w_off), rest, z.w[i]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                load_tail(x[t], e, len, xa[t]);
+                const char *row = x + static_cast<int64_t>(whole) * kActBytes + x_off[t];
+                load_tail(reinterpret_cast<const X *>(row), rest, z.x[t]);
                 if (LO)
-                    load_tail(x[t] + lo, e, len, xl[t]);
+                    load_tail(reinterpret_cast<const X *>(row + lo), rest, z.y[t]);
             }
-            add(wr, xa, xl, s);
+            add(z);
         }
     }
 };
@@ -350,25 +362,29 @@ __device__ __forceinline__ void gate_up_rows(const ExpertArgs &a, int64_t ex, in
                                              f32x4 (*red)[kExpertWaves][2][kWave])
 {
     typedef Product<W, 2, NT, false> P;
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, m = lane % kTile, g = lane / kTile;
-    const int c0 = blockIdx.x * kTile, col = min(c0 + m, a.I - 1);
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), m = lane % kTile, g = lane / kTile;
+    const int c0 = blockIdx.x * kTile, col = min(m, a.I - 1 - c0);
     P p;
     p.clear();
     p.lo = 0;
     p.per_block = a.per_block;
+    // columns and rows past the last one take its place: what they give is not stored
+    p.w_off = static_cast<uint32_t>(col * a.H) * sizeof(typename P::Wt) + 16 * g;
+    p.s_off = col * a.nb;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {  // the gate's row, the up's row
-        const int64_t row = (ex * 2 + i) * a.I + col;
-        p.w[i] = static_cast<const typename P::Wt *>(a.w) + row * a.H;
+    for (int i = 0; i < 2; ++i) {  // the gate's rows, the up's rows
+        const int64_t row = (ex * 2 + i) * a.I + c0;
+        p.w[i] = static_cast<const char *>(a.w) + row * a.H * sizeof(typename P::Wt);
         p.scale[i] = a.scales + row * a.nb;
     }
+    p.x = static_cast<const char *>(a.x);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int r = min(r0 + t * kTile + m, n - 1);
-        p.x[t] = static_cast<const typename P::X *>(a.x) + static_cast<int64_t>(a.plan.order[p0 + r] / a.K) * a.H;
+        p.x_off[t] = static_cast<uint32_t>(a.plan.token[p0 + r] * a.H) * sizeof(typename P::X) + P::kActBytes / 4 * g;
     }
     const int loads = (a.H + kLoadElems<W> - 1) / kLoadElems<W>;
-    p.run(loads * wave / kExpertWaves, loads * (wave + 1) / kExpertWaves, a.H, g);
+    p.run(loads * wave / kExpertWaves, loads * (wave + 1) / kExpertWaves, a.H);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         red[t][wave][0][lane] = p.acc[0][t];
@@ -402,16 +418,18 @@ __device__ __forceinline__ void gate_up_rows(const ExpertArgs &a, int64_t ex, in
     __syncthreads();
 }
 
-template <Weights W>
+// MANY: more than one tile's tokens, so that an expert may have several tiles.
+template <Weights W, bool MANY>
 __global__ __launch_bounds__(kExpertThreads, 4) void gate_up_kernel(ExpertArgs a)
 {
-    __shared__ f32x4 red[4][kExpertWaves][2][kWave];
-    if (static_cast<int>(blockIdx.y) >= a.plan.head[0])
-        return;
+    __shared__ f32x4 red[MANY ? 4 : 1][kExpertWaves][2][kWave];
+    // read together, before it is known whether there is such an expert: the arrays have these entries
+    const int used = a.plan.head[0], p0 = a.plan.start[blockIdx.y], n = a.plan.start[blockIdx.y + 1] - p0;
     const int64_t ex = a.plan.act[blockIdx.y];
-    const int p0 = a.plan.start[blockIdx.y], n = a.plan.start[blockIdx.y + 1] - p0;
-    for (int r0 = 0; r0 < n; r0 += 4 * kTile) {
-        if (n - r0 <= kTile)
+    if (static_cast<int>(blockIdx.y) >= used)
+        return;
+    for (int r0 = 0; r0 < n; r0 += (MANY ? 4 : 1) * kTile) {
+        if (!MANY || n - r0 <= kTile)
             gate_up_rows<W, 1>(a, ex, p0, r0, n, red);
         else if (n - r0 <= 2 * kTile)
             gate_up_rows<W, 2>(a, ex, p0, r0, n, red);
@@ -425,25 +443,30 @@ __global__ __launch_bounds__(kExpertThreads, 4) void gate_up_kernel(ExpertArgs a
 // stretch per wavefront, each wavefront adds its tiles into its own [T][16] sums in LDS when its expert changes, and
 // the wavefronts' sums are put together in order. No atomics: the result does not depend on timing.
 template <Weights W, int NT>
-__device__ __forceinline__ void down_rows(const ExpertArgs &a, int64_t wrow, int p0, int r0, int n, int l0, int l1,
+__device__ __forceinline__ void down_rows(const ExpertArgs &a, int64_t ex, int p0, int r0, int n, int l0, int l1,
                                           float *mine)
 {
     typedef Product<W, 1, NT, W != kWF32> P;
+    constexpr int rows = W == kWF32 ? 1 : 2;  // of h per slot
     const int lane = threadIdx.x & (kWave - 1), m = lane % kTile, g = lane / kTile;
+    const int c0 = blockIdx.x * kTile, col = min(m, a.H - 1 - c0);
     P p;
     p.clear();
-    p.lo = a.I;
+    p.lo = static_cast<int64_t>(a.I) * sizeof(typename P::X);
     p.per_block = a.per_block;
-    p.w[0] = static_cast<const typename P::Wt *>(a.w) + wrow * a.I;
-    p.scale[0] = a.scales + wrow * a.nb;
+    p.w_off = static_cast<uint32_t>(col * a.I) * sizeof(typename P::Wt) + 16 * g;
+    p.s_off = col * a.nb;
+    p.w[0] = static_cast<const char *>(a.w) + (ex * a.H + c0) * a.I * sizeof(typename P::Wt);
+    p.scale[0] = a.scales + (ex * a.H + c0) * a.nb;
+    p.x = static_cast<const char *>(a.h) + static_cast<int64_t>(p0 + r0) * rows * a.I * sizeof(typename P::X);
     int tok[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int q = p0 + min(r0 + t * kTile + m, n - 1);
-        p.x[t] = static_cast<const typename P::X *>(a.h) + static_cast<int64_t>(q) * (W == kWF32 ? 1 : 2) * a.I;
-        tok[t] = a.plan.order[q] / a.K;
+        const int r = min(t * kTile + m, n - 1 - r0);
+        p.x_off[t] = static_cast<uint32_t>(r * rows * a.I) * sizeof(typename P::X) + P::kActBytes / 4 * g;
+        tok[t] = a.plan.token[p0 + r0 + r];
     }
-    p.run(l0, l1, a.I, g);
+    p.run(l0, l1, a.I);
     // this lane holds column m for each tile's rows 4 g .. 4 g + 3. A token that names the expert twice has two rows,
     // neighbours: then the lane groups add one after the other
 #pragma unroll
@@ -462,12 +485,12 @@ __device__ __forceinline__ void down_rows(const ExpertArgs &a, int64_t wrow, int
     }
 }
 
-template <Weights W>
+template <Weights W, bool MANY>
 __global__ __launch_bounds__(kExpertThreads, 4) void down_kernel(ExpertArgs a)
 {
     extern __shared__ float sums[];  // [kExpertWaves][T][kTile]
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int c0 = blockIdx.x * kTile, col = min(c0 + lane % kTile, a.H - 1);
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
+    const int c0 = blockIdx.x * kTile;
     float *mine = sums + wave * a.T * kTile;
     for (int i = lane; i < a.T * kTile; i += kWave)
         mine[i] = 0.0f;
@@ -479,14 +502,14 @@ __global__ __launch_bounds__(kExpertThreads, 4) void down_kernel(ExpertArgs a)
         const int i = u / loads, l0 = u - i * loads, l1 = min(loads, l0 + (u1 - u));
         u += l1 - l0;
         const int p0 = a.plan.start[i], n = a.plan.start[i + 1] - p0;
-        const int64_t wrow = static_cast<int64_t>(a.plan.act[i]) * a.H + col;
-        for (int r0 = 0; r0 < n; r0 += 4 * kTile) {
-            if (n - r0 <= kTile)
-                down_rows<W, 1>(a, wrow, p0, r0, n, l0, l1, mine);
+        const int64_t ex = a.plan.act[i];
+        for (int r0 = 0; r0 < n; r0 += (MANY ? 4 : 1) * kTile) {
+            if (!MANY || n - r0 <= kTile)
+                down_rows<W, 1>(a, ex, p0, r0, n, l0, l1, mine);
             else if (n - r0 <= 2 * kTile)
-                down_rows<W, 2>(a, wrow, p0, r0, n, l0, l1, mine);
+                down_rows<W, 2>(a, ex, p0, r0, n, l0, l1, mine);
             else
-                down_rows<W, 4>(a, wrow, p0, r0, n, l0, l1, mine);
+                down_rows<W, 4>(a, ex, p0, r0, n, l0, l1, mine);
         }
     }
     __syncthreads();
@@ -515,7 +538,7 @@ size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
 // The workspace: logits, plan, h.
 struct Layout {
-    size_t logits, head, act, start, order, h, bytes;
+    size_t logits, head, act, start, order, token, h, bytes;
 };
 
 Layout layout(int64_t T, int64_t E, int64_t K, int64_t I)
@@ -533,6 +556,7 @@ Layout layout(int64_t T, int64_t E, int64_t K, int64_t I)
     l.act = take(4 * used);
     l.start = take(4 * (used + 1));
     l.order = take(4 * slots);
+    l.token = take(4 * slots);
     l.h = take(4 * slots * I);
     l.bytes = at;
     return l;
@@ -581,7 +605,7 @@ moe_status check_layer(const void *x, moe_dtype dt, int64_t T, int64_t H, int64_
     return MOE_OK;
 }
 
-template <Weights W>
+template <Weights W, bool MANY>
 void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t stream)
 {
     // FP8: the scale of load l is l / (loads per block), by a multiplication (exact for l * block / 64 < 2^32)
@@ -590,14 +614,24 @@ void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t
     a.w = w.gate_up;
     a.scales = w.gate_up_scales;
     a.nb = W == kWFp8 ? a.H / w.block : 0;
-    hipLaunchKernelGGL((gate_up_kernel<W>), dim3(static_cast<unsigned>(ceil_div(a.I, kTile)), static_cast<unsigned>(used)),
+    hipLaunchKernelGGL((gate_up_kernel<W, MANY>),
+                       dim3(static_cast<unsigned>(ceil_div(a.I, kTile)), static_cast<unsigned>(used)),
                        dim3(kExpertThreads), 0, stream, a);
     a.w = w.down;
     a.scales = w.down_scales;
     a.nb = W == kWFp8 ? a.I / w.block : 0;
     const size_t lds = sizeof(float) * kExpertWaves * kTile * static_cast<size_t>(a.T);
-    hipLaunchKernelGGL((down_kernel<W>), dim3(static_cast<unsigned>(ceil_div(a.H, kTile))), dim3(kExpertThreads), lds,
+    hipLaunchKernelGGL((down_kernel<W, MANY>), dim3(static_cast<unsigned>(ceil_div(a.H, kTile))), dim3(kExpertThreads), lds,
                        stream, a);
+}
+
+template <Weights W>
+void launch_products_of(const ExpertArgs &a, const ExpertWeights &w, int used, hipStream_t stream)
+{
+    if (a.T <= kTile)
+        launch_products<W, false>(a, w, used, stream);
+    else
+        launch_products<W, true>(a, w, used, stream);
 }
 
 moe_status launch_experts(const void *x, int64_t T, int64_t H, int64_t I, int32_t E, int32_t K, const int32_t *topk_idx,
@@ -608,7 +642,8 @@ moe_status launch_experts(const void *x, int64_t T, int64_t H, int64_t I, int32_
     const int slots = static_cast<int>(T * K), used = E < slots ? E : slots;
     ExpertArgs a{};
     a.plan = Plan{reinterpret_cast<int32_t *>(ws + l.head), reinterpret_cast<int32_t *>(ws + l.act),
-                  reinterpret_cast<int32_t *>(ws + l.start), reinterpret_cast<int32_t *>(ws + l.order)};
+                  reinterpret_cast<int32_t *>(ws + l.start), reinterpret_cast<int32_t *>(ws + l.order),
+                  reinterpret_cast<int32_t *>(ws + l.token)};
     a.x = x;
     a.topk_w = topk_w;
     a.h = ws + l.h;
@@ -620,13 +655,13 @@ moe_status launch_experts(const void *x, int64_t T, int64_t H, int64_t I, int32_
     a.H = static_cast<int>(H);
     a.I = static_cast<int>(I);
     hipLaunchKernelGGL(few_token_plan_kernel, dim3(1), dim3(kPlanThreads), sizeof(uint16_t) * kPlanWaves * E, stream,
-                       topk_idx, slots, E, a.plan);
+                       topk_idx, slots, E, K, a.plan);
     if (w.dt == MOE_FP8_E4M3)
-        launch_products<kWFp8>(a, w, used, stream);
+        launch_products_of<kWFp8>(a, w, used, stream);
     else if (w.dt == MOE_F32)
-        launch_products<kWF32>(a, w, used, stream);
+        launch_products_of<kWF32>(a, w, used, stream);
     else
-        launch_products<kWBf16>(a, w, used, stream);
+        launch_products_of<kWBf16>(a, w, used, stream);
     return launch_status();
 }
 
