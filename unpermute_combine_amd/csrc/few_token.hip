@@ -88,41 +88,186 @@ __device__ __forceinline__ f32x4 multiply(f32x4 acc, const Acts<W> &x, const u32
 }
 
 // ---------------------------------------------------------------- router
-// One workgroup per (expert, kRouterTokens tokens). The sums are double so that which experts are picked does not
-// depend on the order of a float32 sum; products of float32 or bf16 values are exact in double or rounded to it.
-constexpr int kRouterThreads = 256, kRouterTokens = 8;
+// logits = x router^T in double (matrix instructions 16x16x4): which experts are picked then does not depend on the
+// order of a float32 sum, and the products of float32 or bf16 values are exact. A workgroup takes 16 experts, 16 tokens
+// and one of `splits` parts of the hidden dimension, its wavefronts a quarter of that each; the parts' sums are put
+// together in order where the logits are used.
+constexpr int kRouterThreads = 256, kRouterWaves = kRouterThreads / kWave;
+constexpr int kRouterElems = 32;  // of a row per step: 8 in each lane group
+
+typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float to_f32(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
 
-template <typename X>
-__global__ __launch_bounds__(kRouterThreads) void router_logits_kernel(const X *x, const X *router, int T, int H, int E,
-                                                                       float *logits)
+// The wavefront's number as a value known to be the same in its lanes: which loads a wavefront takes decides branches
+// around matrix instructions, and these write every lane whatever the execution mask, so the branches have to be
+// scalar ones.
+__device__ __forceinline__ int wave_id()
 {
-    __shared__ double sh[kRouterThreads / kWave][kRouterTokens];
-    const int e = blockIdx.x, t0 = blockIdx.y * kRouterTokens;
-    const X *r = router + static_cast<int64_t>(e) * H;
-    double acc[kRouterTokens] = {};
-    for (int j = threadIdx.x; j < H; j += kRouterThreads) {
-        const double w = to_f32(r[j]);
+    return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / kWave));
+}
+
+// Parts of the hidden dimension: a workgroup for each CU, and at least one step a wavefront.
+int router_splits(int64_t T, int64_t E, int64_t H)
+{
+    const int64_t tiles = ceil_div(T, kTile) * ceil_div(E, kTile), most = ceil_div(H, kRouterElems * kRouterWaves);
+    const int64_t want = ceil_div(256, tiles);
+    return static_cast<int>(want < most ? want : most);
+}
+
+template <typename X>
+__global__ __launch_bounds__(kRouterThreads) void router_kernel(const X *x, const X *router, int T, int H, int E,
+                                                                double *part)
+{
+    struct Elems {
+        X v[8];
+    };
+    __shared__ f64x4 red[kRouterWaves][kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), m = lane % kTile, g = lane / kTile;
+    const int e0 = blockIdx.x * kTile, t0 = blockIdx.y * kTile;
+    const X *xr = x + static_cast<int64_t>(min(t0 + m, T - 1)) * H, *rr = router + static_cast<int64_t>(min(e0 + m, E - 1)) * H;
+    const int steps = (H + kRouterElems - 1) / kRouterElems, parts = gridDim.z * kRouterWaves;
+    const int mine = blockIdx.z * kRouterWaves + wave;
+    const int s1 = static_cast<int64_t>(steps) * (mine + 1) / parts;
+    f64x4 acc{};
+    for (int s = static_cast<int64_t>(steps) * mine / parts; s < s1; ++s) {
+        const int j = s * kRouterElems + g * 8;
+        Elems a{}, b{};
+        if (j + 8 <= H) {
+            __builtin_memcpy(&a, xr + j, sizeof(a));
+            __builtin_memcpy(&b, rr + j, sizeof(b));
+        } else {
+            load_tail(xr + j, H - j, a);
+            load_tail(rr + j, H - j, b);
+        }
 #pragma unroll
-        for (int i = 0; i < kRouterTokens; ++i)
-            if (t0 + i < T)
-                acc[i] = fma(static_cast<double>(to_f32(x[static_cast<int64_t>(t0 + i) * H + j])), w, acc[i]);
+        for (int i = 0; i < 8; ++i)
+            acc = __builtin_amdgcn_mfma_f64_16x16x4f64(to_f32(a.v[i]), to_f32(b.v[i]), acc, 0, 0, 0);
     }
-#pragma unroll
-    for (int i = 0; i < kRouterTokens; ++i) {
-        for (int off = kWave / 2; off >= 1; off >>= 1)
-            acc[i] += __shfl_xor(acc[i], off);
-        if ((threadIdx.x & (kWave - 1)) == 0)
-            sh[threadIdx.x / kWave][i] = acc[i];
-    }
+    red[wave][lane] = acc;
     __syncthreads();
-    if (threadIdx.x < kRouterTokens && t0 + static_cast<int>(threadIdx.x) < T) {
-        double s = 0.0;
-        for (int w = 0; w < kRouterThreads / kWave; ++w)
-            s += sh[w][threadIdx.x];
-        logits[static_cast<int64_t>(t0 + threadIdx.x) * E + e] = static_cast<float>(s);
+    // register r of lane l holds the tile's token l / 16 + 4 r and expert l % 16
+    const int src = threadIdx.x / 4, r = threadIdx.x % 4, t = t0 + src / kTile + 4 * r, e = e0 + src % kTile;
+    double v = 0.0;
+    for (int w = 0; w < kRouterWaves; ++w)
+        v += red[w][src][r];
+    if (t < T && e < E)
+        part[(static_cast<int64_t>(blockIdx.z) * T + t) * E + e] = v;
+}
+
+// N logits, each the sum of its parts in order; the loads of several parts are in flight together (one after the
+// other they took 37 us of a T = 1, E = 256 call).
+template <int N>
+__device__ __forceinline__ void logits_of(const double *part, int splits, const int (&at)[N], int64_t all, float (&out)[N])
+{
+    constexpr int U = N > 4 ? 2 : 8;
+    double v[N] = {};
+    for (int s = 0; s < splits; s += U) {
+        double p[U][N];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                p[u][n] = part[min(s + u, splits - 1) * all + at[n]];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                v[n] += s + u < splits ? p[u][n] : 0.0;
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        out[n] = static_cast<float>(v[n]);
+}
+
+// The logits themselves, for the group-limited routing.
+__global__ __launch_bounds__(kRouterThreads) void router_sum_kernel(const double *part, int splits, int all, float *logits)
+{
+    const int i = blockIdx.x * kRouterThreads + threadIdx.x;
+    if (i >= all)
+        return;
+    float v[1];
+    logits_of<1>(part, splits, {i}, all, v);
+    logits[i] = v[0];
+}
+
+// ---------------------------------------------------------------- routing
+// moe_route_topk of one token by one wavefront: lane l holds experts l, l + 64, ...; each of the K rounds takes the
+// largest key of the wavefront, of equal ones that of the lowest expert. The softmax as there: double, in slot order.
+constexpr int kDppQuadXor1 = 0xb1, kDppQuadXor2 = 0x4e, kDppRowHalfMirror = 0x141, kDppRowMirror = 0x140;
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v)
+{
+    return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, false)));
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    v = max_dpp<kDppRowMirror>(max_dpp<kDppRowHalfMirror>(max_dpp<kDppQuadXor2>(max_dpp<kDppQuadXor1>(v))));
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    return max(max(a, b), max(c, d));
+}
+
+template <int J>
+__device__ __forceinline__ void route_token(const double *part, int splits, int T, int t, int E, int K,
+                                            int32_t *topk_idx, float *topk_w)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    uint32_t key[J];  // 0: no expert, or taken
+    int at[J];
+    float logit[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        at[j] = t * E + min(lane + kWave * j, E - 1);
+    logits_of<J>(part, splits, at, static_cast<int64_t>(T) * E, logit);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        key[j] = lane + kWave * j < E ? orderable(logit[j]) : 0u;
+    uint32_t slot_key = 0, first = 0;
+    int slot_id = -1;  // of slot `lane`
+    for (int k = 0; k < K; ++k) {
+        uint32_t best = 0;
+        int of = 0;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const bool more = key[j] > best;
+            best = more ? key[j] : best;
+            of = more ? j : of;
+        }
+        const uint32_t top = wave_max(best);
+        if (top == 0)  // only where logits are not numbers
+            break;
+        const uint64_t have = __ballot(best == top);
+        int id = 0;
+        if ((have & (have - 1)) == 0) {
+            const int l = __builtin_ctzll(have);
+            id = l + kWave * __builtin_amdgcn_readlane(of, l);
+        } else {  // equal logits: the lowest id, as the largest of their complements
+            id = static_cast<int>(~wave_max(best == top ? ~static_cast<uint32_t>(lane + kWave * of) : 0u));
+        }
+        if (k == 0)
+            first = top;
+        if (lane == k) {
+            slot_key = top;
+            slot_id = id;
+        }
+        if (lane == id % kWave) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (j == id / kWave)
+                    key[j] = 0;
+        }
+    }
+    const double ex = lane < K ? exp(static_cast<double>(from_orderable(slot_key)) - static_cast<double>(from_orderable(first))) : 0.0;
+    double z = 0.0;
+    for (int k = 0; k < K; ++k)
+        z += __shfl(ex, k);
+    if (lane < K) {
+        topk_idx[static_cast<int64_t>(t) * K + lane] = slot_id;
+        topk_w[static_cast<int64_t>(t) * K + lane] = static_cast<float>(ex / z);
     }
 }
 
@@ -140,7 +285,7 @@ struct Plan {
 
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / kWave;
 
-__global__ __launch_bounds__(kPlanThreads) void few_token_plan_kernel(const int32_t *topk_idx, int n, int E, int K, Plan plan)
+__device__ __forceinline__ void make_plan(const int32_t *topk_idx, int n, int E, int K, const Plan &plan)
 {
     extern __shared__ uint16_t cnt[];  // [kPlanWaves][E]: each wavefront's slots per expert, then its next position
     __shared__ uint32_t wave_total[kPlanWaves];
@@ -218,19 +363,31 @@ __global__ __launch_bounds__(kPlanThreads) void few_token_plan_kernel(const int3
     }
 }
 
+__global__ __launch_bounds__(kPlanThreads) void few_token_plan_kernel(const int32_t *topk_idx, int n, int E, int K, Plan plan)
+{
+    make_plan(topk_idx, n, E, K, plan);
+}
+
+// The routing of up to kPlanWaves tokens (one each wavefront) and the plan of it in one launch, of more tokens the
+// routing alone, kPlanWaves tokens a workgroup.
+template <int J, bool PLAN>
+__global__ __launch_bounds__(kPlanThreads) void few_token_route_kernel(const double *part, int splits, int T, int E, int K,
+                                                                       int32_t *topk_idx, float *topk_w, Plan plan)
+{
+    const int t = blockIdx.x * kPlanWaves + wave_id();
+    if (t < T)
+        route_token<J>(part, splits, T, t, E, K, topk_idx, topk_w);
+    if (PLAN) {
+        __syncthreads();  // the workgroup's own stores of topk_idx have been done
+        make_plan(topk_idx, T * K, E, K, plan);
+    }
+}
+
 // ---------------------------------------------------------------- gate and up products
 // One workgroup per (16 columns of h, expert in use): its wavefronts share the hidden dimension's loads, and their
 // tiles meet in LDS. h goes out in the order of the plan, already multiplied by the slot's weight; beside bf16 or FP8
 // weights as two bf16 rows whose sum it is to 16 bits, so that the down product is one of bf16 operands without
 // bf16's rounding of h.
-// The wavefront's number as a value known to be the same in its lanes: which loads a wavefront takes decides branches
-// around matrix instructions, and these write every lane whatever the execution mask, so the branches have to be
-// scalar ones.
-__device__ __forceinline__ int wave_id()
-{
-    return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / kWave));
-}
-
 constexpr int kExpertThreads = 512, kExpertWaves = kExpertThreads / kWave;
 
 struct ExpertArgs {
@@ -536,12 +693,12 @@ __global__ __launch_bounds__(kExpertThreads, 4) void down_kernel(ExpertArgs a)
 // ---------------------------------------------------------------- host side
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
-// The workspace: logits, plan, h.
+// The workspace: parts of the logits, logits, plan, h.
 struct Layout {
-    size_t logits, head, act, start, order, token, h, bytes;
+    size_t part, logits, head, act, start, order, token, h, bytes;
 };
 
-Layout layout(int64_t T, int64_t E, int64_t K, int64_t I)
+Layout layout(int64_t T, int64_t H, int64_t E, int64_t K, int64_t I)
 {
     Layout l{};
     const int64_t slots = T * K, used = E < slots ? E : slots;
@@ -551,6 +708,7 @@ Layout layout(int64_t T, int64_t E, int64_t K, int64_t I)
         at += round16(n);
         return here;
     };
+    l.part = take(8 * router_splits(T, E, H) * T * E);
     l.logits = take(4 * T * E);
     l.head = take(4);
     l.act = take(4 * used);
@@ -569,6 +727,13 @@ moe_status check_sizes(int64_t T, int64_t H, int64_t I, int32_t E, int32_t K)
     if (T > kMaxFewTokens || E > MOE_MAX_EXPERTS || K > MOE_MAX_TOPK || H > (1 << 20) || I > (1 << 20))
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
+}
+
+Plan plan_in(char *ws, const Layout &l)
+{
+    return Plan{reinterpret_cast<int32_t *>(ws + l.head), reinterpret_cast<int32_t *>(ws + l.act),
+                reinterpret_cast<int32_t *>(ws + l.start), reinterpret_cast<int32_t *>(ws + l.order),
+                reinterpret_cast<int32_t *>(ws + l.token)};
 }
 
 struct ExpertWeights {
@@ -600,10 +765,12 @@ moe_status check_layer(const void *x, moe_dtype dt, int64_t T, int64_t H, int64_
         return MOE_OK;
     if (!x || !w.gate_up || !w.down || !out || (w.dt == MOE_FP8_E4M3 && (!w.gate_up_scales || !w.down_scales)))
         return MOE_ERR_INVALID;
-    if (!workspace || !aligned16(workspace) || workspace_bytes < layout(T, E, K, I).bytes)
+    if (!workspace || !aligned16(workspace) || workspace_bytes < layout(T, H, E, K, I).bytes)
         return MOE_ERR_INVALID;
     return MOE_OK;
 }
+
+size_t plan_lds(int E) { return sizeof(uint16_t) * kPlanWaves * static_cast<size_t>(E); }
 
 template <Weights W, bool MANY>
 void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t stream)
@@ -636,14 +803,12 @@ void launch_products_of(const ExpertArgs &a, const ExpertWeights &w, int used, h
 
 moe_status launch_experts(const void *x, int64_t T, int64_t H, int64_t I, int32_t E, int32_t K, const int32_t *topk_idx,
                           const float *topk_w, const ExpertWeights &w, const void *bias, void *out, moe_dtype out_dt,
-                          char *ws, hipStream_t stream)
+                          char *ws, bool planned, hipStream_t stream)
 {
-    const Layout l = layout(T, E, K, I);
+    const Layout l = layout(T, H, E, K, I);
     const int slots = static_cast<int>(T * K), used = E < slots ? E : slots;
     ExpertArgs a{};
-    a.plan = Plan{reinterpret_cast<int32_t *>(ws + l.head), reinterpret_cast<int32_t *>(ws + l.act),
-                  reinterpret_cast<int32_t *>(ws + l.start), reinterpret_cast<int32_t *>(ws + l.order),
-                  reinterpret_cast<int32_t *>(ws + l.token)};
+    a.plan = plan_in(ws, l);
     a.x = x;
     a.topk_w = topk_w;
     a.h = ws + l.h;
@@ -654,8 +819,9 @@ moe_status launch_experts(const void *x, int64_t T, int64_t H, int64_t I, int32_
     a.K = K;
     a.H = static_cast<int>(H);
     a.I = static_cast<int>(I);
-    hipLaunchKernelGGL(few_token_plan_kernel, dim3(1), dim3(kPlanThreads), sizeof(uint16_t) * kPlanWaves * E, stream,
-                       topk_idx, slots, E, K, a.plan);
+    if (!planned)
+        hipLaunchKernelGGL(few_token_plan_kernel, dim3(1), dim3(kPlanThreads), plan_lds(E), stream, topk_idx, slots, E, K,
+                           a.plan);
     if (w.dt == MOE_FP8_E4M3)
         launch_products_of<kWFp8>(a, w, used, stream);
     else if (w.dt == MOE_F32)
@@ -676,7 +842,7 @@ extern "C" moe_status moe_few_token_workspace_size(int64_t T, int64_t H, int64_t
     const moe_status st = check_sizes(T, H, I, E, K);
     if (st != MOE_OK)
         return st;
-    *bytes = T == 0 ? 0 : layout(T, E, K, I).bytes;
+    *bytes = T == 0 ? 0 : layout(T, H, E, K, I).bytes;
     return MOE_OK;
 }
 
@@ -694,7 +860,8 @@ extern "C" moe_status moe_few_token_experts(const void *x, moe_dtype dt, int64_t
         return st;
     if (!topk_idx)
         return MOE_ERR_INVALID;
-    return launch_experts(x, T, H, I, E, K, topk_idx, topk_w, w, bias, out, out_dt, static_cast<char *>(workspace), stream);
+    return launch_experts(x, T, H, I, E, K, topk_idx, topk_w, w, bias, out, out_dt, static_cast<char *>(workspace),
+                          false, stream);
 }
 
 extern "C" moe_status moe_few_token_layer(const void *x, moe_dtype dt, const void *router, int64_t T, int64_t H,
@@ -718,20 +885,42 @@ extern "C" moe_status moe_few_token_layer(const void *x, moe_dtype dt, const voi
     if (!router || !topk_idx || !topk_w)
         return MOE_ERR_INVALID;
     char *ws = static_cast<char *>(workspace);
-    float *logits = reinterpret_cast<float *>(ws + layout(T, E, K, I).logits);
-    const dim3 grid(static_cast<unsigned>(E), static_cast<unsigned>(ceil_div(T, kRouterTokens)));
+    const Layout l = layout(T, H, E, K, I);
+    double *part = reinterpret_cast<double *>(ws + l.part);
+    const int Ti = static_cast<int>(T), Hi = static_cast<int>(H), splits = router_splits(T, E, H);
+    const dim3 grid(static_cast<unsigned>(ceil_div(E, kTile)), static_cast<unsigned>(ceil_div(T, kTile)),
+                    static_cast<unsigned>(splits));
     if (dt == MOE_F32)
-        hipLaunchKernelGGL(router_logits_kernel<float>, grid, dim3(kRouterThreads), 0, stream, static_cast<const float *>(x),
-                           static_cast<const float *>(router), static_cast<int>(T), static_cast<int>(H), E, logits);
+        hipLaunchKernelGGL(router_kernel<float>, grid, dim3(kRouterThreads), 0, stream, static_cast<const float *>(x),
+                           static_cast<const float *>(router), Ti, Hi, E, part);
     else
-        hipLaunchKernelGGL(router_logits_kernel<uint16_t>, grid, dim3(kRouterThreads), 0, stream,
-                           static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(router), static_cast<int>(T),
-                           static_cast<int>(H), E, logits);
-    if ((st = launch_status()) != MOE_OK)
-        return st;
-    st = gs ? moe_route_topk_grouped(logits, T, E, K, gs, topk_groups, topk_idx, topk_w, stream)
-            : moe_route_topk(logits, T, E, K, topk_idx, topk_w, stream);
-    if (st != MOE_OK)
-        return st;
-    return launch_experts(x, T, H, I, E, K, topk_idx, topk_w, w, bias, out, out_dt, ws, stream);
+        hipLaunchKernelGGL(router_kernel<uint16_t>, grid, dim3(kRouterThreads), 0, stream, static_cast<const uint16_t *>(x),
+                           static_cast<const uint16_t *>(router), Ti, Hi, E, part);
+    const bool planned = gs == 0 && T <= kPlanWaves;
+    if (gs) {
+        float *logits = reinterpret_cast<float *>(ws + l.logits);
+        hipLaunchKernelGGL(router_sum_kernel, dim3(static_cast<unsigned>(ceil_div(T * E, kRouterThreads))),
+                           dim3(kRouterThreads), 0, stream, part, splits, Ti * E, logits);
+        st = moe_route_topk_grouped(logits, T, E, K, gs, topk_groups, topk_idx, topk_w, stream);
+        if (st != MOE_OK)
+            return st;
+    } else {
+        const Plan plan = plan_in(ws, l);
+#define MOE_FEW_ROUTE(J, PLAN)                                                                                       \
+    hipLaunchKernelGGL((few_token_route_kernel<J, PLAN>), dim3(static_cast<unsigned>(ceil_div(T, kPlanWaves))),        \
+                       dim3(kPlanThreads), PLAN ? plan_lds(E) : 0, stream, part, splits, Ti, E, K, topk_idx, topk_w, plan)
+        if (E <= 4 * kWave) {
+            if (planned)
+                MOE_FEW_ROUTE(4, true);
+            else
+                MOE_FEW_ROUTE(4, false);
+        } else {
+            if (planned)
+                MOE_FEW_ROUTE(16, true);
+            else
+                MOE_FEW_ROUTE(16, false);
+        }
+#undef MOE_FEW_ROUTE
+    }
+    return launch_experts(x, T, H, I, E, K, topk_idx, topk_w, w, bias, out, out_dt, ws, planned, stream);
 }

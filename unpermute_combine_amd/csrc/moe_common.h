@@ -104,6 +104,20 @@ __device__ __forceinline__ uint64_t lanemask_lt()
     return lane == 0 ? 0ull : (~0ull >> (64 - lane));
 }
 
+// A logit's order-preserving 32-bit image (larger logit, larger key).
+__device__ __forceinline__ uint32_t orderable(float s)
+{
+    if (s == 0.0f)
+        s = 0.0f;  // -0 and +0 compare equal: same key, so the lower id wins
+    const uint32_t u = __float_as_uint(s);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);  // > 0 for every non-NaN float
+}
+
+__device__ __forceinline__ float from_orderable(uint32_t u)
+{
+    return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
+
 // Workgroups are dispatched to the 8 XCDs round-robin (block b to XCD b % 8). This renumbers the
 // blocks so that each XCD takes one contiguous range of logical blocks (XCD x the x-th eighth,
 // the first nb % 8 XCDs one block more), a bijection on [0, nb).

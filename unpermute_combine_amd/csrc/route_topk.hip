@@ -45,19 +45,6 @@ constexpr int kDppRowHalfMirror = 0x141;
 constexpr int kDppQuadXor2 = 0x4e;  // quad_perm [2,3,0,1]
 constexpr int kDppQuadXor1 = 0xb1;  // quad_perm [1,0,3,2]
 
-__device__ __forceinline__ uint32_t orderable(float s)
-{
-    if (s == 0.0f)
-        s = 0.0f;  // -0 and +0 compare equal: same key, so the lower id wins
-    const uint32_t u = __float_as_uint(s);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);  // > 0 for every non-NaN float
-}
-
-__device__ __forceinline__ float from_orderable(uint32_t u)
-{
-    return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
-}
-
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v)
 {
