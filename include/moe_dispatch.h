@@ -446,7 +446,7 @@ moe_status moe_add_rmsnorm_backward(const void *dout, moe_dtype dout_dt, const v
  *   weight_dt: dt, or MOE_FP8_E4M3 beside bf16 rows: codes with float32 scales, one per row and block of
  *   `block` consecutive elements of the row, as moe_quantize_fp8 of the weight rows gives them
  *   (gate_up_scales [E, 2I, H/block], down_scales [E, H, I/block]); block must divide H and I (else
- *   MOE_ERR_INVALID) and be a multiple of 64 (else MOE_ERR_UNSUPPORTED). Other types of weights:
+ *   MOE_ERR_INVALID) and be a multiple of 128 (else MOE_ERR_UNSUPPORTED). Other types of weights:
  *   MOE_ERR_UNSUPPORTED; block and scales are ignored without FP8.
  *   T <= MOE_MAX_FEW_TOKENS, H and I <= 2^20 (else MOE_ERR_UNSUPPORTED): for more tokens dispatch them.
  * Weights of experts that no token uses are not read. Rows are independent: what is not finite in one token's row

@@ -34,7 +34,7 @@ def draw(seed, *shape, dtype=F32):
 class Layer:
     """Random weights of a layer, as the library takes them and as the values they stand for."""
 
-    def __init__(self, m, H, I, E, kind, seed=1, block=64):
+    def __init__(self, m, H, I, E, kind, seed=1, block=128):
         self.H, self.I, self.E, self.kind = H, I, E, kind
         self.rows = F32 if kind == "f32" else BF16
         self.router = draw(seed, E, H, dtype=self.rows)
@@ -121,6 +121,8 @@ RAGGED = [(1, 1, 1, 1, 1), (2, 7, 3, 4, 2), (5, 33, 17, 3, 3), (19, 100, 36, 7, 
 def test_layer(m, T, H, I, E, K, kind):
     if kind == "fp8" and (T, H, I, E, K) in RAGGED:
         pytest.skip("FP8 weights have whole blocks")
+    if kind == "fp8":
+        H, I = -(-H // 128) * 128, -(-I // 128) * 128
     say(f"layer T={T} H={H} I={I} E={E} K={K} {kind}")
     lay = Layer(m, H, I, E, kind)
     x, bias = draw(7, T, H, dtype=lay.rows), draw(8, T, H, dtype=lay.rows)
@@ -141,10 +143,10 @@ def test_layer(m, T, H, I, E, K, kind):
     assert torch.equal(b2, out)
 
 
-@pytest.mark.parametrize("block", [64, 128, 256])
+@pytest.mark.parametrize("block", [128, 256, 384, 768])
 def test_fp8_blocks(m, block):
-    lay = Layer(m, 512, 256, 6, "fp8", block=block)
-    x = draw(3, 21, 512, dtype=BF16)
+    lay = Layer(m, 1536, 768, 6, "fp8", block=block)
+    x = draw(3, 21, 1536, dtype=BF16)
     out, idx, w = m.few_token_layer(x, lay.router, lay.w13, lay.w2, 3, **lay.scales)
     assert_within(out, *lay.expected(x, idx, w))
 
@@ -162,9 +164,9 @@ def test_every_fp8_code(m):
     w2[0, torch.arange(256), torch.arange(256)] = 0x38
     x = torch.zeros(1, H, dtype=BF16, device=DEV)
     x[0, 0] = x[0, 1] = 1
-    one = torch.ones(1, 2 * I, H // 64, device=DEV)
+    one = torch.ones(1, 2 * I, H // 128, device=DEV)
     out = m.few_token_experts(x, torch.zeros(1, 1, dtype=torch.int32, device=DEV), None, w13, w2, gate_up_scales=one,
-                              down_scales=torch.ones(1, H, I // 64, device=DEV), out_dtype=F32)
+                              down_scales=torch.ones(1, H, I // 128, device=DEV), out_dtype=F32)
     v = q.view(torch.float8_e4m3fn).double()
     want = v * torch.sigmoid(v)
     # exp and the quotient (8 roundings), h kept to 2^-17
@@ -175,7 +177,7 @@ def test_every_fp8_code(m):
     w2.zero_()
     w2[0, :, 0] = q
     out = m.few_token_experts(x, torch.zeros(1, 1, dtype=torch.int32, device=DEV), None, w13, w2, gate_up_scales=one,
-                              down_scales=torch.ones(1, H, I // 64, device=DEV), out_dtype=F32)
+                              down_scales=torch.ones(1, H, I // 128, device=DEV), out_dtype=F32)
     h = torch.tensor(8.0, dtype=torch.float64, device=DEV)
     want = v * (h * torch.sigmoid(h))
     assert bool(((out[0].double() - want).abs() <= (2.0 ** -17 + 8 * U) * want.abs() + 1e-38).all())
@@ -185,7 +187,7 @@ def test_every_fp8_code(m):
 @pytest.mark.parametrize("kind", ["f32", "bf16", "fp8"])
 def test_slots_that_route_nowhere_and_repeats(m, T, K, kind):
     E = 11
-    lay = Layer(m, 192, 128, E, kind, seed=4)
+    lay = Layer(m, 256, 128, E, kind, seed=4)
     g = torch.Generator().manual_seed(T)
     idx = torch.randint(-2, E + 3, (T, K), generator=g).to(torch.int32)  # out of range on both sides, repeats
     idx[T // 2] = -1  # a token without experts
@@ -258,7 +260,7 @@ def test_operands_at_odd_addresses(m):
 
 def test_refusals_of_the_binding(m):
     lay = Layer(m, 128, 64, 4, "bf16")
-    q = Layer(m, 128, 64, 4, "fp8")
+    q = Layer(m, 128, 128, 4, "fp8")
     x = draw(1, 3, 128, dtype=BF16)
     call = lambda x=x, r=lay.router, a=lay.w13, b=lay.w2, k=2, **kw: m.few_token_layer(x, r, a, b, k, **kw)  # noqa: E731
     for bad in (dict(x=x[:, :64].contiguous()), dict(r=lay.router[:3]), dict(a=lay.w13[:3]), dict(b=lay.w2.transpose(1, 2).contiguous()),

@@ -23,26 +23,52 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kMaxFewTokens = MOE_MAX_FEW_TOKENS;
 constexpr int kTile = 16;  // tokens and weight rows of one matrix tile
 
-// Weight element types. A "load" is 16 bytes in each lane: 64 bytes of each of 16 rows, i.e. kLoadElems consecutive
-// elements of the rows, of which lane group g = lane / 16 holds the g-th quarter.
+// Weight element types. A "half" is 64 bytes of each of 16 rows, 16 in each lane: the operand of the matrix instructions,
+// where lane l holds row l % 16 and the (l / 16)-th quarter. A "load" is two halves, 128 bytes of each row.
 enum Weights { kWF32, kWBf16, kWFp8 };
 template <Weights W> constexpr int kLaneElems = W == kWF32 ? 4 : W == kWBf16 ? 8 : 16;
-template <Weights W> constexpr int kLoadElems = 4 * kLaneElems<W>;
+template <Weights W> constexpr int kHalfElems = 4 * kLaneElems<W>;
+template <Weights W> constexpr int kLoadElems = 2 * kHalfElems<W>;
 
-// The activations that meet one load of weights: as many elements, bf16 (or float32 with float32 weights).
+// The activations that meet one half of weights: as many elements, bf16 (or float32 with float32 weights).
 template <Weights W>
 struct Acts {
     u32x4 v[W == kWFp8 ? 2 : 1];
 };
+
+// Weights come in whole cache lines: an instruction reads 128 bytes of 8 rows, the first of two rows 0..7 and the second
+// rows 8..15, and lanes 8..15 of each 16 take the second 64 bytes. This swaps lanes 8..15 of the first with lanes 0..7
+// of the second (DPP moves), which leaves the two halves of all 16 rows. (Reading 64 bytes of 16 rows at once, a line is
+// asked for twice: it has to stay in the 32 KB L1 meanwhile, which few enough lines in flight do.)
+constexpr int kDppRowRor8 = 0x128;
+
+__device__ __forceinline__ void swap_eights(uint32_t &a, uint32_t &b)
+{
+    const int x = static_cast<int>(a), y = static_cast<int>(b);
+    a = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(x, y, kDppRowRor8, 0xf, 0xc, false));
+    b = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(y, x, kDppRowRor8, 0xf, 0x3, false));
+}
+
+__device__ __forceinline__ void to_halves(u32x4 &a, u32x4 &b)
+{
+    swap_eights(a.x, b.x);
+    swap_eights(a.y, b.y);
+    swap_eights(a.z, b.z);
+    swap_eights(a.w, b.w);
+}
 
 // The first `rest` (or none, or all) of a lane's consecutive elements, zeros after them.
 template <typename X, typename R>
 __device__ __forceinline__ void load_tail(const X *p, int rest, R &r)
 {
     constexpr int n = sizeof(R) / sizeof(X);
+    if (rest >= n) {
+        __builtin_memcpy(&r, p, sizeof(r));
+        return;
+    }
     X t[n] = {};
 #pragma unroll
-    for (int i = 0; i < n; ++i)
+    for (int i = 0; i < n - 1; ++i)
         if (i < rest)
             t[i] = p[i];
     __builtin_memcpy(&r, t, sizeof(r));
@@ -64,9 +90,9 @@ __device__ __forceinline__ bf16x8 fp8_to_bf16(uint32_t a, uint32_t b)
     return bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// acc[token, weight row] += sum over the load's elements of act * weight. The tile's rows (A operand) are tokens and
+// acc[token, weight row] += sum over a half's elements of act * weight. The tile's rows (A operand) are tokens and
 // its columns (B operand) weight rows; both operands hold, in lane l, row or column l % 16, and the same elements in
-// the same lane group and register, so any order of the elements inside a load is right.
+// the same lane group and register, so any order of the elements inside a half is right.
 template <Weights W>
 __device__ __forceinline__ f32x4 multiply(f32x4 acc, const Acts<W> &x, const u32x4 &w)
 {
@@ -281,6 +307,7 @@ struct Plan {
     int32_t *start;  // [n + 1] first position of each in order
     int32_t *order;  // [start[n]] slots,
     int32_t *token;  // and the token of each
+    int32_t *place;  // [T * K] each slot's position in order, -1: it routes nowhere
 };
 
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / kWave;
@@ -309,9 +336,11 @@ __device__ __forceinline__ void make_plan(const int32_t *topk_idx, int n, int E,
             }
             const int rank = __popcll(peers & lanemask_lt());
             int pos = 0;
-            if (e < E) {
+            if (e < E)
                 pos = mine[e];
-                if (pass == 1) {
+            if (pass == 1 && s + lane < s1) {
+                plan.place[s + lane] = e < E ? pos + rank : -1;
+                if (e < E) {
                     plan.order[pos + rank] = s + lane;
                     plan.token[pos + rank] = (s + lane) / K;
                 }
@@ -396,42 +425,51 @@ struct ExpertArgs {
     const void *w;            // gate_up or down
     const float *scales;      // FP8
     void *h;                  // [slots][I] float32, or [slots][2][I] bf16
+    float *y;                 // [slots][H]: the slots' products
     const void *bias;
     void *out;
     int T, K, H, I;
     int nb;                   // FP8: scales per row of w,
     uint32_t per_block;       // and 2^32 over the loads of one, rounded up (0: one load each)
+    int parts;                // wavefronts that share a unit's loads
     bool out_bf16;
     Plan plan;
 };
 
 // The products of NW rows of weights (one per lane column) with NT tiles of 16 tokens over a range of loads: LO adds
 // the activations' second bf16 row, `lo` bytes behind the first. The loads run D ahead of the matrix instructions in
-// a ring of registers, so that each wavefront keeps D * NW KiB of weights in flight all the time. Addresses are a
+// a ring of registers, so that each wavefront keeps 2 * D * NW KiB of weights in flight all the time. Addresses are a
 // uniform base, which moves, and a 32-bit offset in each lane, which does not.
 template <Weights W, int NW, int NT, bool LO>
 struct Product {
     typedef typename WeightType<W>::type Wt;
     typedef typename ActType<W>::type X;
-    static constexpr int kSlotRegs = 4 * (NW + NT * (LO ? 2 : 1) * (W == kWFp8 ? 2 : 1)) + (W == kWFp8 ? NW : 0);
+    static constexpr int kSlotRegs = 8 * (NW + NT * (LO ? 2 : 1) * (W == kWFp8 ? 2 : 1)) + (W == kWFp8 ? NW : 0);
     static constexpr int kRoom = ((W == kWFp8 ? 76 : 88) - 4 * NW * NT) / kSlotRegs;
-    static constexpr int D = kRoom > 6 ? 6 : kRoom < 1 ? 1 : kRoom;
-    static constexpr int kActBytes = kLoadElems<W> * sizeof(X);  // of a token's row per load
+    static constexpr int D = kRoom > 4 ? 4 : kRoom < 1 ? 1 : kRoom;
+    static constexpr int kActBytes = kHalfElems<W> * sizeof(X);  // of a token's row per half
     const char *w[NW], *x;
     const float *scale[NW];
-    uint32_t w_off, x_off[NT], s_off;
+    uint32_t w_off[2], w_row, x_off[NT], s_off;
     int64_t lo;
     uint32_t per_block;
     f32x4 acc[NW][NT];
 
     struct Slot {
-        u32x4 w[NW];
-        Acts<W> x[NT], y[NT];
+        u32x4 w[NW][2];
+        Acts<W> x[NT][2], y[NT][2];
         float s[NW];
     };
 
-    __device__ __forceinline__ void clear()
+    // Weight rows 0..15 from w[] on, `stride` elements apart; rows past `last` are read as that one.
+    __device__ __forceinline__ void rows_of(int stride, int last, int nb)
     {
+        const int lane = threadIdx.x & (kWave - 1), m = lane % kTile, g = lane / kTile;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w_off[i] = static_cast<uint32_t>(min(8 * i + m % 8, last) * stride) * sizeof(Wt) + m / 8 * 64 + 16 * g;
+        w_row = static_cast<uint32_t>(min(m, last) * stride) * sizeof(Wt) + 16 * g;
+        s_off = min(m, last) * nb;
 #pragma unroll
         for (int i = 0; i < NW; ++i)
 #pragma unroll
@@ -439,38 +477,59 @@ struct Product {
                 acc[i][t] = f32x4{};
     }
 
-    __device__ __forceinline__ void add(const Slot &q)
+    __device__ __forceinline__ void add(Slot &q)
     {
 #pragma unroll
-        for (int i = 0; i < NW; ++i)
+        for (int i = 0; i < NW; ++i) {
+            to_halves(q.w[i][0], q.w[i][1]);
+            multiply_halves(q, i);
+        }
+    }
+
+    __device__ __forceinline__ void multiply_halves(const Slot &q, int i)
+    {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                f32x4 p = W == kWFp8 ? f32x4{} : acc[i][t];
-                p = multiply<W>(p, q.x[t], q.w[i]);
+        for (int t = 0; t < NT; ++t) {
+            f32x4 p = W == kWFp8 ? f32x4{} : acc[i][t];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                p = multiply<W>(p, q.x[t][h], q.w[i][h]);
                 if (LO)
-                    p = multiply<W>(p, q.y[t], q.w[i]);
-                if (W == kWFp8)  // a load lies in one block of scales
-                    acc[i][t] += p * q.s[i];
-                else
-                    acc[i][t] = p;
+                    p = multiply<W>(p, q.y[t][h], q.w[i][h]);
             }
+            if (W == kWFp8)  // a load lies in one block of scales
+                acc[i][t] += p * q.s[i];
+            else
+                acc[i][t] = p;
+        }
     }
 
     __device__ __forceinline__ void issue(Slot &q, int l)
     {
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
-            __builtin_memcpy(&q.w[i], w[i] + static_cast<int64_t>(l) * 64 + w_off, 16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                q.w[i][h] = load_line(w[i] + static_cast<int64_t>(l) * 128 + w_off[h]);
             if (W == kWFp8)
                 q.s[i] = (scale[i] + (per_block ? __umulhi(l, per_block) : l))[s_off];
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const char *row = x + static_cast<int64_t>(l) * kActBytes;
-            __builtin_memcpy(&q.x[t], row + x_off[t], sizeof(q.x[t]));
-            if (LO)
-                __builtin_memcpy(&q.y[t], row + lo + x_off[t], sizeof(q.y[t]));
-        }
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const char *row = x + static_cast<int64_t>(2 * l + h) * kActBytes;
+                __builtin_memcpy(&q.x[t][h], row + x_off[t], sizeof(q.x[t][h]));
+                if (LO)
+                    __builtin_memcpy(&q.y[t][h], row + lo + x_off[t], sizeof(q.y[t][h]));
+            }
+    }
+
+    __device__ __forceinline__ static u32x4 load_line(const char *p)
+    {
+        u32x4 v;
+        __builtin_memcpy(&v, p, sizeof(v));
+        return v;
     }
 
     // Loads l .. l1 - 1 of rows of len elements.
@@ -496,197 +555,226 @@ struct Product {
                     add(q[u]);
         }
         if (W != kWFp8 && whole < l1) {  // the row's last load, partial
-            const int rest = len - whole * kLoadElems<W> - static_cast<int>(threadIdx.x % kWave / kTile) * kLaneElems<W>;
             Slot z;
 #pragma unroll
-            for (int i = 0; i < NW; ++i)
-                load_tail(reinterpret_cast<const Wt *>(w[i] + static_cast<int64_t>(whole) * 64 + w_off), rest, z.w[i]);
+            for (int h = 0; h < 2; ++h) {
+                const int half = 2 * whole + h;
+                const int rest = len - half * kHalfElems<W> - static_cast<int>(threadIdx.x % kWave / kTile) * kLaneElems<W>;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const char *row = x + static_cast<int64_t>(whole) * kActBytes + x_off[t];
-                load_tail(reinterpret_cast<const X *>(row), rest, z.x[t]);
-                if (LO)
-                    load_tail(reinterpret_cast<const X *>(row + lo), rest, z.y[t]);
+                for (int i = 0; i < NW; ++i)
+                    load_tail(reinterpret_cast<const Wt *>(w[i] + static_cast<int64_t>(half) * 64 + w_row), rest, z.w[i][h]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const char *row = x + static_cast<int64_t>(half) * kActBytes + x_off[t];
+                    load_tail(reinterpret_cast<const X *>(row), rest, z.x[t][h]);
+                    if (LO)
+                        load_tail(reinterpret_cast<const X *>(row + lo), rest, z.y[t][h]);
+                }
             }
-            add(z);
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                multiply_halves(z, i);
         }
+    }
+};
+
+// How a workgroup's wavefronts divide its work: `parts` of them (a power of two) share the loads of one unit of 16 or
+// 32 weight rows, the others take other units.
+struct Share {
+    int unit, part;
+    __device__ __forceinline__ explicit Share(int parts)
+    {
+        const int wave = wave_id();
+        unit = blockIdx.x * (kExpertWaves / parts) + wave / parts;
+        part = wave & (parts - 1);
+    }
+};
+
+// The parts' tiles put together in order: thread = (value of a tile, unit), f(unit's first wavefront, tile row, column,
+// sums of the NW weight rows). Register r of lane l holds the tile's row 4 (l / 16) + r and column l % 16.
+template <int NW, int NT, typename F>
+__device__ __forceinline__ void join_parts(const f32x4 (&acc)[NW][NT], int parts, f32x4 (*red)[NW][NT][kWave], F f)
+{
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            red[wave][i][t][lane] = acc[i][t];
+    __syncthreads();
+    const int values = NT * kTile * kTile;
+    for (int i = threadIdx.x; i < kExpertWaves / parts * values; i += kExpertThreads) {
+        const int first = i / values * parts, v = i % values, t = v / (kTile * kTile), q = v % (kTile * kTile);
+        // neighbouring threads take neighbouring columns
+        const int row = q / kTile, col = q % kTile, src = row / 4 * kTile + col, r = row % 4;
+        float sum[NW] = {};
+        for (int w = first; w < first + parts; ++w)
+#pragma unroll
+            for (int n = 0; n < NW; ++n)
+                sum[n] += red[w][n][t][src][r];
+        f(first / parts, t * kTile + row, col, sum);
+    }
+    __syncthreads();
+}
+
+// The plan's entry of the expert that a workgroup takes; its entries are read together, before it is known whether
+// there is such an expert (the arrays have them).
+struct Entry {
+    int64_t ex;
+    int p0, n;
+    __device__ __forceinline__ Entry(const Plan &plan, int i)
+    {
+        const int used = plan.head[0];
+        ex = plan.act[i];
+        p0 = plan.start[i];
+        n = i < used ? plan.start[i + 1] - p0 : 0;
     }
 };
 
 // SwiGLU of up to NT tiles of an expert's tokens, from row r0 of its n on.
 template <Weights W, int NT>
-__device__ __forceinline__ void gate_up_rows(const ExpertArgs &a, int64_t ex, int p0, int r0, int n,
-                                             f32x4 (*red)[kExpertWaves][2][kWave])
+__device__ __forceinline__ void gate_up_rows(const ExpertArgs &a, const Entry &en, int r0, char *red)
 {
     typedef Product<W, 2, NT, false> P;
-    const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), m = lane % kTile, g = lane / kTile;
-    const int c0 = blockIdx.x * kTile, col = min(m, a.I - 1 - c0);
+    const int lane = threadIdx.x & (kWave - 1), m = lane % kTile, g = lane / kTile;
+    const Share my(a.parts);
+    const int c0 = min(my.unit * kTile, a.I - 1);
     P p;
-    p.clear();
+    // columns and rows past the last one take its place: what they give is not stored
+    p.rows_of(a.H, a.I - 1 - c0, a.nb);
     p.lo = 0;
     p.per_block = a.per_block;
-    // columns and rows past the last one take its place: what they give is not stored
-    p.w_off = static_cast<uint32_t>(col * a.H) * sizeof(typename P::Wt) + 16 * g;
-    p.s_off = col * a.nb;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // the gate's rows, the up's rows
-        const int64_t row = (ex * 2 + i) * a.I + c0;
+        const int64_t row = (en.ex * 2 + i) * a.I + c0;
         p.w[i] = static_cast<const char *>(a.w) + row * a.H * sizeof(typename P::Wt);
         p.scale[i] = a.scales + row * a.nb;
     }
     p.x = static_cast<const char *>(a.x);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int r = min(r0 + t * kTile + m, n - 1);
-        p.x_off[t] = static_cast<uint32_t>(a.plan.token[p0 + r] * a.H) * sizeof(typename P::X) + P::kActBytes / 4 * g;
+        const int r = min(r0 + t * kTile + m, en.n - 1);
+        p.x_off[t] = static_cast<uint32_t>(a.plan.token[en.p0 + r] * a.H) * sizeof(typename P::X) + P::kActBytes / 4 * g;
     }
     const int loads = (a.H + kLoadElems<W> - 1) / kLoadElems<W>;
-    p.run(loads * wave / kExpertWaves, loads * (wave + 1) / kExpertWaves, a.H);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        red[t][wave][0][lane] = p.acc[0][t];
-        red[t][wave][1][lane] = p.acc[1][t];
-    }
-    __syncthreads();
-    // register r of lane l holds the tile's row 4 (l / 16) + r and column l % 16
-    for (int i = threadIdx.x; i < NT * kTile * kTile; i += kExpertThreads) {
-        const int t = i / (kTile * kTile), src = i % (kTile * kTile) / 4, r = i % 4;
-        const int row = r0 + t * kTile + 4 * (src / kTile) + r, c = c0 + src % kTile;
-        float gate = 0.0f, up = 0.0f;
-        for (int w = 0; w < kExpertWaves; ++w) {
-            gate += red[t][w][0][src][r];
-            up += red[t][w][1][src][r];
+    p.run(loads * my.part / a.parts, loads * (my.part + 1) / a.parts, a.H);
+    join_parts(p.acc, a.parts, reinterpret_cast<f32x4(*)[2][NT][kWave]>(red), [&](int unit, int row, int column, const float (&v)[2]) {
+        const int c = (blockIdx.x * (kExpertWaves / a.parts) + unit) * kTile + column, pos = en.p0 + r0 + row;
+        if (r0 + row >= en.n || c >= a.I)
+            return;
+        const float weight = a.topk_w ? a.topk_w[a.plan.order[pos]] : 1.0f;
+        const float h = v[0] / (1.0f + expf(-v[0])) * v[1] * weight;
+        if (W == kWF32) {
+            static_cast<float *>(a.h)[static_cast<int64_t>(pos) * a.I + c] = h;
+        } else {
+            uint16_t *hr = static_cast<uint16_t *>(a.h) + static_cast<int64_t>(pos) * 2 * a.I;
+            const uint32_t hi = f32_to_bf16_bits(h);
+            const float rest = h - __uint_as_float(hi << 16);
+            hr[c] = static_cast<uint16_t>(hi);
+            // an infinite or NaN h is wholly in the first row
+            hr[a.I + c] = (hi & 0x7f80u) == 0x7f80u ? 0 : static_cast<uint16_t>(f32_to_bf16_bits(rest));
         }
-        if (row < n && c < a.I) {
-            const float weight = a.topk_w ? a.topk_w[a.plan.order[p0 + row]] : 1.0f;
-            const float h = gate / (1.0f + expf(-gate)) * up * weight;
-            if (W == kWF32) {
-                static_cast<float *>(a.h)[static_cast<int64_t>(p0 + row) * a.I + c] = h;
-            } else {
-                uint16_t *hr = static_cast<uint16_t *>(a.h) + static_cast<int64_t>(p0 + row) * 2 * a.I;
-                const uint32_t hi = f32_to_bf16_bits(h);
-                const float rest = h - __uint_as_float(hi << 16);
-                hr[c] = static_cast<uint16_t>(hi);
-                // an infinite or NaN h is wholly in the first row
-                hr[a.I + c] = (hi & 0x7f80u) == 0x7f80u ? 0 : static_cast<uint16_t>(f32_to_bf16_bits(rest));
-            }
-        }
-    }
-    __syncthreads();
+    });
 }
 
-// MANY: more than one tile's tokens, so that an expert may have several tiles.
-template <Weights W, bool MANY>
+// A workgroup's LDS: every wavefront's tiles.
+template <int NT>
+constexpr int kRedBytes = kExpertWaves * 2 * NT * kWave * sizeof(f32x4);
+
+template <Weights W, int NT>
 __global__ __launch_bounds__(kExpertThreads, 4) void gate_up_kernel(ExpertArgs a)
 {
-    __shared__ f32x4 red[MANY ? 4 : 1][kExpertWaves][2][kWave];
-    // read together, before it is known whether there is such an expert: the arrays have these entries
-    const int used = a.plan.head[0], p0 = a.plan.start[blockIdx.y], n = a.plan.start[blockIdx.y + 1] - p0;
-    const int64_t ex = a.plan.act[blockIdx.y];
-    if (static_cast<int>(blockIdx.y) >= used)
-        return;
-    for (int r0 = 0; r0 < n; r0 += (MANY ? 4 : 1) * kTile) {
-        if (!MANY || n - r0 <= kTile)
-            gate_up_rows<W, 1>(a, ex, p0, r0, n, red);
-        else if (n - r0 <= 2 * kTile)
-            gate_up_rows<W, 2>(a, ex, p0, r0, n, red);
+    __shared__ __attribute__((aligned(16))) char red[kRedBytes<NT>];
+    const Entry en(a.plan, blockIdx.y);
+    for (int r0 = 0; r0 < en.n; r0 += NT * kTile) {
+        if (NT > 1 && en.n - r0 <= NT / 2 * kTile)
+            gate_up_rows<W, (NT + 1) / 2>(a, en, r0, red);
         else
-            gate_up_rows<W, 4>(a, ex, p0, r0, n, red);
+            gate_up_rows<W, NT>(a, en, r0, red);
     }
 }
 
-// ---------------------------------------------------------------- down product and combine
-// One workgroup per 16 columns of out, for all experts in use: the (expert, load) pairs in order are cut into one
-// stretch per wavefront, each wavefront adds its tiles into its own [T][16] sums in LDS when its expert changes, and
-// the wavefronts' sums are put together in order. No atomics: the result does not depend on timing.
+// ---------------------------------------------------------------- down product
+// As the gate and up products, 32 rows of w_down (columns of out) to a unit, so that the two rows of h are read once
+// for twice the weights. Each slot's product goes to a float32 row of its own; the merge adds them up.
 template <Weights W, int NT>
-__device__ __forceinline__ void down_rows(const ExpertArgs &a, int64_t ex, int p0, int r0, int n, int l0, int l1,
-                                          float *mine)
+__device__ __forceinline__ void down_rows(const ExpertArgs &a, const Entry &en, int r0, char *red)
 {
-    typedef Product<W, 1, NT, W != kWF32> P;
+    typedef Product<W, 2, NT, W != kWF32> P;
     constexpr int rows = W == kWF32 ? 1 : 2;  // of h per slot
     const int lane = threadIdx.x & (kWave - 1), m = lane % kTile, g = lane / kTile;
-    const int c0 = blockIdx.x * kTile, col = min(m, a.H - 1 - c0);
+    const Share my(a.parts);
+    const int c0 = min(my.unit * 2 * kTile, a.H - 1);
     P p;
-    p.clear();
+    // both tiles' rows from one offset: where fewer than 32 columns are left the second tile begins earlier
+    const int c1 = min(kTile, max(a.H - kTile - c0, 0));
+    p.rows_of(a.I, a.H - 1 - c0 - c1, a.nb);
     p.lo = static_cast<int64_t>(a.I) * sizeof(typename P::X);
     p.per_block = a.per_block;
-    p.w_off = static_cast<uint32_t>(col * a.I) * sizeof(typename P::Wt) + 16 * g;
-    p.s_off = col * a.nb;
-    p.w[0] = static_cast<const char *>(a.w) + (ex * a.H + c0) * a.I * sizeof(typename P::Wt);
-    p.scale[0] = a.scales + (ex * a.H + c0) * a.nb;
-    p.x = static_cast<const char *>(a.h) + static_cast<int64_t>(p0 + r0) * rows * a.I * sizeof(typename P::X);
-    int tok[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int r = min(t * kTile + m, n - 1 - r0);
-        p.x_off[t] = static_cast<uint32_t>(r * rows * a.I) * sizeof(typename P::X) + P::kActBytes / 4 * g;
-        tok[t] = a.plan.token[p0 + r0 + r];
+    for (int i = 0; i < 2; ++i) {
+        const int64_t row = en.ex * a.H + c0 + i * c1;
+        p.w[i] = static_cast<const char *>(a.w) + row * a.I * sizeof(typename P::Wt);
+        p.scale[i] = a.scales + row * a.nb;
     }
-    p.run(l0, l1, a.I);
-    // this lane holds column m for each tile's rows 4 g .. 4 g + 3. A token that names the expert twice has two rows,
-    // neighbours: then the lane groups add one after the other
+    p.x = static_cast<const char *>(a.h) + static_cast<int64_t>(en.p0 + r0) * rows * a.I * sizeof(typename P::X);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const bool live = r0 + t * kTile + m < n;
-        const bool twice = __ballot(live && m > 0 && tok[t] == __shfl_up(tok[t], 1)) != 0;
-        for (int turn = 0; turn < (twice ? 4 : 1); ++turn) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int to = __shfl(tok[t], 4 * g + r);
-                if ((!twice || g == turn) && r0 + t * kTile + 4 * g + r < n)
-                    mine[to * kTile + m] += p.acc[0][t][r];
-            }
-            __builtin_amdgcn_wave_barrier();
-        }
+        const int r = min(t * kTile + m, en.n - 1 - r0);
+        p.x_off[t] = static_cast<uint32_t>(r * rows * a.I) * sizeof(typename P::X) + P::kActBytes / 4 * g;
+    }
+    const int loads = (a.I + kLoadElems<W> - 1) / kLoadElems<W>;
+    p.run(loads * my.part / a.parts, loads * (my.part + 1) / a.parts, a.I);
+    join_parts(p.acc, a.parts, reinterpret_cast<f32x4(*)[2][NT][kWave]>(red), [&](int unit, int row, int column, const float (&v)[2]) {
+        const int u0 = (blockIdx.x * (kExpertWaves / a.parts) + unit) * 2 * kTile;
+        if (r0 + row >= en.n || u0 >= a.H)
+            return;
+        float *y = a.y + static_cast<int64_t>(en.p0 + r0 + row) * a.H;
+        const int second = min(kTile, max(a.H - kTile - u0, 0));
+        if (u0 + column < a.H)
+            y[u0 + column] = v[0];
+        if (second > 0 && u0 + second + column < a.H)
+            y[u0 + second + column] = v[1];
+    });
+}
+
+template <Weights W, int NT>
+__global__ __launch_bounds__(kExpertThreads, 4) void down_kernel(ExpertArgs a)
+{
+    __shared__ __attribute__((aligned(16))) char red[kRedBytes<NT>];
+    const Entry en(a.plan, blockIdx.y);
+    for (int r0 = 0; r0 < en.n; r0 += NT * kTile) {
+        if (NT > 1 && en.n - r0 <= NT / 2 * kTile)
+            down_rows<W, (NT + 1) / 2>(a, en, r0, red);
+        else
+            down_rows<W, NT>(a, en, r0, red);
     }
 }
 
-template <Weights W, bool MANY>
-__global__ __launch_bounds__(kExpertThreads, 4) void down_kernel(ExpertArgs a)
+// ---------------------------------------------------------------- merge
+// out[t] = the sum of its slots' rows in slot order (their weights are in h), plus bias.
+constexpr int kMergeThreads = 256;
+
+__global__ __launch_bounds__(kMergeThreads) void merge_kernel(ExpertArgs a)
 {
-    extern __shared__ float sums[];  // [kExpertWaves][T][kTile]
-    const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
-    const int c0 = blockIdx.x * kTile;
-    float *mine = sums + wave * a.T * kTile;
-    for (int i = lane; i < a.T * kTile; i += kWave)
-        mine[i] = 0.0f;
-    __builtin_amdgcn_wave_barrier();
-    const int loads = (a.I + kLoadElems<W> - 1) / kLoadElems<W>;
-    const int all = a.plan.head[0] * loads;
-    const int u1 = static_cast<int64_t>(all) * (wave + 1) / kExpertWaves;
-    for (int u = static_cast<int64_t>(all) * wave / kExpertWaves; u < u1;) {
-        const int i = u / loads, l0 = u - i * loads, l1 = min(loads, l0 + (u1 - u));
-        u += l1 - l0;
-        const int p0 = a.plan.start[i], n = a.plan.start[i + 1] - p0;
-        const int64_t ex = a.plan.act[i];
-        for (int r0 = 0; r0 < n; r0 += (MANY ? 4 : 1) * kTile) {
-            if (!MANY || n - r0 <= kTile)
-                down_rows<W, 1>(a, ex, p0, r0, n, l0, l1, mine);
-            else if (n - r0 <= 2 * kTile)
-                down_rows<W, 2>(a, ex, p0, r0, n, l0, l1, mine);
-            else
-                down_rows<W, 4>(a, ex, p0, r0, n, l0, l1, mine);
-        }
+    const int c = blockIdx.x * kMergeThreads + threadIdx.x, t = blockIdx.y;
+    if (c >= a.H)
+        return;
+    float v = 0.0f;
+    for (int k = 0; k < a.K; ++k) {
+        const int pos = a.plan.place[t * a.K + k];
+        if (pos >= 0)
+            v += a.y[static_cast<int64_t>(pos) * a.H + c];
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.T * kTile; i += kExpertThreads) {
-        const int t = i / kTile, c = c0 + i % kTile;
-        if (c >= a.H)
-            continue;
-        float v = 0.0f;
-        for (int k = 0; k < kExpertWaves; ++k)
-            v += sums[k * a.T * kTile + i];
-        const int64_t o = static_cast<int64_t>(t) * a.H + c;
-        if (a.out_bf16) {
-            if (a.bias)
-                v += to_f32(static_cast<const uint16_t *>(a.bias)[o]);
-            static_cast<uint16_t *>(a.out)[o] = static_cast<uint16_t>(f32_to_bf16_bits(v));
-        } else {
-            if (a.bias)
-                v += static_cast<const float *>(a.bias)[o];
-            static_cast<float *>(a.out)[o] = v;
-        }
+    const int64_t o = static_cast<int64_t>(t) * a.H + c;
+    if (a.out_bf16) {
+        if (a.bias)
+            v += to_f32(static_cast<const uint16_t *>(a.bias)[o]);
+        static_cast<uint16_t *>(a.out)[o] = static_cast<uint16_t>(f32_to_bf16_bits(v));
+    } else {
+        if (a.bias)
+            v += static_cast<const float *>(a.bias)[o];
+        static_cast<float *>(a.out)[o] = v;
     }
 }
 
@@ -695,7 +783,7 @@ size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
 // The workspace: parts of the logits, logits, plan, h.
 struct Layout {
-    size_t part, logits, head, act, start, order, token, h, bytes;
+    size_t part, logits, head, act, start, order, token, place, h, y, bytes;
 };
 
 Layout layout(int64_t T, int64_t H, int64_t E, int64_t K, int64_t I)
@@ -715,7 +803,9 @@ Layout layout(int64_t T, int64_t H, int64_t E, int64_t K, int64_t I)
     l.start = take(4 * (used + 1));
     l.order = take(4 * slots);
     l.token = take(4 * slots);
+    l.place = take(4 * slots);
     l.h = take(4 * slots * I);
+    l.y = take(4 * slots * H);
     l.bytes = at;
     return l;
 }
@@ -733,7 +823,7 @@ Plan plan_in(char *ws, const Layout &l)
 {
     return Plan{reinterpret_cast<int32_t *>(ws + l.head), reinterpret_cast<int32_t *>(ws + l.act),
                 reinterpret_cast<int32_t *>(ws + l.start), reinterpret_cast<int32_t *>(ws + l.order),
-                reinterpret_cast<int32_t *>(ws + l.token)};
+                reinterpret_cast<int32_t *>(ws + l.token), reinterpret_cast<int32_t *>(ws + l.place)};
 }
 
 struct ExpertWeights {
@@ -758,7 +848,7 @@ moe_status check_layer(const void *x, moe_dtype dt, int64_t T, int64_t H, int64_
     if (w.dt == MOE_FP8_E4M3) {
         if (w.block < 1 || H % w.block || I % w.block)
             return MOE_ERR_INVALID;
-        if (w.block % 64)
+        if (w.block % kLoadElems<kWFp8>)
             return MOE_ERR_UNSUPPORTED;
     }
     if (T == 0)
@@ -772,33 +862,50 @@ moe_status check_layer(const void *x, moe_dtype dt, int64_t T, int64_t H, int64_
 
 size_t plan_lds(int E) { return sizeof(uint16_t) * kPlanWaves * static_cast<size_t>(E); }
 
-template <Weights W, bool MANY>
+// Wavefronts that share a unit of weight rows: enough wavefronts for the chip, as long as each has a few loads.
+int share_parts(int64_t units, int64_t loads)
+{
+    int parts = 1;
+    while (parts < kExpertWaves && units * parts < 4096 && loads >= 4 * parts)
+        parts *= 2;
+    return parts;
+}
+
+dim3 product_grid(int64_t units, int parts, int used)
+{
+    return dim3(static_cast<unsigned>(ceil_div(units, kExpertWaves / parts)), static_cast<unsigned>(used));
+}
+
+template <Weights W, int NT>
 void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t stream)
 {
-    // FP8: the scale of load l is l / (loads per block), by a multiplication (exact for l * block / 64 < 2^32)
+    // FP8: the scale of load l is l / (loads per block), by a multiplication (exact for l * block / 128 < 2^32)
     const int lb = W == kWFp8 ? w.block / kLoadElems<kWFp8> : 1;
     a.per_block = lb == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + lb - 1) / lb);
     a.w = w.gate_up;
     a.scales = w.gate_up_scales;
     a.nb = W == kWFp8 ? a.H / w.block : 0;
-    hipLaunchKernelGGL((gate_up_kernel<W, MANY>),
-                       dim3(static_cast<unsigned>(ceil_div(a.I, kTile)), static_cast<unsigned>(used)),
-                       dim3(kExpertThreads), 0, stream, a);
+    int64_t units = ceil_div(a.I, kTile);
+    a.parts = share_parts(units * used, ceil_div(a.H, kLoadElems<W>));
+    hipLaunchKernelGGL((gate_up_kernel<W, NT>), product_grid(units, a.parts, used), dim3(kExpertThreads), 0, stream, a);
     a.w = w.down;
     a.scales = w.down_scales;
     a.nb = W == kWFp8 ? a.I / w.block : 0;
-    const size_t lds = sizeof(float) * kExpertWaves * kTile * static_cast<size_t>(a.T);
-    hipLaunchKernelGGL((down_kernel<W, MANY>), dim3(static_cast<unsigned>(ceil_div(a.H, kTile))), dim3(kExpertThreads), lds,
-                       stream, a);
+    units = ceil_div(a.H, 2 * kTile);
+    a.parts = share_parts(units * used, ceil_div(a.I, kLoadElems<W>));
+    hipLaunchKernelGGL((down_kernel<W, NT>), product_grid(units, a.parts, used), dim3(kExpertThreads), 0, stream, a);
 }
 
 template <Weights W>
 void launch_products_of(const ExpertArgs &a, const ExpertWeights &w, int used, hipStream_t stream)
 {
+    // tiles of tokens that one pass over an expert's weights may meet: by the tokens an expert can have, and has on average
     if (a.T <= kTile)
-        launch_products<W, false>(a, w, used, stream);
+        launch_products<W, 1>(a, w, used, stream);
+    else if (a.T * a.K <= kTile * used)
+        launch_products<W, 2>(a, w, used, stream);
     else
-        launch_products<W, true>(a, w, used, stream);
+        launch_products<W, 4>(a, w, used, stream);
 }
 
 moe_status launch_experts(const void *x, int64_t T, int64_t H, int64_t I, int32_t E, int32_t K, const int32_t *topk_idx,
@@ -812,6 +919,7 @@ moe_status launch_experts(const void *x, int64_t T, int64_t H, int64_t I, int32_
     a.x = x;
     a.topk_w = topk_w;
     a.h = ws + l.h;
+    a.y = reinterpret_cast<float *>(ws + l.y);
     a.bias = bias;
     a.out = out;
     a.out_bf16 = out_dt == MOE_BF16;
@@ -828,6 +936,8 @@ moe_status launch_experts(const void *x, int64_t T, int64_t H, int64_t I, int32_
         launch_products_of<kWF32>(a, w, used, stream);
     else
         launch_products_of<kWBf16>(a, w, used, stream);
+    hipLaunchKernelGGL(merge_kernel, dim3(static_cast<unsigned>(ceil_div(H, kMergeThreads)), static_cast<unsigned>(T)),
+                       dim3(kMergeThreads), 0, stream, a);
     return launch_status();
 }
 

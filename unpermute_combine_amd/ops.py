@@ -770,7 +770,7 @@ def few_token_layer(x: torch.Tensor, router: torch.Tensor, w_gate_up: torch.Tens
     chosen expert's down(silu(gate) * up), the weighted merge and the optional bias (the residual stream, say; it
     may be out itself). x [T, H] and router [E, H] float32 or bfloat16; w_gate_up [E, 2I, H] (gate rows first) and
     w_down [E, H, I] of the same type, or FP8 codes with the scales of quantize_fp8 over their rows (blocks of a
-    multiple of 64). Returns (out [T, H], topk_idx, topk_w)."""
+    multiple of 128). Returns (out [T, H], topk_idx, topk_w)."""
     T, H, I, E, x_dt, w_dt, block = _expert_weights(x, w_gate_up, w_down, gate_up_scales, down_scales)
     _need(router, "router", x.dtype, 2)
     if tuple(router.shape) != (E, H):
