@@ -339,3 +339,19 @@ def test_norm_and_layer_as_a_decode_step(m, T):
     # the dispatched way is in 64 bits up to y's rounding and the merge's K
     mag = (w.abs()[:, :, None] * y[ix.row_of.long()].abs()).sum(1).double()
     assert bool(((merged.double() + stream.double() - want).abs() <= (K + 2) * U * mag + U * want.abs()).all())
+
+
+@pytest.mark.parametrize("T", [1, 20, 150])
+@pytest.mark.parametrize("H,I", [(257, 130), (258, 131), (1024, 77), (71, 512), (130, 1026), (9, 9), (6, 200), (200, 6)])
+@pytest.mark.parametrize("shift", [0, 1, 3])
+def test_rows_on_odd_elements(m, T, H, I, shift):
+    """bf16 rows whose addresses are no multiples of a word, at every offset of the storage."""
+    E, K = 5, 3
+    lay = Layer(m, H, I, E, "bf16", seed=11)
+    off = lambda t: torch.cat([t.new_full((shift,), float("nan")), t.flatten(), t.new_full((3,), float("nan"))])[  # noqa: E731
+        shift: shift + t.numel()].view(t.shape)
+    x = draw(5, T, H, dtype=BF16)
+    idx, w = lay.routed(x, K)
+    w = w.float()
+    out = m.few_token_experts(off(x), idx, w, off(lay.w13), off(lay.w2), out_dtype=F32)
+    assert_within(out, *lay.expected(x, idx, w))
