@@ -11,6 +11,8 @@
 // weight matrix by up to 16 tokens with MFMA 16x16 tiles (few tokens leave most of a tile's columns empty, which
 // costs nothing while the weights' stream sets the pace): 4 lanes read 64 consecutive bytes of each of the 16 rows,
 // straight from memory into the matrix instruction's operand registers, without LDS.
+#include <algorithm>
+
 #include "moe_common.h"
 
 namespace moe {
@@ -127,9 +129,9 @@ __device__ __forceinline__ f32x4 multiply(f32x4 acc, const Acts<W> &x, const u32
 // ---------------------------------------------------------------- router
 // logits = x router^T in double (matrix instructions 16x16x4): which experts are picked then does not depend on the
 // order of a float32 sum, and the products of float32 or bf16 values are exact. A workgroup takes 16 experts, 16 tokens
-// and one of `splits` parts of the hidden dimension, its wavefronts a quarter of that each; the parts' sums are put
+// and one of `splits` parts of the hidden dimension, its wavefronts an equal share of that each; the parts' sums are put
 // together in order where the logits are used.
-constexpr int kRouterThreads = 256, kRouterWaves = kRouterThreads / kWave;
+constexpr int kRouterThreads = 512, kRouterWaves = kRouterThreads / kWave;
 constexpr int kRouterElems = 32;  // of a row per step: 8 in each lane group
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
@@ -145,12 +147,15 @@ __device__ __forceinline__ int wave_id()
     return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / kWave));
 }
 
-// Parts of the hidden dimension: a workgroup for each CU, and at least one step a wavefront.
+// Parts of the hidden dimension: a workgroup for each CU, at least one step a wavefront, and no more than the routing
+// sums with one wait.
+constexpr int kMaxSplits = 8;
+
 int router_splits(int64_t T, int64_t E, int64_t H)
 {
     const int64_t tiles = ceil_div(T, kTile) * ceil_div(E, kTile), most = ceil_div(H, kRouterElems * kRouterWaves);
     const int64_t want = ceil_div(256, tiles);
-    return static_cast<int>(want < most ? want : most);
+    return static_cast<int>(std::min(std::min(want, most), int64_t{kMaxSplits}));
 }
 
 template <typename X>
@@ -184,21 +189,24 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const X *x, cons
     }
     red[wave][lane] = acc;
     __syncthreads();
-    // register r of lane l holds the tile's token l / 16 + 4 r and expert l % 16
-    const int src = threadIdx.x / 4, r = threadIdx.x % 4, t = t0 + src / kTile + 4 * r, e = e0 + src % kTile;
+    if (threadIdx.x >= kTile * kTile)
+        return;
+    // register r of lane l holds the tile's token l / 16 + 4 r and expert l % 16; neighbouring threads take neighbouring
+    // experts
+    const int e = threadIdx.x % kTile, t = threadIdx.x / kTile, src = t % 4 * kTile + e, r = t / 4;
     double v = 0.0;
     for (int w = 0; w < kRouterWaves; ++w)
         v += red[w][src][r];
-    if (t < T && e < E)
-        part[(static_cast<int64_t>(blockIdx.z) * T + t) * E + e] = v;
+    if (t0 + t < T && e0 + e < E)
+        part[(static_cast<int64_t>(blockIdx.z) * T + t0 + t) * E + e0 + e] = v;
 }
 
 // N logits, each the sum of its parts in order; the loads of several parts are in flight together (one after the
-// other they took 37 us of a T = 1, E = 256 call).
+// other they took 37 us of a call with T = 1, E = 256).
 template <int N>
 __device__ __forceinline__ void logits_of(const double *part, int splits, const int (&at)[N], int64_t all, float (&out)[N])
 {
-    constexpr int U = N > 4 ? 2 : 8;
+    constexpr int U = N > 4 ? 2 : kMaxSplits;
     double v[N] = {};
     for (int s = 0; s < splits; s += U) {
         double p[U][N];
@@ -323,8 +331,48 @@ struct Plan {
 
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / kWave;
 
+// At most 64 slots: one wavefront sorts them, a slot in each lane, by the bits of their experts from the lowest (stable).
+__device__ __forceinline__ void make_small_plan(const int32_t *topk_idx, int n, int E, int K, const Plan &plan)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    int e = lane < n ? topk_idx[lane] : E, slot = lane;
+    if (e < 0 || e > E)
+        e = E;  // behind every expert
+    const int bits = 32 - __builtin_clz(E);
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (e >> b) & 1;
+        const uint64_t ones = __ballot(one), below = lanemask_lt();
+        const int to = one ? __popcll(~ones) + __popcll(ones & below) : __popcll(~ones & below);
+        e = __builtin_amdgcn_ds_permute(4 * to, e);
+        slot = __builtin_amdgcn_ds_permute(4 * to, slot);
+    }
+    const int before = __shfl_up(e, 1);
+    const bool first = e < E && (lane == 0 || before != e);
+    const uint64_t firsts = __ballot(first);
+    const int rank = __popcll(firsts & lanemask_lt()), routed = __popcll(__ballot(e < E));
+    if (slot < n)
+        plan.place[slot] = e < E ? lane : -1;
+    if (e < E) {
+        plan.order[lane] = slot;
+        plan.token[lane] = slot / K;
+    }
+    if (first) {
+        plan.act[rank] = e;
+        plan.start[rank] = lane;
+    }
+    if (lane == 0) {
+        plan.head[0] = __popcll(firsts);
+        plan.start[__popcll(firsts)] = routed;
+    }
+}
+
 __device__ __forceinline__ void make_plan(const int32_t *topk_idx, int n, int E, int K, const Plan &plan)
 {
+    if (n <= kWave) {
+        if (threadIdx.x < kWave)
+            make_small_plan(topk_idx, n, E, K, plan);
+        return;
+    }
     extern __shared__ uint16_t cnt[];  // [kPlanWaves][E]: each wavefront's slots per expert, then its next position
     __shared__ uint32_t wave_total[kPlanWaves];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
@@ -428,8 +476,11 @@ __global__ __launch_bounds__(kPlanThreads) void few_token_route_kernel(const dou
 // tiles meet in LDS. h goes out in the order of the plan, already multiplied by the slot's weight; beside bf16 or FP8
 // weights as two bf16 rows whose sum it is to 16 bits, so that the down product is one of bf16 operands without
 // bf16's rounding of h.
+
 // Registers of one load in flight, and the kernels' shape by them: 8 wavefronts of 128 registers, of which 16 share a CU
-// with at least two loads in flight each, or where that is not room enough 4 of 256, of which 8 do.
+// with at least two loads in flight each, or where that is not room enough 4 of 256, of which 8 do. FP8 weights, half of
+// whose time is conversion, are better off with 16 wavefronts and one load each (down, T4 H7168 I1024 K8: 85 -> 61 us,
+// T64 H4096 I2048: 317 -> 300).
 template <Weights W, int NW, int NT, bool LO>
 constexpr int kSlotRegs = 8 * (NW + NT * (LO ? 2 : 1) * (W == kWFp8 ? 2 : 1)) + (W == kWFp8 ? NW : 0);
 
@@ -442,7 +493,7 @@ enum Read { kLines, kWords, kOdd };
 template <Weights W, int NT, bool LO>
 struct Shape {
     static constexpr int kOther = W == kWFp8 ? 52 : 40;  // registers for addresses and what is being multiplied
-    static constexpr bool kWide = (128 - kOther - 8 * NT) / kSlotRegs<W, 2, NT, LO> < 2;
+    static constexpr bool kWide = W != kWFp8 && (128 - kOther - 8 * NT) / kSlotRegs<W, 2, NT, LO> < 2;
     static constexpr int kRegs = (kWide ? 256 : 128) - kOther, kWaves = kWide ? 4 : 8, kThreads = kWaves * kWave;
     static constexpr int kWavesPerSimd = kWide ? 2 : 4;
 };
@@ -851,10 +902,18 @@ __global__ __launch_bounds__(kMergeThreads) void merge_kernel(ExpertArgs a)
     if (c >= a.H)
         return;
     float v = 0.0f;
-    for (int k = 0; k < a.K; ++k) {
-        const int pos = a.plan.place[t * a.K + k];
-        if (pos >= 0)
-            v += a.y[static_cast<int64_t>(pos) * a.H + c];
+    for (int k0 = 0; k0 < a.K; k0 += 8) {  // eight slots' loads in flight together
+        int pos[8];
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            pos[k] = k0 + k < a.K ? a.plan.place[t * a.K + k0 + k] : -1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            y[k] = a.y[static_cast<int64_t>(max(pos[k], 0)) * a.H + c];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v += pos[k] >= 0 ? y[k] : 0.0f;
     }
     const int64_t o = static_cast<int64_t>(t) * a.H + c;
     if (a.out_bf16) {

@@ -8,6 +8,7 @@ of the computation runs in the gfx950 kernels. Calls are asynchronous on
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 from typing import Optional
 
@@ -693,6 +694,7 @@ def add_rmsnorm_backward(dout: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     return dx, dw
 
 
+@functools.lru_cache(maxsize=256)
 def rmsnorm_workspace_bytes(T: int, H: int) -> int:
     """Workspace bytes of add_rmsnorm_backward for these sizes (needed with the weight's gradient only)."""
     n = ctypes.c_size_t(0)
@@ -704,6 +706,7 @@ def rmsnorm_workspace_bytes(T: int, H: int) -> int:
 # ---------------------------------------------------------------- the whole layer for a few tokens
 
 
+@functools.lru_cache(maxsize=256)
 def few_token_workspace_bytes(T: int, H: int, I: int, E: int, K: int) -> int:
     """Workspace bytes of few_token_layer and few_token_experts for these sizes."""
     n = ctypes.c_size_t(0)
