@@ -158,19 +158,17 @@ int router_splits(int64_t T, int64_t E, int64_t H)
     return static_cast<int>(std::min(std::min(want, most), int64_t{kMaxSplits}));
 }
 
+// The mine-th of `parts` parts of a tile's sums: register r of lane l holds token t0 + l / 16 + 4 r and expert e0 + l % 16.
 template <typename X>
-__global__ __launch_bounds__(kRouterThreads) void router_kernel(const X *x, const X *router, int T, int H, int E,
-                                                                double *part)
+__device__ __forceinline__ f64x4 router_tile(const X *x, const X *router, int T, int H, int E, int t0, int e0, int mine,
+                                             int parts)
 {
     struct Elems {
         X v[8];
     };
-    __shared__ f64x4 red[kRouterWaves][kWave];
-    const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), m = lane % kTile, g = lane / kTile;
-    const int e0 = blockIdx.x * kTile, t0 = blockIdx.y * kTile;
+    const int lane = threadIdx.x & (kWave - 1), m = lane % kTile, g = lane / kTile;
     const X *xr = x + static_cast<int64_t>(min(t0 + m, T - 1)) * H, *rr = router + static_cast<int64_t>(min(e0 + m, E - 1)) * H;
-    const int steps = (H + kRouterElems - 1) / kRouterElems, parts = gridDim.z * kRouterWaves;
-    const int mine = blockIdx.z * kRouterWaves + wave;
+    const int steps = (H + kRouterElems - 1) / kRouterElems;
     const int s1 = static_cast<int64_t>(steps) * (mine + 1) / parts;
     f64x4 acc{};
     for (int s = static_cast<int64_t>(steps) * mine / parts; s < s1; ++s) {
@@ -187,12 +185,22 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const X *x, cons
         for (int i = 0; i < 8; ++i)
             acc = __builtin_amdgcn_mfma_f64_16x16x4f64(to_f32(a.v[i]), to_f32(b.v[i]), acc, 0, 0, 0);
     }
-    red[wave][lane] = acc;
+    return acc;
+}
+
+template <typename X>
+__global__ __launch_bounds__(kRouterThreads) void router_kernel(const X *x, const X *router, int T, int H, int E,
+                                                                double *part)
+{
+    __shared__ f64x4 red[kRouterWaves][kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
+    const int e0 = blockIdx.x * kTile, t0 = blockIdx.y * kTile;
+    const int parts = gridDim.z * kRouterWaves, mine = blockIdx.z * kRouterWaves + wave;
+    red[wave][lane] = router_tile(x, router, T, H, E, t0, e0, mine, parts);
     __syncthreads();
     if (threadIdx.x >= kTile * kTile)
         return;
-    // register r of lane l holds the tile's token l / 16 + 4 r and expert l % 16; neighbouring threads take neighbouring
-    // experts
+    // neighbouring threads take neighbouring experts
     const int e = threadIdx.x % kTile, t = threadIdx.x / kTile, src = t % 4 * kTile + e, r = t / 4;
     double v = 0.0;
     for (int w = 0; w < kRouterWaves; ++w)
@@ -256,18 +264,12 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
     return max(max(a, b), max(c, d));
 }
 
+// The token's logits in registers, logit[j] of expert lane + 64 j.
 template <int J>
-__device__ __forceinline__ void route_token(const double *part, int splits, int T, int t, int E, int K,
-                                            int32_t *topk_idx, float *topk_w)
+__device__ __forceinline__ void select_experts(const float (&logit)[J], int t, int E, int K, int32_t *topk_idx, float *topk_w)
 {
     const int lane = threadIdx.x & (kWave - 1);
     uint32_t key[J];  // 0: no expert, or taken
-    int at[J];
-    float logit[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-        at[j] = t * E + min(lane + kWave * j, E - 1);
-    logits_of<J>(part, splits, at, static_cast<int64_t>(T) * E, logit);
 #pragma unroll
     for (int j = 0; j < J; ++j)
         key[j] = lane + kWave * j < E ? orderable(logit[j]) : 0u;
@@ -314,6 +316,19 @@ __device__ __forceinline__ void route_token(const double *part, int splits, int 
         topk_idx[static_cast<int64_t>(t) * K + lane] = slot_id;
         topk_w[static_cast<int64_t>(t) * K + lane] = static_cast<float>(ex / z);
     }
+}
+
+template <int J>
+__device__ __forceinline__ void route_token(const double *part, int splits, int T, int t, int E, int K,
+                                            int32_t *topk_idx, float *topk_w)
+{
+    int at[J];
+    float logit[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        at[j] = t * E + min(static_cast<int>(threadIdx.x % kWave) + kWave * j, E - 1);
+    logits_of<J>(part, splits, at, static_cast<int64_t>(T) * E, logit);
+    select_experts<J>(logit, t, E, K, topk_idx, topk_w);
 }
 
 // ---------------------------------------------------------------- plan
@@ -469,6 +484,38 @@ __global__ __launch_bounds__(kPlanThreads) void few_token_route_kernel(const dou
         __syncthreads();  // the workgroup's own stores of topk_idx have been done
         make_plan(topk_idx, T * K, E, K, plan);
     }
+}
+
+// Router, routing and plan in one launch, for up to 16 tokens and 64 experts with little to read: one workgroup, whose
+// wavefronts share the tiles of 16 experts and the hidden dimension.
+constexpr int kSmallExperts = 64;
+
+template <typename X>
+__global__ __launch_bounds__(kPlanThreads) void few_token_small_route_kernel(const X *x, const X *router, int T, int H, int E,
+                                                                             int K, int32_t *topk_idx, float *topk_w,
+                                                                             Plan plan)
+{
+    __shared__ f64x4 red[kPlanWaves][kWave];
+    __shared__ float logits[kTile][kSmallExperts];
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
+    const int tiles = (E + kTile - 1) / kTile, parts = kPlanWaves / tiles;
+    if (wave < tiles * parts)
+        red[wave][lane] = router_tile(x, router, T, H, E, 0, wave % tiles * kTile, wave / tiles, parts);
+    __syncthreads();
+    const int t = threadIdx.x / kSmallExperts, e = threadIdx.x % kSmallExperts;  // 16 x 64 threads
+    if (t < T && e < E) {
+        double v = 0.0;
+        for (int p = 0; p < parts; ++p)
+            v += red[p * tiles + e / kTile][t % 4 * kTile + e % kTile][t / 4];
+        logits[t][e] = static_cast<float>(v);
+    }
+    __syncthreads();
+    if (wave < T) {
+        const float logit[1] = {logits[wave][min(lane, E - 1)]};
+        select_experts<1>(logit, wave, E, K, topk_idx, topk_w);
+    }
+    __syncthreads();  // the workgroup's own stores of topk_idx have been done
+    make_plan(topk_idx, T * K, E, K, plan);
 }
 
 // ---------------------------------------------------------------- gate and up products
@@ -892,6 +939,78 @@ __global__ __launch_bounds__((Shape<W, NT, W != kWF32>::kThreads), (Shape<W, NT,
     }
 }
 
+// ---------------------------------------------------------------- down product with the merge
+// For up to 16 tokens and little to read: one workgroup per 16 columns of out and all experts in use, whose wavefronts
+// share the (expert, load) pairs in order, each a stretch. A wavefront adds its tiles into sums of its own, [T][16] in
+// LDS, when its expert changes; the wavefronts' sums are put together in order.
+constexpr int kDirectThreads = 1024, kDirectWaves = kDirectThreads / kWave;
+
+__device__ __forceinline__ void store_out(const ExpertArgs &a, int t, int c, float v)
+{
+    const int64_t o = static_cast<int64_t>(t) * a.H + c;
+    if (a.out_bf16) {
+        if (a.bias)
+            v += to_f32(static_cast<const uint16_t *>(a.bias)[o]);
+        static_cast<uint16_t *>(a.out)[o] = static_cast<uint16_t>(f32_to_bf16_bits(v));
+    } else {
+        if (a.bias)
+            v += static_cast<const float *>(a.bias)[o];
+        static_cast<float *>(a.out)[o] = v;
+    }
+}
+
+template <Weights W, Read READ>
+__global__ __launch_bounds__(kDirectThreads) void down_merge_kernel(ExpertArgs a)
+{
+    typedef Product<W, 1, 1, W != kWF32, 128 - Shape<W, 1, W != kWF32>::kOther, READ> P;
+    constexpr int rows = W == kWF32 ? 1 : 2;  // of h per slot
+    __shared__ float sums[kDirectWaves][kTile][kTile];
+    const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), m = lane % kTile, g = lane / kTile;
+    const int c0 = blockIdx.x * kTile;
+    for (int i = lane; i < kTile * kTile; i += kWave)
+        sums[wave][i / kTile][i % kTile] = 0.0f;
+    const int loads = (a.I + kLoadElems<W> - 1) / kLoadElems<W>, all = a.plan.head[0] * loads;
+    const int u1 = all * (wave + 1) / kDirectWaves;
+    for (int u = all * wave / kDirectWaves; u < u1;) {
+        const int i = u / loads, l0 = u - i * loads, l1 = min(loads, l0 + (u1 - u));
+        u += l1 - l0;
+        const int p0 = a.plan.start[i], n = a.plan.start[i + 1] - p0;
+        const int64_t row = static_cast<int64_t>(a.plan.act[i]) * a.H + c0;
+        for (int r0 = 0; r0 < n; r0 += kTile) {
+            P p;
+            p.rows_of(a.I, a.H - 1 - c0, a.nb);
+            p.lo = static_cast<int64_t>(a.hI) * sizeof(typename P::X);
+            p.per_block = a.per_block;
+            p.w[0] = static_cast<const char *>(a.w) + row * a.I * sizeof(typename P::Wt);
+            p.scale[0] = a.scales + row * a.nb;
+            p.x = static_cast<const char *>(a.h) + static_cast<int64_t>(p0 + r0) * rows * a.hI * sizeof(typename P::X);
+            const int r = min(m, n - 1 - r0), tok = a.plan.token[p0 + r0 + r];
+            p.x_row[0] = static_cast<uint32_t>(r * rows * a.hI) * sizeof(typename P::X);
+            p.run(l0, l1, a.I, 0);
+            // this lane holds column m of the tile's rows 4 g .. 4 g + 3. A token that names the expert twice has two
+            // rows, neighbours: then the lane groups add one after the other
+            const bool twice = __ballot(m > 0 && r0 + m < n && tok == __shfl_up(tok, 1)) != 0;
+            for (int turn = 0; turn < (twice ? 4 : 1); ++turn) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int to = __shfl(tok, 4 * g + q);
+                    if ((!twice || g == turn) && r0 + 4 * g + q < n)
+                        sums[wave][to][m] += p.acc[0][0][q];
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+    }
+    __syncthreads();
+    const int t = threadIdx.x / kTile, c = c0 + threadIdx.x % kTile;
+    if (t >= a.T || c >= a.H)
+        return;
+    float v = 0.0f;
+    for (int k = 0; k < kDirectWaves; ++k)
+        v += sums[k][t][threadIdx.x % kTile];
+    store_out(a, t, c, v);
+}
+
 // ---------------------------------------------------------------- merge
 // out[t] = the sum of its slots' rows in slot order (their weights are in h), plus bias.
 constexpr int kMergeThreads = 256;
@@ -915,16 +1034,7 @@ __global__ __launch_bounds__(kMergeThreads) void merge_kernel(ExpertArgs a)
         for (int k = 0; k < 8; ++k)
             v += pos[k] >= 0 ? y[k] : 0.0f;
     }
-    const int64_t o = static_cast<int64_t>(t) * a.H + c;
-    if (a.out_bf16) {
-        if (a.bias)
-            v += to_f32(static_cast<const uint16_t *>(a.bias)[o]);
-        static_cast<uint16_t *>(a.out)[o] = static_cast<uint16_t>(f32_to_bf16_bits(v));
-    } else {
-        if (a.bias)
-            v += static_cast<const float *>(a.bias)[o];
-        static_cast<float *>(a.out)[o] = v;
-    }
+    store_out(a, t, c, v);
 }
 
 // ---------------------------------------------------------------- host side
@@ -1012,6 +1122,9 @@ moe_status check_layer(const void *x, moe_dtype dt, int64_t T, int64_t H, int64_
     return MOE_OK;
 }
 
+// Bytes of router weights up to which one workgroup reads them all and routes too.
+constexpr int64_t kSmallRouter = 128 << 10;
+
 size_t plan_lds(int E) { return sizeof(uint16_t) * kPlanWaves * static_cast<size_t>(E); }
 
 // Wavefronts that share a unit of weight rows: enough wavefronts for the chip, as long as each has a few loads.
@@ -1027,6 +1140,11 @@ int share_parts(int64_t units, int64_t loads, int waves)
 // for the same columns at the same time: there each begins with another load (T64 H4096 I2048 E64 K2: gate and up 352 ->
 // 329 us, down 187 -> 161; rows of 2 or 14 KiB are up to 7% faster read from the start).
 bool stagger(int64_t row_bytes) { return row_bytes % 4096 == 0; }
+
+// Loads of a column tile's experts (by the most experts that may be in use) up to which one workgroup takes them all and
+// merges too: a launch fewer, which is what the smallest calls spend their time on (T1 H512 I1024 K2 float32 21 -> 19 us),
+// against less of the chip at work (T8 H1024 I512 K4, 112 loads: 21 -> 32 us).
+constexpr int64_t kDirectLoads = 64;
 
 template <Weights W>
 Read read_of(const void *w, int64_t row_bytes, const void *x, int64_t x_row_bytes)
@@ -1064,16 +1182,28 @@ void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t
     a.scales = w.down_scales;
     a.nb = W == kWFp8 ? a.I / w.block : 0;
     a.stagger = stagger(int64_t{a.I} * size);
+    read = read_of<W>(a.w, int64_t{a.I} * size, nullptr, 0);
+    if (NT == 1 && used * ceil_div(a.I, kLoadElems<W>) <= kDirectLoads) {
+        grid = dim3(static_cast<unsigned>(ceil_div(a.H, kTile)));
+        if (read == kLines)
+            hipLaunchKernelGGL((down_merge_kernel<W, kLines>), grid, dim3(kDirectThreads), 0, stream, a);
+        else if (W != kWBf16 || read == kWords)
+            hipLaunchKernelGGL((down_merge_kernel<W, kWords>), grid, dim3(kDirectThreads), 0, stream, a);
+        else if constexpr (W == kWBf16)
+            hipLaunchKernelGGL((down_merge_kernel<W, kOdd>), grid, dim3(kDirectThreads), 0, stream, a);
+        return;
+    }
     units = ceil_div(a.H, 2 * kTile);
     a.parts = share_parts(units * used, ceil_div(a.I, kLoadElems<W>), Down::kWaves);
     grid = dim3(static_cast<unsigned>(ceil_div(units, Down::kWaves / a.parts)), static_cast<unsigned>(used));
-    read = read_of<W>(a.w, int64_t{a.I} * size, nullptr, 0);
     if (read == kLines)
         hipLaunchKernelGGL((down_kernel<W, NT, kLines>), grid, dim3(Down::kThreads), 0, stream, a);
     else if (W != kWBf16 || read == kWords)
         hipLaunchKernelGGL((down_kernel<W, NT, kWords>), grid, dim3(Down::kThreads), 0, stream, a);
     else if constexpr (W == kWBf16)
         hipLaunchKernelGGL((down_kernel<W, NT, kOdd>), grid, dim3(Down::kThreads), 0, stream, a);
+    hipLaunchKernelGGL(merge_kernel, dim3(static_cast<unsigned>(ceil_div(a.H, kMergeThreads)), static_cast<unsigned>(a.T)),
+                       dim3(kMergeThreads), 0, stream, a);
 }
 
 template <Weights W>
@@ -1117,8 +1247,6 @@ moe_status launch_experts(const void *x, int64_t T, int64_t H, int64_t I, int32_
         launch_products_of<kWF32>(a, w, used, stream);
     else
         launch_products_of<kWBf16>(a, w, used, stream);
-    hipLaunchKernelGGL(merge_kernel, dim3(static_cast<unsigned>(ceil_div(H, kMergeThreads)), static_cast<unsigned>(T)),
-                       dim3(kMergeThreads), 0, stream, a);
     return launch_status();
 }
 
@@ -1179,6 +1307,18 @@ extern "C" moe_status moe_few_token_layer(const void *x, moe_dtype dt, const voi
     const Layout l = layout(T, H, E, K, I);
     double *part = reinterpret_cast<double *>(ws + l.part);
     const int Ti = static_cast<int>(T), Hi = static_cast<int>(H), splits = router_splits(T, E, H);
+    if (gs == 0 && T <= kTile && E <= kSmallExperts && E * H * (dt == MOE_F32 ? 4 : 2) <= kSmallRouter) {
+        const Plan plan = plan_in(ws, l);
+        if (dt == MOE_F32)
+            hipLaunchKernelGGL(few_token_small_route_kernel<float>, dim3(1), dim3(kPlanThreads), plan_lds(E), stream,
+                               static_cast<const float *>(x), static_cast<const float *>(router), Ti, Hi, E, K, topk_idx,
+                               topk_w, plan);
+        else
+            hipLaunchKernelGGL(few_token_small_route_kernel<uint16_t>, dim3(1), dim3(kPlanThreads), plan_lds(E), stream,
+                               static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(router), Ti, Hi, E, K, topk_idx,
+                               topk_w, plan);
+        return launch_experts(x, T, H, I, E, K, topk_idx, topk_w, w, bias, out, out_dt, ws, true, stream);
+    }
     const dim3 grid(static_cast<unsigned>(ceil_div(E, kTile)), static_cast<unsigned>(ceil_div(T, kTile)),
                     static_cast<unsigned>(splits));
     if (dt == MOE_F32)
