@@ -1,8 +1,9 @@
 """The few-token MoE layer on the GPU against its definition in 64 bits.
 
-Tolerances count roundings of u = 2^-24 (2u where a matrix instruction may truncate) along a term's way, with the
-sums of magnitudes from the same 64-bit computation: a product over n elements split over 8 wavefronts passes at most
-n/8 + 16 roundings of a term."""
+Tolerances count roundings of u = 2^-24 along a term's way, with the sums of magnitudes from the same 64-bit
+computation. A wavefront may take a whole row of n elements: float32 products are then a chain of n fused multiply-adds, a
+rounding each; bf16 ones n/32 matrix instructions, which may truncate (2u) and round a few times inside, fewer than n in
+all. Partial sums, scales and what follows add less than 48."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -70,7 +71,7 @@ class Layer:
         T, I = len(x), self.I
         xd = x.double()
         out, bound = torch.zeros(T, self.H, dtype=torch.float64, device=DEV), torch.zeros(T, self.H, dtype=torch.float64, device=DEV)
-        n_in, n_out = self.H / 8 + 24, self.I / 8 + 24 + idx.shape[1]
+        n_in, n_out = self.H + 48, self.I + 48 + idx.shape[1]
         for e in sorted(set(idx.flatten().tolist())):
             if not 0 <= e < self.E:
                 continue
@@ -78,7 +79,7 @@ class Layer:
             gu = xd[t] @ self.v13[e].t()
             mag = xd[t].abs() @ self.v13[e].abs().t()
             g, up = gu[:, :I], gu[:, I:]
-            dg, du = (2 * U * n_in * mag).split(I, 1)
+            dg, du = (U * n_in * mag).split(I, 1)
             wt = torch.ones(len(t), 1, dtype=torch.float64, device=DEV) if w is None else w[t, k].double()[:, None]
             s = g * torch.sigmoid(g)
             h = wt * s * up
@@ -86,7 +87,7 @@ class Layer:
             dh = wt.abs() * (1.1 * dg * (up.abs() + du) + s.abs() * du) + (8 * U + 2.0 ** -17) * h.abs()
             out.index_add_(0, t, h @ self.v2[e].t())
             mag = h.abs() @ self.v2[e].abs().t()
-            bound.index_add_(0, t, dh @ self.v2[e].abs().t() + 2 * U * n_out * mag)
+            bound.index_add_(0, t, dh @ self.v2[e].abs().t() + U * n_out * mag)
         if bias is not None:
             out = out + bias.double()
             bound = bound + U * out.abs()
@@ -355,3 +356,37 @@ def test_rows_on_odd_elements(m, T, H, I, shift):
     w = w.float()
     out = m.few_token_experts(off(x), idx, w, off(lay.w13), off(lay.w2), out_dtype=F32)
     assert_within(out, *lay.expected(x, idx, w))
+
+
+@pytest.mark.parametrize("T,H,I,kind", [(200, 2056, 1032, "f32"), (200, 2056, 1032, "bf16"), (256, 2048, 1024, "fp8"),
+                                        (150, 2049, 1027, "bf16"), (131, 2176, 1152, "bf16")])
+def test_many_tokens_an_expert(m, T, H, I, kind):
+    """Sizes at which experts with more than one or two tiles of tokens take the products through LDS: experts with a
+    handful of tokens, some tens, and all of them, side by side."""
+    E, K = 32, 8
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    lay = Layer(m, 128, 128, 1, kind)  # replaced below by weights drawn on the GPU
+    lay.H, lay.I, lay.E = H, I, E
+    w13 = torch.randn(E, 2 * I, H, generator=g, device=DEV) * H ** -0.5
+    w2 = torch.randn(E, H, I, generator=g, device=DEV) * I ** -0.5
+    if kind == "fp8":
+        q13, s13 = m.quantize_fp8(w13.view(E * 2 * I, H))
+        q2, s2 = m.quantize_fp8(w2.view(E * H, I))
+        lay.w13, lay.w2 = q13.view(E, 2 * I, H), q2.view(E, H, I)
+        lay.scales = dict(gate_up_scales=s13.view(E, 2 * I, -1), down_scales=s2.view(E, H, -1))
+        value = lambda q, s: q.view(torch.float8_e4m3fn).double() * s.double().repeat_interleave(128, 1)  # noqa: E731
+        lay.v13, lay.v2 = value(q13, s13).view(E, 2 * I, H), value(q2, s2).view(E, H, I)
+    else:
+        lay.w13, lay.w2 = w13.to(lay.rows), w2.to(lay.rows)
+        lay.v13, lay.v2 = lay.w13.double(), lay.w2.double()
+    x = torch.randn(T, H, generator=g, device=DEV).to(lay.rows)
+    # expert 0 takes every token, experts 1..6 most, the others ever fewer
+    p = torch.tensor([1e9] + [8.0] * 6 + [2.0 ** (2 - e / 4) for e in range(E - 7)], device=DEV)
+    idx = torch.multinomial(p.expand(T, E), K, generator=g).to(torch.int32)
+    w = torch.rand(T, K, generator=g, device=DEV)
+    rows = torch.bincount(idx.flatten().long(), minlength=E)
+    assert int(rows.max()) == T and int((rows <= 16).sum()) >= 3 and int(((rows > 16) & (rows <= 32)).sum()) >= 2
+    out = m.few_token_experts(x, idx, w, lay.w13, lay.w2, out_dtype=F32, **lay.scales)
+    assert_within(out, *lay.expected(x, idx, w))
+    assert torch.equal(out, m.few_token_experts(x, idx, w, lay.w13, lay.w2, out_dtype=F32, **lay.scales))

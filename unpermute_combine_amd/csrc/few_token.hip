@@ -21,6 +21,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t vec4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxFewTokens = MOE_MAX_FEW_TOKENS;
 constexpr int kTile = 16;  // tokens and weight rows of one matrix tile
@@ -57,6 +58,28 @@ __device__ __forceinline__ void to_halves(u32x4 &a, u32x4 &b)
     swap_eights(a.y, b.y);
     swap_eights(a.z, b.z);
     swap_eights(a.w, b.w);
+}
+
+// 16 bytes at an even address: the aligned words that hold them (the fifth, where the address is aligned, again the
+// fourth: no word is read that holds none of them), for shift_odd to put together when they have come.
+__device__ __forceinline__ void load_odd(const char *p, u32x4 &v, uint32_t &over)
+{
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~uintptr_t{3};
+    __builtin_memcpy(&v, reinterpret_cast<const char *>(at), sizeof(v));
+    over = *reinterpret_cast<const uint32_t *>(at + 12 + 2 * (reinterpret_cast<uintptr_t>(p) & 2));
+}
+
+__device__ __forceinline__ uint32_t odd_bits(const char *p)
+{
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 2) * 8;
+}
+
+__device__ __forceinline__ void shift_odd(u32x4 &v, uint32_t over, uint32_t bits)
+{
+    v.x = __builtin_amdgcn_alignbit(v.y, v.x, bits);
+    v.y = __builtin_amdgcn_alignbit(v.z, v.y, bits);
+    v.z = __builtin_amdgcn_alignbit(v.w, v.z, bits);
+    v.w = __builtin_amdgcn_alignbit(over, v.w, bits);
 }
 
 // A lane's share of a row's partial load, elements e, e + 1, ... up to len: the vector that ends with the row, zeros in
@@ -524,10 +547,7 @@ __global__ __launch_bounds__(kPlanThreads) void few_token_small_route_kernel(con
 // weights as two bf16 rows whose sum it is to 16 bits, so that the down product is one of bf16 operands without
 // bf16's rounding of h.
 
-// Registers of one load in flight, and the kernels' shape by them: 8 wavefronts of 128 registers, of which 16 share a CU
-// with at least two loads in flight each, or where that is not room enough 4 of 256, of which 8 do. FP8 weights, half of
-// whose time is conversion, are better off with 16 wavefronts and one load each (down, T4 H7168 I1024 K8: 85 -> 61 us,
-// T64 H4096 I2048: 317 -> 300).
+// Registers of one load in flight.
 template <Weights W, int NW, int NT, bool LO>
 constexpr int kSlotRegs = 8 * (NW + NT * (LO ? 2 : 1) * (W == kWFp8 ? 2 : 1)) + (W == kWFp8 ? NW : 0);
 
@@ -537,12 +557,13 @@ constexpr int kSlotRegs = 8 * (NW + NT * (LO ? 2 : 1) * (W == kWFp8 ? 2 : 1)) + 
 // together by shifts). FP8 rows off their words are read as they lie.
 enum Read { kLines, kWords, kOdd };
 
-template <Weights W, int NT, bool LO>
+// The shape of a kernel: 8 wavefronts of 128 registers, of which 16 share a CU with two loads or more in flight each, or
+// where experts may have MANY tokens (more than a tile's) 4 of 256, of which 8 do.
+template <Weights W, bool MANY>
 struct Shape {
     static constexpr int kOther = W == kWFp8 ? 52 : 40;  // registers for addresses and what is being multiplied
-    static constexpr bool kWide = W != kWFp8 && (128 - kOther - 8 * NT) / kSlotRegs<W, 2, NT, LO> < 2;
-    static constexpr int kRegs = (kWide ? 256 : 128) - kOther, kWaves = kWide ? 4 : 8, kThreads = kWaves * kWave;
-    static constexpr int kWavesPerSimd = kWide ? 2 : 4;
+    static constexpr int kRegs = (MANY ? 256 : 128) - kOther, kWaves = MANY ? 4 : 8, kThreads = kWaves * kWave;
+    static constexpr int kWavesPerSimd = MANY ? 2 : 4;
 };
 
 struct ExpertArgs {
@@ -560,36 +581,27 @@ struct ExpertArgs {
     uint32_t per_block;       // and 2^32 over the loads of one, rounded up (0: one load each)
     int parts;                // wavefronts that share a unit's loads
     bool stagger;             // units begin with different loads
+    bool tiled;               // experts with many tokens take the tiled product
     bool out_bf16;
     Plan plan;
 };
 
-// The products of NW rows of weights (one per lane column) with NT tiles of 16 tokens over a range of loads: LO adds
-// the activations' second bf16 row, `lo` bytes behind the first. The loads run D ahead of the matrix instructions in
-// a ring of registers, so that each wavefront keeps 2 * D * NW KiB of weights in flight all the time. Addresses are a
-// uniform base, which moves, and a 32-bit offset in each lane, which does not.
-template <Weights W, int NW, int NT, bool LO, int REGS, Read READ>
-struct Product {
+// NW rows of weights (one per lane column) as they stream through a wavefront. Addresses are a uniform base, which
+// moves, and a 32-bit offset in each lane, which does not.
+template <Weights W, int NW, Read READ>
+struct WeightRows {
     typedef typename WeightType<W>::type Wt;
-    typedef typename ActType<W>::type X;
-    static constexpr int kRoom = (REGS - 4 * NW * NT) / kSlotRegs<W, NW, NT, LO>;
-    static constexpr int D = kRoom > 4 ? 4 : kRoom < 1 ? 1 : kRoom;
-    static constexpr int kActBytes = kHalfElems<W> * sizeof(X);  // of a token's row per half
-    const char *w[NW], *x;
+    const char *w[NW];
     const float *scale[NW];
-    uint32_t w_off[2], w_row, x_row[NT], x_lane, s_off;
-    int64_t lo;
-    uint32_t per_block;
-    f32x4 acc[NW][NT];
+    uint32_t w_off[2], w_row, s_off, per_block;
 
-    struct Slot {
+    struct Load {
         u32x4 w[NW][2];
-        Acts<W> x[NT][2], y[NT][2];
+        uint32_t over[NW][2];  // kOdd
         float s[NW];
-        uint32_t w_over[NW][2], x_over[NT][2];  // kOdd
     };
 
-    // Weight rows 0..15 from w[] on, `stride` elements apart; rows past `last` are read as that one.
+    // Rows 0..15 from w[] on, `stride` elements apart; rows past `last` are read as that one.
     __device__ __forceinline__ void rows_of(int stride, int last, int nb)
     {
         const int lane = threadIdx.x & (kWave - 1), m = lane % kTile, g = lane / kTile;
@@ -597,112 +609,25 @@ struct Product {
         for (int i = 0; i < 2; ++i)
             w_off[i] = static_cast<uint32_t>(min(8 * i + m % 8, last) * stride) * sizeof(Wt) + m / 8 * 64 + 16 * g;
         w_row = static_cast<uint32_t>(min(m, last) * stride) * sizeof(Wt);
-        x_lane = kActBytes / 4 * g;
         s_off = min(m, last) * nb;
-#pragma unroll
-        for (int i = 0; i < NW; ++i)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                acc[i][t] = f32x4{};
     }
 
-    __device__ __forceinline__ void add(Slot &q)
-    {
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            if constexpr (READ == kOdd) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    shift(q.w[i][h], q.w_over[i][h], odd_bits(w[i] + w_off[h]));
-            }
-            to_halves(q.w[i][0], q.w[i][1]);
-        }
-        if constexpr (READ == kOdd && !LO) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    shift(q.x[t][h].v[0], q.x_over[t][h], odd_bits(x + x_row[t]));
-        }
-#pragma unroll
-        for (int i = 0; i < NW; ++i)
-            multiply_halves(q, i);
-    }
-
-    __device__ __forceinline__ static uint32_t odd_bits(const char *p)
-    {
-        return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 2) * 8;
-    }
-
-    __device__ __forceinline__ void multiply_halves(const Slot &q, int i)
-    {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            f32x4 p = W == kWFp8 ? f32x4{} : acc[i][t];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                p = multiply<W>(p, q.x[t][h], q.w[i][h]);
-                if (LO)
-                    p = multiply<W>(p, q.y[t][h], q.w[i][h]);
-            }
-            if (W == kWFp8)  // a load lies in one block of scales
-                acc[i][t] += p * q.s[i];
-            else
-                acc[i][t] = p;
-        }
-    }
-
-    __device__ __forceinline__ void issue_weights(Slot &q, int l)
+    __device__ __forceinline__ void issue(Load &q, int l) const
     {
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                load_line(w[i] + static_cast<int64_t>(l) * 128 + w_off[h], q.w[i][h], q.w_over[i][h]);
+                load_line(w[i] + static_cast<int64_t>(l) * 128 + w_off[h], q.w[i][h], q.over[i][h]);
             if (W == kWFp8)
                 q.s[i] = (scale[i] + (per_block ? __umulhi(l, per_block) : l))[s_off];
         }
     }
 
-    __device__ __forceinline__ void issue_acts(Slot &q, int l)
-    {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const char *row = x + static_cast<int64_t>(2 * l + h) * kActBytes;
-                if constexpr (READ == kOdd && !LO) {
-                    load_odd(row + (x_row[t] + x_lane), q.x[t][h].v[0], q.x_over[t][h]);
-                } else {
-                    __builtin_memcpy(&q.x[t][h], row + (x_row[t] + x_lane), sizeof(q.x[t][h]));
-                    if (LO)
-                        __builtin_memcpy(&q.y[t][h], row + lo + (x_row[t] + x_lane), sizeof(q.y[t][h]));
-                }
-            }
-    }
-
-    // 16 bytes at an even address: the aligned words that hold them (the fifth, where the address is aligned, again the
-    // fourth: no word is read that holds none of them), for `shift` to put together when they have come.
-    __device__ __forceinline__ static void load_odd(const char *p, u32x4 &v, uint32_t &over)
-    {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~uintptr_t{3};
-        __builtin_memcpy(&v, reinterpret_cast<const char *>(at), sizeof(v));
-        over = *reinterpret_cast<const uint32_t *>(at + 12 + 2 * (reinterpret_cast<uintptr_t>(p) & 2));
-    }
-
-    __device__ __forceinline__ static void shift(u32x4 &v, uint32_t over, uint32_t bits)
-    {
-        v.x = __builtin_amdgcn_alignbit(v.y, v.x, bits);
-        v.y = __builtin_amdgcn_alignbit(v.z, v.y, bits);
-        v.z = __builtin_amdgcn_alignbit(v.w, v.z, bits);
-        v.w = __builtin_amdgcn_alignbit(over, v.w, bits);
-    }
-
     __device__ __forceinline__ static void load_line(const char *p, u32x4 &v, uint32_t &over)
     {
         if constexpr (READ == kLines) {
-            typedef uint32_t vec __attribute__((ext_vector_type(4)));
-            const vec n = __builtin_nontemporal_load(reinterpret_cast<const vec *>(p));
+            const vec4 n = __builtin_nontemporal_load(reinterpret_cast<const vec4 *>(p));
             v = u32x4{n.x, n.y, n.z, n.w};
         } else if constexpr (READ == kOdd) {
             load_odd(p, v, over);
@@ -711,9 +636,125 @@ struct Product {
         }
     }
 
+    // A load that has come, made into the matrix instructions' operands.
+    __device__ __forceinline__ void arrange(Load &q) const
+    {
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            if constexpr (READ == kOdd) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    shift_odd(q.w[i][h], q.over[i][h], odd_bits(w[i] + w_off[h]));
+            }
+            to_halves(q.w[i][0], q.w[i][1]);
+        }
+    }
+
+    // The rows' partial load, from element `whole` of len on, as operands.
+    __device__ __forceinline__ void tail(Load &q, int whole, int len) const
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                load_tail(reinterpret_cast<const Wt *>(w[i] + w_row),
+                          whole + h * kHalfElems<W> + static_cast<int>(threadIdx.x % kWave / kTile) * kLaneElems<W>, len,
+                          q.w[i][h]);
+    }
+};
+
+// acc[i] += tile of activations * weight rows i, one half of a load.
+template <Weights W, int NW>
+__device__ __forceinline__ void multiply_rows(f32x4 (&acc)[NW], const Acts<W> &x, const u32x4 (&w)[NW][2], int h)
+{
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+        acc[i] = multiply<W>(acc[i], x, w[i][h]);
+}
+
+// The products of NW rows of weights with NT tiles of 16 tokens over a range of loads: LO adds the activations' second
+// bf16 row, `lo` bytes behind the first. The loads run D ahead of the matrix instructions in a ring of registers, so
+// that each wavefront keeps 2 * D * NW KiB of weights in flight all the time.
+template <Weights W, int NW, int NT, bool LO, int REGS, Read READ>
+struct Product {
+    typedef WeightRows<W, NW, READ> Rows;
+    typedef typename Rows::Wt Wt;
+    typedef typename ActType<W>::type X;
+    static constexpr int kRoom = (REGS - 4 * NW * NT) / kSlotRegs<W, NW, NT, LO>;
+    static constexpr int D = kRoom > 4 ? 4 : kRoom < 1 ? 1 : kRoom;
+    static constexpr int kActBytes = kHalfElems<W> * sizeof(X);  // of a token's row per half
+    Rows rows;
+    const char *x;
+    uint32_t x_row[NT];
+    int64_t lo;
+    f32x4 acc[NT][NW];
+
+    struct Slot {
+        typename Rows::Load w;
+        Acts<W> x[NT][2], y[NT][2];
+        uint32_t x_over[NT][2];  // kOdd
+    };
+
+    __device__ __forceinline__ void multiply_slot(const Slot &q)
+    {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            f32x4 p[NW];
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                p[i] = W == kWFp8 ? f32x4{} : acc[t][i];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                multiply_rows<W, NW>(p, q.x[t][h], q.w.w, h);
+                if (LO)
+                    multiply_rows<W, NW>(p, q.y[t][h], q.w.w, h);
+            }
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                acc[t][i] = W == kWFp8 ? acc[t][i] + p[i] * q.w.s[i] : p[i];  // a load lies in one block of scales
+        }
+    }
+
+    __device__ __forceinline__ void add(Slot &q)
+    {
+        rows.arrange(q.w);
+        if constexpr (READ == kOdd && !LO) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    shift_odd(q.x[t][h].v[0], q.x_over[t][h], odd_bits(x + x_row[t]));
+        }
+        multiply_slot(q);
+    }
+
+    __device__ __forceinline__ void issue_acts(Slot &q, int l)
+    {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const uint32_t off = x_row[t] + kActBytes / 4 * (threadIdx.x % kWave / kTile);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const char *row = x + static_cast<int64_t>(2 * l + h) * kActBytes;
+                if constexpr (READ == kOdd && !LO) {
+                    load_odd(row + off, q.x[t][h].v[0], q.x_over[t][h]);
+                } else {
+                    __builtin_memcpy(&q.x[t][h], row + off, sizeof(q.x[t][h]));
+                    if (LO)
+                        __builtin_memcpy(&q.y[t][h], row + lo + off, sizeof(q.y[t][h]));
+                }
+            }
+        }
+    }
+
     // Loads l0 .. l1 - 1 of rows of len elements, beginning with the turn-th of them.
     __device__ __forceinline__ void run(int l0, int l1, int len, int turn)
     {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                acc[t][i] = f32x4{};
         const int whole = min(l1, len / kLoadElems<W>), n = whole - l0;
         if (n > 0) {
             Slot q[D];
@@ -723,7 +764,7 @@ struct Product {
 #pragma unroll
             for (int u = 0; u < D; ++u) {  // weights first: the activations' addresses are longer in coming
                 first[u] = at;
-                issue_weights(q[u], at);
+                rows.issue(q[u].w, at);
                 next();
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -735,7 +776,7 @@ struct Product {
 #pragma unroll
                 for (int u = 0; u < D; ++u) {
                     add(q[u]);
-                    issue_weights(q[u], at);
+                    rows.issue(q[u].w, at);
                     issue_acts(q[u], at);
                     next();
                     __builtin_amdgcn_sched_barrier(0);  // left alone, the scheduler gathers the loop's loads at its end
@@ -748,23 +789,152 @@ struct Product {
         }
         if (W != kWFp8 && whole < l1) {  // the row's last load, partial
             Slot z;
+            rows.tail(z.w, whole * kLoadElems<W>, len);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int e = (2 * whole + h) * kHalfElems<W> + static_cast<int>(threadIdx.x % kWave / kTile) * kLaneElems<W>;
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < NW; ++i)
-                    load_tail(reinterpret_cast<const Wt *>(w[i] + w_row), e, len, z.w[i][h]);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
+                for (int h = 0; h < 2; ++h) {
+                    const int e = (2 * whole + h) * kHalfElems<W> + static_cast<int>(threadIdx.x % kWave / kTile) * kLaneElems<W>;
                     load_tail(reinterpret_cast<const X *>(x + x_row[t]), e, len, z.x[t][h]);
                     if (LO)
                         load_tail(reinterpret_cast<const X *>(x + x_row[t] + lo), e, len, z.y[t][h]);
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < NW; ++i)
-                multiply_halves(z, i);
+            multiply_slot(z);
         }
+    }
+};
+
+// The products of two rows of weights a lane column with NT tiles of tokens, for a workgroup of 4 wavefronts with
+// different weight rows and the same tokens: per load the tokens' activations go through LDS once for all wavefronts
+// (two buffers, one barrier a load), where every wavefront alone would fetch each of them from L2 (T256 H4096 I2048 E16 K4,
+// 64 tokens an expert: gate and up 290 -> 219 us, down 233 -> 148).
+template <Weights W, int NT, bool LO, Read READ>
+struct TiledProduct {
+    typedef WeightRows<W, 2, READ> Rows;
+    typedef typename ActType<W>::type X;
+    static constexpr int kThreads = 4 * kWave, kRowChunks = W == kWFp8 ? 16 : 8, kPlanes = LO ? 2 : 1;
+    static constexpr int kPlaneChunks = NT * kTile * kRowChunks, kChunks = kPlaneChunks * kPlanes;  // of 16 bytes
+    static constexpr int Q = kChunks / kThreads;  // chunks a thread carries
+    static constexpr int kBytes = 2 * kChunks * 16;
+    // loads in flight: what the registers beside the accumulators hold, eight at most
+    static constexpr int kRoom = (W == kWFp8 ? 110 : 160) / (16 + 4 * Q), D = kRoom > 8 ? 8 : kRoom;
+    static constexpr int kPerLane = kRowChunks / 8;  // chunks of a lane's share of a half
+    Rows rows;
+    const char *x;
+    int64_t lo;
+    f32x4 acc[2][NT];
+
+    struct Slot {
+        typename Rows::Load w;
+        vec4 x[Q];  // of the load after w's
+    };
+
+    // Chunk c of row r, with the rows' chunks permuted so that neighbouring rows' are in different banks.
+    __device__ __forceinline__ static int place(int plane, int r, int c)
+    {
+        return plane * kPlaneChunks + r * kRowChunks + (c ^ (r & 7));
+    }
+
+    __device__ __forceinline__ void multiply_load(const u32x4 *buf, const typename Rows::Load &q)
+    {
+        const int lane = threadIdx.x & (kWave - 1), m = lane % kTile, g = lane / kTile;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            f32x4 p[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                p[i] = W == kWFp8 ? f32x4{} : acc[i][t];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int pl = 0; pl < kPlanes; ++pl) {
+                    Acts<W> a;
+#pragma unroll
+                    for (int i = 0; i < kPerLane; ++i)
+                        a.v[i] = buf[place(pl, t * kTile + m, h * (kRowChunks / 2) + g * kPerLane + i)];
+                    multiply_rows<W, 2>(p, a, q.w, h);
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                acc[i][t] = W == kWFp8 ? acc[i][t] + p[i] * q.s[i] : p[i];
+        }
+    }
+
+    // All loads of rows of len elements; row_of(r) is the byte offset of the r-th token's row from x.
+    template <typename F>
+    __device__ __forceinline__ void run(int len, u32x4 *lds, F row_of)
+    {
+        uint32_t from[Q];
+        int to[Q];
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            const int j = threadIdx.x + i * kThreads, r = j / kRowChunks % (NT * kTile), c = j % kRowChunks;
+            from[i] = row_of(r) + 16 * c;
+            to[i] = place(j / kPlaneChunks, r, c);
+        }
+        auto plane_of = [&](int i) { return x + (LO && i >= Q / 2 ? lo : 0); };
+        auto issue_x = [&](vec4 (&v)[Q], int l) {
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                vec4 n;
+                __builtin_memcpy(&n, plane_of(i) + static_cast<int64_t>(l) * kRowChunks * 16 + from[i], 16);
+                v[i] = n;
+            }
+        };
+        auto stage = [&](const vec4 (&v)[Q], int b) {
+#pragma unroll
+            for (int i = 0; i < Q; ++i)
+                reinterpret_cast<vec4 *>(lds)[b * kChunks + to[i]] = v[i];
+        };
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                acc[i][t] = f32x4{};
+        const int n = len / kLoadElems<W>;
+        int b = 0;
+        if (n > 0) {
+            Slot q[D];
+            vec4 x0[Q];
+            issue_x(x0, 0);
+#pragma unroll
+            for (int u = 0; u < D; ++u) {
+                rows.issue(q[u].w, min(u, n - 1));
+                issue_x(q[u].x, min(u + 1, n - 1));
+            }
+            stage(x0, 0);
+            for (int l = 0; l < n; l += D) {
+#pragma unroll
+                for (int u = 0; u < D; ++u) {
+                    if (l + u < n) {
+                        __syncthreads();
+                        rows.arrange(q[u].w);
+                        multiply_load(lds + b * kChunks, q[u].w);
+                        b ^= 1;
+                        stage(q[u].x, b);
+                        rows.issue(q[u].w, min(l + u + D, n - 1));
+                        issue_x(q[u].x, min(l + u + D + 1, n - 1));
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
+        }
+        if (W != kWFp8 && n * kLoadElems<W> < len) {  // the last load, partial
+            vec4 v[Q];
+            typename Rows::Load z;
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const int c = (threadIdx.x + i * kThreads) % kRowChunks;
+                load_tail(reinterpret_cast<const X *>(plane_of(i) + from[i] - 16 * c), n * kLoadElems<W> + c * kLaneElems<W>,
+                          len, v[i]);
+            }
+            rows.tail(z, n * kLoadElems<W>, len);
+            __syncthreads();
+            stage(v, b);
+            __syncthreads();
+            multiply_load(lds + b * kChunks, z);
+        }
+        __syncthreads();  // the buffers are free again
     }
 };
 
@@ -780,28 +950,28 @@ struct Share {
     }
 };
 
-// The parts' tiles put together in order: thread = (value of a tile, unit), f(unit's first wavefront, tile row, column,
-// sums of the NW weight rows). Register r of lane l holds the tile's row 4 (l / 16) + r and column l % 16.
-template <int WAVES, int NW, int NT, typename F>
-__device__ __forceinline__ void join_parts(const f32x4 (&acc)[NW][NT], int parts, f32x4 (*red)[NW][NT][kWave], F f)
+// The parts' tiles put together in order, f(unit, tile row, column, sums of the two weight rows). Register r of lane l
+// holds the tile's row 4 (l / 16) + r and column l % 16.
+template <int WAVES, int NT, typename F>
+__device__ __forceinline__ void join_parts(const f32x4 (&acc)[NT][2], int parts, f32x4 (*red)[NT][2][kWave], F f)
 {
+    constexpr int values = NT * kTile * kTile;
     const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
 #pragma unroll
-    for (int i = 0; i < NW; ++i)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-            red[wave][i][t][lane] = acc[i][t];
+        for (int i = 0; i < 2; ++i)
+            red[wave][t][i][lane] = acc[t][i];
     __syncthreads();
-    const int values = NT * kTile * kTile;
     for (int i = threadIdx.x; i < WAVES / parts * values; i += WAVES * kWave) {
-        const int first = i / values * parts, v = i % values, t = v / (kTile * kTile), q = v % (kTile * kTile);
+        const int first = i / values * parts, t = i % values / (kTile * kTile), v = i % (kTile * kTile);
         // neighbouring threads take neighbouring columns
-        const int row = q / kTile, col = q % kTile, src = row / 4 * kTile + col, r = row % 4;
-        float sum[NW] = {};
+        const int row = v / kTile, col = v % kTile, src = row / 4 * kTile + col, r = row % 4;
+        float sum[2] = {};
         for (int w = first; w < first + parts; ++w)
 #pragma unroll
-            for (int n = 0; n < NW; ++n)
-                sum[n] += red[w][n][t][src][r];
+            for (int n = 0; n < 2; ++n)
+                sum[n] += red[w][t][n][src][r];
         f(first / parts, t * kTile + row, col, sum);
     }
     __syncthreads();
@@ -821,121 +991,222 @@ struct Entry {
     }
 };
 
-// SwiGLU of up to NT tiles of an expert's tokens, from row r0 of its n on.
-template <Weights W, int NT, typename Sh, Read READ>
-__device__ __forceinline__ void gate_up_rows(const ExpertArgs &a, const Entry &en, int r0, char *red)
+// The weight rows of a gate and up unit: 16 columns of h. Columns past the last one take its place: what they give is
+// not stored.
+template <Weights W, Read READ>
+__device__ __forceinline__ void gate_up_weights(const ExpertArgs &a, const Entry &en, int unit, WeightRows<W, 2, READ> &rows)
 {
-    typedef Product<W, 2, NT, false, Sh::kRegs, READ> P;
-    const int m = threadIdx.x % kTile;
-    const Share my(Sh::kWaves, a.parts);
-    const int c0 = min(my.unit * kTile, a.I - 1);
-    P p;
-    // columns and rows past the last one take its place: what they give is not stored
-    p.rows_of(a.H, a.I - 1 - c0, a.nb);
-    p.lo = 0;
-    p.per_block = a.per_block;
+    const int c0 = min(unit * kTile, a.I - 1);
+    rows.rows_of(a.H, a.I - 1 - c0, a.nb);
+    rows.per_block = a.per_block;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // the gate's rows, the up's rows
         const int64_t row = (en.ex * 2 + i) * a.I + c0;
-        p.w[i] = static_cast<const char *>(a.w) + row * a.H * sizeof(typename P::Wt);
-        p.scale[i] = a.scales + row * a.nb;
+        rows.w[i] = static_cast<const char *>(a.w) + row * a.H * sizeof(typename WeightType<W>::type);
+        rows.scale[i] = a.scales + row * a.nb;
     }
+}
+
+// h of the expert's token `row`, column c.
+template <Weights W>
+__device__ __forceinline__ void store_h(const ExpertArgs &a, const Entry &en, int row, int c, float gate, float up)
+{
+    if (row >= en.n || c >= a.I)
+        return;
+    const int pos = en.p0 + row;
+    const float weight = a.topk_w ? a.topk_w[a.plan.order[pos]] : 1.0f;
+    const float h = gate / (1.0f + expf(-gate)) * up * weight;
+    if (W == kWF32) {
+        static_cast<float *>(a.h)[static_cast<int64_t>(pos) * a.hI + c] = h;
+    } else {
+        uint16_t *hr = static_cast<uint16_t *>(a.h) + static_cast<int64_t>(pos) * 2 * a.hI;
+        const uint32_t hi = f32_to_bf16_bits(h);
+        const float rest = h - __uint_as_float(hi << 16);
+        hr[c] = static_cast<uint16_t>(hi);
+        // an infinite or NaN h is wholly in the first row
+        hr[a.hI + c] = (hi & 0x7f80u) == 0x7f80u ? 0 : static_cast<uint16_t>(f32_to_bf16_bits(rest));
+    }
+}
+
+// Up to NT tiles of an expert's tokens, from row r0 on.
+template <Weights W, int NT, typename Sh, Read READ>
+__device__ __forceinline__ void gate_up_stream(const ExpertArgs &a, const Entry &en, int r0, char *lds)
+{
+    Product<W, 2, NT, false, Sh::kRegs, READ> p;
+    const Share my(Sh::kWaves, a.parts);
+    gate_up_weights<W, READ>(a, en, my.unit, p.rows);
+    p.lo = 0;
     p.x = static_cast<const char *>(a.x);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int r = min(r0 + t * kTile + m, en.n - 1);
-        p.x_row[t] = static_cast<uint32_t>(a.plan.token[en.p0 + r] * a.H) * sizeof(typename P::X);
+        const int r = min(r0 + t * kTile + static_cast<int>(threadIdx.x % kTile), en.n - 1);
+        p.x_row[t] = static_cast<uint32_t>(a.plan.token[en.p0 + r] * a.H) * sizeof(typename ActType<W>::type);
     }
     const int loads = (a.H + kLoadElems<W> - 1) / kLoadElems<W>;
     p.run(loads * my.part / a.parts, loads * (my.part + 1) / a.parts, a.H, a.stagger ? my.unit : 0);
-    join_parts<Sh::kWaves>(p.acc, a.parts, reinterpret_cast<f32x4(*)[2][NT][kWave]>(red), [&](int unit, int row, int column, const float (&v)[2]) {
-        const int c = (blockIdx.x * (Sh::kWaves / a.parts) + unit) * kTile + column, pos = en.p0 + r0 + row;
-        if (r0 + row >= en.n || c >= a.I)
-            return;
-        const float weight = a.topk_w ? a.topk_w[a.plan.order[pos]] : 1.0f;
-        const float h = v[0] / (1.0f + expf(-v[0])) * v[1] * weight;
-        if (W == kWF32) {
-            static_cast<float *>(a.h)[static_cast<int64_t>(pos) * a.hI + c] = h;
-        } else {
-            uint16_t *hr = static_cast<uint16_t *>(a.h) + static_cast<int64_t>(pos) * 2 * a.hI;
-            const uint32_t hi = f32_to_bf16_bits(h);
-            const float rest = h - __uint_as_float(hi << 16);
-            hr[c] = static_cast<uint16_t>(hi);
-            // an infinite or NaN h is wholly in the first row
-            hr[a.hI + c] = (hi & 0x7f80u) == 0x7f80u ? 0 : static_cast<uint16_t>(f32_to_bf16_bits(rest));
-        }
+    join_parts<Sh::kWaves, NT>(p.acc, a.parts, reinterpret_cast<f32x4(*)[NT][2][kWave]>(lds),
+                           [&](int unit, int row, int column, const float (&v)[2]) {
+        store_h<W>(a, en, r0 + row, (blockIdx.x * (Sh::kWaves / a.parts) + unit) * kTile + column, v[0], v[1]);
     });
 }
 
+// The same with the tokens' rows through LDS; the workgroup's wavefronts take a unit each.
 template <Weights W, int NT, Read READ>
-__global__ __launch_bounds__((Shape<W, NT, false>::kThreads), (Shape<W, NT, false>::kWavesPerSimd)) void gate_up_kernel(ExpertArgs a)
+__device__ __forceinline__ void gate_up_tiles(const ExpertArgs &a, const Entry &en, int r0, char *lds)
 {
-    typedef Shape<W, NT, false> Sh;
-    __shared__ __attribute__((aligned(16))) char red[Sh::kWaves * 2 * NT * kWave * sizeof(f32x4)];
+    TiledProduct<W, NT, false, READ> p;
+    const int unit = blockIdx.x * 4 + wave_id(), lane = threadIdx.x & (kWave - 1);
+    gate_up_weights<W, READ>(a, en, unit, p.rows);
+    p.lo = 0;
+    p.x = static_cast<const char *>(a.x);
+    p.run(a.H, reinterpret_cast<u32x4 *>(lds), [&](int r) {
+        return static_cast<uint32_t>(a.plan.token[en.p0 + min(r0 + r, en.n - 1)] * a.H) *
+               static_cast<uint32_t>(sizeof(typename ActType<W>::type));
+    });
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            store_h<W>(a, en, r0 + t * kTile + lane / kTile * 4 + r, unit * kTile + lane % kTile, p.acc[0][t][r], p.acc[1][t][r]);
+}
+
+// LDS of a kernel: the parts' tiles, or the activations of the largest tiled product.
+template <Weights W, bool MANY, bool LO>
+constexpr int kProductLds = MANY ? std::max(Shape<W, MANY>::kWaves * 4 * kWave * 16, TiledProduct<W, 4, LO, kLines>::kBytes)
+                                 : Shape<W, MANY>::kWaves * 2 * kWave * 16;
+
+template <Weights W, bool MANY, Read READ>
+__global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWavesPerSimd)) void gate_up_kernel(ExpertArgs a)
+{
+    typedef Shape<W, MANY> Sh;
+    __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, false>];
     const Entry en(a.plan, blockIdx.y);
-    for (int r0 = 0; r0 < en.n; r0 += NT * kTile) {
-        if (NT > 1 && en.n - r0 <= NT / 2 * kTile)
-            gate_up_rows<W, (NT + 1) / 2, Sh, READ>(a, en, r0, red);
-        else
-            gate_up_rows<W, NT, Sh, READ>(a, en, r0, red);
+    if constexpr (!MANY) {
+        for (int r0 = 0; r0 < en.n; r0 += kTile)
+            gate_up_stream<W, 1, Sh, READ>(a, en, r0, lds);
+    } else if (!a.tiled || en.n <= 2 * kTile) {
+        for (int r0 = 0; r0 < en.n; r0 += 2 * kTile) {
+            if (en.n - r0 <= kTile)
+                gate_up_stream<W, 1, Sh, READ>(a, en, r0, lds);
+            else
+                gate_up_stream<W, 2, Sh, READ>(a, en, r0, lds);
+        }
+    } else if (static_cast<int>(blockIdx.x) * 4 * kTile < a.I) {
+        for (int r0 = 0; r0 < en.n; r0 += 4 * kTile)
+            gate_up_tiles<W, 4, READ>(a, en, r0, lds);
     }
 }
 
 // ---------------------------------------------------------------- down product
 // As the gate and up products, 32 rows of w_down (columns of out) to a unit, so that the two rows of h are read once
-// for twice the weights. Each slot's product goes to a float32 row of its own; the merge adds them up.
-template <Weights W, int NT, typename Sh, Read READ>
-__device__ __forceinline__ void down_rows(const ExpertArgs &a, const Entry &en, int r0, char *red)
+// for twice the weights. Each slot's product goes to a float32 row of its own; the merge adds them up. Where fewer than
+// 32 columns are left a unit's second tile begins earlier, and both store the same values there.
+__device__ __forceinline__ int second_tile(const ExpertArgs &a, int c0)
 {
-    typedef Product<W, 2, NT, W != kWF32, Sh::kRegs, READ> P;
-    constexpr int rows = W == kWF32 ? 1 : 2;  // of h per slot
-    const int m = threadIdx.x % kTile;
-    const Share my(Sh::kWaves, a.parts);
-    const int c0 = min(my.unit * 2 * kTile, a.H - 1);
-    P p;
-    // both tiles' rows from one offset: where fewer than 32 columns are left the second tile begins earlier
-    const int c1 = min(kTile, max(a.H - kTile - c0, 0));
-    p.rows_of(a.I, a.H - 1 - c0 - c1, a.nb);
-    p.lo = static_cast<int64_t>(a.hI) * sizeof(typename P::X);
-    p.per_block = a.per_block;
+    return min(kTile, max(a.H - kTile - c0, 0));
+}
+
+template <Weights W, Read READ>
+__device__ __forceinline__ void down_weights(const ExpertArgs &a, const Entry &en, int unit, WeightRows<W, 2, READ> &rows)
+{
+    const int c0 = min(unit * 2 * kTile, a.H - 1), c1 = second_tile(a, c0);
+    rows.rows_of(a.I, a.H - 1 - c0 - c1, a.nb);
+    rows.per_block = a.per_block;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int64_t row = en.ex * a.H + c0 + i * c1;
-        p.w[i] = static_cast<const char *>(a.w) + row * a.I * sizeof(typename P::Wt);
-        p.scale[i] = a.scales + row * a.nb;
+        rows.w[i] = static_cast<const char *>(a.w) + row * a.I * sizeof(typename WeightType<W>::type);
+        rows.scale[i] = a.scales + row * a.nb;
     }
-    p.x = static_cast<const char *>(a.h) + static_cast<int64_t>(en.p0 + r0) * rows * a.hI * sizeof(typename P::X);
+}
+
+__device__ __forceinline__ void store_y(const ExpertArgs &a, const Entry &en, int row, int unit, int column, float first,
+                                        float second)
+{
+    const int c0 = unit * 2 * kTile;
+    if (row >= en.n || c0 >= a.H)
+        return;
+    float *y = a.y + static_cast<int64_t>(en.p0 + row) * a.H;
+    const int c1 = second_tile(a, c0);
+    if (c0 + column < a.H)
+        y[c0 + column] = first;
+    if (c1 > 0 && c0 + c1 + column < a.H)
+        y[c0 + c1 + column] = second;
+}
+
+template <Weights W>
+constexpr int kHRows = W == kWF32 ? 1 : 2;  // of h per slot
+
+template <Weights W>
+__device__ __forceinline__ const char *h_from(const ExpertArgs &a, int pos)
+{
+    return static_cast<const char *>(a.h) + static_cast<int64_t>(pos) * kHRows<W> * a.hI * sizeof(typename ActType<W>::type);
+}
+
+template <Weights W, int NT, typename Sh, Read READ>
+__device__ __forceinline__ void down_stream(const ExpertArgs &a, const Entry &en, int r0, char *lds)
+{
+    typedef typename ActType<W>::type X;
+    Product<W, 2, NT, W != kWF32, Sh::kRegs, READ> p;
+    const Share my(Sh::kWaves, a.parts);
+    down_weights<W, READ>(a, en, my.unit, p.rows);
+    p.lo = static_cast<int64_t>(a.hI) * sizeof(X);
+    p.x = h_from<W>(a, en.p0 + r0);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int r = min(t * kTile + m, en.n - 1 - r0);
-        p.x_row[t] = static_cast<uint32_t>(r * rows * a.hI) * sizeof(typename P::X);
+        const int r = min(t * kTile + static_cast<int>(threadIdx.x % kTile), en.n - 1 - r0);
+        p.x_row[t] = static_cast<uint32_t>(r * kHRows<W> * a.hI) * sizeof(X);
     }
     const int loads = (a.I + kLoadElems<W> - 1) / kLoadElems<W>;
     p.run(loads * my.part / a.parts, loads * (my.part + 1) / a.parts, a.I, a.stagger ? my.unit : 0);
-    join_parts<Sh::kWaves>(p.acc, a.parts, reinterpret_cast<f32x4(*)[2][NT][kWave]>(red), [&](int unit, int row, int column, const float (&v)[2]) {
-        const int u0 = (blockIdx.x * (Sh::kWaves / a.parts) + unit) * 2 * kTile;
-        if (r0 + row >= en.n || u0 >= a.H)
-            return;
-        float *y = a.y + static_cast<int64_t>(en.p0 + r0 + row) * a.H;
-        const int second = min(kTile, max(a.H - kTile - u0, 0));
-        if (u0 + column < a.H)
-            y[u0 + column] = v[0];
-        if (second > 0 && u0 + second + column < a.H)
-            y[u0 + second + column] = v[1];
+    join_parts<Sh::kWaves, NT>(p.acc, a.parts, reinterpret_cast<f32x4(*)[NT][2][kWave]>(lds),
+                           [&](int unit, int row, int column, const float (&v)[2]) {
+        store_y(a, en, r0 + row, blockIdx.x * (Sh::kWaves / a.parts) + unit, column, v[0], v[1]);
     });
 }
 
 template <Weights W, int NT, Read READ>
-__global__ __launch_bounds__((Shape<W, NT, W != kWF32>::kThreads), (Shape<W, NT, W != kWF32>::kWavesPerSimd)) void down_kernel(ExpertArgs a)
+__device__ __forceinline__ void down_tiles(const ExpertArgs &a, const Entry &en, int r0, char *lds)
 {
-    typedef Shape<W, NT, W != kWF32> Sh;
-    __shared__ __attribute__((aligned(16))) char red[Sh::kWaves * 2 * NT * kWave * sizeof(f32x4)];
+    typedef typename ActType<W>::type X;
+    TiledProduct<W, NT, W != kWF32, READ> p;
+    const int unit = blockIdx.x * 4 + wave_id(), lane = threadIdx.x & (kWave - 1);
+    down_weights<W, READ>(a, en, unit, p.rows);
+    p.lo = static_cast<int64_t>(a.hI) * sizeof(X);
+    p.x = h_from<W>(a, en.p0 + r0);
+    p.run(a.I, reinterpret_cast<u32x4 *>(lds), [&](int r) {
+        return static_cast<uint32_t>(min(r, en.n - 1 - r0) * kHRows<W> * a.hI) * static_cast<uint32_t>(sizeof(X));
+    });
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            store_y(a, en, r0 + t * kTile + lane / kTile * 4 + r, unit, lane % kTile, p.acc[0][t][r], p.acc[1][t][r]);
+}
+
+template <Weights W, bool MANY, Read READ>
+__global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWavesPerSimd)) void down_kernel(ExpertArgs a)
+{
+    typedef Shape<W, MANY> Sh;
+    __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, W != kWF32>];
     const Entry en(a.plan, blockIdx.y);
-    for (int r0 = 0; r0 < en.n; r0 += NT * kTile) {
-        if (NT > 1 && en.n - r0 <= NT / 2 * kTile)
-            down_rows<W, (NT + 1) / 2, Sh, READ>(a, en, r0, red);
-        else
-            down_rows<W, NT, Sh, READ>(a, en, r0, red);
+    if constexpr (!MANY) {
+        for (int r0 = 0; r0 < en.n; r0 += kTile)
+            down_stream<W, 1, Sh, READ>(a, en, r0, lds);
+    } else if (!a.tiled || en.n <= kTile) {
+        for (int r0 = 0; r0 < en.n; r0 += 2 * kTile) {
+            if (en.n - r0 <= kTile)
+                down_stream<W, 1, Sh, READ>(a, en, r0, lds);
+            else
+                down_stream<W, 2, Sh, READ>(a, en, r0, lds);
+        }
+    } else if (static_cast<int>(blockIdx.x) * 4 * 2 * kTile < a.H) {
+        for (int r0 = 0; r0 < en.n; r0 += 4 * kTile) {
+            if (en.n - r0 <= 2 * kTile)
+                down_tiles<W, 2, READ>(a, en, r0, lds);
+            else
+                down_tiles<W, 4, READ>(a, en, r0, lds);
+        }
     }
 }
 
@@ -962,8 +1233,7 @@ __device__ __forceinline__ void store_out(const ExpertArgs &a, int t, int c, flo
 template <Weights W, Read READ>
 __global__ __launch_bounds__(kDirectThreads) void down_merge_kernel(ExpertArgs a)
 {
-    typedef Product<W, 1, 1, W != kWF32, 128 - Shape<W, 1, W != kWF32>::kOther, READ> P;
-    constexpr int rows = W == kWF32 ? 1 : 2;  // of h per slot
+    typedef Product<W, 1, 1, W != kWF32, Shape<W, false>::kRegs, READ> P;
     __shared__ float sums[kDirectWaves][kTile][kTile];
     const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), m = lane % kTile, g = lane / kTile;
     const int c0 = blockIdx.x * kTile;
@@ -978,14 +1248,14 @@ __global__ __launch_bounds__(kDirectThreads) void down_merge_kernel(ExpertArgs a
         const int64_t row = static_cast<int64_t>(a.plan.act[i]) * a.H + c0;
         for (int r0 = 0; r0 < n; r0 += kTile) {
             P p;
-            p.rows_of(a.I, a.H - 1 - c0, a.nb);
+            p.rows.rows_of(a.I, a.H - 1 - c0, a.nb);
+            p.rows.per_block = a.per_block;
+            p.rows.w[0] = static_cast<const char *>(a.w) + row * a.I * sizeof(typename P::Wt);
+            p.rows.scale[0] = a.scales + row * a.nb;
             p.lo = static_cast<int64_t>(a.hI) * sizeof(typename P::X);
-            p.per_block = a.per_block;
-            p.w[0] = static_cast<const char *>(a.w) + row * a.I * sizeof(typename P::Wt);
-            p.scale[0] = a.scales + row * a.nb;
-            p.x = static_cast<const char *>(a.h) + static_cast<int64_t>(p0 + r0) * rows * a.hI * sizeof(typename P::X);
+            p.x = h_from<W>(a, p0 + r0);
             const int r = min(m, n - 1 - r0), tok = a.plan.token[p0 + r0 + r];
-            p.x_row[0] = static_cast<uint32_t>(r * rows * a.hI) * sizeof(typename P::X);
+            p.x_row[0] = static_cast<uint32_t>(r * kHRows<W> * a.hI) * sizeof(typename P::X);
             p.run(l0, l1, a.I, 0);
             // this lane holds column m of the tile's rows 4 g .. 4 g + 3. A token that names the expert twice has two
             // rows, neighbours: then the lane groups add one after the other
@@ -1146,6 +1416,12 @@ bool stagger(int64_t row_bytes) { return row_bytes % 4096 == 0; }
 // against less of the chip at work (T8 H1024 I512 K4, 112 loads: 21 -> 32 us).
 constexpr int64_t kDirectLoads = 64;
 
+// Workgroups from which on the tiled product, whose wavefronts do not share a unit's loads, has the chip filled: T256 H4096
+// I2048 E16 K4 with 512 of them 290 -> 219 us (gate and up); T100 H4096 I1024 E8 K2 with 128 44 -> 88, down with 256 35 ->
+// 43. Gate and up take it from 33 tokens an expert, down, whose activations are twice the bytes, from 17 (T200 H7168 I1024
+// E64 K8, 25 tokens an expert: 446 -> 568 us and 335 -> 290).
+constexpr int64_t kTiledGroups = 512;
+
 template <Weights W>
 Read read_of(const void *w, int64_t row_bytes, const void *x, int64_t x_row_bytes)
 {
@@ -1155,11 +1431,10 @@ Read read_of(const void *w, int64_t row_bytes, const void *x, int64_t x_row_byte
     return at % 128 == 0 ? kLines : kWords;
 }
 
-template <Weights W, int NT>
+template <Weights W, bool MANY>
 void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t stream)
 {
-    typedef Shape<W, NT, false> Up;
-    typedef Shape<W, NT, W != kWF32> Down;
+    typedef Shape<W, MANY> Sh;
     constexpr int size = sizeof(typename WeightType<W>::type);
     // FP8: the scale of load l is l / (loads per block), by a multiplication (exact for l * block / 128 < 2^32)
     const int lb = W == kWFp8 ? w.block / kLoadElems<kWFp8> : 1;
@@ -1169,21 +1444,22 @@ void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t
     a.nb = W == kWFp8 ? a.H / w.block : 0;
     a.stagger = stagger(int64_t{a.H} * size);
     int64_t units = ceil_div(a.I, kTile);
-    a.parts = share_parts(units * used, ceil_div(a.H, kLoadElems<W>), Up::kWaves);
-    dim3 grid(static_cast<unsigned>(ceil_div(units, Up::kWaves / a.parts)), static_cast<unsigned>(used));
+    a.tiled = MANY && units / 4 * used >= kTiledGroups;
+    a.parts = share_parts(units * used, ceil_div(a.H, kLoadElems<W>), Sh::kWaves);
+    dim3 grid(static_cast<unsigned>(ceil_div(units, Sh::kWaves / a.parts)), static_cast<unsigned>(used));
     Read read = read_of<W>(a.w, int64_t{a.H} * size, a.x, int64_t{a.H} * sizeof(typename ActType<W>::type));
     if (read == kLines)
-        hipLaunchKernelGGL((gate_up_kernel<W, NT, kLines>), grid, dim3(Up::kThreads), 0, stream, a);
+        hipLaunchKernelGGL((gate_up_kernel<W, MANY, kLines>), grid, dim3(Sh::kThreads), 0, stream, a);
     else if (W != kWBf16 || read == kWords)
-        hipLaunchKernelGGL((gate_up_kernel<W, NT, kWords>), grid, dim3(Up::kThreads), 0, stream, a);
+        hipLaunchKernelGGL((gate_up_kernel<W, MANY, kWords>), grid, dim3(Sh::kThreads), 0, stream, a);
     else if constexpr (W == kWBf16)
-        hipLaunchKernelGGL((gate_up_kernel<W, NT, kOdd>), grid, dim3(Up::kThreads), 0, stream, a);
+        hipLaunchKernelGGL((gate_up_kernel<W, MANY, kOdd>), grid, dim3(Sh::kThreads), 0, stream, a);
     a.w = w.down;
     a.scales = w.down_scales;
     a.nb = W == kWFp8 ? a.I / w.block : 0;
     a.stagger = stagger(int64_t{a.I} * size);
     read = read_of<W>(a.w, int64_t{a.I} * size, nullptr, 0);
-    if (NT == 1 && used * ceil_div(a.I, kLoadElems<W>) <= kDirectLoads) {
+    if (!MANY && used * ceil_div(a.I, kLoadElems<W>) <= kDirectLoads) {
         grid = dim3(static_cast<unsigned>(ceil_div(a.H, kTile)));
         if (read == kLines)
             hipLaunchKernelGGL((down_merge_kernel<W, kLines>), grid, dim3(kDirectThreads), 0, stream, a);
@@ -1194,14 +1470,15 @@ void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t
         return;
     }
     units = ceil_div(a.H, 2 * kTile);
-    a.parts = share_parts(units * used, ceil_div(a.I, kLoadElems<W>), Down::kWaves);
-    grid = dim3(static_cast<unsigned>(ceil_div(units, Down::kWaves / a.parts)), static_cast<unsigned>(used));
+    a.tiled = MANY && units / 4 * used >= kTiledGroups;
+    a.parts = share_parts(units * used, ceil_div(a.I, kLoadElems<W>), Sh::kWaves);
+    grid = dim3(static_cast<unsigned>(ceil_div(units, Sh::kWaves / a.parts)), static_cast<unsigned>(used));
     if (read == kLines)
-        hipLaunchKernelGGL((down_kernel<W, NT, kLines>), grid, dim3(Down::kThreads), 0, stream, a);
+        hipLaunchKernelGGL((down_kernel<W, MANY, kLines>), grid, dim3(Sh::kThreads), 0, stream, a);
     else if (W != kWBf16 || read == kWords)
-        hipLaunchKernelGGL((down_kernel<W, NT, kWords>), grid, dim3(Down::kThreads), 0, stream, a);
+        hipLaunchKernelGGL((down_kernel<W, MANY, kWords>), grid, dim3(Sh::kThreads), 0, stream, a);
     else if constexpr (W == kWBf16)
-        hipLaunchKernelGGL((down_kernel<W, NT, kOdd>), grid, dim3(Down::kThreads), 0, stream, a);
+        hipLaunchKernelGGL((down_kernel<W, MANY, kOdd>), grid, dim3(Sh::kThreads), 0, stream, a);
     hipLaunchKernelGGL(merge_kernel, dim3(static_cast<unsigned>(ceil_div(a.H, kMergeThreads)), static_cast<unsigned>(a.T)),
                        dim3(kMergeThreads), 0, stream, a);
 }
@@ -1209,13 +1486,10 @@ void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t
 template <Weights W>
 void launch_products_of(const ExpertArgs &a, const ExpertWeights &w, int used, hipStream_t stream)
 {
-    // tiles of tokens that one pass over an expert's weights may meet: by the tokens an expert can have, and has on average
     if (a.T <= kTile)
-        launch_products<W, 1>(a, w, used, stream);
-    else if (W == kWFp8 || a.T * a.K <= kTile * used)
-        launch_products<W, 2>(a, w, used, stream);
-    else if constexpr (W != kWFp8)
-        launch_products<W, 4>(a, w, used, stream);
+        launch_products<W, false>(a, w, used, stream);
+    else
+        launch_products<W, true>(a, w, used, stream);
 }
 
 moe_status launch_experts(const void *x, int64_t T, int64_t H, int64_t I, int32_t E, int32_t K, const int32_t *topk_idx,
