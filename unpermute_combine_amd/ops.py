@@ -26,7 +26,7 @@ _DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.uint8: MOE_FP8_E4
 def _stream() -> int:
     # the current stream of the current device as a hipStream_t (torch.cuda.current_stream() builds a Python
     # stream object first: 2.9 us a call against 0.2)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _p(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -34,6 +34,9 @@ def _p(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, dims=None):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == torch._C._cuda_getDevice()
+            and (dtype is None or t.dtype == dtype) and (dims is None or t.dim() == dims) and t.is_contiguous()):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -45,9 +48,7 @@ def _need(t: torch.Tensor, name: str, dtype=None, dims=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if dims is not None and t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dims, got shape {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _hidden_dt(t: torch.Tensor, name: str) -> int:
@@ -603,7 +604,7 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
             raise ValueError(f"out must be [{T}, {H}]")
     if sum_out is None and residual is not None:
         sum_out = torch.empty_like(residual)
-    rstd = torch.empty(T, dtype=torch.float32, device=x.device) if want_rstd else None
+    rstd = x.new_empty(T, dtype=torch.float32) if want_rstd else None
     check("moe_add_rmsnorm", lib().moe_add_rmsnorm(
         _p(x), x_dt, _p(residual), s_dt, _p(weight), w_dt, T, H, eps, _p(sum_out), _p(out),
         _row_dt(out.dtype, "out"), _p(rstd), _stream()))
@@ -626,7 +627,7 @@ def add_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[to
     else:
         _need(q, "q", torch.uint8, 2)
     if sc is None:
-        sc = torch.empty((T, H // block), dtype=torch.float32, device=x.device)
+        sc = x.new_empty((T, H // block), dtype=torch.float32)
     else:
         _need(sc, "scales", torch.float32, 2)
     if tuple(q.shape) != (T, H) or tuple(sc.shape) != (T, H // block):
@@ -636,7 +637,7 @@ def add_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[to
     o_dtype = out_dtype or x.dtype
     o_dt = _row_dt(o_dtype, "out_dtype")
     rows = torch.empty((T, H), dtype=o_dtype, device=x.device) if want_rows else None
-    rstd = torch.empty(T, dtype=torch.float32, device=x.device) if want_rstd else None
+    rstd = x.new_empty(T, dtype=torch.float32) if want_rstd else None
     check("moe_add_rmsnorm_fp8", lib().moe_add_rmsnorm_fp8(
         _p(x), x_dt, _p(residual), s_dt, _p(weight), w_dt, T, H, eps, block, _p(sum_out), _p(rows), o_dt, _p(q),
         _p(sc), _p(rstd), _stream()))
@@ -678,13 +679,13 @@ def add_rmsnorm_backward(dout: torch.Tensor, h: torch.Tensor, weight: torch.Tens
         dw, workspace, nbytes = None, None, 0
     else:
         if dw is None:
-            dw = torch.empty(H, dtype=torch.float32, device=dout.device)
+            dw = rstd.new_empty(H)
         else:
             _need(dw, "dweight", torch.float32, 1)
             if dw.shape[0] != H:
                 raise ValueError(f"dweight must have {H} elements")
         if workspace is None:
-            workspace = torch.empty(rmsnorm_workspace_bytes(T, H), dtype=torch.uint8, device=dout.device)
+            workspace = rstd.new_empty(rmsnorm_workspace_bytes(T, H), dtype=torch.uint8)
         else:
             _need(workspace, "workspace", torch.uint8, 1)
         nbytes = workspace.numel()
@@ -758,9 +759,9 @@ def _few_token_out(x, bias, out, out_dtype):
     return out, _row_dt(out.dtype, "out")
 
 
-def _few_token_ws(workspace, T, H, I, E, K, device):
+def _few_token_ws(workspace, x, T, H, I, E, K):
     if workspace is None:
-        return torch.empty(few_token_workspace_bytes(T, H, I, E, K), dtype=torch.uint8, device=device)
+        return x.new_empty(few_token_workspace_bytes(T, H, I, E, K), dtype=torch.uint8)
     return _need(workspace, "workspace", torch.uint8, 1)
 
 
@@ -779,9 +780,9 @@ def few_token_layer(x: torch.Tensor, router: torch.Tensor, w_gate_up: torch.Tens
     if tuple(router.shape) != (E, H):
         raise ValueError(f"router must be [{E}, {H}]")
     out, o_dt = _few_token_out(x, bias, out, out_dtype)
-    idx = torch.empty((T, k), dtype=torch.int32, device=x.device)
-    w = torch.empty((T, k), dtype=torch.float32, device=x.device)
-    workspace = _few_token_ws(workspace, T, H, I, E, k, x.device)
+    idx = x.new_empty((T, k), dtype=torch.int32)
+    w = x.new_empty((T, k), dtype=torch.float32)
+    workspace = _few_token_ws(workspace, x, T, H, I, E, k)
     check("moe_few_token_layer", lib().moe_few_token_layer(
         _p(x), x_dt, _p(router), T, H, I, E, k, group_size, topk_groups, _p(w_gate_up), _p(w_down), w_dt,
         _p(gate_up_scales), _p(down_scales), block, _p(bias), _p(out), o_dt, _p(idx), _p(w), _p(workspace),
@@ -806,7 +807,7 @@ def few_token_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: Optional[
         if topk_w.shape != topk_idx.shape:
             raise ValueError("topk_w must have the shape of topk_idx")
     out, o_dt = _few_token_out(x, bias, out, out_dtype)
-    workspace = _few_token_ws(workspace, T, H, I, E, K, x.device)
+    workspace = _few_token_ws(workspace, x, T, H, I, E, K)
     check("moe_few_token_experts", lib().moe_few_token_experts(
         _p(x), x_dt, T, H, I, E, K, _p(topk_idx), _p(topk_w), _p(w_gate_up), _p(w_down), w_dt, _p(gate_up_scales),
         _p(down_scales), block, _p(bias), _p(out), o_dt, _p(workspace), workspace.numel(), _stream()))
