@@ -680,8 +680,10 @@ struct Product {
     typedef WeightRows<W, NW, READ> Rows;
     typedef typename Rows::Wt Wt;
     typedef typename ActType<W>::type X;
+    // 4, 2 or 1: most rows and parts of them are an even number of loads, and three at a time leave one over (T4 H2048
+    // I1024 K4, gate and up: 36 us with three, 29 with two)
     static constexpr int kRoom = (REGS - 4 * NW * NT) / kSlotRegs<W, NW, NT, LO>;
-    static constexpr int D = kRoom > 4 ? 4 : kRoom < 1 ? 1 : kRoom;
+    static constexpr int D = kRoom >= 4 ? 4 : kRoom >= 2 ? 2 : 1;
     static constexpr int kActBytes = kHalfElems<W> * sizeof(X);  // of a token's row per half
     Rows rows;
     const char *x;
@@ -1397,11 +1399,13 @@ constexpr int64_t kSmallRouter = 128 << 10;
 
 size_t plan_lds(int E) { return sizeof(uint16_t) * kPlanWaves * static_cast<size_t>(E); }
 
-// Wavefronts that share a unit of weight rows: enough wavefronts for the chip, as long as each has a few loads.
+// Wavefronts that share a unit of weight rows: more of them while the chip has not several rounds of wavefronts (T8 H4096
+// I2048 E128 K8 FP8 with four against two: 189 -> 181 us and 112 -> 106; T64 H7168 I1024 E128 K8 down, 28672 units, with four
+// against one: 333 -> 388), as long as each keeps four loads or more (T32 H1024 I512 E64 K4 down with two: 23 -> 32 us).
 int share_parts(int64_t units, int64_t loads, int waves)
 {
     int parts = 1;
-    while (parts < waves && units * parts < 16384 && loads >= 4 * parts)
+    while (parts < waves && units * parts < 24576 && loads >= 8 * parts)
         parts *= 2;
     return parts;
 }
