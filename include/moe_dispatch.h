@@ -396,7 +396,7 @@ moe_status moe_route_topk_backward(const int32_t *topk_idx, const float *topk_w,
  *   NULL: s, for the backward.
  * sum_out may be x or residual, and out may be x or residual, where the types are the same (each
  * element is read before it is written); otherwise outputs overlap nothing.
- * T <= 2^31 - 1 (else MOE_ERR_UNSUPPORTED). */
+ * T <= 2^31 - 1 and H <= 2^26 (else MOE_ERR_UNSUPPORTED). */
 moe_status moe_add_rmsnorm(const void *x, moe_dtype x_dt, const void *residual, moe_dtype sum_dt,
                            const void *weight, moe_dtype weight_dt, int64_t T, int64_t H, float eps,
                            void *sum_out, void *out, moe_dtype out_dt, float *rstd, hipStream_t stream);
@@ -442,7 +442,7 @@ moe_status moe_add_rmsnorm_backward(const void *dout, moe_dtype dout_dt, const v
  * [E, H, I] holds D_e. Sums are float32 (their order depends on the sizes and the routing alone: no
  * atomics), h is kept to 16 significant bits or more, and out is rounded once.
  *   x [T, H] and router [E, H] of dtype dt (float32 or bf16); bias [T, H] of dtype out_dt or NULL, which
- *   may be out itself; out [T, H] (out_dt); topk_idx [T, K], topk_w [T, K] out.
+ *   may be out itself; out [T, H] (out_dt), which overlaps no other input; topk_idx [T, K], topk_w [T, K] out.
  *   weight_dt: dt, or MOE_FP8_E4M3 beside bf16 rows: codes with float32 scales, one per row and block of
  *   `block` consecutive elements of the row, as moe_quantize_fp8 of the weight rows gives them
  *   (gate_up_scales [E, 2I, H/block], down_scales [E, H, I/block]); block must divide H and I (else
@@ -450,7 +450,8 @@ moe_status moe_add_rmsnorm_backward(const void *dout, moe_dtype dout_dt, const v
  *   MOE_ERR_UNSUPPORTED; block and scales are ignored without FP8.
  *   T <= MOE_MAX_FEW_TOKENS, H and I <= 2^20 (else MOE_ERR_UNSUPPORTED): for more tokens dispatch them.
  * Weights of experts that no token uses are not read. Rows are independent: what is not finite in one token's row
- * or in an expert's weights reaches only the tokens that use it.
+ * or in an expert's weights reaches only the tokens that use it. A row whose logits are NaN may route anywhere or
+ * nowhere, and an infinite element of a bf16 w_down may give NaN where the formula gives an infinity.
  * The workspace (16-byte aligned, contents need no initialisation and mean nothing after the call) must
  * hold moe_few_token_workspace_size bytes; calls that may overlap need one each. */
 moe_status moe_few_token_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t K, size_t *bytes);

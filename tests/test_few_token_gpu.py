@@ -390,3 +390,45 @@ def test_many_tokens_an_expert(m, T, H, I, kind):
     out = m.few_token_experts(x, idx, w, lay.w13, lay.w2, out_dtype=F32, **lay.scales)
     assert_within(out, *lay.expected(x, idx, w))
     assert torch.equal(out, m.few_token_experts(x, idx, w, lay.w13, lay.w2, out_dtype=F32, **lay.scales))
+
+
+@pytest.mark.parametrize("T,E", [(16, 3), (16, 40), (256, 40)])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "fp8"])
+def test_all_slots_with_one_expert(m, T, E, kind):
+    """32 slots a token, all of them one expert's: as many rows of it as a call can have."""
+    lay = Layer(m, 256, 128, E, kind, seed=4)
+    x, w = draw(9, T, 256, dtype=lay.rows), draw(10, T, 3 if E == 3 else 32).abs()
+    idx = torch.full(w.shape, E - 1, dtype=torch.int32, device=DEV)
+    out = m.few_token_experts(x, idx, w, lay.w13, lay.w2, out_dtype=F32, **lay.scales)
+    assert_within(out, *lay.expected(x, idx, w))
+
+
+@pytest.mark.parametrize("T,E,K", [(3, 8, 2), (16, 600, 32), (37, 8, 2), (100, 1000, 8)])
+@pytest.mark.parametrize("limited", [False, True])
+def test_layer_with_rows_that_are_not_finite(m, T, E, K, limited):
+    """Their logits are not numbers: they route anywhere or nowhere, and the other rows are as before."""
+    groups = (E // 4, 2) if limited else None
+    lay = Layer(m, 192, 64, E, "bf16")
+    x = draw(3, T, 192, dtype=BF16)
+    x[1], x[2, 5] = float("nan"), -float("inf")
+    x[1].view(torch.int16)[:] = -1  # a negative NaN
+    limit = dict(group_size=groups[0], topk_groups=groups[1]) if limited else {}
+    out, idx, w = m.few_token_layer(x, lay.router, lay.w13, lay.w2, K, **limit)
+    assert bool(((idx >= -1) & (idx < E)).all())
+    keep = [t for t in range(T) if t not in (1, 2)]
+    want_idx, want_w = lay.routed(x[keep], K, groups)
+    assert torch.equal(idx[keep], want_idx)
+    assert_weights(w[keep], want_w)
+    assert_within(out[keep], *lay.expected(x[keep], idx[keep], w[keep]))
+
+
+@pytest.mark.parametrize("T", [2, 40])
+@pytest.mark.parametrize("shift", [1, 2, 4, 8])
+def test_fp8_codes_at_odd_addresses(m, T, shift):
+    lay = Layer(m, 384, 256, 7, "fp8")
+    x = draw(5, T, 384, dtype=BF16)
+    off = lambda t: torch.cat([t.new_zeros(shift), t.flatten()])[shift:].view(t.shape)  # noqa: E731
+    want = m.few_token_layer(x, lay.router, lay.w13, lay.w2, 3, **lay.scales)
+    got = m.few_token_layer(off(x), off(lay.router), off(lay.w13), off(lay.w2), 3, gate_up_scales=off(lay.scales["gate_up_scales"]),
+                            down_scales=off(lay.scales["down_scales"]))
+    assert all(torch.equal(a, b) for a, b in zip(want, got))

@@ -293,3 +293,39 @@ def test_norm_to_fp8_dispatch_and_back(m):
     want_dx, bound, want_dw, dw_abs = backward_reference(dn, total, w, rstd, dout)
     assert_within(dx, want_dx, bound * 1.01 + half(BF16) * want_dx.abs(), "dx")
     assert_within(dw, want_dw, dw_roundings(T) * U * dw_abs, "dweight")
+
+
+@pytest.mark.parametrize("block", [8, 128, 40, 640])
+def test_fp8_blocks_of_any_size_of_values(m, block):
+    """Scales from float32's subnormals to its largest values, and zeros of both signs: the codes of quantize_fp8."""
+    T, H = 64, 640
+    x = draw(1, T, H)
+    x[:, 3::16], x[:, 5::16] = 0.0, -0.0
+    size = torch.arange(-148, 128, 276 / H, device=DEV)[:H]
+    for w in (torch.exp2(size), torch.exp2(size.flip(0)), torch.full((H,), 2.0 ** -149, device=DEV), torch.full((H,), 1e-44, device=DEV),
+              torch.full((H,), 3e38 / 8, device=DEV)):
+        w = w.clamp(max=3e38 / 8)  # |x| sqrt(mean x^2) stays under 8: no infinities
+        q, sc, _, rows, _ = m.add_rmsnorm_fp8(x, w, block=block, want_rows=True, out_dtype=F32)
+        assert bool(torch.isfinite(rows).all())
+        q2, sc2 = m.quantize_fp8(rows, block)
+        assert torch.equal(sc, sc2) and torch.equal(q, q2)
+
+
+def test_more_rows_than_a_grid_has_workgroups(m):
+    T, H = (1 << 20) + 77, 6
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    x, r = torch.randn(T, H, generator=g, device=DEV), torch.randn(T, H, generator=g, device=DEV)
+    w = draw(3, H) + 1
+    out, total, rstd = m.add_rmsnorm(x, w, residual=r, want_rstd=True)
+    h, s, n = reference(x, w, r, 1e-6)
+    b = row_bound(H)
+    assert_within(out, n, b * n.abs(), "out")
+    assert_within(rstd, s, b * s, "rstd")
+    dx, dw = m.add_rmsnorm_backward(x, total, w, rstd)
+    want, bound, want_dw, mag = backward_reference(x, total, w, rstd, None)
+    assert_within(dx, want, bound * (1 + U) + U * want.abs(), "dx")
+    assert_within(dw, want_dw, dw_roundings(T) * U * mag, "dweight")
+    q, sc = m.add_rmsnorm_fp8(x, w, residual=r, block=6)[:2]
+    q2, sc2 = m.quantize_fp8(out, 6)
+    assert torch.equal(q, q2) and torch.equal(sc, sc2)

@@ -62,6 +62,16 @@ def test_backward_refusals_and_workspace(capi):
         assert call(**bad) == UNS, bad
 
 
+def test_rows_longer_than_the_grids_take_are_refused(capi):
+    lib, n = capi.lib(), ctypes.c_size_t(0)
+    F, UNS, H = capi.MOE_F32, capi.MOE_ERR_UNSUPPORTED, (1 << 26) + 8
+    assert lib.moe_add_rmsnorm_backward_workspace_size(1, 1 << 26, ctypes.byref(n)) == capi.MOE_OK and n.value == 4 << 26
+    assert lib.moe_add_rmsnorm_backward_workspace_size(1, H, ctypes.byref(n)) == UNS
+    assert lib.moe_add_rmsnorm_backward(P, F, P, F, P, F, P, None, 1, H, P, F, P, P, 4 * H, None) == UNS
+    assert lib.moe_add_rmsnorm(P, F, None, F, P, F, 1, H, 1e-6, None, P, F, None, None) == UNS
+    assert lib.moe_add_rmsnorm_fp8(P, F, None, F, P, F, 1, H, 1e-6, 8, None, None, F, P, P, None, None) == UNS
+
+
 def test_binding_refuses_host_tensors():
     import unpermute_combine_amd as m
     x, w = torch.ones(2, 64), torch.ones(64)

@@ -546,6 +546,9 @@ __global__ __launch_bounds__(512) void rmsnorm_backward_regs_kernel(const G *dou
     }
 }
 
+// rmsnorm_dweight_sum_kernel has 32 threads a column, and a grid fewer than 2^32.
+constexpr int64_t kMaxRow = 1 << 26;
+
 bool row_type(moe_dtype d) { return d == MOE_F32 || d == MOE_BF16; }
 
 moe_status check_norm(const void *x, moe_dtype x_dt, const void *residual, moe_dtype sum_dt, const void *weight,
@@ -556,7 +559,7 @@ moe_status check_norm(const void *x, moe_dtype x_dt, const void *residual, moe_d
     if (T < 0 || H < 1 || !(eps >= 0.0f) || std::isinf(eps) || !row_type(x_dt) || !row_type(sum_dt) ||
         !row_type(weight_dt))
         return MOE_ERR_INVALID;
-    if (T > 0x7fffffff || H > 0x7fffffffLL / 4)
+    if (T > 0x7fffffff || H > kMaxRow)
         return MOE_ERR_UNSUPPORTED;
     if (T > 0 && (!x || !weight))
         return MOE_ERR_INVALID;
@@ -715,7 +718,7 @@ extern "C" moe_status moe_add_rmsnorm_backward_workspace_size(int64_t T, int64_t
     using namespace moe;
     if (!bytes || T < 0 || H < 1)
         return MOE_ERR_INVALID;
-    if (T > 0x7fffffff || H > 0x7fffffffLL / 4)
+    if (T > 0x7fffffff || H > kMaxRow)
         return MOE_ERR_UNSUPPORTED;
     *bytes = sizeof(float) * static_cast<size_t>(dw_ranges(T) * H);
     return MOE_OK;
