@@ -432,3 +432,14 @@ def test_fp8_codes_at_odd_addresses(m, T, shift):
     got = m.few_token_layer(off(x), off(lay.router), off(lay.w13), off(lay.w2), 3, gate_up_scales=off(lay.scales["gate_up_scales"]),
                             down_scales=off(lay.scales["down_scales"]))
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("T", [2, 30, 200])
+@pytest.mark.parametrize("H,I,block", [(5120, 2304, 256), (2432, 4096, 128), (2176, 8704, 2176)])
+def test_fp8_rows_of_many_blocks(m, T, H, I, block):
+    """More scales to a row than are read at a time, blocks of one load and of several, starts apart."""
+    lay = Layer(m, H, I, 3, "fp8", block=block)
+    x = draw(5, T, H, dtype=BF16)
+    idx, w = lay.routed(x, 2)
+    out = m.few_token_experts(x, idx, w.float(), lay.w13, lay.w2, out_dtype=F32, **lay.scales)
+    assert_within(out, *lay.expected(x, idx, w.float()))

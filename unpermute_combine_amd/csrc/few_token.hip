@@ -549,7 +549,7 @@ __global__ __launch_bounds__(kPlanThreads) void few_token_small_route_kernel(con
 
 // Registers of one load in flight.
 template <Weights W, int NW, int NT, bool LO>
-constexpr int kSlotRegs = 8 * (NW + NT * (LO ? 2 : 1) * (W == kWFp8 ? 2 : 1)) + (W == kWFp8 ? NW : 0);
+constexpr int kSlotRegs = 8 * (NW + NT * (LO ? 2 : 1) * (W == kWFp8 ? 2 : 1));
 
 // How rows of weights lie. kLines: they begin on cache lines, so that each line is read by one instruction, past the
 // caches (a line that two instructions share is read from memory twice that way); kWords: on 4-byte words; kOdd: bf16
@@ -561,7 +561,8 @@ enum Read { kLines, kWords, kOdd };
 // where experts may have MANY tokens (more than a tile's) 4 of 256, of which 8 do.
 template <Weights W, bool MANY>
 struct Shape {
-    static constexpr int kOther = W == kWFp8 ? 52 : 40;  // registers for addresses and what is being multiplied
+    // registers for addresses, what is being multiplied, and FP8's scales
+    static constexpr int kOther = W != kWFp8 ? 40 : MANY ? 64 : 52;
     static constexpr int kRegs = (MANY ? 256 : 128) - kOther, kWaves = MANY ? 4 : 8, kThreads = kWaves * kWave;
     static constexpr int kWavesPerSimd = MANY ? 2 : 4;
 };
@@ -586,42 +587,110 @@ struct ExpertArgs {
     Plan plan;
 };
 
+// FP8: the scales of NW rows of weights (one per lane column). They come for 16 loads at a time, 16 of a row side by side,
+// are kept in registers until the wavefront is there, and are read from LDS load by load. (One load's at a time, each
+// instruction would ask for a cache line per row: T8 H4096 I2048 E128 K8 with 51 experts in use 273 -> 221 us.)
+constexpr int kScaleLoads = 16, kScaleStride = kScaleLoads + 1;  // the stride keeps rows in different banks
+template <Weights W, int NW>
+constexpr int kScaleFloats = W == kWFp8 ? NW * kTile * kScaleStride : 1;  // of LDS per wavefront
+
+template <int NW>
+struct Scales {
+    const float *row[NW];
+    int nb, last;        // scales of a row, rows there are but one
+    uint32_t per_block;  // 2^32 over the loads of one scale, rounded up (0: one load each)
+    float *lds;          // the wavefront's
+    float next[4 * NW];
+    int l0, n, left, at;  // loads l0 .. l0 + n - 1; of the 16 in LDS, not yet used; the first of those in `next`
+
+    __device__ __forceinline__ void fetch()
+    {
+        const int lane = threadIdx.x & (kWave - 1), l = l0 + min(at + lane % kTile, n - 1);
+        const int block = per_block ? __umulhi(l, per_block) : l;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                next[4 * i + q] = row[i][min(4 * q + lane / kTile, last) * nb + block];
+    }
+
+    // The first load used will be l0 + first; beyond 16 loads, first is a multiple of 16.
+    __device__ __forceinline__ void begin(int from, int loads, int first)
+    {
+        l0 = from;
+        n = loads;
+        left = 0;
+        at = first & -kScaleLoads;
+        fetch();
+    }
+
+    // Before each load, in order (beyond the last one the first follows).
+    __device__ __forceinline__ void step()
+    {
+        if (left == 0) {
+            const int lane = threadIdx.x & (kWave - 1);
+            // the wavefront's own LDS operations are done in order: this only keeps the compiler from moving them
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    lds[(i * kTile + 4 * q + lane / kTile) * kScaleStride + lane % kTile] = next[4 * i + q];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            left = n <= kScaleLoads ? n : min(kScaleLoads, n - at);
+            at = at + kScaleLoads < n ? at + kScaleLoads : 0;
+            if (n > kScaleLoads)
+                fetch();
+        }
+        --left;
+    }
+
+    // Of load l and weight row i.
+    __device__ __forceinline__ float of(int l, int i) const
+    {
+        return lds[(i * kTile + static_cast<int>(threadIdx.x % kTile)) * kScaleStride + ((l - l0) & (kScaleLoads - 1))];
+    }
+};
+
 // NW rows of weights (one per lane column) as they stream through a wavefront. Addresses are a uniform base, which
 // moves, and a 32-bit offset in each lane, which does not.
 template <Weights W, int NW, Read READ>
 struct WeightRows {
     typedef typename WeightType<W>::type Wt;
     const char *w[NW];
-    const float *scale[NW];
-    uint32_t w_off[2], w_row, s_off, per_block;
+    uint32_t w_off[2], w_row;
+    Scales<NW> scales;  // FP8
 
     struct Load {
         u32x4 w[NW][2];
         uint32_t over[NW][2];  // kOdd
-        float s[NW];
     };
 
     // Rows 0..15 from w[] on, `stride` elements apart; rows past `last` are read as that one.
-    __device__ __forceinline__ void rows_of(int stride, int last, int nb)
+    __device__ __forceinline__ void rows_of(int stride, int last)
     {
         const int lane = threadIdx.x & (kWave - 1), m = lane % kTile, g = lane / kTile;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             w_off[i] = static_cast<uint32_t>(min(8 * i + m % 8, last) * stride) * sizeof(Wt) + m / 8 * 64 + 16 * g;
         w_row = static_cast<uint32_t>(min(m, last) * stride) * sizeof(Wt);
-        s_off = min(m, last) * nb;
+    }
+
+    __device__ __forceinline__ void scales_of(const ExpertArgs &a, int last, float *lds)
+    {
+        scales.nb = a.nb;
+        scales.last = last;
+        scales.per_block = a.per_block;
+        scales.lds = lds + wave_id() * kScaleFloats<W, NW>;
     }
 
     __device__ __forceinline__ void issue(Load &q, int l) const
     {
 #pragma unroll
-        for (int i = 0; i < NW; ++i) {
+        for (int i = 0; i < NW; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 load_line(w[i] + static_cast<int64_t>(l) * 128 + w_off[h], q.w[i][h], q.over[i][h]);
-            if (W == kWFp8)
-                q.s[i] = (scale[i] + (per_block ? __umulhi(l, per_block) : l))[s_off];
-        }
     }
 
     __device__ __forceinline__ static void load_line(const char *p, u32x4 &v, uint32_t &over)
@@ -697,7 +766,7 @@ struct Product {
         uint32_t x_over[NT][2];  // kOdd
     };
 
-    __device__ __forceinline__ void multiply_slot(const Slot &q)
+    __device__ __forceinline__ void multiply_slot(const Slot &q, const float (&scale)[NW])
     {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -713,12 +782,19 @@ struct Product {
             }
 #pragma unroll
             for (int i = 0; i < NW; ++i)
-                acc[t][i] = W == kWFp8 ? acc[t][i] + p[i] * q.w.s[i] : p[i];  // a load lies in one block of scales
+                acc[t][i] = W == kWFp8 ? acc[t][i] + p[i] * scale[i] : p[i];  // a load lies in one block of scales
         }
     }
 
-    __device__ __forceinline__ void add(Slot &q)
+    __device__ __forceinline__ void add(Slot &q, int l)
     {
+        float scale[NW] = {};
+        if (W == kWFp8) {
+            rows.scales.step();
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                scale[i] = rows.scales.of(l, i);
+        }
         rows.arrange(q.w);
         if constexpr (READ == kOdd && !LO) {
 #pragma unroll
@@ -727,7 +803,7 @@ struct Product {
                 for (int h = 0; h < 2; ++h)
                     shift_odd(q.x[t][h].v[0], q.x_over[t][h], odd_bits(x + x_row[t]));
         }
-        multiply_slot(q);
+        multiply_slot(q, scale);
     }
 
     __device__ __forceinline__ void issue_acts(Slot &q, int l)
@@ -749,7 +825,8 @@ struct Product {
         }
     }
 
-    // Loads l0 .. l1 - 1 of rows of len elements, beginning with the turn-th of them.
+    // Loads l0 .. l1 - 1 of rows of len elements, beginning with the turn-th of them (FP8: where they are more than 16, the
+    // turn-th 16).
     __device__ __forceinline__ void run(int l0, int l1, int len, int turn)
     {
 #pragma unroll
@@ -760,9 +837,16 @@ struct Product {
         const int whole = min(l1, len / kLoadElems<W>), n = whole - l0;
         if (n > 0) {
             Slot q[D];
-            int at = l0 + turn % n, first[D];
+            const bool sixteens = W == kWFp8 && n > kScaleLoads;
+            int at = l0 + (sixteens ? turn % ((n + kScaleLoads - 1) / kScaleLoads) * kScaleLoads : turn % n), use = at, first[D];
             const int last = at == l0 ? whole - 1 : at - 1;
             auto next = [&] { at = at == last ? at : at == whole - 1 ? l0 : at + 1; };
+            auto multiply_next = [&](Slot &s) {
+                add(s, use);
+                use = use == whole - 1 ? l0 : use + 1;
+            };
+            if (W == kWFp8)
+                rows.scales.begin(l0, n, at - l0);
 #pragma unroll
             for (int u = 0; u < D; ++u) {  // weights first: the activations' addresses are longer in coming
                 first[u] = at;
@@ -777,7 +861,7 @@ struct Product {
             for (; l + D < n; l += D) {
 #pragma unroll
                 for (int u = 0; u < D; ++u) {
-                    add(q[u]);
+                    multiply_next(q[u]);
                     rows.issue(q[u].w, at);
                     issue_acts(q[u], at);
                     next();
@@ -787,7 +871,7 @@ struct Product {
 #pragma unroll
             for (int u = 0; u < D; ++u)
                 if (l + u < n)
-                    add(q[u]);
+                    multiply_next(q[u]);
         }
         if (W != kWFp8 && whole < l1) {  // the row's last load, partial
             Slot z;
@@ -801,7 +885,7 @@ struct Product {
                     if (LO)
                         load_tail(reinterpret_cast<const X *>(x + x_row[t] + lo), e, len, z.y[t][h]);
                 }
-            multiply_slot(z);
+            multiply_slot(z, {});
         }
     }
 };
@@ -837,7 +921,7 @@ struct TiledProduct {
         return plane * kPlaneChunks + r * kRowChunks + (c ^ (r & 7));
     }
 
-    __device__ __forceinline__ void multiply_load(const u32x4 *buf, const typename Rows::Load &q)
+    __device__ __forceinline__ void multiply_load(const u32x4 *buf, const typename Rows::Load &q, const float (&scale)[2])
     {
         const int lane = threadIdx.x & (kWave - 1), m = lane % kTile, g = lane / kTile;
 #pragma unroll
@@ -858,7 +942,7 @@ struct TiledProduct {
                 }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                acc[i][t] = W == kWFp8 ? acc[i][t] + p[i] * q.s[i] : p[i];
+                acc[i][t] = W == kWFp8 ? acc[i][t] + p[i] * scale[i] : p[i];
         }
     }
 
@@ -898,6 +982,8 @@ struct TiledProduct {
         if (n > 0) {
             Slot q[D];
             vec4 x0[Q];
+            if (W == kWFp8)
+                rows.scales.begin(0, n, 0);
             issue_x(x0, 0);
 #pragma unroll
             for (int u = 0; u < D; ++u) {
@@ -910,8 +996,15 @@ struct TiledProduct {
                 for (int u = 0; u < D; ++u) {
                     if (l + u < n) {
                         __syncthreads();
+                        float scale[2] = {};
+                        if (W == kWFp8) {
+                            rows.scales.step();
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                scale[i] = rows.scales.of(l + u, i);
+                        }
                         rows.arrange(q[u].w);
-                        multiply_load(lds + b * kChunks, q[u].w);
+                        multiply_load(lds + b * kChunks, q[u].w, scale);
                         b ^= 1;
                         stage(q[u].x, b);
                         rows.issue(q[u].w, min(l + u + D, n - 1));
@@ -934,7 +1027,7 @@ struct TiledProduct {
             __syncthreads();
             stage(v, b);
             __syncthreads();
-            multiply_load(lds + b * kChunks, z);
+            multiply_load(lds + b * kChunks, z, {});
         }
         __syncthreads();  // the buffers are free again
     }
@@ -996,16 +1089,17 @@ struct Entry {
 // The weight rows of a gate and up unit: 16 columns of h. Columns past the last one take its place: what they give is
 // not stored.
 template <Weights W, Read READ>
-__device__ __forceinline__ void gate_up_weights(const ExpertArgs &a, const Entry &en, int unit, WeightRows<W, 2, READ> &rows)
+__device__ __forceinline__ void gate_up_weights(const ExpertArgs &a, const Entry &en, int unit, float *scales,
+                                                WeightRows<W, 2, READ> &rows)
 {
     const int c0 = min(unit * kTile, a.I - 1);
-    rows.rows_of(a.H, a.I - 1 - c0, a.nb);
-    rows.per_block = a.per_block;
+    rows.rows_of(a.H, a.I - 1 - c0);
+    rows.scales_of(a, a.I - 1 - c0, scales);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // the gate's rows, the up's rows
         const int64_t row = (en.ex * 2 + i) * a.I + c0;
         rows.w[i] = static_cast<const char *>(a.w) + row * a.H * sizeof(typename WeightType<W>::type);
-        rows.scale[i] = a.scales + row * a.nb;
+        rows.scales.row[i] = a.scales + row * a.nb;
     }
 }
 
@@ -1032,11 +1126,11 @@ __device__ __forceinline__ void store_h(const ExpertArgs &a, const Entry &en, in
 
 // Up to NT tiles of an expert's tokens, from row r0 on.
 template <Weights W, int NT, typename Sh, Read READ>
-__device__ __forceinline__ void gate_up_stream(const ExpertArgs &a, const Entry &en, int r0, char *lds)
+__device__ __forceinline__ void gate_up_stream(const ExpertArgs &a, const Entry &en, int r0, char *lds, float *scales)
 {
     Product<W, 2, NT, false, Sh::kRegs, READ> p;
     const Share my(Sh::kWaves, a.parts);
-    gate_up_weights<W, READ>(a, en, my.unit, p.rows);
+    gate_up_weights<W, READ>(a, en, my.unit, scales, p.rows);
     p.lo = 0;
     p.x = static_cast<const char *>(a.x);
 #pragma unroll
@@ -1054,11 +1148,11 @@ __device__ __forceinline__ void gate_up_stream(const ExpertArgs &a, const Entry 
 
 // The same with the tokens' rows through LDS; the workgroup's wavefronts take a unit each.
 template <Weights W, int NT, Read READ>
-__device__ __forceinline__ void gate_up_tiles(const ExpertArgs &a, const Entry &en, int r0, char *lds)
+__device__ __forceinline__ void gate_up_tiles(const ExpertArgs &a, const Entry &en, int r0, char *lds, float *scales)
 {
     TiledProduct<W, NT, false, READ> p;
     const int unit = blockIdx.x * 4 + wave_id(), lane = threadIdx.x & (kWave - 1);
-    gate_up_weights<W, READ>(a, en, unit, p.rows);
+    gate_up_weights<W, READ>(a, en, unit, scales, p.rows);
     p.lo = 0;
     p.x = static_cast<const char *>(a.x);
     p.run(a.H, reinterpret_cast<u32x4 *>(lds), [&](int r) {
@@ -1082,20 +1176,21 @@ __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWaves
 {
     typedef Shape<W, MANY> Sh;
     __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, false>];
+    __shared__ float scales[Sh::kWaves * kScaleFloats<W, 2>];
     const Entry en(a.plan, blockIdx.y);
     if constexpr (!MANY) {
         for (int r0 = 0; r0 < en.n; r0 += kTile)
-            gate_up_stream<W, 1, Sh, READ>(a, en, r0, lds);
+            gate_up_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
     } else if (!a.tiled || en.n <= 2 * kTile) {
         for (int r0 = 0; r0 < en.n; r0 += 2 * kTile) {
             if (en.n - r0 <= kTile)
-                gate_up_stream<W, 1, Sh, READ>(a, en, r0, lds);
+                gate_up_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
             else
-                gate_up_stream<W, 2, Sh, READ>(a, en, r0, lds);
+                gate_up_stream<W, 2, Sh, READ>(a, en, r0, lds, scales);
         }
     } else if (static_cast<int>(blockIdx.x) * 4 * kTile < a.I) {
         for (int r0 = 0; r0 < en.n; r0 += 4 * kTile)
-            gate_up_tiles<W, 4, READ>(a, en, r0, lds);
+            gate_up_tiles<W, 4, READ>(a, en, r0, lds, scales);
     }
 }
 
@@ -1109,16 +1204,17 @@ __device__ __forceinline__ int second_tile(const ExpertArgs &a, int c0)
 }
 
 template <Weights W, Read READ>
-__device__ __forceinline__ void down_weights(const ExpertArgs &a, const Entry &en, int unit, WeightRows<W, 2, READ> &rows)
+__device__ __forceinline__ void down_weights(const ExpertArgs &a, const Entry &en, int unit, float *scales,
+                                             WeightRows<W, 2, READ> &rows)
 {
     const int c0 = min(unit * 2 * kTile, a.H - 1), c1 = second_tile(a, c0);
-    rows.rows_of(a.I, a.H - 1 - c0 - c1, a.nb);
-    rows.per_block = a.per_block;
+    rows.rows_of(a.I, a.H - 1 - c0 - c1);
+    rows.scales_of(a, a.H - 1 - c0 - c1, scales);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int64_t row = en.ex * a.H + c0 + i * c1;
         rows.w[i] = static_cast<const char *>(a.w) + row * a.I * sizeof(typename WeightType<W>::type);
-        rows.scale[i] = a.scales + row * a.nb;
+        rows.scales.row[i] = a.scales + row * a.nb;
     }
 }
 
@@ -1146,12 +1242,12 @@ __device__ __forceinline__ const char *h_from(const ExpertArgs &a, int pos)
 }
 
 template <Weights W, int NT, typename Sh, Read READ>
-__device__ __forceinline__ void down_stream(const ExpertArgs &a, const Entry &en, int r0, char *lds)
+__device__ __forceinline__ void down_stream(const ExpertArgs &a, const Entry &en, int r0, char *lds, float *scales)
 {
     typedef typename ActType<W>::type X;
     Product<W, 2, NT, W != kWF32, Sh::kRegs, READ> p;
     const Share my(Sh::kWaves, a.parts);
-    down_weights<W, READ>(a, en, my.unit, p.rows);
+    down_weights<W, READ>(a, en, my.unit, scales, p.rows);
     p.lo = static_cast<int64_t>(a.hI) * sizeof(X);
     p.x = h_from<W>(a, en.p0 + r0);
 #pragma unroll
@@ -1168,12 +1264,12 @@ __device__ __forceinline__ void down_stream(const ExpertArgs &a, const Entry &en
 }
 
 template <Weights W, int NT, Read READ>
-__device__ __forceinline__ void down_tiles(const ExpertArgs &a, const Entry &en, int r0, char *lds)
+__device__ __forceinline__ void down_tiles(const ExpertArgs &a, const Entry &en, int r0, char *lds, float *scales)
 {
     typedef typename ActType<W>::type X;
     TiledProduct<W, NT, W != kWF32, READ> p;
     const int unit = blockIdx.x * 4 + wave_id(), lane = threadIdx.x & (kWave - 1);
-    down_weights<W, READ>(a, en, unit, p.rows);
+    down_weights<W, READ>(a, en, unit, scales, p.rows);
     p.lo = static_cast<int64_t>(a.hI) * sizeof(X);
     p.x = h_from<W>(a, en.p0 + r0);
     p.run(a.I, reinterpret_cast<u32x4 *>(lds), [&](int r) {
@@ -1191,23 +1287,24 @@ __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWaves
 {
     typedef Shape<W, MANY> Sh;
     __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, W != kWF32>];
+    __shared__ float scales[Sh::kWaves * kScaleFloats<W, 2>];
     const Entry en(a.plan, blockIdx.y);
     if constexpr (!MANY) {
         for (int r0 = 0; r0 < en.n; r0 += kTile)
-            down_stream<W, 1, Sh, READ>(a, en, r0, lds);
+            down_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
     } else if (!a.tiled || en.n <= kTile) {
         for (int r0 = 0; r0 < en.n; r0 += 2 * kTile) {
             if (en.n - r0 <= kTile)
-                down_stream<W, 1, Sh, READ>(a, en, r0, lds);
+                down_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
             else
-                down_stream<W, 2, Sh, READ>(a, en, r0, lds);
+                down_stream<W, 2, Sh, READ>(a, en, r0, lds, scales);
         }
     } else if (static_cast<int>(blockIdx.x) * 4 * 2 * kTile < a.H) {
         for (int r0 = 0; r0 < en.n; r0 += 4 * kTile) {
             if (en.n - r0 <= 2 * kTile)
-                down_tiles<W, 2, READ>(a, en, r0, lds);
+                down_tiles<W, 2, READ>(a, en, r0, lds, scales);
             else
-                down_tiles<W, 4, READ>(a, en, r0, lds);
+                down_tiles<W, 4, READ>(a, en, r0, lds, scales);
         }
     }
 }
@@ -1236,7 +1333,7 @@ template <Weights W, Read READ>
 __global__ __launch_bounds__(kDirectThreads) void down_merge_kernel(ExpertArgs a)
 {
     typedef Product<W, 1, 1, W != kWF32, Shape<W, false>::kRegs, READ> P;
-    __shared__ float sums[kDirectWaves][kTile][kTile];
+    __shared__ float sums[kDirectWaves][kTile][kTile], scales[kDirectWaves * kScaleFloats<W, 1>];
     const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), m = lane % kTile, g = lane / kTile;
     const int c0 = blockIdx.x * kTile;
     for (int i = lane; i < kTile * kTile; i += kWave)
@@ -1250,10 +1347,10 @@ __global__ __launch_bounds__(kDirectThreads) void down_merge_kernel(ExpertArgs a
         const int64_t row = static_cast<int64_t>(a.plan.act[i]) * a.H + c0;
         for (int r0 = 0; r0 < n; r0 += kTile) {
             P p;
-            p.rows.rows_of(a.I, a.H - 1 - c0, a.nb);
-            p.rows.per_block = a.per_block;
+            p.rows.rows_of(a.I, a.H - 1 - c0);
+            p.rows.scales_of(a, a.H - 1 - c0, scales);
             p.rows.w[0] = static_cast<const char *>(a.w) + row * a.I * sizeof(typename P::Wt);
-            p.rows.scale[0] = a.scales + row * a.nb;
+            p.rows.scales.row[0] = a.scales + row * a.nb;
             p.lo = static_cast<int64_t>(a.hI) * sizeof(typename P::X);
             p.x = h_from<W>(a, p0 + r0);
             const int r = min(m, n - 1 - r0), tok = a.plan.token[p0 + r0 + r];
