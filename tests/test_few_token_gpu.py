@@ -443,3 +443,38 @@ def test_fp8_rows_of_many_blocks(m, T, H, I, block):
     idx, w = lay.routed(x, 2)
     out = m.few_token_experts(x, idx, w.float(), lay.w13, lay.w2, out_dtype=F32, **lay.scales)
     assert_within(out, *lay.expected(x, idx, w.float()))
+
+
+@pytest.mark.parametrize("T,K", [(4, 3), (14, 2), (30, 3), (90, 2)])
+@pytest.mark.parametrize("kind,H,I,shifts", [("bf16", 2057, 2063, (0, 1)), ("bf16", 2056, 2062, (0, 3)), ("bf16", 2060, 2056, (0, 8)),
+                                             ("bf16", 2048, 2112, (2, 5)), ("f32", 2057, 2063, (0, 1)), ("fp8", 2176, 4352, (1, 6))])
+def test_long_rows_off_the_cache_lines(m, T, K, kind, H, I, shifts):
+    """Enough of them that they go through the window, at several places in their storage, between elements that are not
+    numbers."""
+    E = 12
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    lay = Layer(m, 128, 128, 1, kind)  # replaced below by weights drawn on the GPU
+    lay.H, lay.I, lay.E = H, I, E
+    w13 = torch.randn(E, 2 * I, H, generator=g, device=DEV) * H ** -0.5
+    w2 = torch.randn(E, H, I, generator=g, device=DEV) * I ** -0.5
+    if kind == "fp8":
+        q13, s13 = m.quantize_fp8(w13.view(E * 2 * I, H))
+        q2, s2 = m.quantize_fp8(w2.view(E * H, I))
+        lay.w13, lay.w2 = q13.view(E, 2 * I, H), q2.view(E, H, I)
+        lay.scales = dict(gate_up_scales=s13.view(E, 2 * I, -1), down_scales=s2.view(E, H, -1))
+        value = lambda q, s: q.view(torch.float8_e4m3fn).double() * s.double().repeat_interleave(128, 1)  # noqa: E731
+        lay.v13, lay.v2 = value(q13, s13).view(E, 2 * I, H), value(q2, s2).view(E, H, I)
+    else:
+        lay.w13, lay.w2 = w13.to(lay.rows), w2.to(lay.rows)
+        lay.v13, lay.v2 = lay.w13.double(), lay.w2.double()
+    x = torch.randn(T, H, generator=g, device=DEV).to(lay.rows)
+    idx = torch.rand(T, E, generator=g, device=DEV).topk(K, 1)[1].to(torch.int32)
+    w = torch.rand(T, K, generator=g, device=DEV)
+    want = lay.expected(x, idx, w)
+    for shift in shifts:
+        def off(t):
+            fill = 255 if t.dtype == torch.uint8 else float("nan")
+            return torch.cat([t.new_full((shift,), fill), t.flatten(), t.new_full((9,), fill)])[shift: shift + t.numel()].view(t.shape)
+        out = m.few_token_experts(off(x), idx, w, off(lay.w13), off(lay.w2), out_dtype=F32, **lay.scales)
+        assert_within(out, *want)

@@ -7,10 +7,13 @@
 //
 // with expert e's gate rows G_e = w_gate_up[e][0..I), up rows U_e = w_gate_up[e][I..2I) and D_e = w_down[e].
 //
-// The time is that of reading the weights of the experts in use, once each. A wavefront multiplies 16 rows of a
-// weight matrix by up to 16 tokens with MFMA 16x16 tiles (few tokens leave most of a tile's columns empty, which
-// costs nothing while the weights' stream sets the pace): 4 lanes read 64 consecutive bytes of each of the 16 rows,
-// straight from memory into the matrix instruction's operand registers, without LDS.
+// The time is that of reading the weights of the experts in use, once each, and for the smallest calls that of the
+// launches. A wavefront multiplies 32 rows of a weight matrix (16 of the gate's and the 16 of the up's, or 32 of the down's)
+// by 16 or 32 tokens with MFMA 16x16 tiles: few tokens leave most of a tile empty, which costs nothing while the weights'
+// stream sets the pace. The weights go from memory straight into the matrix instructions' operand registers, whole cache
+// lines at a time, several loads ahead in a ring of registers. Measured with cold caches, of the bytes of the weights in
+// use: T64 H7168 I1024 E256 K8 bf16 gate and up 6.0 TB/s, down 5.4 (plain reads of so many bytes the same way reach
+// 6.7); T1 of it 6.3 and 5.2 in 74 us, of which 16 are router, routing, merge and launches.
 #include <algorithm>
 
 #include "moe_common.h"
@@ -542,8 +545,8 @@ __global__ __launch_bounds__(kPlanThreads) void few_token_small_route_kernel(con
 }
 
 // ---------------------------------------------------------------- gate and up products
-// One workgroup per (16 columns of h, expert in use): its wavefronts share the hidden dimension's loads, and their
-// tiles meet in LDS. h goes out in the order of the plan, already multiplied by the slot's weight; beside bf16 or FP8
+// A unit is 16 columns of h of one expert, 16 rows of gate and 16 of up; wavefronts take a unit each, or share the hidden
+// dimension's loads of one, and then their tiles meet in LDS. h goes out in the order of the plan, already multiplied by the slot's weight; beside bf16 or FP8
 // weights as two bf16 rows whose sum it is to 16 bits, so that the down product is one of bf16 operands without
 // bf16's rounding of h.
 
@@ -551,11 +554,21 @@ __global__ __launch_bounds__(kPlanThreads) void few_token_small_route_kernel(con
 template <Weights W, int NW, int NT, bool LO>
 constexpr int kSlotRegs = 8 * (NW + NT * (LO ? 2 : 1) * (W == kWFp8 ? 2 : 1));
 
-// How rows of weights lie. kLines: they begin on cache lines, so that each line is read by one instruction, past the
-// caches (a line that two instructions share is read from memory twice that way); kWords: on 4-byte words; kOdd: bf16
-// rows on odd elements (16-byte reads from there run at half the rate of those from words, so whole words are read and put
-// together by shifts). FP8 rows off their words are read as they lie.
-enum Read { kLines, kWords, kOdd };
+// How rows of weights lie and are read. kLines: they begin on cache lines, a load is a line, and each line is read by one
+// instruction, past the caches (a line that two instructions share is read from memory twice that way). Others are read as
+// they lie, most lines by two instructions: kWords, where they begin on 4-byte words; kOdd, where bf16 rows or their
+// activations' do not (16-byte reads from there run at half the rate of those from words, so whole words are read and put
+// together by shifts; FP8 rows off their words are read by kWords all the same). kWindow: a load lies in two lines, other
+// bytes of them in each row, and the lines, read as with kLines, go through a window of two in LDS, a row each, from which
+// the load is read wherever it begins; kWindowOdd: and the activations as with kOdd.
+enum Read { kLines, kWords, kOdd, kWindow, kWindowOdd };
+constexpr bool windowed(Read r) { return r == kWindow || r == kWindowOdd; }
+constexpr bool odd_acts(Read r) { return r == kOdd || r == kWindowOdd; }
+
+// LDS of the window: 16 rows of two lines, whose first 16 bytes stand behind the second line too, for what begins at its end.
+constexpr int kWindowRow = 2 * 128 + 16 + 8;  // bytes; 8 more keep rows in different banks, whose lengths are mostly multiples of 16
+template <int NW>
+constexpr int kWindowBytes = NW * kTile * kWindowRow;
 
 // The shape of a kernel: 8 wavefronts of 128 registers, of which 16 share a CU with two loads or more in flight each, or
 // where experts may have MANY tokens (more than a tile's) 4 of 256, of which 8 do.
@@ -565,7 +578,13 @@ struct Shape {
     static constexpr int kOther = W != kWFp8 ? 40 : MANY ? 64 : 52;
     static constexpr int kRegs = (MANY ? 256 : 128) - kOther, kWaves = MANY ? 4 : 8, kThreads = kWaves * kWave;
     static constexpr int kWavesPerSimd = MANY ? 2 : 4;
+    // bytes of LDS of a wavefront: its window, later its tiles
+    template <Read READ>
+    static constexpr int kStretch = windowed(READ) ? kWindowBytes<2> : (MANY ? 2 : 1) * 2 * kWave * 16;
 };
+
+template <Weights W, bool MANY, Read READ>
+constexpr int kStretches = Shape<W, MANY>::kWaves * Shape<W, MANY>::template kStretch<READ>;
 
 struct ExpertArgs {
     const void *x;            // [T, H] activations
@@ -658,7 +677,12 @@ template <Weights W, int NW, Read READ>
 struct WeightRows {
     typedef typename WeightType<W>::type Wt;
     const char *w[NW];
-    uint32_t w_off[2], w_row;
+    uint32_t w_row;
+    uint32_t w_off[windowed(READ) ? NW : 1][2];
+    // windowed: offsets from row 0's line; the first and last 16-byte word that holds a byte of the row
+    uint32_t low[NW][2], high[NW][2];
+    uint32_t at[NW];  // of the lane's share of load 0 in its row of the window
+    char *window;
     Scales<NW> scales;  // FP8
 
     struct Load {
@@ -666,15 +690,35 @@ struct WeightRows {
         uint32_t over[NW][2];  // kOdd
     };
 
-    // Rows 0..15 from w[] on, `stride` elements apart; rows past `last` are read as that one.
-    __device__ __forceinline__ void rows_of(int stride, int last)
+    // Rows 0..15 from w[] on, of len elements each; rows past `last` are read as that one.
+    __device__ __forceinline__ void rows_of(int len, int last, char *lds)
     {
-        const int lane = threadIdx.x & (kWave - 1), m = lane % kTile, g = lane / kTile;
+        const int lane = threadIdx.x & (kWave - 1), m = lane % kTile, g = lane / kTile, chunk = m / 8 * 4 + g;
+        const uint32_t bytes = static_cast<uint32_t>(len) * sizeof(Wt);
+        w_row = min(m, last) * bytes;
+        window = lds;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            w_off[i] = static_cast<uint32_t>(min(8 * i + m % 8, last) * stride) * sizeof(Wt) + m / 8 * 64 + 16 * g;
-        w_row = static_cast<uint32_t>(min(m, last) * stride) * sizeof(Wt);
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t row = min(8 * h + m % 8, last) * bytes;
+            if constexpr (!windowed(READ)) {
+                w_off[0][h] = row + 16 * chunk;
+            } else {
+#pragma unroll
+                for (int i = 0; i < NW; ++i) {
+                    const uint32_t from = row + in_line(w[i]);
+                    w_off[i][h] = (from & ~127u) + 16 * chunk;
+                    low[i][h] = from & ~15u;
+                    high[i][h] = (from + bytes - 1) & ~15u;
+                }
+            }
+        }
+        if constexpr (windowed(READ))
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                at[i] = ((in_line(w[i]) + w_row) & 127u) + 16 * g;
     }
+
+    __device__ __forceinline__ static uint32_t in_line(const char *p) { return reinterpret_cast<uintptr_t>(p) & 127u; }
 
     __device__ __forceinline__ void scales_of(const ExpertArgs &a, int last, float *lds)
     {
@@ -684,38 +728,88 @@ struct WeightRows {
         scales.lds = lds + wave_id() * kScaleFloats<W, NW>;
     }
 
-    __device__ __forceinline__ void issue(Load &q, int l) const
+    __device__ __forceinline__ static void load_word(const char *p, u32x4 &v)
+    {
+        const vec4 n = __builtin_nontemporal_load(reinterpret_cast<const vec4 *>(p));
+        v = u32x4{n.x, n.y, n.z, n.w};
+    }
+
+    // Windowed: line l of the rows.
+    __device__ __forceinline__ void issue_line(Load &q, int l) const
     {
 #pragma unroll
         for (int i = 0; i < NW; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                load_line(w[i] + static_cast<int64_t>(l) * 128 + w_off[h], q.w[i][h], q.over[i][h]);
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t off = min(max(w_off[i][h] + 128 * l, low[i][h]), high[i][h]);
+                load_word(w[i] - in_line(w[i]) + off, q.w[i][h]);
+            }
     }
 
-    __device__ __forceinline__ static void load_line(const char *p, u32x4 &v, uint32_t &over)
+    __device__ __forceinline__ void issue(Load &q, int l) const
     {
-        if constexpr (READ == kLines) {
-            const vec4 n = __builtin_nontemporal_load(reinterpret_cast<const vec4 *>(p));
-            v = u32x4{n.x, n.y, n.z, n.w};
-        } else if constexpr (READ == kOdd) {
-            load_odd(p, v, over);
+        if constexpr (windowed(READ)) {
+            issue_line(q, l + 1);
         } else {
-            __builtin_memcpy(&v, p, sizeof(v));
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const char *p = w[i] + static_cast<int64_t>(l) * 128 + w_off[0][h];
+                    if constexpr (READ == kLines)
+                        load_word(p, q.w[i][h]);
+                    else if constexpr (READ == kOdd)
+                        load_odd(p, q.w[i][h], q.over[i][h]);
+                    else
+                        __builtin_memcpy(&q.w[i][h], p, sizeof(q.w[i][h]));
+                }
         }
     }
 
-    // A load that has come, made into the matrix instructions' operands.
-    __device__ __forceinline__ void arrange(Load &q) const
+    // Windowed: line l, which has come, into the window. (The wavefront's own LDS operations are done in order: the fences only
+    // keep the compiler from moving them.)
+    __device__ __forceinline__ void put_line(const Load &q, int l) const
     {
+        const int lane = threadIdx.x & (kWave - 1), m = lane % kTile, chunk = m / 8 * 4 + lane / kTile;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            if constexpr (READ == kOdd) {
+        for (int i = 0; i < NW; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    shift_odd(q.w[i][h], q.over[i][h], odd_bits(w[i] + w_off[h]));
+            for (int h = 0; h < 2; ++h) {
+                char *row = window + (i * kTile + 8 * h + m % 8) * kWindowRow;
+                __builtin_memcpy(__builtin_assume_aligned(row + (l & 1) * 128 + 16 * chunk, 8), &q.w[i][h], 16);
+                if ((l & 1) == 0 && chunk == 0)
+                    __builtin_memcpy(__builtin_assume_aligned(row + 256, 8), &q.w[i][h], 16);
             }
-            to_halves(q.w[i][0], q.w[i][1]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+
+    // Load l, which has come, made into the matrix instructions' operands.
+    __device__ __forceinline__ void arrange(Load &q, int l) const
+    {
+        if constexpr (windowed(READ)) {
+            put_line(q, l + 1);
+            const int m = threadIdx.x % kTile;
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t from = (at[i] + 64 * h + (l & 1) * 128) & 255u;
+                    const uint32_t *p = reinterpret_cast<const uint32_t *>(window + (i * kTile + m) * kWindowRow + (from & ~3u));
+                    q.w[i][h] = u32x4{p[0], p[1], p[2], p[3]};
+                    if (W != kWF32)
+                        shift_odd(q.w[i][h], p[4], (from & 3u) * 8);
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+                if constexpr (READ == kOdd) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        shift_odd(q.w[i][h], q.over[i][h], odd_bits(w[i] + w_off[0][h]));
+                }
+                to_halves(q.w[i][0], q.w[i][1]);
+            }
         }
     }
 
@@ -763,7 +857,7 @@ struct Product {
     struct Slot {
         typename Rows::Load w;
         Acts<W> x[NT][2], y[NT][2];
-        uint32_t x_over[NT][2];  // kOdd
+        uint32_t x_over[NT][2];  // odd_acts
     };
 
     __device__ __forceinline__ void multiply_slot(const Slot &q, const float (&scale)[NW])
@@ -795,8 +889,8 @@ struct Product {
             for (int i = 0; i < NW; ++i)
                 scale[i] = rows.scales.of(l, i);
         }
-        rows.arrange(q.w);
-        if constexpr (READ == kOdd && !LO) {
+        rows.arrange(q.w, l);
+        if constexpr (odd_acts(READ) && !LO) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -814,7 +908,7 @@ struct Product {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const char *row = x + static_cast<int64_t>(2 * l + h) * kActBytes;
-                if constexpr (READ == kOdd && !LO) {
+                if constexpr (odd_acts(READ) && !LO) {
                     load_odd(row + off, q.x[t][h].v[0], q.x_over[t][h]);
                 } else {
                     __builtin_memcpy(&q.x[t][h], row + off, sizeof(q.x[t][h]));
@@ -826,7 +920,7 @@ struct Product {
     }
 
     // Loads l0 .. l1 - 1 of rows of len elements, beginning with the turn-th of them (FP8: where they are more than 16, the
-    // turn-th 16).
+    // turn-th 16; windowed: the first).
     __device__ __forceinline__ void run(int l0, int l1, int len, int turn)
     {
 #pragma unroll
@@ -838,7 +932,7 @@ struct Product {
         if (n > 0) {
             Slot q[D];
             const bool sixteens = W == kWFp8 && n > kScaleLoads;
-            int at = l0 + (sixteens ? turn % ((n + kScaleLoads - 1) / kScaleLoads) * kScaleLoads : turn % n), use = at, first[D];
+            int at = windowed(READ) ? l0 : l0 + (sixteens ? turn % ((n + kScaleLoads - 1) / kScaleLoads) * kScaleLoads : turn % n), use = at, first[D];
             const int last = at == l0 ? whole - 1 : at - 1;
             auto next = [&] { at = at == last ? at : at == whole - 1 ? l0 : at + 1; };
             auto multiply_next = [&](Slot &s) {
@@ -847,6 +941,9 @@ struct Product {
             };
             if (W == kWFp8)
                 rows.scales.begin(l0, n, at - l0);
+            typename Rows::Load line;
+            if constexpr (windowed(READ))
+                rows.issue_line(line, l0);
 #pragma unroll
             for (int u = 0; u < D; ++u) {  // weights first: the activations' addresses are longer in coming
                 first[u] = at;
@@ -857,6 +954,8 @@ struct Product {
 #pragma unroll
             for (int u = 0; u < D; ++u)
                 issue_acts(q[u], first[u]);
+            if constexpr (windowed(READ))
+                rows.put_line(line, l0);
             int l = 0;
             for (; l + D < n; l += D) {
 #pragma unroll
@@ -1003,7 +1102,7 @@ struct TiledProduct {
                             for (int i = 0; i < 2; ++i)
                                 scale[i] = rows.scales.of(l + u, i);
                         }
-                        rows.arrange(q[u].w);
+                        rows.arrange(q[u].w, l + u);
                         multiply_load(lds + b * kChunks, q[u].w, scale);
                         b ^= 1;
                         stage(q[u].x, b);
@@ -1047,16 +1146,19 @@ struct Share {
 
 // The parts' tiles put together in order, f(unit, tile row, column, sums of the two weight rows). Register r of lane l
 // holds the tile's row 4 (l / 16) + r and column l % 16.
-template <int WAVES, int NT, typename F>
-__device__ __forceinline__ void join_parts(const f32x4 (&acc)[NT][2], int parts, f32x4 (*red)[NT][2][kWave], F f)
+template <int WAVES, int NT, int STRIDE, typename F>
+__device__ __forceinline__ void join_parts(const f32x4 (&acc)[NT][2], int parts, char *lds, F f)
 {
     constexpr int values = NT * kTile * kTile;
-    const int lane = threadIdx.x & (kWave - 1), wave = wave_id();
+    const int lane = threadIdx.x & (kWave - 1);
+    auto tile = [&](int wave, int t, int i) {  // each wavefront's own stretch of LDS holds its tiles
+        return reinterpret_cast<f32x4 *>(lds + wave * STRIDE) + (t * 2 + i) * kWave;
+    };
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            red[wave][t][i][lane] = acc[t][i];
+            tile(wave_id(), t, i)[lane] = acc[t][i];
     __syncthreads();
     for (int i = threadIdx.x; i < WAVES / parts * values; i += WAVES * kWave) {
         const int first = i / values * parts, t = i % values / (kTile * kTile), v = i % (kTile * kTile);
@@ -1066,7 +1168,7 @@ __device__ __forceinline__ void join_parts(const f32x4 (&acc)[NT][2], int parts,
         for (int w = first; w < first + parts; ++w)
 #pragma unroll
             for (int n = 0; n < 2; ++n)
-                sum[n] += red[w][t][n][src][r];
+                sum[n] += tile(w, t, n)[src][r];
         f(first / parts, t * kTile + row, col, sum);
     }
     __syncthreads();
@@ -1089,18 +1191,18 @@ struct Entry {
 // The weight rows of a gate and up unit: 16 columns of h. Columns past the last one take its place: what they give is
 // not stored.
 template <Weights W, Read READ>
-__device__ __forceinline__ void gate_up_weights(const ExpertArgs &a, const Entry &en, int unit, float *scales,
+__device__ __forceinline__ void gate_up_weights(const ExpertArgs &a, const Entry &en, int unit, char *window, float *scales,
                                                 WeightRows<W, 2, READ> &rows)
 {
     const int c0 = min(unit * kTile, a.I - 1);
-    rows.rows_of(a.H, a.I - 1 - c0);
-    rows.scales_of(a, a.I - 1 - c0, scales);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // the gate's rows, the up's rows
         const int64_t row = (en.ex * 2 + i) * a.I + c0;
         rows.w[i] = static_cast<const char *>(a.w) + row * a.H * sizeof(typename WeightType<W>::type);
         rows.scales.row[i] = a.scales + row * a.nb;
     }
+    rows.rows_of(a.H, a.I - 1 - c0, window);
+    rows.scales_of(a, a.I - 1 - c0, scales);
 }
 
 // h of the expert's token `row`, column c.
@@ -1130,7 +1232,7 @@ __device__ __forceinline__ void gate_up_stream(const ExpertArgs &a, const Entry 
 {
     Product<W, 2, NT, false, Sh::kRegs, READ> p;
     const Share my(Sh::kWaves, a.parts);
-    gate_up_weights<W, READ>(a, en, my.unit, scales, p.rows);
+    gate_up_weights<W, READ>(a, en, my.unit, lds + wave_id() * Sh::template kStretch<READ>, scales, p.rows);
     p.lo = 0;
     p.x = static_cast<const char *>(a.x);
 #pragma unroll
@@ -1140,8 +1242,7 @@ __device__ __forceinline__ void gate_up_stream(const ExpertArgs &a, const Entry 
     }
     const int loads = (a.H + kLoadElems<W> - 1) / kLoadElems<W>;
     p.run(loads * my.part / a.parts, loads * (my.part + 1) / a.parts, a.H, a.stagger ? my.unit : 0);
-    join_parts<Sh::kWaves, NT>(p.acc, a.parts, reinterpret_cast<f32x4(*)[NT][2][kWave]>(lds),
-                           [&](int unit, int row, int column, const float (&v)[2]) {
+    join_parts<Sh::kWaves, NT, Sh::template kStretch<READ>>(p.acc, a.parts, lds, [&](int unit, int row, int column, const float (&v)[2]) {
         store_h<W>(a, en, r0 + row, (blockIdx.x * (Sh::kWaves / a.parts) + unit) * kTile + column, v[0], v[1]);
     });
 }
@@ -1152,7 +1253,7 @@ __device__ __forceinline__ void gate_up_tiles(const ExpertArgs &a, const Entry &
 {
     TiledProduct<W, NT, false, READ> p;
     const int unit = blockIdx.x * 4 + wave_id(), lane = threadIdx.x & (kWave - 1);
-    gate_up_weights<W, READ>(a, en, unit, scales, p.rows);
+    gate_up_weights<W, READ>(a, en, unit, nullptr, scales, p.rows);
     p.lo = 0;
     p.x = static_cast<const char *>(a.x);
     p.run(a.H, reinterpret_cast<u32x4 *>(lds), [&](int r) {
@@ -1166,22 +1267,22 @@ __device__ __forceinline__ void gate_up_tiles(const ExpertArgs &a, const Entry &
             store_h<W>(a, en, r0 + t * kTile + lane / kTile * 4 + r, unit * kTile + lane % kTile, p.acc[0][t][r], p.acc[1][t][r]);
 }
 
-// LDS of a kernel: the parts' tiles, or the activations of the largest tiled product.
-template <Weights W, bool MANY, bool LO>
-constexpr int kProductLds = MANY ? std::max(Shape<W, MANY>::kWaves * 4 * kWave * 16, TiledProduct<W, 4, LO, kLines>::kBytes)
-                                 : Shape<W, MANY>::kWaves * 2 * kWave * 16;
+// LDS of a kernel: the wavefronts' stretches, or the activations of the largest tiled product.
+template <Weights W, bool MANY, bool LO, Read READ>
+constexpr int kProductLds = MANY && !windowed(READ) ? std::max(kStretches<W, MANY, READ>, TiledProduct<W, 4, LO, READ>::kBytes)
+                                                    : kStretches<W, MANY, READ>;
 
 template <Weights W, bool MANY, Read READ>
 __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWavesPerSimd)) void gate_up_kernel(ExpertArgs a)
 {
     typedef Shape<W, MANY> Sh;
-    __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, false>];
+    __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, false, READ>];
     __shared__ float scales[Sh::kWaves * kScaleFloats<W, 2>];
     const Entry en(a.plan, blockIdx.y);
     if constexpr (!MANY) {
         for (int r0 = 0; r0 < en.n; r0 += kTile)
             gate_up_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
-    } else if (!a.tiled || en.n <= 2 * kTile) {
+    } else if (windowed(READ) || !a.tiled || en.n <= 2 * kTile) {
         for (int r0 = 0; r0 < en.n; r0 += 2 * kTile) {
             if (en.n - r0 <= kTile)
                 gate_up_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
@@ -1189,8 +1290,9 @@ __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWaves
                 gate_up_stream<W, 2, Sh, READ>(a, en, r0, lds, scales);
         }
     } else if (static_cast<int>(blockIdx.x) * 4 * kTile < a.I) {
-        for (int r0 = 0; r0 < en.n; r0 += 4 * kTile)
-            gate_up_tiles<W, 4, READ>(a, en, r0, lds, scales);
+        if constexpr (!windowed(READ))
+            for (int r0 = 0; r0 < en.n; r0 += 4 * kTile)
+                gate_up_tiles<W, 4, READ>(a, en, r0, lds, scales);
     }
 }
 
@@ -1204,18 +1306,18 @@ __device__ __forceinline__ int second_tile(const ExpertArgs &a, int c0)
 }
 
 template <Weights W, Read READ>
-__device__ __forceinline__ void down_weights(const ExpertArgs &a, const Entry &en, int unit, float *scales,
+__device__ __forceinline__ void down_weights(const ExpertArgs &a, const Entry &en, int unit, char *window, float *scales,
                                              WeightRows<W, 2, READ> &rows)
 {
     const int c0 = min(unit * 2 * kTile, a.H - 1), c1 = second_tile(a, c0);
-    rows.rows_of(a.I, a.H - 1 - c0 - c1);
-    rows.scales_of(a, a.H - 1 - c0 - c1, scales);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int64_t row = en.ex * a.H + c0 + i * c1;
         rows.w[i] = static_cast<const char *>(a.w) + row * a.I * sizeof(typename WeightType<W>::type);
         rows.scales.row[i] = a.scales + row * a.nb;
     }
+    rows.rows_of(a.I, a.H - 1 - c0 - c1, window);
+    rows.scales_of(a, a.H - 1 - c0 - c1, scales);
 }
 
 __device__ __forceinline__ void store_y(const ExpertArgs &a, const Entry &en, int row, int unit, int column, float first,
@@ -1247,7 +1349,7 @@ __device__ __forceinline__ void down_stream(const ExpertArgs &a, const Entry &en
     typedef typename ActType<W>::type X;
     Product<W, 2, NT, W != kWF32, Sh::kRegs, READ> p;
     const Share my(Sh::kWaves, a.parts);
-    down_weights<W, READ>(a, en, my.unit, scales, p.rows);
+    down_weights<W, READ>(a, en, my.unit, lds + wave_id() * Sh::template kStretch<READ>, scales, p.rows);
     p.lo = static_cast<int64_t>(a.hI) * sizeof(X);
     p.x = h_from<W>(a, en.p0 + r0);
 #pragma unroll
@@ -1257,8 +1359,7 @@ __device__ __forceinline__ void down_stream(const ExpertArgs &a, const Entry &en
     }
     const int loads = (a.I + kLoadElems<W> - 1) / kLoadElems<W>;
     p.run(loads * my.part / a.parts, loads * (my.part + 1) / a.parts, a.I, a.stagger ? my.unit : 0);
-    join_parts<Sh::kWaves, NT>(p.acc, a.parts, reinterpret_cast<f32x4(*)[NT][2][kWave]>(lds),
-                           [&](int unit, int row, int column, const float (&v)[2]) {
+    join_parts<Sh::kWaves, NT, Sh::template kStretch<READ>>(p.acc, a.parts, lds, [&](int unit, int row, int column, const float (&v)[2]) {
         store_y(a, en, r0 + row, blockIdx.x * (Sh::kWaves / a.parts) + unit, column, v[0], v[1]);
     });
 }
@@ -1269,7 +1370,7 @@ __device__ __forceinline__ void down_tiles(const ExpertArgs &a, const Entry &en,
     typedef typename ActType<W>::type X;
     TiledProduct<W, NT, W != kWF32, READ> p;
     const int unit = blockIdx.x * 4 + wave_id(), lane = threadIdx.x & (kWave - 1);
-    down_weights<W, READ>(a, en, unit, scales, p.rows);
+    down_weights<W, READ>(a, en, unit, nullptr, scales, p.rows);
     p.lo = static_cast<int64_t>(a.hI) * sizeof(X);
     p.x = h_from<W>(a, en.p0 + r0);
     p.run(a.I, reinterpret_cast<u32x4 *>(lds), [&](int r) {
@@ -1286,13 +1387,13 @@ template <Weights W, bool MANY, Read READ>
 __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWavesPerSimd)) void down_kernel(ExpertArgs a)
 {
     typedef Shape<W, MANY> Sh;
-    __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, W != kWF32>];
+    __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, W != kWF32, READ>];
     __shared__ float scales[Sh::kWaves * kScaleFloats<W, 2>];
     const Entry en(a.plan, blockIdx.y);
     if constexpr (!MANY) {
         for (int r0 = 0; r0 < en.n; r0 += kTile)
             down_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
-    } else if (!a.tiled || en.n <= kTile) {
+    } else if (windowed(READ) || !a.tiled || en.n <= kTile) {
         for (int r0 = 0; r0 < en.n; r0 += 2 * kTile) {
             if (en.n - r0 <= kTile)
                 down_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
@@ -1300,12 +1401,13 @@ __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWaves
                 down_stream<W, 2, Sh, READ>(a, en, r0, lds, scales);
         }
     } else if (static_cast<int>(blockIdx.x) * 4 * 2 * kTile < a.H) {
-        for (int r0 = 0; r0 < en.n; r0 += 4 * kTile) {
-            if (en.n - r0 <= 2 * kTile)
-                down_tiles<W, 2, READ>(a, en, r0, lds, scales);
-            else
-                down_tiles<W, 4, READ>(a, en, r0, lds, scales);
-        }
+        if constexpr (!windowed(READ))
+            for (int r0 = 0; r0 < en.n; r0 += 4 * kTile) {
+                if (en.n - r0 <= 2 * kTile)
+                    down_tiles<W, 2, READ>(a, en, r0, lds, scales);
+                else
+                    down_tiles<W, 4, READ>(a, en, r0, lds, scales);
+            }
     }
 }
 
@@ -1347,10 +1449,10 @@ __global__ __launch_bounds__(kDirectThreads) void down_merge_kernel(ExpertArgs a
         const int64_t row = static_cast<int64_t>(a.plan.act[i]) * a.H + c0;
         for (int r0 = 0; r0 < n; r0 += kTile) {
             P p;
-            p.rows.rows_of(a.I, a.H - 1 - c0);
-            p.rows.scales_of(a, a.H - 1 - c0, scales);
             p.rows.w[0] = static_cast<const char *>(a.w) + row * a.I * sizeof(typename P::Wt);
             p.rows.scales.row[0] = a.scales + row * a.nb;
+            p.rows.rows_of(a.I, a.H - 1 - c0, nullptr);
+            p.rows.scales_of(a, a.H - 1 - c0, scales);
             p.lo = static_cast<int64_t>(a.hI) * sizeof(typename P::X);
             p.x = h_from<W>(a, p0 + r0);
             const int r = min(m, n - 1 - r0), tok = a.plan.token[p0 + r0 + r];
@@ -1499,10 +1601,12 @@ size_t plan_lds(int E) { return sizeof(uint16_t) * kPlanWaves * static_cast<size
 // Wavefronts that share a unit of weight rows: more of them while the chip has not several rounds of wavefronts (T8 H4096
 // I2048 E128 K8 FP8 with four against two: 189 -> 181 us and 112 -> 106; T64 H7168 I1024 E128 K8 down, 28672 units, with four
 // against one: 333 -> 388), as long as each keeps four loads or more (T32 H1024 I512 E64 K4 down with two: 23 -> 32 us).
-int share_parts(int64_t units, int64_t loads, int waves)
+// Through the window each of them reads a line more, so they are fewer (T133 H2056 I1399 E64 K2 with the others' limits 292
+// us, with 16 loads 256, with 8192 units too 234).
+int share_parts(int64_t units, int64_t loads, int waves, bool window)
 {
     int parts = 1;
-    while (parts < waves && units * parts < 24576 && loads >= 8 * parts)
+    while (parts < waves && units * parts < (window ? 8192 : 24576) && loads >= (window ? 16 : 8) * parts)
         parts *= 2;
     return parts;
 }
@@ -1523,13 +1627,22 @@ constexpr int64_t kDirectLoads = 64;
 // E64 K8, 25 tokens an expert: 446 -> 568 us and 335 -> 290).
 constexpr int64_t kTiledGroups = 512;
 
+// Rows off the cache lines go through the window where there is much to read (kWindowWork loads of all units, 100 MB) for
+// few tokens an expert: a wavefront's stretch costs a line more that way, and a step through LDS, which the tiled product
+// and small calls do not earn back (T133 H2056 I1399 E64 K2 304 -> 234 us, T64 H7170 I1026 E64 K8 700 -> 564, T8 H2057 I1399
+// E64 K4 float32 197 -> 177; with the window T4 H1000 I500 E16 K4 22 -> 42, T200 H4100 I2050 E16 K4 309 -> 354).
+constexpr int64_t kWindowWork = 24576;
+
 template <Weights W>
-Read read_of(const void *w, int64_t row_bytes, const void *x, int64_t x_row_bytes)
+Read read_of(const void *w, int64_t row_bytes, const void *x, int64_t x_row_bytes, bool window)
 {
     const uintptr_t at = reinterpret_cast<uintptr_t>(w) | static_cast<uintptr_t>(row_bytes);
-    if (W == kWBf16 && (at | reinterpret_cast<uintptr_t>(x) | static_cast<uintptr_t>(x_row_bytes)) % 4)
-        return kOdd;
-    return at % 128 == 0 ? kLines : kWords;
+    const bool odd_x = W == kWBf16 && (reinterpret_cast<uintptr_t>(x) | static_cast<uintptr_t>(x_row_bytes)) % 4;
+    if (at % 128 == 0 && !odd_x)
+        return kLines;
+    if (window)
+        return odd_x ? kWindowOdd : kWindow;
+    return odd_x || (W == kWBf16 && at % 4) ? kOdd : kWords;
 }
 
 template <Weights W, bool MANY>
@@ -1546,21 +1659,34 @@ void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t
     a.stagger = stagger(int64_t{a.H} * size);
     int64_t units = ceil_div(a.I, kTile);
     a.tiled = MANY && units / 4 * used >= kTiledGroups;
-    a.parts = share_parts(units * used, ceil_div(a.H, kLoadElems<W>), Sh::kWaves);
+    int64_t loads = ceil_div(a.H, kLoadElems<W>);
+    const bool few = a.T * a.K <= kTile * used;
+    Read read = read_of<W>(a.w, int64_t{a.H} * size, a.x, int64_t{a.H} * sizeof(typename ActType<W>::type),
+                           (few || !a.tiled) && units * used * loads >= kWindowWork);
+    a.parts = share_parts(units * used, loads, Sh::kWaves, windowed(read));
     dim3 grid(static_cast<unsigned>(ceil_div(units, Sh::kWaves / a.parts)), static_cast<unsigned>(used));
-    Read read = read_of<W>(a.w, int64_t{a.H} * size, a.x, int64_t{a.H} * sizeof(typename ActType<W>::type));
+#define MOE_FEW_PRODUCT(KERNEL, READ) hipLaunchKernelGGL((KERNEL<W, MANY, READ>), grid, dim3(Sh::kThreads), 0, stream, a)
     if (read == kLines)
-        hipLaunchKernelGGL((gate_up_kernel<W, MANY, kLines>), grid, dim3(Sh::kThreads), 0, stream, a);
+        MOE_FEW_PRODUCT(gate_up_kernel, kLines);
+    else if (read == kWindow)
+        MOE_FEW_PRODUCT(gate_up_kernel, kWindow);
     else if (W != kWBf16 || read == kWords)
-        hipLaunchKernelGGL((gate_up_kernel<W, MANY, kWords>), grid, dim3(Sh::kThreads), 0, stream, a);
-    else if constexpr (W == kWBf16)
-        hipLaunchKernelGGL((gate_up_kernel<W, MANY, kOdd>), grid, dim3(Sh::kThreads), 0, stream, a);
+        MOE_FEW_PRODUCT(gate_up_kernel, kWords);
+    else if constexpr (W == kWBf16) {
+        if (read == kOdd)
+            MOE_FEW_PRODUCT(gate_up_kernel, kOdd);
+        else
+            MOE_FEW_PRODUCT(gate_up_kernel, kWindowOdd);
+    }
     a.w = w.down;
     a.scales = w.down_scales;
     a.nb = W == kWFp8 ? a.I / w.block : 0;
     a.stagger = stagger(int64_t{a.I} * size);
-    read = read_of<W>(a.w, int64_t{a.I} * size, nullptr, 0);
-    if (!MANY && used * ceil_div(a.I, kLoadElems<W>) <= kDirectLoads) {
+    units = ceil_div(a.H, 2 * kTile);
+    a.tiled = MANY && units / 4 * used >= kTiledGroups;
+    loads = ceil_div(a.I, kLoadElems<W>);
+    if (!MANY && used * loads <= kDirectLoads) {
+        read = read_of<W>(a.w, int64_t{a.I} * size, nullptr, 0, false);
         grid = dim3(static_cast<unsigned>(ceil_div(a.H, kTile)));
         if (read == kLines)
             hipLaunchKernelGGL((down_merge_kernel<W, kLines>), grid, dim3(kDirectThreads), 0, stream, a);
@@ -1570,16 +1696,18 @@ void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t
             hipLaunchKernelGGL((down_merge_kernel<W, kOdd>), grid, dim3(kDirectThreads), 0, stream, a);
         return;
     }
-    units = ceil_div(a.H, 2 * kTile);
-    a.tiled = MANY && units / 4 * used >= kTiledGroups;
-    a.parts = share_parts(units * used, ceil_div(a.I, kLoadElems<W>), Sh::kWaves);
+    read = read_of<W>(a.w, int64_t{a.I} * size, nullptr, 0, (few || !a.tiled) && units * used * loads >= kWindowWork);
+    a.parts = share_parts(units * used, loads, Sh::kWaves, windowed(read));
     grid = dim3(static_cast<unsigned>(ceil_div(units, Sh::kWaves / a.parts)), static_cast<unsigned>(used));
     if (read == kLines)
-        hipLaunchKernelGGL((down_kernel<W, MANY, kLines>), grid, dim3(Sh::kThreads), 0, stream, a);
+        MOE_FEW_PRODUCT(down_kernel, kLines);
+    else if (read == kWindow)
+        MOE_FEW_PRODUCT(down_kernel, kWindow);
     else if (W != kWBf16 || read == kWords)
-        hipLaunchKernelGGL((down_kernel<W, MANY, kWords>), grid, dim3(Sh::kThreads), 0, stream, a);
+        MOE_FEW_PRODUCT(down_kernel, kWords);
     else if constexpr (W == kWBf16)
-        hipLaunchKernelGGL((down_kernel<W, MANY, kOdd>), grid, dim3(Sh::kThreads), 0, stream, a);
+        MOE_FEW_PRODUCT(down_kernel, kOdd);
+#undef MOE_FEW_PRODUCT
     hipLaunchKernelGGL(merge_kernel, dim3(static_cast<unsigned>(ceil_div(a.H, kMergeThreads)), static_cast<unsigned>(a.T)),
                        dim3(kMergeThreads), 0, stream, a);
 }
