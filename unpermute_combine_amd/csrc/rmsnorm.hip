@@ -192,29 +192,34 @@ __global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(NormArgs a)
 }
 
 // ---------------------------------------------------------------- rows in registers
-// 8 consecutive elements of a row; the address need not be aligned beyond its element (gfx950's global
-// memory instructions take any), so odd lengths and offsets use the same wide accesses. Elements past
-// the row's end read as 0 and are not written.
+// 8 consecutive elements of a row of 8 or more; the address need not be aligned beyond its element (gfx950's global memory
+// instructions take any), so odd lengths and offsets use the same wide accesses. Vectors past the row's end read as 0 and
+// are not written.
 template <typename X>
 struct Raw8 {
     u32x4 v[sizeof(X) / 2];
 };
 
-// TAIL: the row's last vector may be partial (its length is no multiple of 8).
-template <bool TAIL, typename X>
+// Where vector e of a row is. TAIL: the row's length is no multiple of 8; its last vector then ends with the row, and the
+// elements it shares with the one before (`shared` of them) count once in sums and are stored twice, the same: one access
+// in place of seven dependent ones (T16384 H7167 bf16 271 -> 208 us, backward of T8192 H7167 159 -> 115).
+struct Vec {
+    int at, shared;
+};
+
+template <bool TAIL>
+__device__ __forceinline__ Vec vec(int e, int H)
+{
+    const int at = TAIL && e < H ? min(e, H - 8) : e;
+    return Vec{at, e - at};
+}
+
+template <typename X>
 __device__ __forceinline__ Raw8<X> load_raw(const X *row, int e, int H)
 {
     Raw8<X> q{};
-    if (TAIL ? e + 8 <= H : e < H) {
+    if (e < H)
         __builtin_memcpy(&q, row + e, sizeof(q));
-    } else if (TAIL && e < H) {
-        X t[8] = {};
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (e + i < H)
-                t[i] = row[e + i];
-        __builtin_memcpy(&q, t, sizeof(q));
-    }
     return q;
 }
 
@@ -237,28 +242,21 @@ __device__ __forceinline__ void narrow(const float (&f)[8], Raw8<uint16_t> &q)
 
 __device__ __forceinline__ void narrow(const float (&f)[8], Raw8<float> &q) { __builtin_memcpy(&q, f, sizeof(q)); }
 
-template <bool TAIL, typename X>
+template <typename X>
 __device__ __forceinline__ void store8(X *row, int e, int H, const float (&f)[8])
 {
     Raw8<X> q;
     narrow(f, q);
-    if (TAIL ? e + 8 <= H : e < H) {
+    if (e < H)
         __builtin_memcpy(row + e, &q, sizeof(q));
-    } else if (TAIL) {
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (e + i < H)
-                store_f(row + e + i, f[i]);
-    }
 }
 
-template <bool TAIL>
 __device__ __forceinline__ void load_weight8(const Row &w, int e, int H, float (&f)[8])
 {
     if (w.bf16)
-        widen(load_raw<TAIL>(static_cast<const uint16_t *>(w.p), e, H), f);
+        widen(load_raw(static_cast<const uint16_t *>(w.p), e, H), f);
     else
-        widen(load_raw<TAIL>(static_cast<const float *>(w.p), e, H), f);
+        widen(load_raw(static_cast<const float *>(w.p), e, H), f);
 }
 
 // Sum over the workgroup in every thread, in a fixed order, with one barrier: consecutive calls alternate
@@ -302,19 +300,23 @@ __global__ __launch_bounds__(NV == 2 ? 512 : 1024) void add_rmsnorm_regs_kernel(
     Raw8<S> r[NV];
     float w[NV][8];
     const int block = static_cast<int>(a.block);
+    Vec v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        v[i] = vec<TAIL>(e0 + i * step, H);
     int turn = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
         const X *xs = static_cast<const X *>(a.x) + t * H;
         const S *rs = a.residual ? static_cast<const S *>(a.residual) + t * H : nullptr;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            x[i] = load_raw<TAIL>(xs, e0 + i * step, H);
+            x[i] = load_raw(xs, v[i].at, H);
             if (rs)
-                r[i] = load_raw<TAIL>(rs, e0 + i * step, H);
+                r[i] = load_raw(rs, v[i].at, H);
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            load_weight8<TAIL>(a.weight, e0 + i * step, H, w[i]);
+            load_weight8(a.weight, v[i].at, H, w[i]);
         float h[NV][8];
         float ss = 0.0f;
 #pragma unroll
@@ -329,7 +331,7 @@ __global__ __launch_bounds__(NV == 2 ? 512 : 1024) void add_rmsnorm_regs_kernel(
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                ss = fmaf(h[i][j], h[i][j], ss);
+                ss = !TAIL || j >= v[i].shared ? fmaf(h[i][j], h[i][j], ss) : ss;
         }
         const float s = 1.0f / sqrtf(block_sum1(ss, turn) / static_cast<float>(H) + a.eps);
         if (a.rstd && threadIdx.x == 0)
@@ -338,7 +340,7 @@ __global__ __launch_bounds__(NV == 2 ? 512 : 1024) void add_rmsnorm_regs_kernel(
         if (a.sum_out) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                store8<TAIL>(static_cast<S *>(a.sum_out) + t * H, e0 + i * step, H, h[i]);
+                store8(static_cast<S *>(a.sum_out) + t * H, v[i].at, H, h[i]);
         }
         float top = 0.0f;
 #pragma unroll
@@ -357,7 +359,7 @@ __global__ __launch_bounds__(NV == 2 ? 512 : 1024) void add_rmsnorm_regs_kernel(
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int e = e0 + i * step;
+            const int e = v[i].at;
             if (OUT != kRows) {
                 float scale = row_scale;
                 if (OUT == kBlocks) {  // H is a multiple of 8 here: no partial vectors
@@ -377,20 +379,14 @@ __global__ __launch_bounds__(NV == 2 ? 512 : 1024) void add_rmsnorm_regs_kernel(
                 q.x = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
                 lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
                 q.y = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], lo, true);
-                if (TAIL ? e + 8 <= H : e < H) {
+                if (e < H)
                     __builtin_memcpy(a.q + t * H + e, &q, sizeof(q));
-                } else if (TAIL) {
-#pragma unroll
-                    for (int j = 0; j < 7; ++j)
-                        if (e + j < H)
-                            a.q[t * H + e + j] = static_cast<uint8_t>((j < 4 ? q.x >> (8 * j) : q.y >> (8 * (j - 4))) & 0xffu);
-                }
             }
             if (OUT == kRows || a.out.p) {
                 if (a.out.bf16)
-                    store8<TAIL>(static_cast<uint16_t *>(a.out.p) + t * H, e, H, h[i]);
+                    store8(static_cast<uint16_t *>(a.out.p) + t * H, e, H, h[i]);
                 else
-                    store8<TAIL>(static_cast<float *>(a.out.p) + t * H, e, H, h[i]);
+                    store8(static_cast<float *>(a.out.p) + t * H, e, H, h[i]);
             }
         }
     }
@@ -479,15 +475,19 @@ __global__ __launch_bounds__(512) void rmsnorm_backward_regs_kernel(const G *dou
     Raw8<D> dq[NV];
     float w[NV][8], dw[NV][8];
     int64_t t = blockIdx.x;
+    Vec vs[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        vs[i] = vec<TAIL>(e0 + i * step, H);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        gq[i] = load_raw<TAIL>(dout + t * H, e0 + i * step, H);
-        hq[i] = load_raw<TAIL>(h + t * H, e0 + i * step, H);
+        gq[i] = load_raw(dout + t * H, vs[i].at, H);
+        hq[i] = load_raw(h + t * H, vs[i].at, H);
     }
     float s = rstd[t];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        load_weight8<TAIL>(weight, e0 + i * step, H, w[i]);
+        load_weight8(weight, vs[i].at, H, w[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             dw[i][j] = 0.0f;
@@ -496,7 +496,7 @@ __global__ __launch_bounds__(512) void rmsnorm_backward_regs_kernel(const G *dou
         if (d_sum) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                dq[i] = load_raw<TAIL>(d_sum + t * H, e0 + i * step, H);
+                dq[i] = load_raw(d_sum + t * H, vs[i].at, H);
         }
         float a[NV][8], x[NV][8];
         float ah = 0.0f;
@@ -508,7 +508,7 @@ __global__ __launch_bounds__(512) void rmsnorm_backward_regs_kernel(const G *dou
             for (int j = 0; j < 8; ++j) {
                 dw[i][j] = fmaf(a[i][j] * s, x[i][j], dw[i][j]);
                 a[i][j] *= w[i][j];
-                ah = fmaf(a[i][j], x[i][j], ah);
+                ah = !TAIL || j >= vs[i].shared ? fmaf(a[i][j], x[i][j], ah) : ah;
             }
         }
         const int64_t now = t;
@@ -517,8 +517,8 @@ __global__ __launch_bounds__(512) void rmsnorm_backward_regs_kernel(const G *dou
         if (t < T) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                gq[i] = load_raw<TAIL>(dout + t * H, e0 + i * step, H);
-                hq[i] = load_raw<TAIL>(h + t * H, e0 + i * step, H);
+                gq[i] = load_raw(dout + t * H, vs[i].at, H);
+                hq[i] = load_raw(h + t * H, vs[i].at, H);
             }
             s = rstd[t];
         }
@@ -536,18 +536,21 @@ __global__ __launch_bounds__(512) void rmsnorm_backward_regs_kernel(const G *dou
                 for (int j = 0; j < 8; ++j)
                     v[j] += f[j];
             }
-            store8<TAIL>(dx + now * H, e0 + i * step, H, v);
+            store8(dx + now * H, vs[i].at, H, v);
         }
     }
     if (part) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            store8<TAIL>(part + static_cast<int64_t>(blockIdx.x) * H, e0 + i * step, H, dw[i]);
+            store8(part + static_cast<int64_t>(blockIdx.x) * H, vs[i].at, H, dw[i]);
     }
 }
 
 // rmsnorm_dweight_sum_kernel has 32 threads a column, and a grid fewer than 2^32.
 constexpr int64_t kMaxRow = 1 << 26;
+
+// Rows of a vector or more, up to NV of them a thread, are kept in registers.
+bool in_registers(int64_t H, int64_t threads, int64_t nv) { return H >= 8 && H <= 8 * nv * threads; }
 
 bool row_type(moe_dtype d) { return d == MOE_F32 || d == MOE_BF16; }
 
@@ -587,7 +590,7 @@ template <typename X, typename S>
 moe_status launch_norm_xs(const NormArgs &a, hipStream_t stream)
 {
     const bool blocks = a.q && pow2(a.block) && a.block >= 8 && a.block <= 8 * kWave;
-    if (a.H > 8 * 4 * 1024 || (a.q && !blocks && a.block != a.H))
+    if (!in_registers(a.H, 1024, 4) || (a.q && !blocks && a.block != a.H))
         hipLaunchKernelGGL((add_rmsnorm_kernel<X, S>), dim3(row_blocks(a.T)), dim3(kNormThreads), 0, stream, a);
     else if (blocks)
         launch_norm_regs<X, S, kBlocks, false>(a, stream);
@@ -622,7 +625,7 @@ moe_status launch_backward(const void *dout, const void *h, Row weight, const fl
     const S *hs = static_cast<const S *>(h);
     const D *ds = static_cast<const D *>(d_sum);
     const int64_t vecs = ceil_div(H, 8), ranges = dw_ranges(T);
-    if (vecs <= 4 * 512) {
+    if (in_registers(H, 512, 4)) {
         const int nv = vecs <= 256 ? 1 : vecs <= 2 * 512 ? 2 : 4;
         const dim3 grid(static_cast<unsigned>(ranges)), block(static_cast<unsigned>(ceil_div(ceil_div(vecs, nv), kWave) * kWave));
 #define MOE_BACKWARD_LAUNCH(NV, TAIL)                                                                                  \
