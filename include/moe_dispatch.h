@@ -402,8 +402,11 @@ moe_status moe_add_rmsnorm(const void *x, moe_dtype x_dt, const void *residual, 
                            void *sum_out, void *out, moe_dtype out_dt, float *rstd, hipStream_t stream);
 
 /* moe_add_rmsnorm with its output as the rows of the FP8 dispatch: per block of `block` consecutive
- * elements the scale and codes of moe_quantize_fp8, taken from the float32 values of out (one rounding,
- * not that of out's type first).
+ * elements the scale of moe_quantize_fp8, taken from the float32 values of out (not those of out's type), and
+ * the codes of 448 h[t,j] weight[j] / max_k |h[t,k] weight[k]|, in which s has no part: with h in float32, that
+ * in float64 up to one rounding to float32. They are moe_quantize_fp8's of the float32 values but for about one
+ * in a million, whose value float32's roundings carry over a boundary between two codes there. Blocks whose
+ * scale is under 2^-100 have moe_quantize_fp8's codes.
  *   q [T, H] E4M3 codes, scales [T, H/block] float32; out [T, H] (out_dt) or NULL: the rows themselves
  *   too (the router's input). block >= 1 must divide H (else MOE_ERR_INVALID). A block that holds a NaN
  *   or an infinity has unspecified codes. The other arguments as in moe_add_rmsnorm; q and scales overlap

@@ -136,6 +136,17 @@ def e4m3(q):
     return q.view(torch.float8_e4m3fn).double()
 
 
+def codes_of(m, h, w, rows, sc, block):
+    """The codes by the definition: of 448 h w / max |h w| over the block, h the float32 sum, in 64 bits up to one rounding
+    to float32; blocks of zeros and those whose scale is under 2^-100 as quantize_fp8 of the float32 rows."""
+    T, H = rows.shape
+    p = (h.double() * w.double()).view(T, -1, block)
+    top = p.abs().amax(2, keepdim=True)
+    codes = (p * (448 / top)).float().to(torch.float8_e4m3fn).view(torch.uint8).view(T, H)
+    by_ratio = ((rows.view(T, -1, block).abs().amax(2) > 0) & (sc >= 2.0 ** -100)).repeat_interleave(block, 1)
+    return torch.where(by_ratio, codes, m.quantize_fp8(rows, block)[0])
+
+
 @pytest.mark.parametrize("T,H,block", [(1, 128, 128), (64, 4096, 128), (33, 7168, 128), (7, 1024, 1024), (5, 2048, 8),
                                        (4, 1000, 8), (3, 1000, 40), (6, 999, 27), (3, 77, 77), (2, 20480, 128),
                                        (9, 4096, 256), (5, 4096, 512), (5, 4096, 4096), (3, 65, 1), (3, 40960, 64),
@@ -160,9 +171,9 @@ def test_fp8(m, T, H, block, dt, s_dt):
     assert_within(rows, n, b * n.abs(), "rows")
     assert_within(rstd, s, b * s, "rstd")
     assert torch.equal(total, (x.float() + r.float()).to(s_dt))
-    # bit for bit the quantization of the float32 rows
-    q2, sc2 = m.quantize_fp8(rows, block)
-    assert torch.equal(q, q2) and torch.equal(sc, sc2)
+    # bit for bit the definition's codes, and the scales of the float32 rows
+    assert torch.equal(sc, m.quantize_fp8(rows, block)[1])
+    assert torch.equal(q, codes_of(m, x.float() + r.float(), w, rows, sc, block))
     # and without the rows, in place, the same
     r2 = r.clone()
     q3, sc3, total3, none, none2 = m.add_rmsnorm_fp8(x, w, residual=r2, block=block, sum_out=r2)
@@ -297,7 +308,7 @@ def test_norm_to_fp8_dispatch_and_back(m):
 
 @pytest.mark.parametrize("block", [8, 128, 40, 640])
 def test_fp8_blocks_of_any_size_of_values(m, block):
-    """Scales from float32's subnormals to its largest values, and zeros of both signs: the codes of quantize_fp8."""
+    """Scales from float32's subnormals to its largest values, and zeros of both signs."""
     T, H = 64, 640
     x = draw(1, T, H)
     x[:, 3::16], x[:, 5::16] = 0.0, -0.0
@@ -307,8 +318,21 @@ def test_fp8_blocks_of_any_size_of_values(m, block):
         w = w.clamp(max=3e38 / 8)  # |x| sqrt(mean x^2) stays under 8: no infinities
         q, sc, _, rows, _ = m.add_rmsnorm_fp8(x, w, block=block, want_rows=True, out_dtype=F32)
         assert bool(torch.isfinite(rows).all())
-        q2, sc2 = m.quantize_fp8(rows, block)
-        assert torch.equal(sc, sc2) and torch.equal(q, q2)
+        assert torch.equal(sc, m.quantize_fp8(rows, block)[1])
+        assert torch.equal(q, codes_of(m, x, w, rows, sc, block))
+
+
+@pytest.mark.parametrize("T,H,block", [(4096, 4096, 128), (2100, 2048, 512), (512, 7168, 7168), (300, 4800, 96)])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_fp8_codes_beside_rounding_boundaries(m, T, H, block, dt):
+    """Enough values that hundreds of them lie within float32's roundings of a boundary between two codes."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    x, r = torch.randn(T, H, generator=g, device=DEV).to(dt), torch.randn(T, H, generator=g, device=DEV).to(dt)
+    w = draw(3, H) + 1
+    q, sc, _, rows, _ = m.add_rmsnorm_fp8(x, w, residual=r, block=block, want_rows=True, out_dtype=F32)
+    assert torch.equal(q, codes_of(m, x.float() + r.float(), w, rows, sc, block))
+    assert int((q != m.quantize_fp8(rows, block)[0]).sum()) < T * H / 1e5
 
 
 def test_more_rows_than_a_grid_has_workgroups(m):
@@ -327,5 +351,4 @@ def test_more_rows_than_a_grid_has_workgroups(m):
     assert_within(dx, want, bound * (1 + U) + U * want.abs(), "dx")
     assert_within(dw, want_dw, dw_roundings(T) * U * mag, "dweight")
     q, sc = m.add_rmsnorm_fp8(x, w, residual=r, block=6)[:2]
-    q2, sc2 = m.quantize_fp8(out, 6)
-    assert torch.equal(q, q2) and torch.equal(sc, sc2)
+    assert torch.equal(sc, m.quantize_fp8(out, 6)[1]) and torch.equal(q, codes_of(m, total, w, out, sc, 6))

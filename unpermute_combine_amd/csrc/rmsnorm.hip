@@ -3,11 +3,13 @@
 //
 //   h[t,j] = x[t,j] + residual[t,j]          s[t] = 1 / sqrt(mean_j h[t,j]^2 + eps)
 //   out[t,j] = h[t,j] * s[t] * weight[j]
-// FP8: the blocks of out quantized as moe_quantize_fp8 does, from the float32 values of out.
+// FP8, for each block of out: scale = max |out| / 448 in float32, and since s is common to the block, the codes of
+//   448 h[t,j] weight[j] / max_k |h[t,k] weight[k]|
+// in float64 up to one rounding to float32 and that to E4M3: neither s's rounding nor the scale's moves a code.
 // Backward, g = d out, a = g * weight, m[t] = s[t]^2 * mean_j a[t,j] h[t,j]:
 //   dx[t,j] = s[t] * (a[t,j] - h[t,j] * m[t]) (+ d_sum[t,j]),   dweight[j] = sum_t g[t,j] h[t,j] s[t]
 //
-// Everything between the loads and the one rounding of each output is float32.
+// Otherwise everything between the loads and the one rounding of each output is float32.
 #include <cmath>
 
 #include "moe_common.h"
@@ -86,23 +88,79 @@ __device__ __forceinline__ float lanes_max(float v, int lanes)
 
 __device__ __forceinline__ float wave_max(float v) { return lanes_max(v, kWave); }
 
-// v[i] / scale for eight values, each the correctly rounded quotient, with one division: with y the correctly
-// rounded reciprocal, q = v y corrected by its exact remainder, q + (v - q scale) y, is v / scale rounded once
-// (Markstein's theorem; the range keeps the reciprocal, and every remainder that can decide a code, normal).
-__device__ __forceinline__ void divide8(const float (&v)[8], float scale, float (&c)[8])
+__device__ __forceinline__ double lanes_max(double v, int lanes)
 {
-    if (scale >= 0x1p-90f && scale <= 0x1p+90f) {
-        const float y = 1.0f / scale;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float q = v[j] * y;
-            c[j] = copysignf(fmaf(fmaf(-q, scale, v[j]), y, q), v[j]);  // the sums above lose a -0
-        }
-    } else {
+    for (int d = 1; d < lanes; d *= 2)
+        v = fmax(v, __shfl_xor(v, d));
+    return v;
+}
+
+// A block's scale, and how its codes come of it.
+struct BlockScale {
+    float scale, to_code;
+    bool ratio;  // codes by the ratio to the block's largest value; else, of zeros and near float32's subnormals, by the scale
+    __device__ __forceinline__ explicit BlockScale(float amax)
+        : scale(amax > 0.0f ? amax / kE4M3Max : 1.0f), to_code(__builtin_amdgcn_rcpf(scale)), ratio(amax > 0.0f && scale >= 0x1p-100f)
+    {
+    }
+};
+
+__device__ __forceinline__ uint2 codes8(const float (&c)[8])
+{
+    uint2 q;
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+    q.x = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
+    q.y = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], lo, true);
+    return q;
+}
+
+// Codes of eight float32 values n = h s w, and whether all of them are sure: n and the block's largest have two roundings
+// each, the scale one, its reciprocal two and the products two, 9 of 2^-24, so where 2^-20 more and less have the same code,
+// that is the ratio's own. (Values that float32 rounds as subnormals have the code 0 in a block of such a scale.)
+__device__ __forceinline__ uint2 sure_codes8(const float (&n)[8], const BlockScale &b, bool &sure)
+{
+    const float lower = b.to_code * (1.0f - 0x1p-20f), upper = b.to_code * (1.0f + 0x1p-20f);
+    float less[8], more[8];
+    if (!b.ratio) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            c[j] = v[j] / scale;
+            less[j] = n[j] / b.scale;
+        sure = true;
+        return codes8(less);
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        less[j] = n[j] * lower;
+        more[j] = n[j] * upper;
+    }
+    const uint2 q = codes8(less), r = codes8(more);
+    sure = q.x == r.x && q.y == r.y;
+    return q;
+}
+
+// The codes by the definition: about 1 wavefront in 100 has a value that is not sure.
+__device__ __forceinline__ double max8(const float (&h)[8], const float (&w)[8])
+{
+    double top = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        top = fmax(top, fabs(static_cast<double>(h[j]) * static_cast<double>(w[j])));
+        __builtin_amdgcn_sched_barrier(0);  // seldom run: few registers matter more than its time
+    }
+    return top;
+}
+
+__device__ __forceinline__ uint2 exact_codes8(const float (&h)[8], const float (&w)[8], double top)
+{
+    const double to_code = static_cast<double>(kE4M3Max) / top;
+    float c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        c[j] = static_cast<float>(static_cast<double>(h[j]) * static_cast<double>(w[j]) * to_code);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    return codes8(c);
 }
 
 // Sum over the workgroup in every thread, in a fixed order.
@@ -156,18 +214,21 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, int64_t t)
         const int64_t nb = a.H / a.block;
         for (int64_t b = threadIdx.x / kWave; b < nb; b += kNormWaves) {
             float amax = 0.0f;
+            double top = 0.0;
             for (int64_t j = b * a.block + lane; j < (b + 1) * a.block; j += kWave) {
-                const float h = r ? load_f(x + j) + load_f(r + j) : load_f(x + j);
-                amax = fmaxf(amax, fabsf(h * s * a.weight[j]));
+                const float h = r ? load_f(x + j) + load_f(r + j) : load_f(x + j), w = a.weight[j];
+                amax = fmaxf(amax, fabsf(h * s * w));
+                top = fmax(top, fabs(static_cast<double>(h) * static_cast<double>(w)));
             }
-            amax = wave_max(amax);
-            const float scale = amax > 0.0f ? amax / kE4M3Max : 1.0f;
+            const BlockScale block(wave_max(amax));
+            const double to_code = static_cast<double>(kE4M3Max) / lanes_max(top, kWave);
             if (lane == 0)
-                a.scales[t * nb + b] = scale;
+                a.scales[t * nb + b] = block.scale;
             for (int64_t j = b * a.block + lane; j < (b + 1) * a.block; j += kWave) {
-                const float h = r ? load_f(x + j) + load_f(r + j) : load_f(x + j);
-                const float n = h * s * a.weight[j];
-                a.q[t * a.H + j] = static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(n / scale, 0.0f, 0, false));
+                const float h = r ? load_f(x + j) + load_f(r + j) : load_f(x + j), w = a.weight[j], n = h * s * w;
+                const float c = block.ratio ? static_cast<float>(static_cast<double>(h) * static_cast<double>(w) * to_code)
+                                            : n / block.scale;
+                a.q[t * a.H + j] = static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, 0.0f, 0, false));
                 if (a.out.p)
                     a.out.set(t * a.H + j, n);
                 if (so)
@@ -274,16 +335,17 @@ __device__ __forceinline__ float block_sum1(float v, int turn)
     return s;
 }
 
-__device__ __forceinline__ float block_max1(float v, int turn)
+template <typename F>
+__device__ __forceinline__ F block_max1(F v, int turn)
 {
-    __shared__ float sh[2][16];
-    v = wave_max(v);
+    __shared__ F sh[2][16];
+    v = lanes_max(v, kWave);
     if ((threadIdx.x & (kWave - 1)) == 0)
         sh[turn][threadIdx.x / kWave] = v;
     __syncthreads();
-    float s = 0.0f;
+    F s = 0;
     for (int w = 0; w < static_cast<int>(blockDim.x) / kWave; ++w)
-        s = fmaxf(s, sh[turn][w]);
+        s = s > sh[turn][w] ? s : sh[turn][w];
     return s;
 }
 
@@ -336,58 +398,78 @@ __global__ __launch_bounds__(NV == 2 ? 512 : 1024) void add_rmsnorm_regs_kernel(
         const float s = 1.0f / sqrtf(block_sum1(ss, turn) / static_cast<float>(H) + a.eps);
         if (a.rstd && threadIdx.x == 0)
             a.rstd[t] = s;
-        float row_scale = 1.0f;
         if (a.sum_out) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 store8(static_cast<S *>(a.sum_out) + t * H, v[i].at, H, h[i]);
         }
-        float top = 0.0f;
+        auto values = [&](int i, float (&n)[8]) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                h[i][j] = h[i][j] * s * w[i][j];
-                if (OUT == kWholeRow)
-                    top = fmaxf(top, fabsf(h[i][j]));
-            }
+            for (int j = 0; j < 8; ++j)
+                n[j] = h[i][j] * s * w[i][j];
+        };
+        uint2 q[NV];
         if (OUT == kWholeRow) {
-            top = block_max1(top, turn);
-            row_scale = top > 0.0f ? top / kE4M3Max : 1.0f;
+            float top = 0.0f, n[8];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                values(i, n);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    top = fmaxf(top, fabsf(n[j]));
+            }
+            const BlockScale scale(block_max1(top, turn));
             if (threadIdx.x == 0)
-                a.scales[t] = row_scale;
+                a.scales[t] = scale.scale;
+            bool sure = true;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                bool one;
+                values(i, n);
+                q[i] = sure_codes8(n, scale, one);
+                sure = sure && one;
+            }
+            if (__syncthreads_or(!sure)) {
+                double exact = 0.0;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    exact = fmax(exact, max8(h[i], w[i]));
+                exact = block_max1(exact, turn);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    q[i] = exact_codes8(h[i], w[i], exact);
+            }
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = v[i].at;
-            if (OUT != kRows) {
-                float scale = row_scale;
-                if (OUT == kBlocks) {  // H is a multiple of 8 here: no partial vectors
-                    float amax = 0.0f;
+            float n[8];
+            values(i, n);
+            if (OUT == kBlocks) {  // H is a multiple of 8 here: no partial vectors
+                float amax = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        amax = fmaxf(amax, fabsf(h[i][j]));
-                    amax = lanes_max(amax, block / 8);
-                    scale = amax > 0.0f ? amax / kE4M3Max : 1.0f;
-                    if (e < H && e % block == 0)
-                        a.scales[t * (H / block) + e / block] = scale;
+                for (int j = 0; j < 8; ++j)
+                    amax = fmaxf(amax, fabsf(n[j]));
+                const BlockScale scale(lanes_max(amax, block / 8));
+                if (e < H && e % block == 0)
+                    a.scales[t * (H / block) + e / block] = scale.scale;
+                bool sure;
+                q[i] = sure_codes8(n, scale, sure);
+                if (__ballot(!sure)) {
+                    const uint2 exact = exact_codes8(h[i], w[i], lanes_max(max8(h[i], w[i]), block / 8));
+                    q[i] = scale.ratio ? exact : q[i];
                 }
-                float c[8];
-                divide8(h[i], scale, c);
-                uint2 q;
-                int lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
-                q.x = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
-                lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
-                q.y = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], lo, true);
-                if (e < H)
-                    __builtin_memcpy(a.q + t * H + e, &q, sizeof(q));
             }
+            if (OUT != kRows && e < H)
+                __builtin_memcpy(a.q + t * H + e, &q[i], sizeof(q[i]));
             if (OUT == kRows || a.out.p) {
                 if (a.out.bf16)
-                    store8(static_cast<uint16_t *>(a.out.p) + t * H, e, H, h[i]);
+                    store8(static_cast<uint16_t *>(a.out.p) + t * H, e, H, n);
                 else
-                    store8(static_cast<float *>(a.out.p) + t * H, e, H, h[i]);
+                    store8(static_cast<float *>(a.out.p) + t * H, e, H, n);
             }
+            if (OUT == kBlocks)
+                __builtin_amdgcn_sched_barrier(0);  // one vector's values in registers at a time
         }
     }
 }

@@ -614,9 +614,9 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
 def add_rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
                     block: int = 128, want_rows: bool = False, out_dtype: Optional[torch.dtype] = None,
                     want_rstd: bool = False, out=None, sum_out: Optional[torch.Tensor] = None):
-    """add_rmsnorm with its output quantized per (token, block) as quantize_fp8 does, from the float32
-    values: the FP8 dispatch's rows. Returns (q [T, H] uint8, scales [T, H/block] float32, sum, rows, rstd);
-    rows (the norm's output itself, for the router) only with want_rows; out = (q, scales)."""
+    """add_rmsnorm with its output quantized per (token, block): the FP8 dispatch's rows. Scales as quantize_fp8's of
+    the float32 values, codes those of the exact ratios to the blocks' largest values. Returns (q [T, H] uint8, scales [T, H/block] float32, sum,
+    rows, rstd); rows (the norm's output itself, for the router) only with want_rows; out = (q, scales)."""
     T, H, sum_dtype = _norm_inputs(x, weight, residual, sum_out)
     x_dt, s_dt, w_dt = _row_dt(x.dtype, "x"), _row_dt(sum_dtype, "residual"), _row_dt(weight.dtype, "weight")
     if block < 1 or H % block:
