@@ -156,7 +156,7 @@ __device__ __forceinline__ f32x4 multiply(f32x4 acc, const Acts<W> &x, const u32
 // logits = x router^T in double (matrix instructions 16x16x4): which experts are picked then does not depend on the
 // order of a float32 sum, and the products of float32 or bf16 values are exact. A workgroup takes 16 experts, 16 tokens
 // and one of `splits` parts of the hidden dimension, its wavefronts an equal share of that each; the parts' sums are put
-// together in order where the logits are used.
+// together in order where the logits are used. A launch and a chain of memory latencies: T1 H7168 E256 5.7 us, T64 9.9.
 constexpr int kRouterThreads = 512, kRouterWaves = kRouterThreads / kWave;
 constexpr int kRouterElems = 32;  // of a row per step: 8 in each lane group
 
@@ -274,6 +274,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_sum_kernel(const double
 // ---------------------------------------------------------------- routing
 // moe_route_topk of one token by one wavefront: lane l holds experts l, l + 64, ...; each of the K rounds takes the
 // largest key of the wavefront, of equal ones that of the lowest expert. The softmax as there: double, in slot order.
+// With the plan in the same launch T1 E256 K8 5.7 us; T64 8.2, and 4.9 for the plan's own launch.
 constexpr int kDppQuadXor1 = 0xb1, kDppQuadXor2 = 0x4e, kDppRowHalfMirror = 0x141, kDppRowMirror = 0x140;
 
 template <int CTRL>
@@ -546,9 +547,10 @@ __global__ __launch_bounds__(kPlanThreads) void few_token_small_route_kernel(con
 
 // ---------------------------------------------------------------- gate and up products
 // A unit is 16 columns of h of one expert, 16 rows of gate and 16 of up; wavefronts take a unit each, or share the hidden
-// dimension's loads of one, and then their tiles meet in LDS. h goes out in the order of the plan, already multiplied by the slot's weight; beside bf16 or FP8
-// weights as two bf16 rows whose sum it is to 16 bits, so that the down product is one of bf16 operands without
-// bf16's rounding of h.
+// dimension's loads of one, and then their tiles meet in LDS. h goes out in the order of the plan, already multiplied by
+// the slot's weight; beside bf16 or FP8 weights as two bf16 rows whose sum it is to 16 bits, so that the down product is
+// one of bf16 operands without bf16's rounding of h. Memory bounds it: T64 H7168 I1024 E256 K8 bf16 479 us, 5.9 TB/s of the
+// weights in use; FP8 T8 H4096 I2048 E128 K8 69 us, 5.8; rows off the lines T133 H2056 I1399 E64 K2 103 us, 4.3.
 
 // Registers of one load in flight.
 template <Weights W, int NW, int NT, bool LO>
@@ -844,9 +846,10 @@ struct Product {
     typedef typename Rows::Wt Wt;
     typedef typename ActType<W>::type X;
     // 4, 2 or 1: most rows and parts of them are an even number of loads, and three at a time leave one over (T4 H2048
-    // I1024 K4, gate and up: 36 us with three, 29 with two)
+    // I1024 K4, gate and up: 36 us with three, 29 with two). Through the window two at most (T30 H2057 I1399 E64 K4 with four
+    // 228 us, two 201, one 197; T64 H7170 I1026 E64 K8 with two 567, one 584)
     static constexpr int kRoom = (REGS - 4 * NW * NT) / kSlotRegs<W, NW, NT, LO>;
-    static constexpr int D = kRoom >= 4 ? 4 : kRoom >= 2 ? 2 : 1;
+    static constexpr int D = kRoom >= 4 && !windowed(READ) ? 4 : kRoom >= 2 ? 2 : 1;
     static constexpr int kActBytes = kHalfElems<W> * sizeof(X);  // of a token's row per half
     Rows rows;
     const char *x;
@@ -1279,11 +1282,12 @@ __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWaves
     __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, false, READ>];
     __shared__ float scales[Sh::kWaves * kScaleFloats<W, 2>];
     const Entry en(a.plan, blockIdx.y);
+    [[maybe_unused]] const int z = blockIdx.z, nz = gridDim.z;  // tiles of an expert's tokens that go side by side
     if constexpr (!MANY) {
         for (int r0 = 0; r0 < en.n; r0 += kTile)
             gate_up_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
     } else if (windowed(READ) || !a.tiled || en.n <= 2 * kTile) {
-        for (int r0 = 0; r0 < en.n; r0 += 2 * kTile) {
+        for (int r0 = 2 * kTile * z; r0 < en.n; r0 += 2 * kTile * nz) {
             if (en.n - r0 <= kTile)
                 gate_up_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
             else
@@ -1291,7 +1295,7 @@ __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWaves
         }
     } else if (static_cast<int>(blockIdx.x) * 4 * kTile < a.I) {
         if constexpr (!windowed(READ))
-            for (int r0 = 0; r0 < en.n; r0 += 4 * kTile)
+            for (int r0 = 4 * kTile * z; r0 < en.n; r0 += 4 * kTile * nz)
                 gate_up_tiles<W, 4, READ>(a, en, r0, lds, scales);
     }
 }
@@ -1299,7 +1303,9 @@ __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWaves
 // ---------------------------------------------------------------- down product
 // As the gate and up products, 32 rows of w_down (columns of out) to a unit, so that the two rows of h are read once
 // for twice the weights. Each slot's product goes to a float32 row of its own; the merge adds them up. Where fewer than
-// 32 columns are left a unit's second tile begins earlier, and both store the same values there.
+// 32 columns are left a unit's second tile begins earlier, and both store the same values there. Memory bounds it, less
+// well fed than the gate and up products by its shorter rows and twice the activations: the cases above 260 us, 5.4 TB/s; 45
+// us, 4.4; 90 us, 2.5.
 __device__ __forceinline__ int second_tile(const ExpertArgs &a, int c0)
 {
     return min(kTile, max(a.H - kTile - c0, 0));
@@ -1390,11 +1396,12 @@ __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWaves
     __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, W != kWF32, READ>];
     __shared__ float scales[Sh::kWaves * kScaleFloats<W, 2>];
     const Entry en(a.plan, blockIdx.y);
+    [[maybe_unused]] const int z = blockIdx.z, nz = gridDim.z;  // tiles of an expert's tokens that go side by side
     if constexpr (!MANY) {
         for (int r0 = 0; r0 < en.n; r0 += kTile)
             down_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
     } else if (windowed(READ) || !a.tiled || en.n <= kTile) {
-        for (int r0 = 0; r0 < en.n; r0 += 2 * kTile) {
+        for (int r0 = 2 * kTile * z; r0 < en.n; r0 += 2 * kTile * nz) {
             if (en.n - r0 <= kTile)
                 down_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
             else
@@ -1402,7 +1409,7 @@ __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWaves
         }
     } else if (static_cast<int>(blockIdx.x) * 4 * 2 * kTile < a.H) {
         if constexpr (!windowed(READ))
-            for (int r0 = 0; r0 < en.n; r0 += 4 * kTile) {
+            for (int r0 = 4 * kTile * z; r0 < en.n; r0 += 4 * kTile * nz) {
                 if (en.n - r0 <= 2 * kTile)
                     down_tiles<W, 2, READ>(a, en, r0, lds, scales);
                 else
@@ -1483,7 +1490,8 @@ __global__ __launch_bounds__(kDirectThreads) void down_merge_kernel(ExpertArgs a
 }
 
 // ---------------------------------------------------------------- merge
-// out[t] = the sum of its slots' rows in slot order (their weights are in h), plus bias.
+// out[t] = the sum of its slots' rows in slot order (their weights are in h), plus bias. Little more than a launch: 4.5 us at
+// T1 H7168 K8, 5.1 at T64.
 constexpr int kMergeThreads = 256;
 
 __global__ __launch_bounds__(kMergeThreads) void merge_kernel(ExpertArgs a)
@@ -1645,6 +1653,11 @@ Read read_of(const void *w, int64_t row_bytes, const void *x, int64_t x_row_byte
     return odd_x || (W == kWBf16 && at % 4) ? kOdd : kWords;
 }
 
+// Workgroups that take an expert's tiles of tokens in turn, side by side, where there may be several: an expert with many
+// tokens among others with few would be what a call ends with (T133 H2056 I1399 E64 K2 with experts of 1 to 55 tokens 192 ->
+// 174 us; T256 H4096 I2048 E16 K4 FP8 230 -> 215; with four of them 172 and 215, but T64 H4096 I2048 E64 K4 FP8 332 -> 343).
+unsigned turns(int T) { return T > 2 * kTile ? 2u : 1u; }
+
 template <Weights W, bool MANY>
 void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t stream)
 {
@@ -1664,7 +1677,7 @@ void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t
     Read read = read_of<W>(a.w, int64_t{a.H} * size, a.x, int64_t{a.H} * sizeof(typename ActType<W>::type),
                            (few || !a.tiled) && units * used * loads >= kWindowWork);
     a.parts = share_parts(units * used, loads, Sh::kWaves, windowed(read));
-    dim3 grid(static_cast<unsigned>(ceil_div(units, Sh::kWaves / a.parts)), static_cast<unsigned>(used));
+    dim3 grid(static_cast<unsigned>(ceil_div(units, Sh::kWaves / a.parts)), static_cast<unsigned>(used), MANY ? turns(a.T) : 1u);
 #define MOE_FEW_PRODUCT(KERNEL, READ) hipLaunchKernelGGL((KERNEL<W, MANY, READ>), grid, dim3(Sh::kThreads), 0, stream, a)
     if (read == kLines)
         MOE_FEW_PRODUCT(gate_up_kernel, kLines);
@@ -1698,7 +1711,7 @@ void launch_products(ExpertArgs a, const ExpertWeights &w, int used, hipStream_t
     }
     read = read_of<W>(a.w, int64_t{a.I} * size, nullptr, 0, (few || !a.tiled) && units * used * loads >= kWindowWork);
     a.parts = share_parts(units * used, loads, Sh::kWaves, windowed(read));
-    grid = dim3(static_cast<unsigned>(ceil_div(units, Sh::kWaves / a.parts)), static_cast<unsigned>(used));
+    grid = dim3(static_cast<unsigned>(ceil_div(units, Sh::kWaves / a.parts)), static_cast<unsigned>(used), MANY ? turns(a.T) : 1u);
     if (read == kLines)
         MOE_FEW_PRODUCT(down_kernel, kLines);
     else if (read == kWindow)
