@@ -550,7 +550,7 @@ __global__ __launch_bounds__(kPlanThreads) void few_token_small_route_kernel(con
 // dimension's loads of one, and then their tiles meet in LDS. h goes out in the order of the plan, already multiplied by
 // the slot's weight; beside bf16 or FP8 weights as two bf16 rows whose sum it is to 16 bits, so that the down product is
 // one of bf16 operands without bf16's rounding of h. Memory bounds it: T64 H7168 I1024 E256 K8 bf16 479 us, 5.9 TB/s of the
-// weights in use; FP8 T8 H4096 I2048 E128 K8 69 us, 5.8; rows off the lines T133 H2056 I1399 E64 K2 103 us, 4.3.
+// weights in use; FP8 T8 H4096 I2048 E128 K8 69 us, 5.8; rows off the lines T133 H2056 I1399 E64 K2 102 us, 4.4.
 
 // Registers of one load in flight.
 template <Weights W, int NW, int NT, bool LO>
@@ -568,7 +568,9 @@ constexpr bool windowed(Read r) { return r == kWindow || r == kWindowOdd; }
 constexpr bool odd_acts(Read r) { return r == kOdd || r == kWindowOdd; }
 
 // LDS of the window: 16 rows of two lines, whose first 16 bytes stand behind the second line too, for what begins at its end.
-constexpr int kWindowRow = 2 * 128 + 16 + 8;  // bytes; 8 more keep rows in different banks, whose lengths are mostly multiples of 16
+// In bytes; the last 8 keep rows, whose lengths are mostly multiples of 16, in different banks (T133 H2056 I1400 E64 K2
+// without them 315 us, with them 290).
+constexpr int kWindowRow = 2 * 128 + 16 + 8;
 template <int NW>
 constexpr int kWindowBytes = NW * kTile * kWindowRow;
 
@@ -935,7 +937,8 @@ struct Product {
         if (n > 0) {
             Slot q[D];
             const bool sixteens = W == kWFp8 && n > kScaleLoads;
-            int at = windowed(READ) ? l0 : l0 + (sixteens ? turn % ((n + kScaleLoads - 1) / kScaleLoads) * kScaleLoads : turn % n), use = at, first[D];
+            const int skip = sixteens ? turn % ((n + kScaleLoads - 1) / kScaleLoads) * kScaleLoads : turn % n;
+            int at = windowed(READ) ? l0 : l0 + skip, use = at, first[D];
             const int last = at == l0 ? whole - 1 : at - 1;
             auto next = [&] { at = at == last ? at : at == whole - 1 ? l0 : at + 1; };
             auto multiply_next = [&](Slot &s) {
@@ -1245,7 +1248,8 @@ __device__ __forceinline__ void gate_up_stream(const ExpertArgs &a, const Entry 
     }
     const int loads = (a.H + kLoadElems<W> - 1) / kLoadElems<W>;
     p.run(loads * my.part / a.parts, loads * (my.part + 1) / a.parts, a.H, a.stagger ? my.unit : 0);
-    join_parts<Sh::kWaves, NT, Sh::template kStretch<READ>>(p.acc, a.parts, lds, [&](int unit, int row, int column, const float (&v)[2]) {
+    join_parts<Sh::kWaves, NT, Sh::template kStretch<READ>>(p.acc, a.parts, lds,
+                                                            [&](int unit, int row, int column, const float (&v)[2]) {
         store_h<W>(a, en, r0 + row, (blockIdx.x * (Sh::kWaves / a.parts) + unit) * kTile + column, v[0], v[1]);
     });
 }
@@ -1305,7 +1309,7 @@ __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWaves
 // for twice the weights. Each slot's product goes to a float32 row of its own; the merge adds them up. Where fewer than
 // 32 columns are left a unit's second tile begins earlier, and both store the same values there. Memory bounds it, less
 // well fed than the gate and up products by its shorter rows and twice the activations: the cases above 260 us, 5.4 TB/s; 45
-// us, 4.4; 90 us, 2.5.
+// us, 4.4; 75 us, 3.0.
 __device__ __forceinline__ int second_tile(const ExpertArgs &a, int c0)
 {
     return min(kTile, max(a.H - kTile - c0, 0));
@@ -1365,7 +1369,8 @@ __device__ __forceinline__ void down_stream(const ExpertArgs &a, const Entry &en
     }
     const int loads = (a.I + kLoadElems<W> - 1) / kLoadElems<W>;
     p.run(loads * my.part / a.parts, loads * (my.part + 1) / a.parts, a.I, a.stagger ? my.unit : 0);
-    join_parts<Sh::kWaves, NT, Sh::template kStretch<READ>>(p.acc, a.parts, lds, [&](int unit, int row, int column, const float (&v)[2]) {
+    join_parts<Sh::kWaves, NT, Sh::template kStretch<READ>>(p.acc, a.parts, lds,
+                                                            [&](int unit, int row, int column, const float (&v)[2]) {
         store_y(a, en, r0 + row, blockIdx.x * (Sh::kWaves / a.parts) + unit, column, v[0], v[1]);
     });
 }
