@@ -565,25 +565,36 @@ def route_topk_backward(topk_idx: torch.Tensor, topk_w: torch.Tensor, d_topk_w: 
 def _norm_inputs(x, weight, residual, sum_out):
     """Checks shared by the two forward norms; returns (T, H, dtype of the sum)."""
     _need(x, "x", None, 2)
-    T, H = x.shape
+    shape = x.shape
+    T, H = shape
     _need(weight, "weight", None, 1)
     if weight.shape[0] != H:
         raise ValueError(f"weight must have {H} elements")
-    for t, name in ((residual, "residual"), (sum_out, "sum_out")):
-        if t is not None:
-            _need(t, name, None, 2)
-            if t.shape != x.shape:
-                raise ValueError(f"{name} must be [{T}, {H}]")
-    sum_dtype = residual.dtype if residual is not None else (sum_out.dtype if sum_out is not None else x.dtype)
-    if sum_out is not None and sum_out.dtype != sum_dtype:
-        raise TypeError(f"sum_out must be {sum_dtype}, got {sum_out.dtype}")
+    sum_dtype = x.dtype
+    if residual is not None:
+        _need(residual, "residual", None, 2)
+        if residual.shape != shape:
+            raise ValueError(f"residual must be [{T}, {H}]")
+        sum_dtype = residual.dtype
+    if sum_out is not None:
+        _need(sum_out, "sum_out", None, 2)
+        if sum_out.shape != shape:
+            raise ValueError(f"sum_out must be [{T}, {H}]")
+        if residual is None:
+            sum_dtype = sum_out.dtype
+        elif sum_out.dtype != sum_dtype:
+            raise TypeError(f"sum_out must be {sum_dtype}, got {sum_out.dtype}")
     return T, H, sum_dtype
 
 
+_ROW_DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
 def _row_dt(dtype: torch.dtype, name: str) -> int:
-    if dtype not in (torch.float32, torch.bfloat16):
+    dt = _ROW_DT.get(dtype)
+    if dt is None:
         raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
-    return _DT[dtype]
+    return dt
 
 
 def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
