@@ -451,7 +451,8 @@ moe_status moe_add_rmsnorm_backward(const void *dout, moe_dtype dout_dt, const v
  *   (gate_up_scales [E, 2I, H/block], down_scales [E, H, I/block]); block must divide H and I (else
  *   MOE_ERR_INVALID) and be a multiple of 128 (else MOE_ERR_UNSUPPORTED). Other types of weights:
  *   MOE_ERR_UNSUPPORTED; block and scales are ignored without FP8.
- *   T <= MOE_MAX_FEW_TOKENS, H and I <= 2^20 (else MOE_ERR_UNSUPPORTED): for more tokens dispatch them.
+ *   K <= E (else MOE_ERR_INVALID); T <= MOE_MAX_FEW_TOKENS, H and I <= 2^20 (else MOE_ERR_UNSUPPORTED): for more
+ *   tokens dispatch them.
  * Weights of experts that no token uses are not read. Rows are independent: what is not finite in one token's row
  * or in an expert's weights reaches only the tokens that use it. A row whose logits are NaN may route anywhere or
  * nowhere, and an infinite element of a bf16 w_down may give NaN where the formula gives an infinity.
@@ -467,8 +468,11 @@ moe_status moe_few_token_layer(const void *x, moe_dtype dt, const void *router, 
 
 /* The experts of moe_few_token_layer after a routing that the caller has: topk_idx [T, K] (an id outside
  * [0, E) routes nowhere, so a rank can name the experts it does not hold -1; an id may repeat within a row, each slot
- * counting), topk_w [T, K] or NULL (unit weights). A token without experts gets zeros (or its bias).
- * Arguments, limits and workspace as above. */
+ * counting), topk_w [T, K] or NULL (unit weights). A token without experts gets zeros (or its bias). E is the number of
+ * experts whose weights are given, and may be less than K <= MOE_MAX_TOPK.
+ * Arguments, limits and workspace otherwise as above; its size is moe_few_token_experts_workspace_size's, which is
+ * moe_few_token_workspace_size's where K <= E. */
+moe_status moe_few_token_experts_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t K, size_t *bytes);
 moe_status moe_few_token_experts(const void *x, moe_dtype dt, int64_t T, int64_t H, int64_t I, int32_t E,
                                  int32_t K, const int32_t *topk_idx, const float *topk_w, const void *w_gate_up,
                                  const void *w_down, moe_dtype weight_dt, const float *gate_up_scales,

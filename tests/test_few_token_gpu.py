@@ -478,3 +478,22 @@ def test_long_rows_off_the_cache_lines(m, T, K, kind, H, I, shifts):
             return torch.cat([t.new_full((shift,), fill), t.flatten(), t.new_full((9,), fill)])[shift: shift + t.numel()].view(t.shape)
         out = m.few_token_experts(off(x), idx, w, off(lay.w13), off(lay.w2), out_dtype=F32, **lay.scales)
         assert_within(out, *want)
+
+
+@pytest.mark.parametrize("T", [1, 9, 40, 256])
+@pytest.mark.parametrize("E,K", [(1, 8), (3, 8), (1, 32), (3, 32), (4, 5)])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "fp8"])
+def test_fewer_experts_than_slots_a_token(m, T, E, K, kind):
+    """A rank that holds E of the experts a token may choose: most slots name others (-1), some its own, a few the same twice."""
+    lay = Layer(m, 384, 128, E, kind, seed=4)
+    g = torch.Generator().manual_seed(T + K)
+    ids = torch.where(torch.rand(T, K, generator=g) < 0.7, torch.full((T, K), -1), torch.randint(0, E, (T, K), generator=g))
+    idx = ids.to(torch.int32).to(DEV)
+    w = torch.rand(T, K, generator=g).to(DEV)
+    x, bias = draw(9, T, lay.H, dtype=lay.rows), draw(10, T, lay.H, dtype=lay.rows)
+    ws = torch.empty(m.few_token_workspace_bytes(T, lay.H, lay.I, E, K), dtype=torch.uint8, device=DEV)
+    for i, weights in ((idx, w), (idx, None), (torch.zeros_like(idx), w), (torch.full_like(idx, -1), w)):
+        out = m.few_token_experts(x, i, weights, lay.w13, lay.w2, bias=bias, out=torch.empty_like(x), workspace=ws, **lay.scales)
+        assert_within(out, *lay.expected(x, i, weights, bias))
+    with pytest.raises(m.MoeError):  # the layer's own routing names K different experts
+        m.few_token_layer(x, lay.router, lay.w13, lay.w2, K, **lay.scales)

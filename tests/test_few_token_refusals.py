@@ -66,3 +66,30 @@ def test_binding_refuses_host_tensors():
         m.few_token_layer(x, r, a, b, 2)
     with pytest.raises(ValueError, match="GPU tensor"):
         m.few_token_experts(x, torch.zeros(2, 2, dtype=torch.int32), None, a, b)
+
+
+def test_a_rank_may_hold_fewer_experts_than_slots_a_token(capi):
+    """moe_few_token_experts takes a routing whose ids repeat or name experts held elsewhere, so K may exceed E; the layer, which
+    routes by itself, needs K different experts."""
+    lib, n = capi.lib(), ctypes.c_size_t(0)
+    size = lambda f, *a: (f(*a, ctypes.byref(n)), n.value)  # noqa: E731
+    experts, layer = lib.moe_few_token_experts_workspace_size, lib.moe_few_token_workspace_size
+    for sizes in ((1, 64, 64, 4, 2), (16, 512, 256, 8, 8), (256, 4096, 2048, 64, 8)):
+        assert size(experts, *sizes) == size(layer, *sizes) and n.value > 0
+    for E, K in ((1, 32), (3, 8), (7, 8)):
+        st, need = size(experts, 256, 512, 128, E, K)
+        assert st == capi.MOE_OK and need >= 4 * 256 * K * (512 + 128)  # h and the products of every slot
+        assert size(layer, 256, 512, 128, E, K)[0] == capi.MOE_ERR_INVALID
+    assert size(experts, 0, 64, 64, 4, 5) == (capi.MOE_OK, 0)
+    assert experts(1, 64, 64, 4, 2, None) == capi.MOE_ERR_INVALID
+    for bad in ((-1, 64, 64, 4, 2), (1, 0, 64, 4, 2), (1, 64, 0, 4, 2), (1, 64, 64, 0, 1), (1, 64, 64, 4, 0)):
+        assert size(experts, *bad)[0] == capi.MOE_ERR_INVALID, bad
+    for bad in ((257, 64, 64, 4, 5), (1, 64, 64, 1025, 2), (1, 64, 64, 4, 33), (1, (1 << 20) + 1, 64, 4, 5)):
+        assert size(experts, *bad)[0] == capi.MOE_ERR_UNSUPPORTED, bad
+    B = capi.MOE_BF16
+    assert lib.moe_few_token_experts(P, B, 0, 256, 128, 3, 8, P, P, P, P, B, None, None, 0, None, P, B, None, 0, None) == capi.MOE_OK
+    need = size(experts, 4, 256, 128, 3, 8)[1]
+    assert lib.moe_few_token_experts(P, B, 4, 256, 128, 3, 8, P, P, P, P, B, None, None, 0, None, P, B, P, need - 1,
+                                     None) == capi.MOE_ERR_INVALID
+    assert lib.moe_few_token_layer(P, B, P, 0, 256, 128, 3, 8, 0, 0, P, P, B, None, None, 0, None, P, B, P, P, P, need,
+                                   None) == capi.MOE_ERR_INVALID

@@ -58,6 +58,7 @@ SIGNATURES = {
     "moe_add_rmsnorm_backward": (ctypes.c_int, [_P, _dt, _P, _dt, _P, _dt, _P, _P, _i64, _i64, _P, _dt, _P, _P, _size,
                                                 _P]),
     "moe_few_token_workspace_size": (ctypes.c_int, [_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_size)]),
+    "moe_few_token_experts_workspace_size": (ctypes.c_int, [_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_size)]),
     "moe_few_token_layer": (ctypes.c_int, [_P, _dt, _P, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _P, _P, _dt, _P, _P,
                                            _i32, _P, _P, _dt, _P, _P, _P, _size, _P]),
     "moe_few_token_experts": (ctypes.c_int, [_P, _dt, _i64, _i64, _i64, _i32, _i32, _P, _P, _P, _P, _dt, _P, _P, _i32,

@@ -1556,12 +1556,25 @@ Layout layout(int64_t T, int64_t H, int64_t E, int64_t K, int64_t I)
     return l;
 }
 
-moe_status check_sizes(int64_t T, int64_t H, int64_t I, int32_t E, int32_t K)
+// The layer's own routing names K different experts (`distinct`); a routing that the caller has may name fewer of them, or one
+// several times, and then E, the experts held here, may be less than K.
+moe_status check_sizes(int64_t T, int64_t H, int64_t I, int32_t E, int32_t K, bool distinct)
 {
-    if (T < 0 || H < 1 || I < 1 || E < 1 || K < 1 || K > E)
+    if (T < 0 || H < 1 || I < 1 || E < 1 || K < 1 || (distinct && K > E))
         return MOE_ERR_INVALID;
     if (T > kMaxFewTokens || E > MOE_MAX_EXPERTS || K > MOE_MAX_TOPK || H > (1 << 20) || I > (1 << 20))
         return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+moe_status workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t K, bool distinct, size_t *bytes)
+{
+    if (!bytes)
+        return MOE_ERR_INVALID;
+    const moe_status st = check_sizes(T, H, I, E, K, distinct);
+    if (st != MOE_OK)
+        return st;
+    *bytes = T == 0 ? 0 : layout(T, H, E, K, I).bytes;
     return MOE_OK;
 }
 
@@ -1581,9 +1594,9 @@ struct ExpertWeights {
 
 moe_status check_layer(const void *x, moe_dtype dt, int64_t T, int64_t H, int64_t I, int32_t E, int32_t K,
                        const ExpertWeights &w, const void *out, moe_dtype out_dt, const void *workspace,
-                       size_t workspace_bytes)
+                       size_t workspace_bytes, bool distinct)
 {
-    moe_status st = check_sizes(T, H, I, E, K);
+    const moe_status st = check_sizes(T, H, I, E, K, distinct);
     if (st != MOE_OK)
         return st;
     if ((dt != MOE_F32 && dt != MOE_BF16 && dt != MOE_FP8_E4M3) || (w.dt != MOE_F32 && w.dt != MOE_BF16 && w.dt != MOE_FP8_E4M3) ||
@@ -1776,14 +1789,13 @@ moe_status launch_experts(const void *x, int64_t T, int64_t H, int64_t I, int32_
 
 extern "C" moe_status moe_few_token_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t K, size_t *bytes)
 {
-    using namespace moe;
-    if (!bytes)
-        return MOE_ERR_INVALID;
-    const moe_status st = check_sizes(T, H, I, E, K);
-    if (st != MOE_OK)
-        return st;
-    *bytes = T == 0 ? 0 : layout(T, H, E, K, I).bytes;
-    return MOE_OK;
+    return moe::workspace_size(T, H, I, E, K, true, bytes);
+}
+
+extern "C" moe_status moe_few_token_experts_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t K,
+                                                           size_t *bytes)
+{
+    return moe::workspace_size(T, H, I, E, K, false, bytes);
 }
 
 extern "C" moe_status moe_few_token_experts(const void *x, moe_dtype dt, int64_t T, int64_t H, int64_t I, int32_t E,
@@ -1795,7 +1807,7 @@ extern "C" moe_status moe_few_token_experts(const void *x, moe_dtype dt, int64_t
 {
     using namespace moe;
     const ExpertWeights w{w_gate_up, w_down, weight_dt, gate_up_scales, down_scales, block};
-    const moe_status st = check_layer(x, dt, T, H, I, E, K, w, out, out_dt, workspace, workspace_bytes);
+    const moe_status st = check_layer(x, dt, T, H, I, E, K, w, out, out_dt, workspace, workspace_bytes, false);
     if (st != MOE_OK || T == 0)
         return st;
     if (!topk_idx)
@@ -1814,7 +1826,7 @@ extern "C" moe_status moe_few_token_layer(const void *x, moe_dtype dt, const voi
 {
     using namespace moe;
     const ExpertWeights w{w_gate_up, w_down, weight_dt, gate_up_scales, down_scales, block};
-    moe_status st = check_layer(x, dt, T, H, I, E, K, w, out, out_dt, workspace, workspace_bytes);
+    moe_status st = check_layer(x, dt, T, H, I, E, K, w, out, out_dt, workspace, workspace_bytes, true);
     if (st != MOE_OK)
         return st;
     // the routing's own argument errors, before anything is launched

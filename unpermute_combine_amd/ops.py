@@ -720,9 +720,10 @@ def rmsnorm_workspace_bytes(T: int, H: int) -> int:
 
 @functools.lru_cache(maxsize=256)
 def few_token_workspace_bytes(T: int, H: int, I: int, E: int, K: int) -> int:
-    """Workspace bytes of few_token_layer and few_token_experts for these sizes."""
+    """Workspace bytes of few_token_layer and few_token_experts for these sizes (the latter's E may be less than K)."""
     n = ctypes.c_size_t(0)
-    check("moe_few_token_workspace_size", lib().moe_few_token_workspace_size(T, H, I, E, K, ctypes.byref(n)))
+    check("moe_few_token_experts_workspace_size",
+          lib().moe_few_token_experts_workspace_size(T, H, I, E, K, ctypes.byref(n)))
     return int(n.value)
 
 
@@ -807,7 +808,7 @@ def few_token_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: Optional[
                       out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
                       workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """few_token_layer after a routing that the caller has: ids outside [0, E) route nowhere (the experts of other
-    ranks, say), topk_w None means unit weights. Returns out [T, H]."""
+    ranks, say, of which there may be more than E to a token), topk_w None means unit weights. Returns out [T, H]."""
     T, H, I, E, x_dt, w_dt, block = _expert_weights(x, w_gate_up, w_down, gate_up_scales, down_scales)
     _need(topk_idx, "topk_idx", torch.int32, 2)
     if topk_idx.shape[0] != T:
