@@ -352,3 +352,16 @@ def test_more_rows_than_a_grid_has_workgroups(m):
     assert_within(dw, want_dw, dw_roundings(T) * U * mag, "dweight")
     q, sc = m.add_rmsnorm_fp8(x, w, residual=r, block=6)[:2]
     assert torch.equal(sc, m.quantize_fp8(out, 6)[1]) and torch.equal(q, codes_of(m, total, w, out, sc, 6))
+
+
+@pytest.mark.parametrize("H,block", [(256, 128), (4096, 512), (640, 40), (256, 256), (999, 999)])
+def test_fp8_codes_of_products_below_float32s_normal_range(m, H, block):
+    """Elements whose h s is a float32 subnormal, under weights that bring them back: h s has lost bits there, the ratio of
+    h w has not."""
+    x, w = draw(1, 16, H), draw(2, H)
+    small = torch.arange(H, device=DEV) < max(block, H // 2) // (2 if block == H else 1)
+    x, w = x * torch.where(small, 1e-25, 1e17), w * torch.where(small, 1e20, 1e-22)
+    q, sc, _, rows, _ = m.add_rmsnorm_fp8(x, w, block=block, want_rows=True, out_dtype=F32)
+    assert bool((sc >= 2.0 ** -100).all())
+    assert torch.equal(sc, m.quantize_fp8(rows, block)[1])
+    assert torch.equal(q, codes_of(m, x, w, rows, sc, block))

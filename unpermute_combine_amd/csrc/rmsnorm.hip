@@ -117,8 +117,10 @@ __device__ __forceinline__ uint2 codes8(const float (&c)[8])
 
 // Codes of eight float32 values n = h s w, and whether all of them are sure: n and the block's largest have two roundings
 // each, the scale one, its reciprocal two and the products two, 9 of 2^-24, so where 2^-20 more and less have the same code,
-// that is the ratio's own. (Values that float32 rounds as subnormals have the code 0 in a block of such a scale.)
-__device__ __forceinline__ uint2 sure_codes8(const float (&n)[8], const BlockScale &b, bool &sure)
+// that is the ratio's own. (Values that float32 rounds as subnormals have the code 0 in a block of such a scale. h s is none
+// where the code is not 0 and |w| is 2^16 or less: codes begin at 2^-10 of the scale, which is 2^-100 or more, so |h s| is
+// 2^-126 or more. The codes of larger weights, `large`, are not sure.)
+__device__ __forceinline__ uint2 sure_codes8(const float (&n)[8], bool large, const BlockScale &b, bool &sure)
 {
     const float lower = b.to_code * (1.0f - 0x1p-20f), upper = b.to_code * (1.0f + 0x1p-20f);
     float less[8], more[8];
@@ -135,7 +137,7 @@ __device__ __forceinline__ uint2 sure_codes8(const float (&n)[8], const BlockSca
         more[j] = n[j] * upper;
     }
     const uint2 q = codes8(less), r = codes8(more);
-    sure = q.x == r.x && q.y == r.y;
+    sure = q.x == r.x && q.y == r.y && !large;
     return q;
 }
 
@@ -398,6 +400,16 @@ __global__ __launch_bounds__(NV == 2 ? 512 : 1024) void add_rmsnorm_regs_kernel(
             for (int j = 0; j < 8; ++j)
                 ss = !TAIL || j >= v[i].shared ? fmaf(h[i][j], h[i][j], ss) : ss;
         }
+        bool large = false;
+        if (OUT != kRows) {
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    top = fmaxf(top, fabsf(w[i][j]));
+            large = top > 0x1p16f;
+        }
         const float s = 1.0f / sqrtf(block_sum1(ss, turn) / static_cast<float>(H) + a.eps);
         if (a.rstd && threadIdx.x == 0)
             a.rstd[t] = s;
@@ -429,7 +441,7 @@ __global__ __launch_bounds__(NV == 2 ? 512 : 1024) void add_rmsnorm_regs_kernel(
             for (int i = 0; i < NV; ++i) {
                 bool one;
                 values(i, n);
-                q[i] = sure_codes8(n, scale, one);
+                q[i] = sure_codes8(n, large, scale, one);
                 sure = sure && one;
             }
             if (__syncthreads_or(!sure)) {
@@ -457,7 +469,7 @@ __global__ __launch_bounds__(NV == 2 ? 512 : 1024) void add_rmsnorm_regs_kernel(
                 if (e < H && e % block == 0)
                     a.scales[t * (H / block) + e / block] = scale.scale;
                 bool sure;
-                q[i] = sure_codes8(n, scale, sure);
+                q[i] = sure_codes8(n, large, scale, sure);
                 if (__ballot(!sure)) {
                     const uint2 exact = exact_codes8(h[i], w[i], lanes_max(max8(h[i], w[i]), block / 8));
                     q[i] = scale.ratio ? exact : q[i];
