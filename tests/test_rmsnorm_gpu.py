@@ -365,3 +365,21 @@ def test_fp8_codes_of_products_below_float32s_normal_range(m, H, block):
     assert bool((sc >= 2.0 ** -100).all())
     assert torch.equal(sc, m.quantize_fp8(rows, block)[1])
     assert torch.equal(q, codes_of(m, x, w, rows, sc, block))
+
+
+@pytest.mark.parametrize("T,H", [(4096, 2), (4096, 8), (4096, 64), (2048, 1024), (64, 65536)])
+def test_rstd_is_rounded_once(m, T, H):
+    """Rows of small integers, whose mean of squares float32 holds: what is left is the reciprocal root's one rounding."""
+    x = torch.randint(1, 12, (T, H), generator=torch.Generator().manual_seed(H)).float().to(DEV)
+    rstd = m.add_rmsnorm(x, torch.ones(H, device=DEV), eps=0.0, want_rstd=True)[2]
+    assert torch.equal(rstd, (1 / x.double().square().mean(1).sqrt()).float())
+
+
+def test_rstd_of_the_smallest_and_the_largest_rows(m):
+    """Means of squares from float32's subnormals to its largest values, zeros and what passes its range."""
+    size = torch.tensor([2.0 ** -74, 2.0 ** -70, 2.0 ** -63, 2.0 ** -62, 2.0 ** -30, 1.0, 2.0 ** 40, 2.0 ** 60, 0.0, 2.0 ** 70])
+    x = size[:, None].expand(-1, 64).contiguous().to(DEV)
+    out, _, rstd = m.add_rmsnorm(x, torch.ones(64, device=DEV), eps=0.0, want_rstd=True)
+    assert torch.equal(rstd[:8], 1 / x[:8, 0]) and torch.equal(out[:8], torch.ones_like(out[:8]))
+    assert bool(torch.isinf(rstd[8])) and bool(torch.isnan(out[8]).all())
+    assert float(rstd[9]) == 0 and not out[9].any()

@@ -95,6 +95,18 @@ __device__ __forceinline__ double lanes_max(double v, int lanes)
     return v;
 }
 
+// 1 / sqrt(v), rounded once: y, the instruction's value, one step of 2^-23 off at most, and a Newton step of it with v y in two
+// floats, which leaves 2^-45 before the rounding (1 / sqrtf(v) rounds twice and is another value for every fourth v). The
+// instruction does not take subnormals, so what is near them is scaled; of zero, infinity and NaN y is the value.
+__device__ __forceinline__ float reciprocal_root(float v)
+{
+    const bool tiny = v < 0x1p-100f;
+    const float u = tiny ? v * 0x1p100f : v, y = __builtin_amdgcn_rsqf(u), high = u * y, low = fmaf(u, y, -high);
+    float s = fmaf(0.5f * y, fmaf(-low, y, fmaf(-high, y, 1.0f)), y);
+    s = s == s ? s : y;
+    return tiny ? s * 0x1p50f : s;
+}
+
 // A block's scale, and how its codes come of it.
 struct BlockScale {
     float scale, to_code;
@@ -208,7 +220,7 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, int64_t t)
         const float h = r ? load_f(x + j) + load_f(r + j) : load_f(x + j);
         ss = fmaf(h, h, ss);
     }
-    const float s = 1.0f / sqrtf(block_sum(ss) / static_cast<float>(a.H) + a.eps);
+    const float s = reciprocal_root(block_sum(ss) / static_cast<float>(a.H) + a.eps);
     if (a.rstd && threadIdx.x == 0)
         a.rstd[t] = s;
     if (a.q) {
@@ -410,7 +422,7 @@ __global__ __launch_bounds__(NV == 2 ? 512 : 1024) void add_rmsnorm_regs_kernel(
                     top = fmaxf(top, fabsf(w[i][j]));
             large = top > 0x1p16f;
         }
-        const float s = 1.0f / sqrtf(block_sum1(ss, turn) / static_cast<float>(H) + a.eps);
+        const float s = reciprocal_root(block_sum1(ss, turn) / static_cast<float>(H) + a.eps);
         if (a.rstd && threadIdx.x == 0)
             a.rstd[t] = s;
         if (a.sum_out) {
