@@ -383,3 +383,25 @@ def test_rstd_of_the_smallest_and_the_largest_rows(m):
     assert torch.equal(rstd[:8], 1 / x[:8, 0]) and torch.equal(out[:8], torch.ones_like(out[:8]))
     assert bool(torch.isinf(rstd[8])) and bool(torch.isnan(out[8]).all())
     assert float(rstd[9]) == 0 and not out[9].any()
+
+
+@pytest.mark.parametrize("H", [1 << 20, (1 << 24) + 3])
+def test_long_rows_of_like_values(m, H):
+    """Adding like values one after the other rounds the same way each time: a float32 chain of 65536 of them is up to 0.1% off.
+    The threads' chains over rows that do not fit in registers are in double, so what is left are their rounding to float32, six
+    of the wavefront's tree and four of the wavefronts': 11."""
+    c = torch.tensor([0.1, 0.7, 1.3, 3.1], device=DEV)
+    x, w = c[:, None].expand(-1, H).contiguous(), torch.full((H,), 1.5, device=DEV)
+    out, _, rstd = m.add_rmsnorm(x, w, want_rstd=True)
+    s = 1 / torch.sqrt(c.double().square() + 1e-6)
+    # the sum, the length as float32, the mean and eps, halved by the root, and the reciprocal root
+    assert bool(((rstd.double() - s).abs() <= ((11 + 3) / 2 + 1) * U * s).all())
+    # and the two products
+    want = (c.double() * s * 1.5)[:, None]
+    assert bool(((out.double() - want).abs() <= ((11 + 3) / 2 + 3) * U * want).all())
+    g = torch.full_like(x, 0.3)
+    dx, _ = m.add_rmsnorm_backward(g, x, w, rstd, want_dw=False)
+    a, hd, s = g[:, :1].double() * 1.5, c.double()[:, None], rstd.double()[:, None]
+    hm = hd * s * s * (a * hd)
+    # a's product, m's (that, the sum, the length, the mean, two products), the fused difference and its product with s
+    assert bool(((dx.double() - s * (a - hm)).abs() <= s * (3 * U * a.abs() + (1 + 11 + 4 + 2) * U * hm.abs())).all())

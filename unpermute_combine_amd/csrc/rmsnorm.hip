@@ -196,6 +196,7 @@ __device__ __forceinline__ float block_sum(float v)
 // One workgroup per row: a pass for the sum of squares and a pass for the outputs (and with FP8
 // codes one wavefront per block: its largest value, then its codes). Outputs may lie on the inputs
 // element for element: each element's inputs are read by the thread that writes it, before it does.
+// A thread's chain may be 2^18 elements here (like values one after the other in float32: up to 0.4% off), so it is in double.
 struct NormArgs {
     const void *x, *residual;
     Row weight;
@@ -215,12 +216,12 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, int64_t t)
     const X *x = static_cast<const X *>(a.x) + t * a.H;
     const S *r = a.residual ? static_cast<const S *>(a.residual) + t * a.H : nullptr;
     S *so = a.sum_out ? static_cast<S *>(a.sum_out) + t * a.H : nullptr;
-    float ss = 0.0f;
+    double ss = 0.0;
     for (int64_t j = threadIdx.x; j < a.H; j += kNormThreads) {
-        const float h = r ? load_f(x + j) + load_f(r + j) : load_f(x + j);
-        ss = fmaf(h, h, ss);
+        const double h = r ? load_f(x + j) + load_f(r + j) : load_f(x + j);
+        ss = fma(h, h, ss);
     }
-    const float s = reciprocal_root(block_sum(ss) / static_cast<float>(a.H) + a.eps);
+    const float s = reciprocal_root(block_sum(static_cast<float>(ss)) / static_cast<float>(a.H) + a.eps);
     if (a.rstd && threadIdx.x == 0)
         a.rstd[t] = s;
     if (a.q) {
@@ -503,7 +504,7 @@ __global__ __launch_bounds__(NV == 2 ? 512 : 1024) void add_rmsnorm_regs_kernel(
 
 // ---------------------------------------------------------------- backward, any length
 // dx: one workgroup per row. dweight: columns by thread over ranges of rows, the ranges' sums put
-// together in order by a second kernel.
+// together in order by a second kernel. The threads' chains in double, as in the forward.
 template <typename G, typename S, typename D>
 __global__ __launch_bounds__(kNormThreads) void rmsnorm_dx_kernel(const G *dout, const S *h, Row weight,
                                                                   const float *rstd, const D *d_sum, int64_t T, int64_t H,
@@ -511,10 +512,10 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_dx_kernel(const G *dout,
 {
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
         const float s = rstd[t];
-        float ah = 0.0f;
+        double ah = 0.0;
         for (int64_t j = threadIdx.x; j < H; j += kNormThreads)
-            ah = fmaf(load_f(dout + t * H + j) * weight[j], load_f(h + t * H + j), ah);
-        const float m = s * s * (block_sum(ah) / static_cast<float>(H));
+            ah = fma(static_cast<double>(load_f(dout + t * H + j) * weight[j]), static_cast<double>(load_f(h + t * H + j)), ah);
+        const float m = s * s * (block_sum(static_cast<float>(ah)) / static_cast<float>(H));
         for (int64_t j = threadIdx.x; j < H; j += kNormThreads) {
             float v = s * fmaf(-load_f(h + t * H + j), m, load_f(dout + t * H + j) * weight[j]);
             if (d_sum)
