@@ -405,3 +405,20 @@ def test_long_rows_of_like_values(m, H):
     hm = hd * s * s * (a * hd)
     # a's product, m's (that, the sum, the length, the mean, two products), the fused difference and its product with s
     assert bool(((dx.double() - s * (a - hm)).abs() <= s * (3 * U * a.abs() + (1 + 11 + 4 + 2) * U * hm.abs())).all())
+
+
+@pytest.mark.parametrize("H", [6, 8])
+def test_weight_gradient_of_very_many_like_rows(m, H):
+    """No chain of float32 additions is longer than 1024 rows (32768 like ones after the other: up to 0.05% off)."""
+    T = 1 << 24
+    g, h = torch.linspace(0.3, 1.7, H, device=DEV).expand(T, H).contiguous(), torch.linspace(1.9, 0.4, H, device=DEV).expand(T, H).contiguous()
+    dw = m.add_rmsnorm_backward(g, h, torch.ones(H, device=DEV), torch.ones(T, device=DEV))[1]
+    want = T * g[0].double() * h[0].double()
+    # a term's product, the chain, the sum's rounding
+    assert bool(((dw.double() - want).abs() <= (1 + 1024 + 1) * U * want).all())
+
+
+def test_backward_workspace_of_very_many_rows(m):
+    """A range of rows is at most 1024 of them; there are 512 as long as that holds."""
+    assert m.rmsnorm_workspace_bytes(512 * 1024, 8) == 512 * 8 * 4
+    assert m.rmsnorm_workspace_bytes((1 << 31) - 1, 8) == (1 << 21) * 8 * 4

@@ -10,6 +10,7 @@
 //   dx[t,j] = s[t] * (a[t,j] - h[t,j] * m[t]) (+ d_sum[t,j]),   dweight[j] = sum_t g[t,j] h[t,j] s[t]
 //
 // Otherwise everything between the loads and the one rounding of each output is float32.
+#include <algorithm>
 #include <cmath>
 
 #include "moe_common.h"
@@ -533,23 +534,23 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_dweight_kernel(const G *
     if (j >= H)
         return;
     const int64_t t0 = blockIdx.y * rows, t1 = min(T, t0 + rows);
-    float v = 0.0f;
+    double v = 0.0;
     for (int64_t t = t0; t < t1; ++t)
-        v = fmaf(load_f(dout + t * H + j) * rstd[t], load_f(h + t * H + j), v);
-    part[blockIdx.y * H + j] = v;
+        v = fma(static_cast<double>(load_f(dout + t * H + j) * rstd[t]), static_cast<double>(load_f(h + t * H + j)), v);
+    part[blockIdx.y * H + j] = static_cast<float>(v);
 }
 
 // dweight = the ranges' sums put together: a workgroup takes 32 columns, its 32 rows of threads every 32nd range
-// each, and the 32 partial sums meet in order.
+// each, and the 32 partial sums meet in order. In double: there may be 2^21 ranges.
 constexpr int kSumCols = 32, kSumRows = 32;
 
 __global__ __launch_bounds__(kSumCols *kSumRows) void rmsnorm_dweight_sum_kernel(const float *part, int64_t ranges,
                                                                                   int64_t H, float *dweight)
 {
-    __shared__ float sh[kSumRows][kSumCols];
+    __shared__ double sh[kSumRows][kSumCols];
     const int c = threadIdx.x % kSumCols, g = threadIdx.x / kSumCols;
     const int64_t j = static_cast<int64_t>(blockIdx.x) * kSumCols + c;
-    float v = 0.0f;
+    double v = 0.0;
     if (j < H) {
 #pragma unroll 4
         for (int64_t p = g; p < ranges; p += kSumRows)
@@ -560,16 +561,17 @@ __global__ __launch_bounds__(kSumCols *kSumRows) void rmsnorm_dweight_sum_kernel
     if (g == 0 && j < H) {
         for (int k = 1; k < kSumRows; ++k)
             v += sh[k][c];
-        dweight[j] = v;
+        dweight[j] = static_cast<float>(v);
     }
 }
 
 // One workgroup per row up to 2^20 of them (a grid holds fewer than 2^32 threads), then several rows each.
 unsigned row_blocks(int64_t T) { return static_cast<unsigned>(T < (1 << 20) ? T : (1 << 20)); }
 
-// Ranges of rows whose dweight sums are formed apart.
-constexpr int64_t kDwMaxRanges = 512;
-int64_t dw_ranges(int64_t T) { return T < kDwMaxRanges ? T : kDwMaxRanges; }
+// Ranges of rows whose dweight sums are formed apart: 512, and more where a range would be over 1024 rows, so that no float32
+// chain is longer (over 32768 rows of like values one is up to 0.05% off, over 2^22 6%).
+constexpr int64_t kDwRanges = 512, kDwRows = 1024;
+int64_t dw_ranges(int64_t T) { return std::min(T, std::max(kDwRanges, ceil_div(T, kDwRows))); }
 
 // Rows in registers as in the forward: thread i keeps its columns' weights and their gradient's sums while its
 // workgroup takes rows blockIdx, blockIdx + gridDim, ...; the sums of the gridDim workgroups are put together in
@@ -737,7 +739,8 @@ moe_status launch_backward(const void *dout, const void *h, Row weight, const fl
     const G *g = static_cast<const G *>(dout);
     const S *hs = static_cast<const S *>(h);
     const D *ds = static_cast<const D *>(d_sum);
-    const int64_t vecs = ceil_div(H, 8), ranges = dw_ranges(T);
+    const int64_t vecs = ceil_div(H, 8);
+    int64_t ranges = dw_ranges(T);
     if (in_registers(H, 512, 4)) {
         const int nv = vecs <= 256 ? 1 : vecs <= 2 * 512 ? 2 : 4;
         const dim3 grid(static_cast<unsigned>(ranges)), block(static_cast<unsigned>(ceil_div(ceil_div(vecs, nv), kWave) * kWave));
@@ -763,6 +766,7 @@ moe_status launch_backward(const void *dout, const void *h, Row weight, const fl
     } else {
         hipLaunchKernelGGL((rmsnorm_dx_kernel<G, S, D>), dim3(row_blocks(T)), dim3(kNormThreads), 0, stream, g, hs, weight,
                            rstd, ds, T, H, static_cast<D *>(dx));
+        ranges = std::min(T, kDwRanges);  // of any length: their chains are in double
         if (dweight)
             hipLaunchKernelGGL((rmsnorm_dweight_kernel<G, S>),
                                dim3(static_cast<unsigned>(ceil_div(H, kNormThreads)), static_cast<unsigned>(ranges)),
