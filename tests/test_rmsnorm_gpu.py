@@ -422,3 +422,33 @@ def test_backward_workspace_of_very_many_rows(m):
     """A range of rows is at most 1024 of them; there are 512 as long as that holds."""
     assert m.rmsnorm_workspace_bytes(512 * 1024, 8) == 512 * 8 * 4
     assert m.rmsnorm_workspace_bytes((1 << 31) - 1, 8) == (1 << 21) * 8 * 4
+
+
+@pytest.mark.parametrize("H,block", [(8, 8), (9, 9), (8, 0), (9, 0), (520, 520), (1032, 8), (1033, 0)])
+def test_more_rows_than_a_grid_has_workgroups_with_rows_in_registers(m, H, block):
+    """A workgroup takes several rows one after the other: of one wavefront and of several, with whole and partial vectors, as rows
+    and as FP8 with one scale a block or a row, in place too. bf16 rows, looked at in the places that the first, the second and
+    the last workgroups have written."""
+    T = (1 << 20) + 77
+    g = torch.Generator(device=DEV)
+    g.manual_seed(H)
+    x = torch.randn(T, H, generator=g, device=DEV, dtype=BF16)
+    r = torch.randn(T, H, generator=g, device=DEV, dtype=BF16)
+    w = draw(3, H) + 1
+    at = torch.cat([torch.arange(0, 300), torch.arange((1 << 20) - 200, T)]).to(DEV)
+    h, s, n = reference(x[at], w, r[at], 1e-6)
+    b = row_bound(H)
+    if block:
+        q, sc, total, rows, rstd = m.add_rmsnorm_fp8(x, w, residual=r, block=block, want_rows=True, want_rstd=True, out_dtype=F32)
+        assert torch.equal(sc[at], m.quantize_fp8(rows[at], block)[1])
+        assert torch.equal(q[at], codes_of(m, x[at].float() + r[at].float(), w, rows[at], sc[at], block))
+    else:
+        rows, total, rstd = m.add_rmsnorm(x, w, residual=r, want_rstd=True, out_dtype=F32)
+    assert_within(rows[at], n, b * n.abs(), "out")
+    assert_within(rstd[at], s, b * s, "rstd")
+    assert torch.equal(total[at], (x[at].float() + r[at].float()).to(BF16))
+    del rows
+    if not block:
+        want = m.add_rmsnorm(x[at], w, residual=r[at])[0]
+        m.add_rmsnorm(x, w, residual=r, out=x, sum_out=r)
+        assert torch.equal(x[at], want) and torch.equal(r, total)
