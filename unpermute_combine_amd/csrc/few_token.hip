@@ -574,14 +574,16 @@ constexpr int kWindowRow = 2 * 128 + 16 + 8;
 template <int NW>
 constexpr int kWindowBytes = NW * kTile * kWindowRow;
 
-// The shape of a kernel: 8 wavefronts of 128 registers, of which 16 share a CU with two loads or more in flight each, or
+// The shape of a kernel: 8 wavefronts of 128 registers, of which 16 share a CU with two loads or more in flight each (8 of up
+// to 256 where FP8 rows go through the window: its 70 KiB of LDS with the scales' 17 leave room for one workgroup), or
 // where experts may have MANY tokens (more than a tile's) 4 of 256, of which 8 do.
 template <Weights W, bool MANY>
 struct Shape {
     // registers for addresses, what is being multiplied, and FP8's scales
     static constexpr int kOther = W != kWFp8 ? 40 : MANY ? 64 : 52;
     static constexpr int kRegs = (MANY ? 256 : 128) - kOther, kWaves = MANY ? 4 : 8, kThreads = kWaves * kWave;
-    static constexpr int kWavesPerSimd = MANY ? 2 : 4;
+    template <Read READ>
+    static constexpr int kWavesPerSimd = MANY || (W == kWFp8 && windowed(READ)) ? 2 : 4;
     // bytes of LDS of a wavefront: its window, later its tiles
     template <Read READ>
     static constexpr int kStretch = windowed(READ) ? kWindowBytes<2> : (MANY ? 2 : 1) * 2 * kWave * 16;
@@ -1280,7 +1282,8 @@ constexpr int kProductLds = MANY && !windowed(READ) ? std::max(kStretches<W, MAN
                                                     : kStretches<W, MANY, READ>;
 
 template <Weights W, bool MANY, Read READ>
-__global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWavesPerSimd)) void gate_up_kernel(ExpertArgs a)
+__global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::template kWavesPerSimd<READ>)) void gate_up_kernel(
+    ExpertArgs a)
 {
     typedef Shape<W, MANY> Sh;
     __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, false, READ>];
@@ -1395,7 +1398,8 @@ __device__ __forceinline__ void down_tiles(const ExpertArgs &a, const Entry &en,
 }
 
 template <Weights W, bool MANY, Read READ>
-__global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::kWavesPerSimd)) void down_kernel(ExpertArgs a)
+__global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::template kWavesPerSimd<READ>)) void down_kernel(
+    ExpertArgs a)
 {
     typedef Shape<W, MANY> Sh;
     __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, W != kWF32, READ>];
