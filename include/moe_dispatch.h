@@ -442,8 +442,8 @@ moe_status moe_add_rmsnorm_backward(const void *dout, moe_dtype dout_dt, const v
  *   h[t,k,:] = topk_w[t,k] * silu(G_e x[t]) * (U_e x[t]),   e = topk_idx[t,k], silu(g) = g / (1 + exp(-g))
  *   out[t,:] = sum_k D_e h[t,k,:] (+ bias[t,:])
  * where w_gate_up [E, 2I, H] holds G_e in rows [0, I) and U_e in rows [I, 2I) of expert e, and w_down
- * [E, H, I] holds D_e. Sums are float32 (their order depends on the sizes and the routing alone: no
- * atomics), h is kept to 16 significant bits or more, and out is rounded once.
+ * [E, H, I] holds D_e. Sums are float32 (no atomics: their order depends on the sizes, the routing and the
+ * alignment of the arrays alone), h is kept to 16 significant bits or more, and out is rounded once.
  *   x [T, H] and router [E, H] of dtype dt (float32 or bf16); bias [T, H] of dtype out_dt or NULL, which
  *   may be out itself; out [T, H] (out_dt), which overlaps no other input; topk_idx [T, K], topk_w [T, K] out.
  *   weight_dt: dt, or MOE_FP8_E4M3 beside bf16 rows: codes with float32 scales, one per row and block of

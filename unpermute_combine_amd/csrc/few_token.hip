@@ -7,13 +7,14 @@
 //
 // with expert e's gate rows G_e = w_gate_up[e][0..I), up rows U_e = w_gate_up[e][I..2I) and D_e = w_down[e].
 //
-// The time is that of reading the weights of the experts in use, once each, and for the smallest calls that of the
-// launches. A wavefront multiplies 32 rows of a weight matrix (16 of the gate's and the 16 of the up's, or 32 of the down's)
-// by 16 or 32 tokens with MFMA 16x16 tiles: few tokens leave most of a tile empty, which costs nothing while the weights'
-// stream sets the pace. The weights go from memory straight into the matrix instructions' operand registers, whole cache
-// lines at a time, several loads ahead in a ring of registers. Measured with cold caches, of the bytes of the weights in
-// use: T64 H7168 I1024 E256 K8 bf16 gate and up 6.0 TB/s, down 5.4 (plain reads of so many bytes the same way reach
-// 6.7); T1 of it 6.3 and 5.2 in 74 us, of which 16 are router, routing, merge and launches.
+// The time is that of reading the weights of the experts in use, once each (again for each further 64 tokens of an expert, or 32
+// where the products do not go through LDS), and for the smallest calls that of the launches. A wavefront multiplies 32 rows of
+// a weight matrix (16 of the gate's and the 16 of the up's, or 32 of the down's) by 16 or 32 tokens with MFMA 16x16 tiles: few
+// tokens leave most of a tile empty, which costs nothing while the weights' stream sets the pace. The weights go from memory
+// straight into the matrix instructions' operand registers, whole cache lines at a time, several loads ahead in a ring of
+// registers. Measured with cold caches, of the bytes of the weights in use: T64 H7168 I1024 E256 K8 bf16 with 96 experts in use
+// and up to 37 tokens on one gate and up 5.7-6.0 TB/s, down 5.0-5.4, with 221 and up to 7 on one 6.8 and 6.1; T1 of it 6.2 and
+// 5.1 (plain reads of so many bytes the same way reach 6.7) in 74 us, of which 16 are router, routing, merge and launches.
 #include <algorithm>
 
 #include "moe_common.h"
@@ -1289,7 +1290,7 @@ __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::templa
     __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, false, READ>];
     __shared__ float scales[Sh::kWaves * kScaleFloats<W, 2>];
     const Entry en(a.plan, blockIdx.y);
-    [[maybe_unused]] const int z = blockIdx.z, nz = gridDim.z;  // tiles of an expert's tokens that go side by side
+    [[maybe_unused]] const int z = blockIdx.z, nz = gridDim.z;  // of the workgroups that share an expert's tiles of tokens
     if constexpr (!MANY) {
         for (int r0 = 0; r0 < en.n; r0 += kTile)
             gate_up_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
@@ -1405,7 +1406,7 @@ __global__ __launch_bounds__((Shape<W, MANY>::kThreads), (Shape<W, MANY>::templa
     __shared__ __attribute__((aligned(16))) char lds[kProductLds<W, MANY, W != kWF32, READ>];
     __shared__ float scales[Sh::kWaves * kScaleFloats<W, 2>];
     const Entry en(a.plan, blockIdx.y);
-    [[maybe_unused]] const int z = blockIdx.z, nz = gridDim.z;  // tiles of an expert's tokens that go side by side
+    [[maybe_unused]] const int z = blockIdx.z, nz = gridDim.z;  // of the workgroups that share an expert's tiles of tokens
     if constexpr (!MANY) {
         for (int r0 = 0; r0 < en.n; r0 += kTile)
             down_stream<W, 1, Sh, READ>(a, en, r0, lds, scales);
@@ -1628,6 +1629,9 @@ constexpr int64_t kSmallRouter = 128 << 10;
 
 size_t plan_lds(int E) { return sizeof(uint16_t) * kPlanWaves * static_cast<size_t>(E); }
 
+// The host does not know how many experts a call uses: `used` of the rules below is the most there may be, min(E, T K), and so
+// are the sizes beside them (routers whose logits have something in common use a third to two thirds of them).
+
 // Wavefronts that share a unit of weight rows: more of them while the chip has not several rounds of wavefronts (T8 H4096
 // I2048 E128 K8 FP8 with four against two: 189 -> 181 us and 112 -> 106; T64 H7168 I1024 E128 K8 down, 28672 units, with four
 // against one: 333 -> 388), as long as each keeps four loads or more (T32 H1024 I512 E64 K4 down with two: 23 -> 32 us).
@@ -1648,7 +1652,8 @@ bool stagger(int64_t row_bytes) { return row_bytes % 4096 == 0; }
 
 // Loads of a column tile's experts (by the most experts that may be in use) up to which one workgroup takes them all and
 // merges too: a launch fewer, which is what the smallest calls spend their time on (T1 H512 I1024 K2 float32 21 -> 19 us),
-// against less of the chip at work (T8 H1024 I512 K4, 112 loads: 21 -> 32 us).
+// against less of the chip at work (T8 H1024 I512 K4, 112 loads: 21 -> 32 us). In between, replayed from a graph: 64 loads 24
+// and 24 us, 70 25 -> 24, 80 26 -> 27, 96 24 -> 28, 29 -> 30 and 35 -> 38.
 constexpr int64_t kDirectLoads = 64;
 
 // Workgroups from which on the tiled product, whose wavefronts do not share a unit's loads, has the chip filled: T256 H4096
@@ -1675,9 +1680,11 @@ Read read_of(const void *w, int64_t row_bytes, const void *x, int64_t x_row_byte
     return odd_x || (W == kWBf16 && at % 4) ? kOdd : kWords;
 }
 
-// Workgroups that take an expert's tiles of tokens in turn, side by side, where there may be several: an expert with many
-// tokens among others with few would be what a call ends with (T133 H2056 I1399 E64 K2 with experts of 1 to 55 tokens 192 ->
-// 174 us; T256 H4096 I2048 E16 K4 FP8 230 -> 215; with four of them 172 and 215, but T64 H4096 I2048 E64 K4 FP8 332 -> 343).
+// Workgroups that take an expert's tiles of tokens in turn, where there may be several: an expert with many tokens among others
+// with few would be what a call ends with. They are the slowest index of the grid, so that all experts' first tiles begin
+// before any second ones, and two of an expert share no read of its weights. T133 H2056 I1399 E64 K2 with experts of 1 to 55
+// tokens 192 -> 174 us; T256 H4096 I2048 E16 K4 FP8 230 -> 215; with four of them 172 and 215, but T64 H4096 I2048 E64 K4 FP8
+// 332 -> 343.
 unsigned turns(int T) { return T > 2 * kTile ? 2u : 1u; }
 
 template <Weights W, bool MANY>

@@ -369,8 +369,10 @@ __device__ __forceinline__ F block_max1(F v, int turn)
 // them), so that each row is read once. FP8 (kBlocks): a block of 8 << n elements lies in 1 << n neighbouring
 // lanes; (kWholeRow): one scale for the row, through LDS. Memory bounds it: T16384 H7168 bf16 with a residual 163 us, 5.8
 // TB/s, a large copy's rate (two passes over the row 723; workgroups that stay and have the next row's loads in flight
-// 180); T1 H7168 3.0 us, a row's latency; to FP8 T8192 H7168 96 us, 4.3 TB/s, with five wavefronts a SIMD where
-// the rows alone leave room for seven.
+// 180); T1 H7168 3.0 us, a row's latency; to FP8 T8192 H7168 94 us, 4.4 TB/s, with five wavefronts a SIMD where
+// the rows alone leave room for seven. Rows of more than 8192 elements are four vectors a thread, of which the compiler spills
+// 19 to 34 registers to FP8 by blocks, 66 to 115 with one scale a row, up to 10 of float32 rows: T4096 H12288 bf16 78 us (5.1
+// TB/s), to FP8 109 and 233, T4096 H16384 99, 125 and 266; float32 H16384 203, 254 and 368.
 enum NormOut { kRows, kBlocks, kWholeRow };
 
 template <typename X, typename S, int NV, NormOut OUT, bool TAIL>
@@ -577,7 +579,9 @@ int64_t dw_ranges(int64_t T) { return std::min(T, std::max(kDwRanges, ceil_div(T
 // workgroup takes rows blockIdx, blockIdx + gridDim, ...; the sums of the gridDim workgroups are put together in
 // order by rmsnorm_dweight_sum_kernel. Each of dout, h and d_sum is read once. T8192 H7168 bf16: 89 + 5 us, 5.3 TB/s (apart,
 // with dx by rows and dweight by columns, 337); the next row's loads are in flight while a row's sum is formed. 512
-// workgroups: two a CU; T16384 H4096 100 us, with 768 or 256 of them 103 and 116.
+// workgroups: two a CU; T16384 H4096 100 us, with 768 or 256 of them 103 and 116. Of rows of more than 8192 elements (four
+// vectors a thread) two float32 operands or more spill 6 to 104 registers: T4096 H16384 bf16 114 us (4.7 TB/s), float32 255.
+// Many short rows leave the chip waiting on 512 workgroups of a wavefront or two: T200000 H64 bf16 369 us, 0.28 TB/s.
 template <typename G, typename S, typename D, int NV, bool TAIL>
 __global__ __launch_bounds__(512) void rmsnorm_backward_regs_kernel(const G *dout, const S *h, Row weight,
                                                                      const float *rstd, const D *d_sum, int64_t T,
