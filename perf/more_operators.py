@@ -1,0 +1,288 @@
+"""Cases and plain forms of a router's balance loss (with per-expert counts and the gradient) and of the experts'
+products in microscaled 4-bit floating point (MXFP4: E2M1 codes, an E8M0 scale for each 32 of a row): quantisation of
+rows, and the product of each expert's rows with its weights. ``own`` selects the library's kernels; without it the
+plain forms run (elementary torch operations)."""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+BLOCK = 32
+COEF = 0.01
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+SIZE = {"f32": 4, "bf16": 2}
+
+
+def listed():
+    return [
+        # a small model's micro-batch: latency only
+        dict(name="balance_small", op="balance", T=64, E=8, K=2, mask=False, skew=1.0),
+        # a training step's routing at the size of the largest dispatch workload
+        dict(name="balance_train", op="balance", T=16384, E=256, K=8, mask=False, skew=1.2),
+        # a padded batch with odd sizes: its padding tokens count nowhere
+        dict(name="balance_padded", op="balance", T=5001, E=100, K=6, mask=True, skew=0.0),
+        # the training step's gradient, joined with the one that comes through the routing weights
+        dict(name="balance_backward_train", op="balance_backward", T=16384, E=256, K=8, mask=False, add=True, skew=1.2),
+        # a padded batch's gradient alone, rows that no vector width divides
+        dict(name="balance_backward_padded", op="balance_backward", T=2999, E=61, K=4, mask=True, add=False, skew=1.0),
+        # a decode batch's rows on their way to the experts
+        dict(name="quantize_decode", op="quantize", T=8, H=7168, dtype="bf16"),
+        # a prefill batch's
+        dict(name="quantize_prefill", op="quantize", T=16384, H=7168, dtype="bf16"),
+        # a ragged float32 batch with an odd number of blocks a row
+        dict(name="quantize_f32_ragged", op="quantize", T=3001, H=1056, dtype="f32"),
+        # one decoded token, gate and up of its experts, the rows taken through the index: latency and few weights
+        dict(name="product_one_token", op="product", T=1, K=8, E=256, H=7168, N=1024, gated=True, gather=True, out="bf16", skew=1.2),
+        # the down product of a decode batch: weights' bytes
+        dict(name="product_decode", op="product", T=64, K=8, E=128, H=2048, N=4096, gated=False, gather=False, out="bf16", skew=0.0),
+        # gate and up of a prefill batch at the size of the largest dispatch workload: matrix instructions
+        dict(name="product_prefill", op="product", T=16384, K=8, E=256, H=7168, N=1024, gated=True, gather=True, out="bf16", skew=0.0),
+        # a ragged batch over few experts with a skewed router, float32 out, sizes that no tile divides
+        dict(name="product_ragged", op="product", T=333, K=3, E=24, H=2080, N=1399, gated=False, gather=False, out="f32", skew=1.0),
+    ]
+
+
+def _size(rng, lo, hi, multiple=1):
+    """A size in [lo, hi], spread over its logarithm; some odd, some multiples of 8 or 128."""
+    n = int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+    m = max(multiple, rng.choice((1, 8, 8, 128)))
+    return max(lo, min(hi, n // m * m)) if n >= m else max(lo, n // multiple * multiple)
+
+
+def draw(rng):
+    op = rng.choice(("balance", "balance_backward", "quantize", "product", "product", "product"))
+    while True:
+        if op in ("balance", "balance_backward"):
+            E = rng.choice((8, 16, 24, 61, 64, 100, 128, 160, 256, 384))
+            c = dict(op=op, T=_size(rng, 16, 32768), E=E, K=rng.randint(1, 8), mask=rng.random() < 0.4, skew=rng.choice((0.0, 1.0, 1.2)))
+            if op == "balance_backward":
+                c["add"] = rng.random() < 0.5
+            return c
+        if op == "quantize":
+            c = dict(op=op, T=_size(rng, 1, 16384), H=_size(rng, 64, 8192, BLOCK), dtype=rng.choice(("f32", "bf16", "bf16")))
+            if c["T"] * c["H"] * SIZE[c["dtype"]] <= 16384 * 7168 * 2:
+                return c
+        else:
+            c = dict(op=op, T=_size(rng, 1, 16384), K=rng.randint(1, 8), E=rng.choice((8, 16, 24, 64, 100, 128, 256)),
+                     H=_size(rng, 256, 7168, BLOCK), N=_size(rng, 128, 4096), gated=rng.random() < 0.4,
+                     gather=rng.random() < 0.5, out=rng.choice(("bf16", "bf16", "f32")), skew=rng.choice((0.0, 1.0, 1.2)))
+            n = c["N"] * (2 if c["gated"] else 1)
+            if c["E"] * c["H"] * n <= 256 * 7168 * 2048 and c["T"] * c["K"] * c["H"] * n <= 16384 * 8 * 7168 * 2048:
+                return c
+
+
+def _zipf_bias(E, s):
+    """Logit biases log p_e, p_e proportional to (e + 1)^-s: the low ids are popular (0: none)."""
+    r = np.arange(1, E + 1, dtype=np.float64) ** -float(s)
+    return np.log(r / r.sum()) * (s > 0)
+
+
+def _quantized(x):
+    """Codes, two a byte (the even element in the low half), and the bytes of the blocks' scales: the scale is the
+    largest power of two not above the block's largest magnitude, over 4 (1 for a block of zeros), and a code the
+    nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (ties to the even code, 6 beyond) to the element over the scale."""
+    v = x.float().view(*x.shape[:-1], -1, BLOCK)
+    amax = v.abs().amax(-1)
+    biased = amax.view(torch.int32) >> 23
+    s = torch.where(amax > 0, (biased - 2).clamp_min(0), 127)
+    r = torch.ldexp(v, (127 - s)[..., None])
+    a = r.abs()
+    c = ((a > 0.25).byte() + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5)) | (torch.signbit(r).byte() << 3)
+    c = c.view(*x.shape[:-1], -1, 2)
+    return c[..., 0] | (c[..., 1] << 4), s.byte()
+
+
+def _rows(g, T, H, dtype="f32"):
+    return torch.randn(T, H, generator=g, device="cuda").to(DT[dtype])
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    c = dict(case)
+    if c["op"] == "quantize":
+        # normalised hidden rows, a few channels of which are far larger than the others
+        x = torch.randn(c["T"], c["H"], generator=g, device="cuda")
+        x *= torch.exp(0.5 * torch.randn(c["H"], generator=g, device="cuda"))
+        return dict(case=c, x=x.to(DT[c["dtype"]]))
+    T, E, K = c["T"], c["E"], c["K"]
+    logits = torch.randn(T, E, generator=g, device="cuda") + torch.from_numpy(_zipf_bias(E, c["skew"])).float().cuda()
+    idx = torch.topk(logits, K, dim=1).indices
+    if c["op"] != "product":
+        s = dict(case=c, logits=logits, idx=idx.to(torch.int32), mask=None, d_logits=None)
+        if c["mask"]:
+            s["mask"] = torch.rand(T, generator=g, device="cuda") < 0.8
+        if c["op"] == "balance_backward":
+            s["counts"], s["tokens"] = _plain_counts(s)
+            s["d_loss"] = torch.rand((), generator=g, device="cuda") + 0.5
+            if c["add"]:
+                s["d_logits"] = torch.randn(T, E, generator=g, device="cuda") * (1.0 / T)
+        return s
+    H, n = c["H"], c["N"] * (2 if c["gated"] else 1)
+    counts = torch.bincount(idx.reshape(-1), minlength=E)
+    ends = counts.cumsum(0)
+    s = dict(case=c, group_list=ends.to(torch.int32), ends=ends.tolist(), src_row=None)
+    if c["gather"]:
+        s["src_row"] = (torch.sort(idx.reshape(-1), stable=True).indices // K).to(torch.int32)
+    s["x"], s["xs"] = _quantized(_rows(g, T if c["gather"] else T * K, H))
+    s["w"] = torch.empty(E, n, H // 2, dtype=torch.uint8, device="cuda")
+    s["ws"] = torch.empty(E, n, H // BLOCK, dtype=torch.uint8, device="cuda")
+    for e in range(E):
+        s["w"][e], s["ws"][e] = _quantized(_rows(g, n, H).mul_(H ** -0.5))
+    return s
+
+
+# ---------------------------------------------------------------- plain forms
+
+
+def _plain_counts(s):
+    c, idx = s["case"], s["idx"].long()
+    hits = torch.zeros(c["T"], c["E"], dtype=torch.int32, device=idx.device).scatter_(1, idx, 1)
+    if s["mask"] is None:
+        return hits.sum(0, dtype=torch.int32), torch.full((1,), c["T"], dtype=torch.int32, device=idx.device)
+    return (hits * s["mask"][:, None]).sum(0, dtype=torch.int32), s["mask"].sum(dtype=torch.int32).view(1)
+
+
+def _plain_probs(s):
+    e = torch.exp(s["logits"] - s["logits"].amax(1, keepdim=True))
+    p = e / e.sum(1, keepdim=True)
+    return p if s["mask"] is None else p * s["mask"][:, None]
+
+
+def _plain_balance(s):
+    c = s["case"]
+    counts, n = _plain_counts(s)
+    total = _plain_probs(s).sum(0)
+    loss = COEF * c["E"] * ((counts / (n * c["K"])) * (total / n)).sum()
+    return {"loss": loss, "counts": counts, "prob_sum": total, "tokens": n}
+
+
+def _plain_balance_backward(s):
+    c, p = s["case"], _plain_probs(s)
+    f = s["counts"] / (s["tokens"] * c["K"])
+    d = (s["d_loss"] * COEF * c["E"] / s["tokens"]) * p * (f - (p * f).sum(1, keepdim=True))
+    return d if s["d_logits"] is None else d + s["d_logits"]
+
+
+_VALUES = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0]
+
+
+def _values(codes, scales, dtype=torch.float32):
+    """The values that codes and scales stand for."""
+    pairs = torch.tensor([[_VALUES[b & 15], _VALUES[b >> 4]] for b in range(256)], dtype=dtype).to(codes.device, non_blocking=True)
+    v = pairs[codes.int()].view(*scales.shape, BLOCK)
+    return torch.ldexp(v, (scales.int() - 127)[..., None]).view(*scales.shape[:-1], -1)
+
+
+def _plain_product(s):
+    c = s["case"]
+    out = torch.zeros(c["T"] * c["K"], c["N"], device=s["x"].device, dtype=DT[c["out"]])
+    x = _values(s["x"], s["xs"])
+    at = 0
+    for e, end in enumerate(s["ends"]):
+        if end > at:
+            rows = x[at:end] if s["src_row"] is None else x[s["src_row"][at:end]]
+            y = torch.matmul(rows, _values(s["w"][e], s["ws"][e]).t())
+            if c["gated"]:
+                gate, up = y[:, : c["N"]], y[:, c["N"]:]
+                y = gate / (1 + torch.exp(-gate)) * up
+            out[at:end] = y.to(out.dtype)
+        at = end
+    return out
+
+
+def run(s):
+    c = s["case"]
+    op = c["op"]
+    if own:
+        import unpermute_combine_amd as m
+
+        if op == "balance":
+            loss, counts, total, n = m.balance_loss(s["logits"], s["idx"], coef=COEF, token_mask=s["mask"])
+            return {"loss": loss, "counts": counts, "prob_sum": total, "tokens": n}
+        if op == "balance_backward":
+            return m.balance_loss_backward(s["logits"], s["counts"], s["tokens"], c["K"], d_loss=s["d_loss"], coef=COEF,
+                                           token_mask=s["mask"], d_logits=s["d_logits"])
+        if op == "quantize":
+            codes, scales = m.quantize_mxfp4(s["x"])
+        else:
+            return m.grouped_product_mxfp4(s["x"], s["xs"], s["w"], s["ws"], s["group_list"], src_row=s["src_row"],
+                                           gated=c["gated"], out_dtype=DT[c["out"]])
+    elif op == "quantize":
+        codes, scales = _quantized(s["x"])
+    else:
+        return {"balance": _plain_balance, "balance_backward": _plain_balance_backward, "product": _plain_product}[op](s)
+    # bytes of two codes each, as a program hands them on (equal bytes are equal values); scales as their values
+    return {"codes": codes, "scales": scales.view(torch.float8_e8m0fnu)}
+
+
+def work(case):
+    c = case
+    if c["op"] == "quantize":
+        T, H = c["T"], c["H"]
+        return {"bytes": T * H * SIZE[c["dtype"]] + T * H // 2 + T * H // BLOCK, "flops": 3 * T * H}
+    T, E, K = c["T"], c["E"], c["K"]
+    if c["op"] == "balance":
+        return {"bytes": 4 * T * E + 4 * T * K + (T if c["mask"] else 0) + 8 * E, "flops": 5 * T * E}
+    if c["op"] == "balance_backward":
+        return {"bytes": 4 * T * E * (3 if c["add"] else 2) + (T if c["mask"] else 0) + 4 * E, "flops": 8 * T * E}
+    # experts that T tokens use, on the average over routings of these logits
+    r = np.random.default_rng(7)
+    n = max(1, min(16, 65536 // (T * E)))
+    z = r.standard_normal((n, min(T, 4096), E)) + _zipf_bias(E, c["skew"])
+    top = np.argpartition(-z, K - 1, axis=2)[:, :, :K] if K < E else np.broadcast_to(np.arange(E), (n, z.shape[1], E))
+    used = np.mean([np.unique(t).size for t in top])
+    cols, row = c["N"] * (2 if c["gated"] else 1), c["H"] // 2 + c["H"] // BLOCK
+    return {"bytes": int(used * cols * row) + (T if c["gather"] else T * K) * row + T * K * c["N"] * SIZE[c["out"]]
+            + (4 * T * K if c["gather"] else 0) + 4 * E, "flops": 2 * T * K * cols * c["H"]}
+
+
+# ---------------------------------------------------------------- the definition in 64 bits
+
+
+def exact(case, seed):
+    s, c = prepare(case, seed), case
+    if c["op"] == "quantize":
+        return _exact_quantized(s["x"].double())
+    if c["op"] == "product":
+        return _exact_product(c, s)
+    keep = torch.ones(c["T"], dtype=torch.bool, device="cuda") if s["mask"] is None else s["mask"]
+    p = torch.softmax(s["logits"].double(), 1)
+    if c["op"] == "balance":
+        ids = s["idx"][keep].long().reshape(-1)
+        n, total = int(keep.sum()), p[keep].sum(0)
+        counts = torch.bincount(ids, minlength=c["E"])
+        loss = COEF * c["E"] * torch.dot(counts.double() / (n * c["K"]), total / n)
+        return {"loss": loss, "counts": None, "prob_sum": total, "tokens": None}
+    f = s["counts"].double() / (int(s["tokens"]) * c["K"])
+    # d p_j / d z_e = p_e ((e = j) - p_j), for each token that counts
+    d = p * f - p * (p @ f)[:, None]
+    d = torch.where(keep[:, None], d, 0) * (s["d_loss"].double() * COEF * c["E"] / int(s["tokens"]))
+    return d if s["d_logits"] is None else d + s["d_logits"].double()
+
+
+def _exact_quantized(x):
+    blocks = x.reshape(x.shape[0], -1, BLOCK)
+    top = blocks.abs().max(2).values
+    e = torch.where(top > 0, torch.frexp(top).exponent - 3, 0).clamp(-127, 127)  # frexp: top in [2^(exponent-1), 2^exponent)
+    scale = torch.ldexp(torch.ones_like(top), e)
+    r = (blocks / scale[:, :, None]).abs()
+    step = torch.where(r < 2, 0.5, torch.where(r < 4, 1.0, 2.0))
+    r = ((r / step).round() * step).clamp_max(6)
+    code = (torch.searchsorted(torch.tensor(_VALUES[:8], dtype=torch.float64, device=x.device), r) + 8 * torch.signbit(blocks)).to(torch.uint8)
+    code = code.reshape(x.shape)
+    return {"codes": code[:, 0::2] + 16 * code[:, 1::2], "scales": scale}
+
+
+def _exact_product(c, s):
+    out = torch.empty(c["T"] * c["K"], c["N"], dtype=torch.float64, device="cuda")
+    starts = [0] + s["ends"][:-1]
+    for e, (a, b) in enumerate(zip(starts, s["ends"])):
+        if a == b:
+            continue
+        rows = torch.arange(a, b, device="cuda") if s["src_row"] is None else s["src_row"][a:b].long()
+        y = _values(s["x"][rows], s["xs"][rows], torch.float64) @ _values(s["w"][e], s["ws"][e], torch.float64).t()
+        out[a:b] = y if not c["gated"] else y[:, : c["N"]] * torch.sigmoid(y[:, : c["N"]]) * y[:, c["N"]:]
+    return out
