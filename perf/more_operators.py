@@ -79,6 +79,13 @@ def _zipf_bias(E, s):
     return np.log(r / r.sum()) * (s > 0)
 
 
+def _pow2(e, dtype):
+    """2^e by the exponent's field (e an integer tensor in the type's normal range)."""
+    if dtype == torch.float64:
+        return ((e.long() + 1023) << 52).view(dtype)
+    return ((e.int() + 127) << 23).view(dtype)
+
+
 def _quantized(x):
     """Codes, two a byte (the even element in the low half), and the bytes of the blocks' scales: the scale is the
     largest power of two not above the block's largest magnitude, over 4 (1 for a block of zeros), and a code the
@@ -87,7 +94,7 @@ def _quantized(x):
     amax = v.abs().amax(-1)
     biased = amax.view(torch.int32) >> 23
     s = torch.where(amax > 0, (biased - 2).clamp_min(0), 127)
-    r = torch.ldexp(v, (127 - s)[..., None])
+    r = v * _pow2(127 - s, torch.float32)[..., None]
     a = r.abs()
     c = ((a > 0.25).byte() + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5)) | (torch.signbit(r).byte() << 3)
     c = c.view(*x.shape[:-1], -1, 2)
@@ -169,11 +176,11 @@ def _plain_balance_backward(s):
 _VALUES = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0]
 
 
-def _values(codes, scales, dtype=torch.float32):
+def _values(codes, scales):
     """The values that codes and scales stand for."""
-    pairs = torch.tensor([[_VALUES[b & 15], _VALUES[b >> 4]] for b in range(256)], dtype=dtype).to(codes.device, non_blocking=True)
+    pairs = torch.tensor([[_VALUES[b & 15], _VALUES[b >> 4]] for b in range(256)]).to(codes.device, non_blocking=True)
     v = pairs[codes.int()].view(*scales.shape, BLOCK)
-    return torch.ldexp(v, (scales.int() - 127)[..., None]).view(*scales.shape[:-1], -1)
+    return (v * _pow2(scales.int() - 127, torch.float32)[..., None]).view(*scales.shape[:-1], -1)
 
 
 def _plain_product(s):
@@ -267,13 +274,23 @@ def _exact_quantized(x):
     blocks = x.reshape(x.shape[0], -1, BLOCK)
     top = blocks.abs().max(2).values
     e = torch.where(top > 0, torch.frexp(top).exponent - 3, 0).clamp(-127, 127)  # frexp: top in [2^(exponent-1), 2^exponent)
-    scale = torch.ldexp(torch.ones_like(top), e)
+    scale = _pow2(e, torch.float64)
     r = (blocks / scale[:, :, None]).abs()
     step = torch.where(r < 2, 0.5, torch.where(r < 4, 1.0, 2.0))
     r = ((r / step).round() * step).clamp_max(6)
     code = (torch.searchsorted(torch.tensor(_VALUES[:8], dtype=torch.float64, device=x.device), r) + 8 * torch.signbit(blocks)).to(torch.uint8)
     code = code.reshape(x.shape)
     return {"codes": code[:, 0::2] + 16 * code[:, 1::2], "scales": scale}
+
+
+def _exact_values(codes, scales):
+    """(-1)^sign * mantissa * 2^exponent from the fields of each code, times its block's scale."""
+    code = torch.empty(*codes.shape[:-1], 2 * codes.shape[-1], dtype=torch.int64, device=codes.device)
+    code[..., 0::2], code[..., 1::2] = codes % 16, codes // 16
+    exponent, odd = code // 2 % 4, code % 2
+    v = torch.where(exponent > 0, (2 + odd) * (1 << (exponent - 1).clamp_min(0)), odd).double() / 2
+    v = torch.where(code >= 8, -v, v)
+    return v * _pow2(scales.int() - 127, torch.float64).repeat_interleave(BLOCK, -1)
 
 
 def _exact_product(c, s):
@@ -283,6 +300,6 @@ def _exact_product(c, s):
         if a == b:
             continue
         rows = torch.arange(a, b, device="cuda") if s["src_row"] is None else s["src_row"][a:b].long()
-        y = _values(s["x"][rows], s["xs"][rows], torch.float64) @ _values(s["w"][e], s["ws"][e], torch.float64).t()
+        y = _exact_values(s["x"][rows], s["xs"][rows]) @ _exact_values(s["w"][e], s["ws"][e]).t()
         out[a:b] = y if not c["gated"] else y[:, : c["N"]] * torch.sigmoid(y[:, : c["N"]]) * y[:, c["N"]:]
     return out
