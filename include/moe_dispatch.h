@@ -383,6 +383,33 @@ moe_status moe_unpermute_combine_backward(const void *dout, moe_dtype dout_dt, c
 moe_status moe_route_topk_backward(const int32_t *topk_idx, const float *topk_w, const float *d_topk_w, int64_t T,
                                    int32_t E, int32_t K, float *d_logits, hipStream_t stream);
 
+/* The router's balance loss, beside the routing weights' own gradient: with p[t,:] the softmax of token t's logits over
+ * all E experts, n the number of tokens that count and f_e = counts[e] / (n K) each expert's share of the slots,
+ *   loss = coef * E * sum_e f_e * (1/n) sum_t p[t,e]      (coef for a router that spreads its tokens evenly; 0 when n = 0)
+ *   logits [T, E] float32 (-inf: p = 0; a row with nothing but -inf gives p = 0 throughout); topk_idx [T, K], ids outside
+ *   [0, E) count nowhere; token_mask [T] bytes or NULL: tokens with 0 (padding) count nowhere, whatever their logits hold.
+ *   loss [1] float32; counts [E] int32: slots of each expert; prob_sum [E] float32: sum_t p[t,e]; tokens [1] int32: n. With
+ *   tokens on several ranks counts, prob_sum and tokens are what is summed over the ranks (the loss follows from them).
+ * p is float32, its sums and the loss are double, rounded once; no result depends on timing. coef must be finite.
+ * T * K <= 2^31 - 1 (else MOE_ERR_UNSUPPORTED). T = 0 writes zeros. The workspace (16-byte aligned, contents need no
+ * initialisation and mean nothing after the call) must hold moe_balance_loss_workspace_size bytes; calls that may overlap
+ * need one each. */
+moe_status moe_balance_loss_workspace_size(int64_t T, int32_t E, size_t *bytes);
+moe_status moe_balance_loss(const float *logits, const int32_t *topk_idx, const uint8_t *token_mask, int64_t T, int32_t E,
+                            int32_t K, float coef, float *loss, int32_t *counts, float *prob_sum, int32_t *tokens,
+                            void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Backward of moe_balance_loss, from its counts and tokens (or their sums over ranks: the gradient is then that of the loss
+ * of all ranks' tokens):
+ *   d_logits[t,e] = d_loss * coef * (E/n) * p[t,e] * (f_e - sum_j f_j p[t,j])  (+ d_logits_in[t,e])
+ * and 0 (+ d_logits_in) for tokens that do not count, and where n <= 0; the counts, piecewise constant, have no gradient. The
+ * sum over j and the difference are double, the rest float32.
+ *   d_loss [1] float32 (NULL: 1); d_logits_in [T, E] or NULL: the gradient that reaches the logits by other ways
+ *   (moe_route_topk_backward's); d_logits [T, E], which may be d_logits_in. */
+moe_status moe_balance_loss_backward(const float *logits, const uint8_t *token_mask, const int32_t *counts,
+                                     const int32_t *tokens, const float *d_loss, int64_t T, int32_t E, int32_t K,
+                                     float coef, const float *d_logits_in, float *d_logits, hipStream_t stream);
+
 /* Residual addition and RMS norm, the step before an MoE layer's router and dispatch:
  *   h[t,j] = x[t,j] + residual[t,j]   (residual NULL: h = x)
  *   s[t]   = 1 / sqrt(mean_j h[t,j]^2 + eps)
@@ -478,6 +505,38 @@ moe_status moe_few_token_experts(const void *x, moe_dtype dt, int64_t T, int64_t
                                  const void *w_down, moe_dtype weight_dt, const float *gate_up_scales,
                                  const float *down_scales, int32_t block, const void *bias, void *out,
                                  moe_dtype out_dt, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Rows in microscaled 4-bit floating point (the OCP MX format MXFP4): each 32 consecutive elements of a row share a scale, a
+ * power of two, and an element is one of +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} times it:
+ *   amax = max |x|, scale = 2^(floor(log2 amax) - 2), but at least 2^-127; 1 when amax is 0
+ *   code = the nearest of those values to x / scale (a tie goes to the even code, what is above 6 to 6; the sign is kept)
+ *   x [T, H] (x_dt float32 or bf16); H a multiple of 32 (else MOE_ERR_INVALID), at most 2^26.
+ *   q [T, H/2] bytes: two codes each, the even element's in the low half. scales [T, H/32] bytes: the exponent + 127; 255
+ *   (which stands for NaN) for a block that holds a NaN or an infinity, whose codes are 0.
+ * Both are byte rows that the permutes move as MOE_FP8_E4M3 rows of H/2 and H/32 elements. */
+moe_status moe_quantize_mxfp4(const void *x, moe_dtype x_dt, int64_t T, int64_t H, uint8_t *q, uint8_t *scales,
+                              hipStream_t stream);
+
+/* Each expert's product of its rows with its weights, between dispatch and combine ([Scratch] §11-13: the grouped product over
+ * expert-major rows; [Combine] §6 for aligned segments), both operands as moe_quantize_mxfp4's rows:
+ *   y[r, :] = W_e X[r]  for the rows r of expert e's segment; float32 sums, no atomics, an order that depends on the sizes alone
+ *   out[r, n] = y[r, n], or with gated != 0: silu(y[r, n]) * y[r, N + n],  silu(g) = g / (1 + exp(-g)); rounded once
+ *   w [E, N, H/2], w_scales [E, N, H/32]; gated: [E, 2N, ...], expert e's gate rows first, then its up rows.
+ *   X[r] is row r of x, or row src_row[r] of it (a row of zeros where that is outside [0, x_rows)): with
+ *   moe_index.sorted_indices the token rows need not be dispatched first. x [x_rows, H/2], x_scales [x_rows, H/32];
+ *   src_row [R] or NULL (then x_rows >= R).
+ *   Segments: group_list [E] is moe_index.group_list, expert e's rows ending before group_list[e] and beginning where the
+ *   previous expert's end; with counts [E] (may be NULL) only the first counts[e] of them (moe_index.counts with expert
+ *   alignment: the padding rows take no part). capacity > 0 is the drop-and-pad layout: the first counts[e]
+ *   (moe_index.kept_counts) rows from e * capacity, group_list is not read, R >= E * capacity.
+ *   out [R, N] (float32 or bf16), which overlaps no input. Rows in no segment are left untouched. Segments are cut to [0, R);
+ *   ones that overlap give unspecified rows.
+ * Rows are independent: a NaN scale makes NaN of its own row or column alone. H a multiple of 32 (else MOE_ERR_INVALID);
+ * H, N <= 2^20, x and w 16-byte aligned (else MOE_ERR_UNSUPPORTED). */
+moe_status moe_grouped_product_mxfp4(const uint8_t *x, const uint8_t *x_scales, int64_t x_rows, const int32_t *src_row,
+                                     int64_t R, int64_t H, const uint8_t *w, const uint8_t *w_scales, int32_t E, int64_t N,
+                                     int32_t gated, const int32_t *group_list, const int32_t *counts, int32_t capacity,
+                                     void *out, moe_dtype out_dt, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -63,6 +63,12 @@ SIGNATURES = {
                                            _i32, _P, _P, _dt, _P, _P, _P, _size, _P]),
     "moe_few_token_experts": (ctypes.c_int, [_P, _dt, _i64, _i64, _i64, _i32, _i32, _P, _P, _P, _P, _dt, _P, _P, _i32,
                                              _P, _P, _dt, _P, _size, _P]),
+    "moe_balance_loss_workspace_size": (ctypes.c_int, [_i64, _i32, ctypes.POINTER(_size)]),
+    "moe_balance_loss": (ctypes.c_int, [_P, _P, _P, _i64, _i32, _i32, _f32, _P, _P, _P, _P, _P, _size, _P]),
+    "moe_balance_loss_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _i64, _i32, _i32, _f32, _P, _P, _P]),
+    "moe_quantize_mxfp4": (ctypes.c_int, [_P, _dt, _i64, _i64, _P, _P, _P]),
+    "moe_grouped_product_mxfp4": (ctypes.c_int, [_P, _P, _i64, _P, _i64, _i64, _P, _P, _i32, _i64, _i32, _P, _P, _i32, _P,
+                                                 _dt, _P]),
 }
 
 

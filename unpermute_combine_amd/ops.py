@@ -824,3 +824,150 @@ def few_token_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: Optional[
         _p(x), x_dt, T, H, I, E, K, _p(topk_idx), _p(topk_w), _p(w_gate_up), _p(w_down), w_dt, _p(gate_up_scales),
         _p(down_scales), block, _p(bias), _p(out), o_dt, _p(workspace), workspace.numel(), _stream()))
     return out
+
+
+# ---------------------------------------------------------------- the router's balance loss
+
+
+@functools.lru_cache(maxsize=256)
+def balance_workspace_bytes(T: int, E: int) -> int:
+    """Workspace bytes of balance_loss for these sizes."""
+    n = ctypes.c_size_t(0)
+    check("moe_balance_loss_workspace_size", lib().moe_balance_loss_workspace_size(T, E, ctypes.byref(n)))
+    return int(n.value)
+
+
+def _token_mask(mask, T):
+    if mask is None:
+        return None
+    if not isinstance(mask, torch.Tensor) or mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError("token_mask must be a bool or uint8 tensor")
+    _need(mask, "token_mask", None, 1)
+    if mask.shape[0] != T:
+        raise ValueError(f"token_mask must have {T} elements")
+    return mask.data_ptr()
+
+
+def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, coef: float = 1.0, token_mask: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None):
+    """coef * E * sum_e f_e P_e, f_e the share of expert e of the routed slots and P_e the mean of its probability in the
+    softmax over all E logits, over the tokens that token_mask (bool or uint8 [T]; None: all) keeps.
+
+    Returns (loss float32 [], counts int32 [E], prob_sum float32 [E], tokens int32 [1]): slots of each expert, sums of its
+    probability and the number of tokens counted, for balance_loss_backward and for sums over ranks."""
+    _need(logits, "logits", torch.float32, 2)
+    T, E = logits.shape
+    _need(topk_idx, "topk_idx", torch.int32, 2)
+    if topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must have one row per row of logits")
+    mask = _token_mask(token_mask, T)
+    loss, prob_sum = logits.new_empty(()), logits.new_empty(E)
+    counts, tokens = topk_idx.new_empty(E), topk_idx.new_empty(1)
+    if workspace is None:
+        nbytes = balance_workspace_bytes(T, E)
+        workspace = logits.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    else:
+        nbytes = _need(workspace, "workspace", torch.uint8, 1).numel()
+    check("moe_balance_loss", lib().moe_balance_loss(
+        _p(logits), _p(topk_idx), mask, T, E, topk_idx.shape[1], coef, _p(loss), _p(counts), _p(prob_sum), _p(tokens),
+        _p(workspace), nbytes, _stream()))
+    return loss, counts, prob_sum, tokens
+
+
+def balance_loss_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor, k: int,
+                          d_loss: Optional[torch.Tensor] = None, coef: float = 1.0, token_mask: Optional[torch.Tensor] = None,
+                          d_logits: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of the logits [T, E] through balance_loss, from its counts and tokens (of all ranks, where they were summed);
+    d_loss a float32 tensor of one element (None: 1). d_logits, the gradient that reaches the logits by other ways
+    (route_topk_backward's), is added; out may be d_logits."""
+    _need(logits, "logits", torch.float32, 2)
+    T, E = logits.shape
+    _need(counts, "counts", torch.int32, 1)
+    _need(tokens, "tokens", torch.int32)
+    if counts.shape[0] != E or tokens.numel() != 1:
+        raise ValueError(f"counts must have {E} elements and tokens one")
+    if d_loss is not None and _need(d_loss, "d_loss", torch.float32).numel() != 1:
+        raise ValueError("d_loss must have one element")
+    mask = _token_mask(token_mask, T)
+    if d_logits is not None and _need(d_logits, "d_logits", torch.float32, 2).shape != logits.shape:
+        raise ValueError(f"d_logits must be [{T}, {E}]")
+    if out is None:
+        out = torch.empty_like(logits)
+    elif _need(out, "out", torch.float32, 2).shape != logits.shape:
+        raise ValueError(f"out must be [{T}, {E}]")
+    check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
+        _p(logits), mask, _p(counts), _p(tokens), _p(d_loss), T, E, k, coef, _p(d_logits), _p(out), _stream()))
+    return out
+
+
+# ---------------------------------------------------------------- 4-bit rows and the experts' products
+
+
+def quantize_mxfp4(x: torch.Tensor, out=None):
+    """Rows in microscaled 4-bit floating point (MXFP4): q [T, H/2] uint8, two E2M1 codes a byte (the even element's in the low
+    half), and scales [T, H/32] uint8, exponent + 127 of each 32 elements' power of two. H a multiple of 32."""
+    _need(x, "x", None, 2)
+    dt = _row_dt(x.dtype, "x")
+    T, H = x.shape
+    if H < 1 or H % 32:
+        raise ValueError("rows must be a multiple of 32 elements")
+    q, sc = (None, None) if out is None else out
+    q = x.new_empty((T, H // 2), dtype=torch.uint8) if q is None else _need(q, "q", torch.uint8, 2)
+    sc = x.new_empty((T, H // 32), dtype=torch.uint8) if sc is None else _need(sc, "scales", torch.uint8, 2)
+    if tuple(q.shape) != (T, H // 2) or tuple(sc.shape) != (T, H // 32):
+        raise ValueError(f"output shapes must be [{T}, {H // 2}] and [{T}, {H // 32}]")
+    check("moe_quantize_mxfp4", lib().moe_quantize_mxfp4(_p(x), dt, T, H, _p(q), _p(sc), _stream()))
+    return q, sc
+
+
+def grouped_product_mxfp4(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                          group_list: Optional[torch.Tensor], counts: Optional[torch.Tensor] = None, capacity: int = 0,
+                          src_row: Optional[torch.Tensor] = None, gated: bool = False,
+                          out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Each expert's product of its rows with its weights: out[r] = W_e X[r] (gated: silu(G_e X[r]) * (U_e X[r]), w holding the
+    gate's rows before the up's), all as quantize_mxfp4 gives them: x [., H/2] with x_scales [., H/32], w [E, N, H/2] (gated:
+    [E, 2N, H/2]) with w_scales. X[r] is row r of x, or row src_row[r] (index.sorted_indices: the tokens' rows, not dispatched).
+
+    Segments are an index's: group_list; with expert alignment counts=index.counts too; drop-and-pad counts=index.kept_counts
+    and capacity (group_list is not read). Rows of out in no segment are left as they are. Returns out [R, N]."""
+    _need(x, "x", torch.uint8, 2)
+    _need(x_scales, "x_scales", torch.uint8, 2)
+    _need(w, "w", torch.uint8, 3)
+    _need(w_scales, "w_scales", torch.uint8, 3)
+    rows, half = x.shape
+    E, wrows, _ = w.shape
+    nb = half // 16
+    if half < 16 or half % 16 or w.shape[2] != half:
+        raise ValueError("rows of x and w must have the same H, a multiple of 32")
+    if tuple(x_scales.shape) != (rows, nb) or tuple(w_scales.shape) != (E, wrows, nb):
+        raise ValueError(f"scales must be [{rows}, {nb}] and [{E}, {wrows}, {nb}]")
+    if gated and wrows % 2:
+        raise ValueError("gated weights hold as many gate rows as up rows")
+    N = wrows // 2 if gated else wrows
+    if group_list is not None:
+        _need(group_list, "group_list", torch.int32, 1)
+    if counts is not None:
+        _need(counts, "counts", torch.int32, 1)
+    if capacity > 0:
+        if counts is None:
+            raise ValueError("the drop-and-pad layout needs counts")
+    elif group_list is None:
+        raise ValueError("group_list is needed without capacity")
+    for t in (group_list, counts):
+        if t is not None and t.shape[0] != E:
+            raise ValueError(f"group_list and counts must have {E} elements")
+    if src_row is not None:
+        _need(src_row, "src_row", torch.int32, 1)
+        R = src_row.shape[0]
+    else:
+        R = rows
+    if out is None:
+        out = torch.empty((R, N), dtype=out_dtype, device=x.device)
+    else:
+        _need(out, "out", None, 2)
+        if tuple(out.shape) != (R, N):
+            raise ValueError(f"out must be [{R}, {N}]")
+    check("moe_grouped_product_mxfp4", lib().moe_grouped_product_mxfp4(
+        _p(x), _p(x_scales), rows, _p(src_row), R, half * 2, _p(w), _p(w_scales), E, N, int(gated), _p(group_list),
+        _p(counts), capacity, _p(out), _row_dt(out.dtype, "out"), _stream()))
+    return out
