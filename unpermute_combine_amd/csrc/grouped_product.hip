@@ -46,15 +46,18 @@ __device__ __forceinline__ void segment(const ProductArgs &a, int e, int64_t &st
     len = end - start;
 }
 
+// A workgroup's share: columns from `col` tiles on, of `rows` rows from `first` on, of expert e.
 struct Tile {
-    int32_t e;      // expert, -1: no such tile
-    int32_t rows;   // rows of the tile
-    int64_t first;  // its first row
+    int32_t e;      // -1: none
+    int32_t rows;
+    int64_t first;
+    int32_t col;
 };
 
-// The m-th tile of BM rows, experts in order. Every thread of a workgroup of kPlanThreads calls it and gets the same.
+// The i-th of the (rows, columns) tiles of BM rows, experts in order, an expert's tiles of the same columns beside each other.
+// Every thread of a workgroup of kPlanThreads calls it and gets the same.
 template <int BM>
-__device__ __forceinline__ Tile find_tile(const ProductArgs &a, int64_t m)
+__device__ __forceinline__ Tile find_tile(const ProductArgs &a, int64_t i)
 {
     __shared__ int64_t wave_tiles[kPlanThreads / kWave];
     __shared__ Tile found;
@@ -63,13 +66,13 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs &a, int64_t m)
     const int e0 = threadIdx.x * per;
     int64_t tiles[kPer], mine = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        tiles[i] = 0;
-        if (i < per && e0 + i < a.E) {
+    for (int j = 0; j < kPer; ++j) {
+        tiles[j] = 0;
+        if (j < per && e0 + j < a.E) {
             int64_t start, len;
-            segment(a, e0 + i, start, len);
-            tiles[i] = ceil_div(len, BM);
-            mine += tiles[i];
+            segment(a, e0 + j, start, len);
+            tiles[j] = ceil_div(len, BM);
+            mine += tiles[j];
         }
     }
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
@@ -82,21 +85,23 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs &a, int64_t m)
     if (lane == kWave - 1)
         wave_tiles[wave] = upto;
     if (threadIdx.x == 0)
-        found = Tile{-1, 0, 0};
+        found = Tile{-1, 0, 0, 0};
     __syncthreads();
     int64_t before = upto - mine;
     for (int v = 0; v < wave; ++v)
         before += wave_tiles[v];
-    if (m >= before && m < before + mine) {
-        int64_t k = m - before;
+    int64_t k = i - before * a.col_tiles;
+    if (k >= 0 && k < mine * a.col_tiles) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (k >= 0 && k < tiles[i]) {
+        for (int j = 0; j < kPer; ++j) {
+            if (k >= 0 && k < tiles[j] * a.col_tiles) {
                 int64_t start, len;
-                segment(a, e0 + i, start, len);
-                found = Tile{e0 + i, static_cast<int32_t>(min(len - k * BM, int64_t{BM})), start + k * BM};
+                segment(a, e0 + j, start, len);
+                const int64_t m = k % tiles[j];
+                found = Tile{e0 + j, static_cast<int32_t>(min(len - m * BM, int64_t{BM})), start + m * BM,
+                             static_cast<int32_t>(k / tiles[j])};
             }
-            k -= tiles[i];
+            k -= tiles[j] * a.col_tiles;
         }
     }
     __syncthreads();
@@ -125,11 +130,11 @@ __device__ __forceinline__ void load_block(const uint8_t *codes, const uint8_t *
 template <typename O, bool GATED>
 __global__ __launch_bounds__(kPlanThreads) void grouped_product_kernel(ProductArgs a)
 {
-    const Tile tile = find_tile<16>(a, blockIdx.x / a.col_tiles);
+    const Tile tile = find_tile<16>(a, blockIdx.x);
     if (tile.e < 0)
         return;
     const int lane = threadIdx.x & (kWave - 1), r = lane & 15, g = lane >> 4;
-    const int64_t n0 = (static_cast<int64_t>(blockIdx.x % a.col_tiles) * (kPlanThreads / kWave) + threadIdx.x / kWave) * 16;
+    const int64_t n0 = (static_cast<int64_t>(tile.col) * (kPlanThreads / kWave) + threadIdx.x / kWave) * 16;
     if (n0 >= a.N)
         return;
     const int64_t blocks = a.H / kMxBlock;
@@ -161,12 +166,253 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_product_kernel(ProductAr
     }
 }
 
+// ---------------------------------------------------------------- tiles through LDS
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kTileRows = 256, kTileCols = 256;  // rows and weight rows of the largest tile
+constexpr int kStageBytes = 128;                 // of each row a stage: 256 elements, a cache line
+constexpr int kStageBlocks = kStageBytes / 16;
+
+// The 16-byte chunk c of row r lies in slot c ^ swizzle(r) of its 128 bytes: 8 and 16 consecutive rows' same chunk fall into
+// different banks.
+__device__ __forceinline__ int swizzle(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+struct Buffers {
+    uint8_t codes[2][(kTileRows + kTileCols) * kStageBytes];
+    uint64_t scales[2][kTileRows + kTileCols];
+};
+
+// Scale bytes of 8 blocks of a row from block b on, 1.0 past its end.
+__device__ __forceinline__ uint64_t load_scales(const uint8_t *row, int b, int blocks)
+{
+    uint64_t v;
+    if (b + 8 <= blocks) {
+        __builtin_memcpy(&v, row + b, 8);
+        return v;
+    }
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v |= static_cast<uint64_t>(b + i < blocks ? row[b + i] : 127) << (8 * i);
+    return v;
+}
+
+__device__ __forceinline__ void to_lds(const uint8_t *from, uint8_t *to)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                     (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+}
+
+// A tile of up to 32 MS WM rows by 256 weight rows (gated: 128 of the gate and 128 of the up), four wavefronts, WM beside each
+// other along the rows: a wavefront has 32 MS rows by 32 NS weight rows.
+template <typename O, bool GATED, int MS, int NS, int WM>
+__device__ __forceinline__ void tile_product(const ProductArgs &a, const Tile &tile, Buffers &sh)
+{
+    constexpr int kRows = 32 * MS * WM, kWN = 4 / WM;  // wavefronts along the columns
+    static_assert(32 * NS * kWN == kTileCols, "");
+    constexpr int kWaveCols = 32 * NS, kHalf = kWaveCols / 2;
+    constexpr int kOutCols = GATED ? kTileCols / 2 : kTileCols;
+    constexpr int kXLoads = kRows / 32, kWLoads = kTileCols / 32;  // 16-byte loads a thread and stage
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int blocks = static_cast<int>(a.H / kMxBlock), stages = (blocks + kStageBlocks - 1) / kStageBlocks;
+    const int64_t row_bytes = a.H / 2, n0 = static_cast<int64_t>(tile.col) * kOutCols;
+    const uint8_t *xbase = a.x_rows > 0 ? a.x : a.w, *xsbase = a.x_rows > 0 ? a.xs : a.ws;
+
+    // the row of x behind row r of the tile (any one where there is none: the epilogue drops it)
+    auto x_row = [&](int r) -> int64_t {
+        int64_t row = tile.first + min(r, tile.rows - 1);
+        if (a.src_row) {
+            row = a.src_row[row];
+            row = row >= 0 && row < a.x_rows ? row : 0;
+        }
+        return row;
+    };
+    // the weight row behind row b of the tile's weights: gated, a wavefront's first half are gates and its second the ups of them
+    auto w_row = [&](int b) -> int64_t {
+        if (!GATED)
+            return tile.e * a.N + min(n0 + b, a.N - 1);
+        const int in = b % kWaveCols;
+        const int64_t n = min(n0 + b / kWaveCols * kHalf + in % kHalf, a.N - 1);
+        return tile.e * 2 * a.N + n + (in >= kHalf ? a.N : 0);
+    };
+
+    // thread t loads chunk slot t % 8 of rows t / 8 + 32 j
+    const int chunk = (lane & 7) ^ swizzle(threadIdx.x / 8);
+    const uint8_t *xp[kXLoads], *wp[kWLoads];
+#pragma unroll
+    for (int j = 0; j < kXLoads; ++j)
+        xp[j] = xbase + x_row(threadIdx.x / 8 + 32 * j) * row_bytes;
+#pragma unroll
+    for (int j = 0; j < kWLoads; ++j)
+        wp[j] = a.w + w_row(threadIdx.x / 8 + 32 * j) * row_bytes;
+    const uint8_t *xsp = xsbase + x_row(min(static_cast<int>(threadIdx.x), kRows - 1)) * blocks;
+    const uint8_t *wsp = a.ws + w_row(threadIdx.x) * blocks;
+
+    auto issue = [&](int s) {
+        uint8_t *to = sh.codes[s & 1] + wave * 8 * kStageBytes;
+        const int at = min(s * kStageBlocks + chunk, blocks - 1) * 16;  // past the end: any chunk
+#pragma unroll
+        for (int j = 0; j < kXLoads; ++j)
+            to_lds(xp[j] + at, to + 32 * j * kStageBytes);
+#pragma unroll
+        for (int j = 0; j < kWLoads; ++j)
+            to_lds(wp[j] + at, to + (kTileRows + 32 * j) * kStageBytes);
+    };
+    uint64_t xsc, wsc;
+    auto load_sc = [&](int s) {
+        xsc = load_scales(xsp, s * kStageBlocks, blocks);
+        wsc = load_scales(wsp, s * kStageBlocks, blocks);
+    };
+    auto store_sc = [&](int s) {
+        if (threadIdx.x < kRows)
+            sh.scales[s & 1][threadIdx.x] = xsc;
+        sh.scales[s & 1][kTileRows + threadIdx.x] = wsc;
+    };
+    // chunks past the end of the rows: zeros for x (the weights' are some codes, and zero times them is zero)
+    auto clear_tail = [&]() {
+        if (blocks % kStageBlocks == 0)
+            return;
+        uint8_t *x = sh.codes[(stages - 1) & 1];
+        for (int i = threadIdx.x; i < kRows * kStageBlocks; i += kPlanThreads) {
+            const int r = i / kStageBlocks, c = i % kStageBlocks;
+            if (c >= blocks % kStageBlocks)
+                *reinterpret_cast<i32x4 *>(x + r * kStageBytes + (c ^ swizzle(r)) * 16) = i32x4{0, 0, 0, 0};
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    auto arrive = [&](int s) {  // stage s has come, for every wavefront
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (s == stages - 1)
+            clear_tail();
+    };
+
+    const int half = lane >> 5, r32 = lane & 31;
+    const int x0 = (wave % WM) * 32 * MS + r32, w0 = kTileRows + (wave / WM) * kWaveCols + r32;
+    const int swz = swizzle(r32);
+    auto frag = [&](int s, int row, int ks) -> i32x8 {
+        const i32x4 v = *reinterpret_cast<const i32x4 *>(sh.codes[s & 1] + row * kStageBytes + ((4 * half + ks) ^ swz) * 16);
+        return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
+    };
+    auto scale = [&](int s, int row) -> int {
+        return reinterpret_cast<const int *>(sh.scales[s & 1] + row)[half];
+    };
+
+    f32x16 acc[NS][MS];
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int m = 0; m < MS; ++m)
+            acc[n][m] = f32x16{};
+    issue(0);
+    load_sc(0);
+    store_sc(0);
+    if (stages > 1)
+        load_sc(1);
+    arrive(0);
+    for (int s = 0; s < stages; ++s) {
+        if (s > 0)
+            arrive(s);
+        if (s + 1 < stages) {
+            issue(s + 1);
+            store_sc(s + 1);
+            if (s + 2 < stages)
+                load_sc(s + 2);
+        }
+        int xs[MS], ws[NS];
+#pragma unroll
+        for (int m = 0; m < MS; ++m)
+            xs[m] = scale(s, x0 + 32 * m);
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+            ws[n] = scale(s, w0 + 32 * n);
+#define MOE_STEP(KS)                                                                                              \
+    do {                                                                                                          \
+        i32x8 fx[MS], fw[NS];                                                                                     \
+        _Pragma("unroll") for (int m = 0; m < MS; ++m) fx[m] = frag(s, x0 + 32 * m, KS);                           \
+        _Pragma("unroll") for (int n = 0; n < NS; ++n) fw[n] = frag(s, w0 + 32 * n, KS);                           \
+        _Pragma("unroll") for (int n = 0; n < NS; ++n)                                                            \
+            _Pragma("unroll") for (int m = 0; m < MS; ++m)                                                        \
+                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[n], fx[m], acc[n][m], kFp4, kFp4,  \
+                                                                            KS, ws[n], KS, xs[m]);                \
+    } while (0)
+        MOE_STEP(0);
+        MOE_STEP(1);
+        MOE_STEP(2);
+        MOE_STEP(3);
+#undef MOE_STEP
+    }
+    // lane l holds row l % 32 of x and, in each four registers, four consecutive weight rows
+#pragma unroll
+    for (int m = 0; m < MS; ++m) {
+        const int r = (wave % WM) * 32 * MS + 32 * m + r32;
+        if (r >= tile.rows)
+            continue;
+        const int64_t row = tile.first + r;
+        bool there = true;
+        if (a.src_row) {
+            const int64_t from = a.src_row[row];
+            there = from >= 0 && from < a.x_rows;
+        }
+        O *out = static_cast<O *>(a.out) + row * a.N;
+#pragma unroll
+        for (int n = 0; n < (GATED ? NS / 2 : NS); ++n) {
+            const int64_t c0 = n0 + (wave / WM) * (GATED ? kHalf : kWaveCols) + 32 * n + 4 * half;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                const int64_t c = c0 + 8 * (q / 4) + q % 4;
+                const float v = GATED ? silu(acc[n][m][q]) * acc[n + NS / 2][m][q] : acc[n][m][q];
+                if (c < a.N)
+                    store_out(out + c, there ? v : 0.0f);
+            }
+        }
+    }
+}
+
+// Workgroup b of nb, dealt to the XCDs in turn, takes the place that keeps runs of kRun neighbours on one XCD.
+constexpr uint32_t kRun = 16;
+__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t nb)
+{
+    const uint32_t round = b / (kXcds * kRun), in = b % (kXcds * kRun);
+    return (round + 1) * kXcds * kRun > nb ? b : round * kXcds * kRun + in % kXcds * kRun + in / kXcds;
+}
+
+template <typename O, bool GATED>
+__global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs a)
+{
+    __shared__ __attribute__((aligned(128))) Buffers sh;
+    const Tile tile = find_tile<kTileRows>(a, xcd_run(blockIdx.x, gridDim.x));
+    if (tile.e < 0)
+        return;
+    if (tile.rows > 128)
+        tile_product<O, GATED, 4, 4, 2>(a, tile, sh);
+    else if (tile.rows > 64)
+        tile_product<O, GATED, 4, 2, 1>(a, tile, sh);
+    else if (tile.rows > 32)
+        tile_product<O, GATED, 2, 2, 1>(a, tile, sh);
+    else
+        tile_product<O, GATED, 1, 2, 1>(a, tile, sh);
+}
+
 // Tiles of BM rows that R rows in E segments can need.
 int64_t max_tiles(int64_t R, int64_t E, int64_t BM) { return R / BM + std::min(R, E); }
 
 template <typename O, bool GATED>
 moe_status launch_product(ProductArgs a, hipStream_t stream)
 {
+    if (a.R > 16 * static_cast<int64_t>(a.E)) {
+        a.col_tiles = static_cast<uint32_t>(ceil_div(a.N, GATED ? kTileCols / 2 : kTileCols));
+        const int64_t grid = max_tiles(a.R, a.E, kTileRows) * a.col_tiles;
+        if (grid > 0x7fffffff)
+            return MOE_ERR_UNSUPPORTED;
+        hipLaunchKernelGGL((grouped_tile_kernel<O, GATED>), dim3(static_cast<unsigned>(grid)), dim3(kPlanThreads), 0, stream, a);
+        return launch_status();
+    }
     a.col_tiles = static_cast<uint32_t>(ceil_div(a.N, 16 * (kPlanThreads / kWave)));
     const int64_t grid = max_tiles(a.R, a.E, 16) * a.col_tiles;
     if (grid > 0x7fffffff)
