@@ -113,6 +113,13 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 __device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(uint16_t *p, float v) { *p = static_cast<uint16_t>(f32_to_bf16_bits(v)); }
 
+// Four values into LDS.
+__device__ __forceinline__ void put4(float *p, const float (&v)[4]) { *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]}; }
+__device__ __forceinline__ void put4(uint16_t *p, const float (&v)[4])
+{
+    *reinterpret_cast<uint64_t *>(p) = pack_bf16x2(v[0], v[1]) | static_cast<uint64_t>(pack_bf16x2(v[2], v[3])) << 32;
+}
+
 // A lane's block of a row: zeros where there is none (block >= blocks or no row).
 __device__ __forceinline__ void load_block(const uint8_t *codes, const uint8_t *scales, int64_t row, int64_t blocks, int64_t b,
                                            bool there, i32x8 &v, int &scale)
@@ -347,30 +354,53 @@ __device__ __forceinline__ void tile_product(const ProductArgs &a, const Tile &t
         MOE_STEP(3);
 #undef MOE_STEP
     }
-    // lane l holds row l % 32 of x and, in each four registers, four consecutive weight rows
+    // Lane l holds row l % 32 of x and, in each four registers, four consecutive weight rows. 32 rows at a time go through LDS, a
+    // wavefront's own part of it, and out in whole vectors of a row.
+    constexpr int kOut = GATED ? kHalf : kWaveCols, kPad = 16 / sizeof(O), kPitch = kOut + kPad, kVec = 16 / sizeof(O);
+    static_assert(4 * 32 * kPitch * sizeof(O) <= sizeof(sh.codes), "");
+    __syncthreads();
+    O *part = reinterpret_cast<O *>(&sh.codes[0][0]) + wave * 32 * kPitch;
+    const int64_t c0 = n0 + (wave / WM) * kOut;
+    const int cols = static_cast<int>(min(static_cast<int64_t>(kOut), a.N - c0));
+    const bool vectors = a.N % kVec == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
 #pragma unroll
     for (int m = 0; m < MS; ++m) {
-        const int r = (wave % WM) * 32 * MS + 32 * m + r32;
-        if (r >= tile.rows)
-            continue;
-        const int64_t row = tile.first + r;
+        const int r0 = (wave % WM) * 32 * MS + 32 * m, rows = min(32, tile.rows - r0);
+        if (rows <= 0)
+            break;
         bool there = true;
-        if (a.src_row) {
-            const int64_t from = a.src_row[row];
+        if (a.src_row && r32 < rows) {
+            const int64_t from = a.src_row[tile.first + r0 + r32];
             there = from >= 0 && from < a.x_rows;
         }
-        O *out = static_cast<O *>(a.out) + row * a.N;
 #pragma unroll
-        for (int n = 0; n < (GATED ? NS / 2 : NS); ++n) {
-            const int64_t c0 = n0 + (wave / WM) * (GATED ? kHalf : kWaveCols) + 32 * n + 4 * half;
+        for (int n = 0; n < (GATED ? NS / 2 : NS); ++n)
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                const int64_t c = c0 + 8 * (q / 4) + q % 4;
-                const float v = GATED ? silu(acc[n][m][q]) * acc[n + NS / 2][m][q] : acc[n][m][q];
-                if (c < a.N)
-                    store_out(out + c, there ? v : 0.0f);
+            for (int q = 0; q < 16; q += 4) {
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = GATED ? silu(acc[n][m][q + i]) * acc[n + NS / 2][m][q + i] : acc[n][m][q + i];
+                    v[i] = there ? v[i] : 0.0f;
+                }
+                put4(part + r32 * kPitch + 32 * n + 2 * q + 4 * half, v);
             }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        O *out = static_cast<O *>(a.out) + (tile.first + r0) * a.N + c0;
+        if (vectors) {
+            constexpr int kLanes = kOut / kVec;  // lanes a row
+#pragma unroll
+            for (int i = 0; i < 32 * kLanes / kWave; ++i) {
+                const int r = i * (kWave / kLanes) + lane / kLanes, c = lane % kLanes * kVec;
+                if (r < rows && c < cols)
+                    st16(out + r * a.N + c, ld16(part + r * kPitch + c));
+            }
+        } else {
+            for (int r = 0; r < rows; ++r)
+                for (int c = lane; c < cols; c += kWave)
+                    out[r * a.N + c] = part[r * kPitch + c];
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
