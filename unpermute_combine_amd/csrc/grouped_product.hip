@@ -4,6 +4,7 @@
 // A matrix instruction (v_mfma_scale_f32_16x16x128) takes 16 rows of each operand by 128 elements: lane l holds the 32
 // elements of block l / 16 of row l % 16, and the block's scale.
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_common.h"
 
@@ -191,26 +192,40 @@ struct Buffers {
     uint64_t scales[2][kTileRows + kTileCols];
 };
 
-// Scale bytes of 8 blocks of a row from block b on, 1.0 past its end.
+// Scale bytes of 8 blocks of a row from block b on, the last 8 of the row where fewer are left (rows of 8 blocks at least).
 __device__ __forceinline__ uint64_t load_scales(const uint8_t *row, int b, int blocks)
 {
     uint64_t v;
-    if (b + 8 <= blocks) {
-        __builtin_memcpy(&v, row + b, 8);
-        return v;
-    }
-    v = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v |= static_cast<uint64_t>(b + i < blocks ? row[b + i] : 127) << (8 * i);
+    __builtin_memcpy(&v, row + min(b, blocks - 8), 8);
     return v;
 }
 
-__device__ __forceinline__ void to_lds(const uint8_t *from, uint8_t *to)
+// Of what load_scales gave, the bytes from block b on in their places; past the row's end any but NaN.
+__device__ __forceinline__ uint64_t placed_scales(uint64_t v, int b, int blocks)
+{
+    return v >> (8 * (b - min(b, blocks - 8)));
+}
+
+// The scale bytes of a row of fewer than 8 blocks.
+__device__ __forceinline__ uint64_t short_scales(const uint8_t *row, int blocks)
+{
+    uint64_t v = 0;
+    for (int i = 0; i < blocks; ++i)
+        v |= static_cast<uint64_t>(row[i]) << (8 * i);
+    return v;
+}
+
+// 16 bytes a lane into LDS, lane l's to address `to` + 16 l (one for the wavefront).
+__device__ __forceinline__ void to_lds(const uint8_t *from, uint32_t to)
 {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                     (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+                                     reinterpret_cast<__attribute__((address_space(3))) void *>(to), 16, 0, 0);
 }
+
+template <int MS, int NS>
+struct Frags {
+    i32x8 x[MS], w[NS];
+};
 
 // A tile of up to 32 MS WM rows by 256 weight rows (gated: 128 of the gate and 128 of the up), four wavefronts, WM beside each
 // other along the rows: a wavefront has 32 MS rows by 32 NS weight rows.
@@ -222,7 +237,7 @@ __device__ __forceinline__ void tile_product(const ProductArgs &a, const Tile &t
     constexpr int kWaveCols = 32 * NS, kHalf = kWaveCols / 2;
     constexpr int kOutCols = GATED ? kTileCols / 2 : kTileCols;
     constexpr int kXLoads = kRows / 32, kWLoads = kTileCols / 32;  // 16-byte loads a thread and stage
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / kWave));
     const int blocks = static_cast<int>(a.H / kMxBlock), stages = (blocks + kStageBlocks - 1) / kStageBlocks;
     const int64_t row_bytes = a.H / 2, n0 = static_cast<int64_t>(tile.col) * kOutCols;
     const uint8_t *xbase = a.x_rows > 0 ? a.x : a.w, *xsbase = a.x_rows > 0 ? a.xs : a.ws;
@@ -257,8 +272,12 @@ __device__ __forceinline__ void tile_product(const ProductArgs &a, const Tile &t
     const uint8_t *xsp = xsbase + x_row(min(static_cast<int>(threadIdx.x), kRows - 1)) * blocks;
     const uint8_t *wsp = a.ws + w_row(threadIdx.x) * blocks;
 
+    // The stages' addresses as plain numbers: of what it sees to lie in the array the compiler would wait for every load under
+    // way into it, those of the next stage included, before each read. What a read needs has come by `meet`.
+    uint32_t codes = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)&sh.codes[0][0]));
+    asm volatile("" : "+s"(codes));
     auto issue = [&](int s) {
-        uint8_t *to = sh.codes[s & 1] + wave * 8 * kStageBytes;
+        const uint32_t to = codes + (s & 1) * sizeof(sh.codes[0]) + wave * 8 * kStageBytes;
         const int at = min(s * kStageBlocks + chunk, blocks - 1) * 16;  // past the end: any chunk
 #pragma unroll
         for (int j = 0; j < kXLoads; ++j)
@@ -268,14 +287,13 @@ __device__ __forceinline__ void tile_product(const ProductArgs &a, const Tile &t
             to_lds(wp[j] + at, to + (kTileRows + 32 * j) * kStageBytes);
     };
     uint64_t xsc, wsc;
-    auto load_sc = [&](int s) {
+    auto load_sc = [&](int s) {  // (past the last stage: what nothing uses)
         xsc = load_scales(xsp, s * kStageBlocks, blocks);
         wsc = load_scales(wsp, s * kStageBlocks, blocks);
     };
     auto store_sc = [&](int s) {
-        if (threadIdx.x < kRows)
-            sh.scales[s & 1][threadIdx.x] = xsc;
-        sh.scales[s & 1][kTileRows + threadIdx.x] = wsc;
+        sh.scales[s & 1][threadIdx.x] = placed_scales(xsc, s * kStageBlocks, blocks);
+        sh.scales[s & 1][kTileRows + threadIdx.x] = placed_scales(wsc, s * kStageBlocks, blocks);
     };
     // chunks past the end of the rows: zeros for x (the weights' are some codes, and zero times them is zero)
     auto clear_tail = [&]() {
@@ -291,19 +309,12 @@ __device__ __forceinline__ void tile_product(const ProductArgs &a, const Tile &t
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
-    auto arrive = [&](int s) {  // stage s has come, for every wavefront
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (s == stages - 1)
-            clear_tail();
-    };
-
     const int half = lane >> 5, r32 = lane & 31;
     const int x0 = (wave % WM) * 32 * MS + r32, w0 = kTileRows + (wave / WM) * kWaveCols + r32;
     const int swz = swizzle(r32);
     auto frag = [&](int s, int row, int ks) -> i32x8 {
-        const i32x4 v = *reinterpret_cast<const i32x4 *>(sh.codes[s & 1] + row * kStageBytes + ((4 * half + ks) ^ swz) * 16);
+        const uint32_t at = codes + (s & 1) * sizeof(sh.codes[0]) + row * kStageBytes + ((4 * half + ks) ^ swz) * 16;
+        const i32x4 v = *reinterpret_cast<const __attribute__((address_space(3))) i32x4 *>(at);
         return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
     };
     auto scale = [&](int s, int row) -> int {
@@ -316,44 +327,102 @@ __device__ __forceinline__ void tile_product(const ProductArgs &a, const Tile &t
 #pragma unroll
         for (int m = 0; m < MS; ++m)
             acc[n][m] = f32x16{};
-    issue(0);
-    load_sc(0);
-    store_sc(0);
-    if (stages > 1)
-        load_sc(1);
-    arrive(0);
-    for (int s = 0; s < stages; ++s) {
-        if (s > 0)
-            arrive(s);
-        if (s + 1 < stages) {
-            issue(s + 1);
-            store_sc(s + 1);
-            if (s + 2 < stages)
-                load_sc(s + 2);
-        }
-        int xs[MS], ws[NS];
+    Frags<MS, NS> f[2];
+    int xs[2][MS], ws[2][NS];
+    auto read = [&](int s, int ks, Frags<MS, NS> &to) {
 #pragma unroll
         for (int m = 0; m < MS; ++m)
-            xs[m] = scale(s, x0 + 32 * m);
+            to.x[m] = frag(s, x0 + 32 * m, ks);
 #pragma unroll
         for (int n = 0; n < NS; ++n)
-            ws[n] = scale(s, w0 + 32 * n);
-#define MOE_STEP(KS)                                                                                              \
-    do {                                                                                                          \
-        i32x8 fx[MS], fw[NS];                                                                                     \
-        _Pragma("unroll") for (int m = 0; m < MS; ++m) fx[m] = frag(s, x0 + 32 * m, KS);                           \
-        _Pragma("unroll") for (int n = 0; n < NS; ++n) fw[n] = frag(s, w0 + 32 * n, KS);                           \
-        _Pragma("unroll") for (int n = 0; n < NS; ++n)                                                            \
-            _Pragma("unroll") for (int m = 0; m < MS; ++m)                                                        \
-                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[n], fx[m], acc[n][m], kFp4, kFp4,  \
-                                                                            KS, ws[n], KS, xs[m]);                \
-    } while (0)
-        MOE_STEP(0);
-        MOE_STEP(1);
-        MOE_STEP(2);
-        MOE_STEP(3);
-#undef MOE_STEP
+            to.w[n] = frag(s, w0 + 32 * n, ks);
+    };
+    auto read_scales = [&](int s, int (&x)[MS], int (&w)[NS]) {
+#pragma unroll
+        for (int m = 0; m < MS; ++m)
+            x[m] = scale(s, x0 + 32 * m);
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+            w[n] = scale(s, w0 + 32 * n);
+    };
+    auto meet = [&]() {  // what each wavefront asked for has come, and what it read has been read
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+#define MOE_PRODUCTS(KS, F)                                                                                           \
+    _Pragma("unroll") for (int n = 0; n < NS; ++n) _Pragma("unroll") for (int m = 0; m < MS; ++m) acc[n][m] =         \
+        __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(F.w[n], F.x[m], acc[n][m], kFp4, kFp4, KS, ws[0][n], KS, xs[0][m])
+    // the reads of the next step go between the first products of this one
+#define MOE_INTERLEAVE()                                                   \
+    _Pragma("unroll") for (int i = 0; i < MS + NS; ++i)                    \
+    {                                                                      \
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                 \
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                 \
+    }                                                                      \
+    __builtin_amdgcn_sched_group_barrier(0x008, MS *NS, 0)
+    // A stage: four steps of 64 elements, the operands of the next step on their way. Before the last step the next stage has come
+    // (turn), and as every wavefront has read all of this one the loads of the stage after it go where this one was (more).
+    auto stage = [&](int s, auto turn, auto more) {
+        read(s, 1, f[1]);
+        MOE_PRODUCTS(0, f[0]);
+        MOE_INTERLEAVE();
+        read(s, 2, f[0]);
+        MOE_PRODUCTS(1, f[1]);
+        MOE_INTERLEAVE();
+        read(s, 3, f[1]);
+        MOE_PRODUCTS(2, f[0]);
+        MOE_INTERLEAVE();
+        if constexpr (turn) {
+            meet();
+            if constexpr (!more)
+                clear_tail();
+            read(s + 1, 0, f[0]);
+            read_scales(s + 1, xs[1], ws[1]);
+            if constexpr (more) {
+                asm volatile("" : "+v"(xsc), "+v"(wsc));  // used from here on: before, they would be waited for
+                issue(s + 2);
+                store_sc(s + 2);
+                load_sc(s + 3);
+            }
+        }
+        MOE_PRODUCTS(3, f[1]);
+        if constexpr (turn) {
+#pragma unroll
+            for (int m = 0; m < MS; ++m)
+                xs[0][m] = xs[1][m];
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+                ws[0][n] = ws[1][n];
+        }
+    };
+    issue(0);
+    if (blocks >= 8) {
+        load_sc(0);
+        store_sc(0);
+    } else {
+        sh.scales[0][threadIdx.x] = short_scales(xsp, blocks);
+        sh.scales[0][kTileRows + threadIdx.x] = short_scales(wsp, blocks);
     }
+    if (stages > 1) {
+        issue(1);
+        load_sc(1);
+        store_sc(1);
+        load_sc(2);
+    }
+    meet();
+    if (stages == 1)
+        clear_tail();
+    read(0, 0, f[0]);
+    read_scales(0, xs[0], ws[0]);
+    int s = 0;
+    for (; s < stages - 2; ++s)
+        stage(s, std::true_type{}, std::true_type{});
+    if (s < stages - 1)
+        stage(s++, std::true_type{}, std::false_type{});
+    stage(s, std::false_type{}, std::false_type{});
+#undef MOE_PRODUCTS
+#undef MOE_INTERLEAVE
     // Lane l holds row l % 32 of x and, in each four registers, four consecutive weight rows. 32 rows at a time go through LDS, a
     // wavefront's own part of it, and out in whole vectors of a row.
     constexpr int kOut = GATED ? kHalf : kWaveCols, kPad = 16 / sizeof(O), kPitch = kOut + kPad, kVec = 16 / sizeof(O);
