@@ -106,7 +106,12 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs &a, int64_t i)
         }
     }
     __syncthreads();
-    return found;
+    // one for the wavefront: into scalar registers
+    const int64_t first = found.first;
+    return Tile{__builtin_amdgcn_readfirstlane(found.e), __builtin_amdgcn_readfirstlane(found.rows),
+                static_cast<int64_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(first >> 32))) << 32 |
+                    static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(first))),
+                __builtin_amdgcn_readfirstlane(found.col)};
 }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
@@ -180,46 +185,49 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kTileRows = 256, kTileCols = 256;  // rows and weight rows of the largest tile
-constexpr int kStageBytes = 128;                 // of each row a stage: 256 elements, a cache line
+constexpr int kStageBytes = 64;                  // of each row a stage: 128 elements
 constexpr int kStageBlocks = kStageBytes / 16;
+constexpr int kStages = 4;                       // of which LDS has room
+constexpr int kScaleStages = 4;                  // stages whose scales come at a time: 16 bytes of a row
 
-// The 16-byte chunk c of row r lies in slot c ^ swizzle(r) of its 128 bytes: 8 and 16 consecutive rows' same chunk fall into
+// The 16-byte chunk c of row r lies in slot c ^ swizzle(r) of its 64 bytes: 8 and 16 consecutive rows' same chunk fall into
 // different banks.
-__device__ __forceinline__ int swizzle(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+__device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
 
 struct Buffers {
-    uint8_t codes[2][(kTileRows + kTileCols) * kStageBytes];
-    uint64_t scales[2][kTileRows + kTileCols];
+    uint8_t codes[kStages][(kTileRows + kTileCols) * kStageBytes];
+    uint32_t scales[2][kTileRows + kTileCols][4];
 };
 
-// Scale bytes of 8 blocks of a row from block b on, the last 8 of the row where fewer are left (rows of 8 blocks at least).
-__device__ __forceinline__ uint64_t load_scales(const uint8_t *row, int b, int blocks)
+// The bytes of v from byte n (< 16) on, zeros behind them.
+__device__ __forceinline__ u32x4 shifted(const u32x4 &v, int n)
 {
-    uint64_t v;
-    __builtin_memcpy(&v, row + min(b, blocks - 8), 8);
-    return v;
+    const uint32_t w0 = n & 8 ? v.z : v.x, w1 = n & 8 ? v.w : v.y, w2 = n & 8 ? 0 : v.z, w3 = n & 8 ? 0 : v.w;
+    const uint32_t u0 = n & 4 ? w1 : w0, u1 = n & 4 ? w2 : w1, u2 = n & 4 ? w3 : w2, u3 = n & 4 ? 0 : w3;
+    return u32x4{__builtin_amdgcn_alignbyte(u1, u0, n), __builtin_amdgcn_alignbyte(u2, u1, n),
+                 __builtin_amdgcn_alignbyte(u3, u2, n), __builtin_amdgcn_alignbyte(0, u3, n)};
 }
 
-// Of what load_scales gave, the bytes from block b on in their places; past the row's end any but NaN.
-__device__ __forceinline__ uint64_t placed_scales(uint64_t v, int b, int blocks)
+// The scale bytes of a row of fewer than 16 blocks.
+__device__ __forceinline__ u32x4 short_scales(const uint8_t *row, int blocks)
 {
-    return v >> (8 * (b - min(b, blocks - 8)));
-}
-
-// The scale bytes of a row of fewer than 8 blocks.
-__device__ __forceinline__ uint64_t short_scales(const uint8_t *row, int blocks)
-{
-    uint64_t v = 0;
+    uint64_t w[2] = {0, 0};
     for (int i = 0; i < blocks; ++i)
-        v |= static_cast<uint64_t>(row[i]) << (8 * i);
-    return v;
+        w[i / 8] |= static_cast<uint64_t>(row[i]) << (8 * (i % 8));
+    return u32x4{static_cast<uint32_t>(w[0]), static_cast<uint32_t>(w[0] >> 32), static_cast<uint32_t>(w[1]),
+                 static_cast<uint32_t>(w[1] >> 32)};
 }
 
-// 16 bytes a lane into LDS, lane l's to address `to` + 16 l (one for the wavefront).
-__device__ __forceinline__ void to_lds(const uint8_t *from, uint32_t to)
+// 16 bytes a lane into LDS, lane l's to address `to` + 16 l (one for the wavefront). Past the resource's end: zeros.
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t from, uint32_t offset, uint32_t to)
 {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                     reinterpret_cast<__attribute__((address_space(3))) void *>(to), 16, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, reinterpret_cast<__attribute__((address_space(3))) void *>(to), 16,
+                                             static_cast<int>(offset), 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t capped(int64_t bytes)
+{
+    return static_cast<uint32_t>(min(bytes, static_cast<int64_t>(0xffffffffu)));
 }
 
 template <int MS, int NS>
@@ -236,11 +244,11 @@ __device__ __forceinline__ void tile_product(const ProductArgs &a, const Tile &t
     static_assert(32 * NS * kWN == kTileCols, "");
     constexpr int kWaveCols = 32 * NS, kHalf = kWaveCols / 2;
     constexpr int kOutCols = GATED ? kTileCols / 2 : kTileCols;
-    constexpr int kXLoads = kRows / 32, kWLoads = kTileCols / 32;  // 16-byte loads a thread and stage
+    constexpr int kXLoads = kRows < 64 ? 1 : kRows / 64, kWLoads = kTileCols / 64;  // 16-byte loads a thread and stage
+    constexpr int kLoads = kXLoads + kWLoads, kEarly = kLoads / 2;
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / kWave));
     const int blocks = static_cast<int>(a.H / kMxBlock), stages = (blocks + kStageBlocks - 1) / kStageBlocks;
     const int64_t row_bytes = a.H / 2, n0 = static_cast<int64_t>(tile.col) * kOutCols;
-    const uint8_t *xbase = a.x_rows > 0 ? a.x : a.w, *xsbase = a.x_rows > 0 ? a.xs : a.ws;
 
     // the row of x behind row r of the tile (any one where there is none: the epilogue drops it)
     auto x_row = [&](int r) -> int64_t {
@@ -251,74 +259,99 @@ __device__ __forceinline__ void tile_product(const ProductArgs &a, const Tile &t
         }
         return row;
     };
-    // the weight row behind row b of the tile's weights: gated, a wavefront's first half are gates and its second the ups of them
+    // the weight row, from n0 on, behind row b of the tile's weights: gated, a wavefront's first half are gates, its second the ups
+    // of the same columns (is_up)
     auto w_row = [&](int b) -> int64_t {
-        if (!GATED)
-            return tile.e * a.N + min(n0 + b, a.N - 1);
-        const int in = b % kWaveCols;
-        const int64_t n = min(n0 + b / kWaveCols * kHalf + in % kHalf, a.N - 1);
-        return tile.e * 2 * a.N + n + (in >= kHalf ? a.N : 0);
+        const int64_t n = GATED ? b / kWaveCols * kHalf + b % kHalf : b;
+        return min(n, a.N - 1 - n0);
     };
+    auto is_up = [&](int b) { return GATED && b % kWaveCols >= kHalf; };
 
-    // thread t loads chunk slot t % 8 of rows t / 8 + 32 j
-    const int chunk = (lane & 7) ^ swizzle(threadIdx.x / 8);
-    const uint8_t *xp[kXLoads], *wp[kWLoads];
+    // A load takes 16 rows a wavefront, 4 lanes a row: thread t chunk slot t % 4 of rows 64 j + t / 4. Loads go by buffer resources,
+    // whose bounds keep what lies past the last row's end unread. x is from its tile's first row on, or whole with a map.
+    const int chunk = (lane & 3) ^ swizzle(lane >> 2);
+    const int64_t x_at = a.src_row ? 0 : tile.first;
+    const uint8_t *xbase = a.x + x_at * row_bytes;
+    const uint32_t xbytes = capped((a.x_rows - x_at) * row_bytes);
+    const int64_t wrows = a.N * (GATED ? 2 : 1), w_at = tile.e * wrows + n0;
+    uint32_t xo[kXLoads], wo[kWLoads];
 #pragma unroll
     for (int j = 0; j < kXLoads; ++j)
-        xp[j] = xbase + x_row(threadIdx.x / 8 + 32 * j) * row_bytes;
+        xo[j] = static_cast<uint32_t>((x_row(64 * j + threadIdx.x / 4) - x_at) * row_bytes) + chunk * 16;
 #pragma unroll
     for (int j = 0; j < kWLoads; ++j)
-        wp[j] = a.w + w_row(threadIdx.x / 8 + 32 * j) * row_bytes;
-    const uint8_t *xsp = xsbase + x_row(min(static_cast<int>(threadIdx.x), kRows - 1)) * blocks;
-    const uint8_t *wsp = a.ws + w_row(threadIdx.x) * blocks;
+        wo[j] = static_cast<uint32_t>(w_row(64 * j + threadIdx.x / 4) * row_bytes) + chunk * 16;
+    const uint8_t *xsp = a.x_rows > 0 ? a.xs + x_row(threadIdx.x) * blocks : a.ws;  // (any, where x has no rows)
+    const uint8_t *wsp = a.ws + (w_at + w_row(threadIdx.x) + (is_up(threadIdx.x) ? a.N : 0)) * blocks;
 
     // The stages' addresses as plain numbers: of what it sees to lie in the array the compiler would wait for every load under
-    // way into it, those of the next stage included, before each read. What a read needs has come by `meet`.
+    // way into it, those of later stages included, before each read. What a read needs has come by `meet`.
     uint32_t codes = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)&sh.codes[0][0]));
     asm volatile("" : "+s"(codes));
-    auto issue = [&](int s) {
-        const uint32_t to = codes + (s & 1) * sizeof(sh.codes[0]) + wave * 8 * kStageBytes;
-        const int at = min(s * kStageBlocks + chunk, blocks - 1) * 16;  // past the end: any chunk
+    // Loads FROM to TO of stage s. x's chunks past the end of the rows are zeros (beside them the weights' are some codes, and zero
+    // times them is zero); past the last stage nothing is read, but the number of loads is the same in every stage.
+    auto issue = [&](int s, auto from, auto to) {
+        const uint32_t at = codes + (s % kStages) * sizeof(sh.codes[0]) + wave * 16 * kStageBytes, k = s * kStageBytes;
+        const bool there = s < stages, in_row = s * kStageBlocks + chunk < blocks;
 #pragma unroll
-        for (int j = 0; j < kXLoads; ++j)
-            to_lds(xp[j] + at, to + 32 * j * kStageBytes);
-#pragma unroll
-        for (int j = 0; j < kWLoads; ++j)
-            to_lds(wp[j] + at, to + (kTileRows + 32 * j) * kStageBytes);
-    };
-    uint64_t xsc, wsc;
-    auto load_sc = [&](int s) {  // (past the last stage: what nothing uses)
-        xsc = load_scales(xsp, s * kStageBlocks, blocks);
-        wsc = load_scales(wsp, s * kStageBlocks, blocks);
-    };
-    auto store_sc = [&](int s) {
-        sh.scales[s & 1][threadIdx.x] = placed_scales(xsc, s * kStageBlocks, blocks);
-        sh.scales[s & 1][kTileRows + threadIdx.x] = placed_scales(wsc, s * kStageBlocks, blocks);
-    };
-    // chunks past the end of the rows: zeros for x (the weights' are some codes, and zero times them is zero)
-    auto clear_tail = [&]() {
-        if (blocks % kStageBlocks == 0)
-            return;
-        uint8_t *x = sh.codes[(stages - 1) & 1];
-        for (int i = threadIdx.x; i < kRows * kStageBlocks; i += kPlanThreads) {
-            const int r = i / kStageBlocks, c = i % kStageBlocks;
-            if (c >= blocks % kStageBlocks)
-                *reinterpret_cast<i32x4 *>(x + r * kStageBytes + (c ^ swizzle(r)) * 16) = i32x4{0, 0, 0, 0};
+        for (int j = from; j < to; ++j) {
+            if (j < kXLoads) {
+                to_lds(make_rsrc(xbase, xbytes), in_row ? xo[j] + k : 0xfffffff0u, at + 64 * j * kStageBytes);
+            } else {
+                const int i = j - kXLoads;
+                const int64_t row = w_at + (is_up(64 * i + 16 * wave) ? a.N : 0);
+                to_lds(make_rsrc(a.w + row * row_bytes, there ? capped((a.E * wrows - row) * row_bytes) : 0), wo[i] + k,
+                       at + (kTileRows + 64 * i) * kStageBytes);
+            }
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
     };
+    const auto none = std::integral_constant<int, 0>{};
+    const auto early = std::integral_constant<int, kEarly>{};
+    const auto all = std::integral_constant<int, kLoads>{};
+
+    // Scales come for kScaleStages stages (a group) at a time, x's and the weights' in turns: thread t has row t's. A row's 16 bytes
+    // are put down as what each half of a wavefront needs of them: blocks 0, 1 of each stage's four, then blocks 2, 3.
+    const uint8_t *const xsl = blocks >= 16 ? xsp : a.w, *const wsl = blocks >= 16 ? wsp : a.w;  // (rows of 16 bytes to read)
+    u32x4 sc;
+    auto load_sc = [&](bool w, int g) {  // past the end: what nothing uses
+        __builtin_memcpy(&sc, (w ? wsl : xsl) + max(min(16 * g, blocks - 16), 0), sizeof(sc));
+    };
+    auto put_sc = [&](bool w, int g, const u32x4 &v) {
+        st16(sh.scales[g & 1][(w ? kTileRows : 0) + threadIdx.x],
+             u32x4{__builtin_amdgcn_perm(v.y, v.x, 0x05040100u), __builtin_amdgcn_perm(v.w, v.z, 0x05040100u),
+                   __builtin_amdgcn_perm(v.y, v.x, 0x07060302u), __builtin_amdgcn_perm(v.w, v.z, 0x07060302u)});
+    };
+    auto store_sc = [&](bool w, int g) { put_sc(w, g, shifted(sc, min(16 * g - max(min(16 * g, blocks - 16), 0), 15))); };
+
     const int half = lane >> 5, r32 = lane & 31;
     const int x0 = (wave % WM) * 32 * MS + r32, w0 = kTileRows + (wave / WM) * kWaveCols + r32;
-    const int swz = swizzle(r32);
+    // a lane's 16 bytes in steps 0 and 1 of a stage: chunks 2 half and 2 half + 1
+    const uint32_t lane_at[2] = {codes + x0 * kStageBytes + ((2 * half) ^ swizzle(r32)) * 16,
+                                 codes + x0 * kStageBytes + ((2 * half + 1) ^ swizzle(r32)) * 16};
     auto frag = [&](int s, int row, int ks) -> i32x8 {
-        const uint32_t at = codes + (s & 1) * sizeof(sh.codes[0]) + row * kStageBytes + ((4 * half + ks) ^ swz) * 16;
+        const uint32_t at = lane_at[ks] + (s % kStages) * sizeof(sh.codes[0]) + row * kStageBytes;
         const i32x4 v = *reinterpret_cast<const __attribute__((address_space(3))) i32x4 *>(at);
         return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
     };
-    auto scale = [&](int s, int row) -> int {
-        return reinterpret_cast<const int *>(sh.scales[s & 1] + row)[half];
+    Frags<MS, NS> f[2];
+    auto read = [&](int s, int ks, Frags<MS, NS> &to) {
+#pragma unroll
+        for (int m = 0; m < MS; ++m)
+            to.x[m] = frag(s, 32 * m, ks);
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+            to.w[n] = frag(s, w0 - x0 + 32 * n, ks);
+    };
+    // Scales of stages s and s + 1, s even: steps 0 to 3 have bytes 0 to 3.
+    int xs[MS], ws[NS], next_xs[MS], next_ws[NS];
+    auto read_scales = [&](int s, int (&x)[MS], int (&w)[NS]) {
+        const int word = 2 * half + (s / 2) % 2, g = s / kScaleStages & 1;
+#pragma unroll
+        for (int m = 0; m < MS; ++m)
+            x[m] = static_cast<int>(sh.scales[g][x0 + 32 * m][word]);
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+            w[n] = static_cast<int>(sh.scales[g][w0 + 32 * n][word]);
     };
 
     f32x16 acc[NS][MS];
@@ -327,102 +360,82 @@ __device__ __forceinline__ void tile_product(const ProductArgs &a, const Tile &t
 #pragma unroll
         for (int m = 0; m < MS; ++m)
             acc[n][m] = f32x16{};
-    Frags<MS, NS> f[2];
-    int xs[2][MS], ws[2][NS];
-    auto read = [&](int s, int ks, Frags<MS, NS> &to) {
-#pragma unroll
-        for (int m = 0; m < MS; ++m)
-            to.x[m] = frag(s, x0 + 32 * m, ks);
-#pragma unroll
-        for (int n = 0; n < NS; ++n)
-            to.w[n] = frag(s, w0 + 32 * n, ks);
-    };
-    auto read_scales = [&](int s, int (&x)[MS], int (&w)[NS]) {
-#pragma unroll
-        for (int m = 0; m < MS; ++m)
-            x[m] = scale(s, x0 + 32 * m);
-#pragma unroll
-        for (int n = 0; n < NS; ++n)
-            w[n] = scale(s, w0 + 32 * n);
-    };
-    auto meet = [&]() {  // what each wavefront asked for has come, and what it read has been read
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+#define MOE_PRODUCTS(STEP, F)                                                                                         \
+    _Pragma("unroll") for (int n = 0; n < NS; ++n) _Pragma("unroll") for (int m = 0; m < MS; ++m) acc[n][m] =         \
+        __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(F.w[n], F.x[m], acc[n][m], kFp4, kFp4, STEP, ws[n], STEP, xs[m])
+    // the next step's reads, then loads, each before a product of this step
+#define MOE_INTERLEAVE(READS, LOADS)                                                                           \
+    _Pragma("unroll") for (int i = 0; i < (READS); ++i)                                                        \
+    {                                                                                                          \
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                                                     \
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                                     \
+    }                                                                                                          \
+    _Pragma("unroll") for (int i = 0; i < (LOADS); ++i)                                                        \
+    {                                                                                                          \
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);                                                     \
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                                     \
+    }
+    // Stage s, whose number is J more than an even one: two steps of 64 elements, with the operands of the next step on their way.
+    // Between the steps the next stage has come, and as every wavefront has read all of this one, loads of the stage kStages on go
+    // where it was.
+    auto stage = [&](int s, auto J) {
+        read(s, 1, f[1]);
+        issue(s + kStages - 1, early, all);
+        MOE_PRODUCTS(2 * J, f[0]);
+        MOE_INTERLEAVE(MS + NS, kLoads - kEarly);
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * kLoads) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-    };
-#define MOE_PRODUCTS(KS, F)                                                                                           \
-    _Pragma("unroll") for (int n = 0; n < NS; ++n) _Pragma("unroll") for (int m = 0; m < MS; ++m) acc[n][m] =         \
-        __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(F.w[n], F.x[m], acc[n][m], kFp4, kFp4, KS, ws[0][n], KS, xs[0][m])
-    // the reads of the next step go between the first products of this one
-#define MOE_INTERLEAVE()                                                   \
-    _Pragma("unroll") for (int i = 0; i < MS + NS; ++i)                    \
-    {                                                                      \
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                 \
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                 \
-    }                                                                      \
-    __builtin_amdgcn_sched_group_barrier(0x008, MS *NS, 0)
-    // A stage: four steps of 64 elements, the operands of the next step on their way. Before the last step the next stage has come
-    // (turn), and as every wavefront has read all of this one the loads of the stage after it go where this one was (more).
-    auto stage = [&](int s, auto turn, auto more) {
-        read(s, 1, f[1]);
-        MOE_PRODUCTS(0, f[0]);
-        MOE_INTERLEAVE();
-        read(s, 2, f[0]);
-        MOE_PRODUCTS(1, f[1]);
-        MOE_INTERLEAVE();
-        read(s, 3, f[1]);
-        MOE_PRODUCTS(2, f[0]);
-        MOE_INTERLEAVE();
-        if constexpr (turn) {
-            meet();
-            if constexpr (!more)
-                clear_tail();
-            read(s + 1, 0, f[0]);
-            read_scales(s + 1, xs[1], ws[1]);
-            if constexpr (more) {
-                asm volatile("" : "+v"(xsc), "+v"(wsc));  // used from here on: before, they would be waited for
-                issue(s + 2);
-                store_sc(s + 2);
-                load_sc(s + 3);
-            }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (J == 0) {
+            const bool odd = s & 2;
+            asm volatile("" : "+v"(sc.x), "+v"(sc.y), "+v"(sc.z), "+v"(sc.w));  // used from here on: before, it would be waited for
+            store_sc(!odd, s / kScaleStages + 1);
+            load_sc(odd, s / kScaleStages + (odd ? 2 : 1));
         }
-        MOE_PRODUCTS(3, f[1]);
-        if constexpr (turn) {
+        read(s + 1, 0, f[0]);
+        issue(s + kStages, none, early);
+        if constexpr (J == 1)
+            read_scales(s + 1, next_xs, next_ws);
+        MOE_PRODUCTS(2 * J + 1, f[1]);
+        MOE_INTERLEAVE(MS + NS, kEarly);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (J == 1) {
 #pragma unroll
             for (int m = 0; m < MS; ++m)
-                xs[0][m] = xs[1][m];
+                xs[m] = next_xs[m];
 #pragma unroll
             for (int n = 0; n < NS; ++n)
-                ws[0][n] = ws[1][n];
+                ws[n] = next_ws[n];
         }
     };
-    issue(0);
-    if (blocks >= 8) {
-        load_sc(0);
-        store_sc(0);
+    if (blocks >= 16) {
+        load_sc(false, 0);
+        store_sc(false, 0);
+        load_sc(true, 0);
+        store_sc(true, 0);
     } else {
-        sh.scales[0][threadIdx.x] = short_scales(xsp, blocks);
-        sh.scales[0][kTileRows + threadIdx.x] = short_scales(wsp, blocks);
+        put_sc(false, 0, short_scales(xsp, blocks));
+        put_sc(true, 0, short_scales(wsp, blocks));
     }
-    if (stages > 1) {
-        issue(1);
-        load_sc(1);
-        store_sc(1);
-        load_sc(2);
-    }
-    meet();
-    if (stages == 1)
-        clear_tail();
+    load_sc(true, 1);
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s)
+        issue(s, none, all);
+    issue(kStages - 1, none, early);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * kLoads + kEarly) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
     read(0, 0, f[0]);
-    read_scales(0, xs[0], ws[0]);
-    int s = 0;
-    for (; s < stages - 2; ++s)
-        stage(s, std::true_type{}, std::true_type{});
-    if (s < stages - 1)
-        stage(s++, std::true_type{}, std::false_type{});
-    stage(s, std::false_type{}, std::false_type{});
-#undef MOE_PRODUCTS
+    read_scales(0, xs, ws);
+    for (int s = 0; s < stages; s += 2) {  // after an odd number one of zeros
+        stage(s, std::integral_constant<int, 0>{});
+        stage(s + 1, std::integral_constant<int, 1>{});
+    }
 #undef MOE_INTERLEAVE
+#undef MOE_PRODUCTS
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads past the last stage still write zeros
     // Lane l holds row l % 32 of x and, in each four registers, four consecutive weight rows. 32 rows at a time go through LDS, a
     // wavefront's own part of it, and out in whole vectors of a row.
     constexpr int kOut = GATED ? kHalf : kWaveCols, kPad = 16 / sizeof(O), kPitch = kOut + kPad, kVec = 16 / sizeof(O);
@@ -504,7 +517,8 @@ int64_t max_tiles(int64_t R, int64_t E, int64_t BM) { return R / BM + std::min(R
 template <typename O, bool GATED>
 moe_status launch_product(ProductArgs a, hipStream_t stream)
 {
-    if (a.R > 16 * static_cast<int64_t>(a.E)) {
+    // (rows through a map are addressed in 32 bits there)
+    if (a.R > 16 * static_cast<int64_t>(a.E) && (!a.src_row || a.x_rows * (a.H / 2) <= 0xffffffff)) {
         a.col_tiles = static_cast<uint32_t>(ceil_div(a.N, GATED ? kTileCols / 2 : kTileCols));
         const int64_t grid = max_tiles(a.R, a.E, kTileRows) * a.col_tiles;
         if (grid > 0x7fffffff)
