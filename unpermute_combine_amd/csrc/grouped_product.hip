@@ -55,32 +55,37 @@ struct Tile {
     int32_t col;
 };
 
-// The i-th of the (rows, columns) tiles of BM rows, experts in order, an expert's tiles of the same columns beside each other.
+// The i-th of the (rows, columns) tiles of BM rows: experts in order, of an expert kGroup tiles of the same columns beside each
+// other. (Those that run at the same time on an XCD then share both their weights and their rows in its L2: one expert of 8192
+// cubed 334 -> 298 us against all the rows' tiles first.)
+constexpr uint32_t kGroup = 8;
 // Every thread of a workgroup of kPlanThreads calls it and gets the same.
 template <int BM>
-__device__ __forceinline__ Tile find_tile(const ProductArgs &a, int64_t i)
+__device__ __forceinline__ Tile find_tile(const ProductArgs &a, uint32_t i)
 {
-    __shared__ int64_t wave_tiles[kPlanThreads / kWave];
+    __shared__ uint32_t wave_tiles[kPlanThreads / kWave];
     __shared__ Tile found;
     constexpr int kPer = MOE_MAX_EXPERTS / kPlanThreads;
-    const int per = static_cast<int>(ceil_div(a.E, kPlanThreads));
-    const int e0 = threadIdx.x * per;
-    int64_t tiles[kPer], mine = 0;
+    const int per = static_cast<int>((a.E + kPlanThreads - 1) / kPlanThreads), e0 = threadIdx.x * per;
+    uint32_t tiles[kPer], start[kPer], len[kPer], mine = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        tiles[j] = 0;
+        tiles[j] = start[j] = len[j] = 0;
         if (j < per && e0 + j < a.E) {
-            int64_t start, len;
-            segment(a, e0 + j, start, len);
-            tiles[j] = ceil_div(len, BM);
+            int64_t s, l;
+            segment(a, e0 + j, s, l);
+            start[j] = static_cast<uint32_t>(s);
+            len[j] = static_cast<uint32_t>(l);
+            tiles[j] = (len[j] + BM - 1) / BM * a.col_tiles;
             mine += tiles[j];
         }
     }
+    // (the launch has made sure that their number fits)
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    int64_t upto = mine;
+    uint32_t upto = mine;
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) {
-        const int64_t o = __shfl_up(upto, d);
+        const uint32_t o = __shfl_up(upto, d);
         upto += lane >= d ? o : 0;
     }
     if (lane == kWave - 1)
@@ -88,21 +93,20 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs &a, int64_t i)
     if (threadIdx.x == 0)
         found = Tile{-1, 0, 0, 0};
     __syncthreads();
-    int64_t before = upto - mine;
-    for (int v = 0; v < wave; ++v)
-        before += wave_tiles[v];
-    int64_t k = i - before * a.col_tiles;
-    if (k >= 0 && k < mine * a.col_tiles) {
+    uint32_t k = i - (upto - mine);
+#pragma unroll
+    for (int v = 0; v < kPlanThreads / kWave - 1; ++v)
+        k -= v < wave ? wave_tiles[v] : 0;
+    if (k < mine) {  // (before this thread's tiles k is negative, as a large number)
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            if (k >= 0 && k < tiles[j] * a.col_tiles) {
-                int64_t start, len;
-                segment(a, e0 + j, start, len);
-                const int64_t m = k % tiles[j];
-                found = Tile{e0 + j, static_cast<int32_t>(min(len - m * BM, int64_t{BM})), start + m * BM,
-                             static_cast<int32_t>(k / tiles[j])};
+            if (k < tiles[j]) {
+                const uint32_t n = (len[j] + BM - 1) / BM, g = k / (kGroup * a.col_tiles), in = k % (kGroup * a.col_tiles);
+                const uint32_t high = min(kGroup, n - kGroup * g), m = kGroup * g + in % high;
+                found = Tile{e0 + j, static_cast<int32_t>(min(len[j] - m * BM, static_cast<uint32_t>(BM))),
+                             static_cast<int64_t>(start[j]) + m * BM, static_cast<int32_t>(in / high)};
             }
-            k -= tiles[j] * a.col_tiles;
+            k -= tiles[j];
         }
     }
     __syncthreads();
@@ -114,68 +118,212 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs &a, int64_t i)
                 __builtin_amdgcn_readfirstlane(found.col)};
 }
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+// g / (1 + exp(-g)) by the instructions for 2^x and 1 / x, right to an ulp each: with the argument's rounding (|g| + 6) u in all.
+__device__ __forceinline__ float silu(float g)
+{
+    constexpr float kLog2e = 1.44269504088896340736f;
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * g));
+}
 
 __device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(uint16_t *p, float v) { *p = static_cast<uint16_t>(f32_to_bf16_bits(v)); }
 
-// Four values into LDS.
+// Four values to consecutive places.
 __device__ __forceinline__ void put4(float *p, const float (&v)[4]) { *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]}; }
 __device__ __forceinline__ void put4(uint16_t *p, const float (&v)[4])
 {
     *reinterpret_cast<uint64_t *>(p) = pack_bf16x2(v[0], v[1]) | static_cast<uint64_t>(pack_bf16x2(v[2], v[3])) << 32;
 }
 
-// A lane's block of a row: zeros where there is none (block >= blocks or no row).
-__device__ __forceinline__ void load_block(const uint8_t *codes, const uint8_t *scales, int64_t row, int64_t blocks, int64_t b,
-                                           bool there, i32x8 &v, int &scale)
+// ---------------------------------------------------------------- few rows an expert
+
+// The bytes of v from byte n (< 16) on, zeros behind them.
+__device__ __forceinline__ u32x4 shifted(const u32x4 &v, int n)
 {
-    u32x4 c{0, 0, 0, 0};
-    scale = 127;
-    if (there && b < blocks) {
-        c = ld16(codes + (row * blocks + b) * 16);
-        scale = scales[row * blocks + b];
-    }
-    v = i32x8{static_cast<int>(c.x), static_cast<int>(c.y), static_cast<int>(c.z), static_cast<int>(c.w), 0, 0, 0, 0};
+    const uint32_t w0 = n & 8 ? v.z : v.x, w1 = n & 8 ? v.w : v.y, w2 = n & 8 ? 0 : v.z, w3 = n & 8 ? 0 : v.w;
+    const uint32_t u0 = n & 4 ? w1 : w0, u1 = n & 4 ? w2 : w1, u2 = n & 4 ? w3 : w2, u3 = n & 4 ? 0 : w3;
+    return u32x4{__builtin_amdgcn_alignbyte(u1, u0, n), __builtin_amdgcn_alignbyte(u2, u1, n),
+                 __builtin_amdgcn_alignbyte(u3, u2, n), __builtin_amdgcn_alignbyte(0, u3, n)};
 }
 
-// Four wavefronts a workgroup, each a tile of 16 rows by 16 columns.
-template <typename O, bool GATED>
-__global__ __launch_bounds__(kPlanThreads) void grouped_product_kernel(ProductArgs a)
+// The scale bytes of a row of fewer than 16 blocks.
+__device__ __forceinline__ u32x4 short_scales(const uint8_t *row, int blocks)
 {
+    uint64_t w[2] = {0, 0};
+    for (int i = 0; i < blocks; ++i)
+        w[i / 8] |= static_cast<uint64_t>(row[i]) << (8 * (i % 8));
+    return u32x4{static_cast<uint32_t>(w[0]), static_cast<uint32_t>(w[0] >> 32), static_cast<uint32_t>(w[1]),
+                 static_cast<uint32_t>(w[1] >> 32)};
+}
+
+constexpr int kRunBytes = 256, kRunBlocks = kRunBytes / 16;  // of each row at a time: 512 elements, 16 scale bytes
+constexpr int kDppRowRor8 = 0x128;
+
+// Weights come in whole cache lines: an instruction reads 128 bytes of 8 rows, rows 0..7 into a and 8..15 into b, lanes 8..15 of
+// each 16 the second 64 bytes. Swapping lanes 8..15 of a with 0..7 of b leaves the two 64-byte halves of all 16 rows.
+__device__ __forceinline__ void swap_eights(uint32_t &a, uint32_t &b)
+{
+    const int x = static_cast<int>(a), y = static_cast<int>(b);
+    a = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(x, y, kDppRowRor8, 0xf, 0xc, false));
+    b = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(y, x, kDppRowRor8, 0xf, 0x3, false));
+}
+
+__device__ __forceinline__ i32x8 operand(const u32x4 &v)
+{
+    return i32x8{static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w), 0, 0, 0, 0};
+}
+
+// A wavefront's share of 512 elements: 32 weight rows, 16 rows of x, and their scales.
+struct Run {
+    u32x4 w[2][4], x[4], ws[2], xs;
+};
+
+// Up to 16 rows of an expert by 32 weight rows (gated: 16 of the gate and the 16 of the up of the same columns) a wavefront. The
+// weights go from memory into the matrix instructions' operand registers, the next 512 elements on their way while these are
+// multiplied. SPLIT wavefronts share the columns and take parts of the sum, put together in LDS.
+template <typename O, bool GATED, int SPLIT>
+__global__ __launch_bounds__(kPlanThreads) void grouped_rows_kernel(ProductArgs a)
+{
+    constexpr int kWaves = kPlanThreads / kWave, kCols = GATED ? 16 : 32;  // columns a wavefront
+    __shared__ f32x4 sums[SPLIT > 1 ? kWaves : 1][2][kWave];
     const Tile tile = find_tile<16>(a, blockIdx.x);
     if (tile.e < 0)
         return;
-    const int lane = threadIdx.x & (kWave - 1), r = lane & 15, g = lane >> 4;
-    const int64_t n0 = (static_cast<int64_t>(tile.col) * (kPlanThreads / kWave) + threadIdx.x / kWave) * 16;
-    if (n0 >= a.N)
-        return;
-    const int64_t blocks = a.H / kMxBlock;
-    int64_t row = tile.first + min(r, tile.rows - 1);
-    bool there = r < tile.rows;
-    if (a.src_row) {
-        row = a.src_row[row];
-        there = there && row >= 0 && row < a.x_rows;
-        row = there ? row : 0;
-    }
-    const int64_t n = n0 + r, wrows = a.N * (GATED ? 2 : 1), wrow = tile.e * wrows + n;
-    f32x4 acc{0, 0, 0, 0}, up{0, 0, 0, 0};
-    for (int64_t b = g; b < blocks + g; b += 4) {
-        i32x8 vx, vw;
-        int sx, sw;
-        load_block(a.x, a.xs, row, blocks, b, there, vx, sx);
-        load_block(a.w, a.ws, wrow, blocks, b, n < a.N, vw, sw);
-        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vx, vw, acc, kFp4, kFp4, 0, sx, 0, sw);
-        if constexpr (GATED) {
-            load_block(a.w, a.ws, wrow + a.N, blocks, b, n < a.N, vw, sw);
-            up = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vx, vw, up, kFp4, kFp4, 0, sx, 0, sw);
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / kWave));
+    const int r = lane & 15, g = lane >> 4, part = wave % SPLIT;
+    const int64_t n0 = (static_cast<int64_t>(tile.col) * (kWaves / SPLIT) + wave / SPLIT) * kCols;
+    const int blocks = static_cast<int>(a.H / kMxBlock), runs = (blocks + kRunBlocks - 1) / kRunBlocks;
+    const int64_t row_bytes = a.H / 2, wrows = a.N * (GATED ? 2 : 1);
+    f32x4 acc[2] = {};
+    if (n0 < a.N) {
+        // x's row r, and the scales' row r of each 16 weight rows
+        int64_t row = tile.first + min(r, tile.rows - 1);
+        bool there = r < tile.rows;
+        if (a.src_row) {
+            row = a.src_row[row];
+            there = there && row >= 0 && row < a.x_rows;
+            row = there ? row : 0;
+        }
+        const uint8_t *const x = a.x + row * row_bytes, *const xs = there ? a.xs + row * blocks : a.ws;
+        // the weight rows from w_at(i) on; of the last columns' those past the end are the last one
+        auto w_at = [&](int i) { return tile.e * wrows + n0 + (GATED ? i * a.N : 16 * i); };
+        auto last = [&](int i) { return static_cast<int>(min(a.N - n0 - (GATED ? 0 : 16 * i), int64_t{16})) - 1; };
+        uint32_t wo[2][2];
+        const uint8_t *ws[2];
+        __amdgpu_buffer_rsrc_t wr[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int end = max(last(i), 0);
+            const int64_t at = min(w_at(i), a.E * wrows - 1);
+            wr[i] = make_rsrc(a.w + at * row_bytes, static_cast<uint32_t>(min((a.E * wrows - at) * row_bytes, int64_t{0xfffffff0})));
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                wo[i][j] = static_cast<uint32_t>(min(8 * j + (r & 7), end) * row_bytes) + (g + (r & 8) / 2) * 16;
+            ws[i] = a.ws + (at + min(r, end)) * blocks;
+        }
+        auto scales = [&](const uint8_t *from, int run) -> u32x4 {
+            if (blocks < kRunBlocks)
+                return short_scales(from, blocks);
+            u32x4 v;
+            __builtin_memcpy(&v, from + min(run * kRunBlocks, blocks - kRunBlocks), sizeof(v));
+            return v;
+        };
+        auto load = [&](int run, Run &to) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    to.w[i][j] = ld16_buf<0>(wr[i], wo[i][j & 1] + run * kRunBytes + (j >> 1) * 128);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int b = run * kRunBlocks + 4 * j + g;
+                to.x[j] = u32x4{0, 0, 0, 0};
+                if (there && b < blocks)
+                    to.x[j] = ld16(x + b * 16);
+            }
+            to.ws[0] = scales(ws[0], run);
+            to.ws[1] = scales(ws[1], run);
+            to.xs = scales(xs, run);
+        };
+        auto multiply = [&](int run, Run &f) {
+            const int past = blocks < kRunBlocks ? 0 : run * kRunBlocks - min(run * kRunBlocks, blocks - kRunBlocks);
+            const u32x4 sx = shifted(f.xs, past);
+            const uint32_t keep = there ? 0xffffffffu : 0;
+            const uint32_t s[4] = {sx.x & keep, sx.y & keep, sx.z & keep, sx.w & keep};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const u32x4 sw = shifted(f.ws[i], past);
+                const uint32_t t[4] = {sw.x, sw.y, sw.z, sw.w};
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                    u32x4 &p = f.w[i][j], &q = f.w[i][j + 1];
+                    swap_eights(p.x, q.x);
+                    swap_eights(p.y, q.y);
+                    swap_eights(p.z, q.z);
+                    swap_eights(p.w, q.w);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        operand(f.w[i][j]), operand(f.x[j]), acc[i], kFp4, kFp4, 0, static_cast<int>(t[j] >> (8 * g)), 0,
+                        static_cast<int>(s[j] >> (8 * g)));
+            }
+        };
+        const int from = runs * part / SPLIT, to = runs * (part + 1) / SPLIT;
+        if (from < to) {
+            Run f[2];
+            load(from, f[0]);
+            int run = from;
+            for (; run + 2 < to; run += 2) {
+                load(run + 1, f[1]);
+                multiply(run, f[0]);
+                load(run + 2, f[0]);
+                multiply(run + 1, f[1]);
+            }
+            if (run + 1 < to) {
+                load(run + 1, f[1]);
+                multiply(run, f[0]);
+                multiply(run + 1, f[1]);
+            } else {
+                multiply(run, f[0]);
+            }
         }
     }
+    if constexpr (SPLIT > 1) {
+        if (part > 0) {
+            sums[wave][0][lane] = acc[0];
+            sums[wave][1][lane] = acc[1];
+        }
+        __syncthreads();
+        if (part > 0)
+            return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = 4 * g + i;
-        if (m < tile.rows && n < a.N)
-            store_out(static_cast<O *>(a.out) + (tile.first + m) * a.N + n, GATED ? silu(acc[i]) * up[i] : acc[i]);
+        for (int p = 1; p < SPLIT; ++p) {
+            acc[0] += sums[wave + p][0][lane];
+            acc[1] += sums[wave + p][1][lane];
+        }
+    }
+    // lane l holds row l % 16 and four consecutive columns of each 16
+    if (r >= tile.rows)
+        return;
+    O *const out = static_cast<O *>(a.out) + (tile.first + r) * a.N;
+    const bool vectors = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & (4 * sizeof(O) - 1)) == 0;
+#pragma unroll
+    for (int i = 0; i < (GATED ? 1 : 2); ++i) {
+        const int64_t c = n0 + 16 * i + 4 * g;
+        float v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            v[q] = GATED ? silu(acc[0][q]) * acc[1][q] : acc[i][q];
+        if (vectors) {
+            if (c < a.N)
+                put4(out + c, v);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (c + q < a.N)
+                    store_out(out + c + q, v[q]);
+        }
     }
 }
 
@@ -198,25 +346,6 @@ struct Buffers {
     uint8_t codes[kStages][(kTileRows + kTileCols) * kStageBytes];
     uint32_t scales[2][kTileRows + kTileCols][4];
 };
-
-// The bytes of v from byte n (< 16) on, zeros behind them.
-__device__ __forceinline__ u32x4 shifted(const u32x4 &v, int n)
-{
-    const uint32_t w0 = n & 8 ? v.z : v.x, w1 = n & 8 ? v.w : v.y, w2 = n & 8 ? 0 : v.z, w3 = n & 8 ? 0 : v.w;
-    const uint32_t u0 = n & 4 ? w1 : w0, u1 = n & 4 ? w2 : w1, u2 = n & 4 ? w3 : w2, u3 = n & 4 ? 0 : w3;
-    return u32x4{__builtin_amdgcn_alignbyte(u1, u0, n), __builtin_amdgcn_alignbyte(u2, u1, n),
-                 __builtin_amdgcn_alignbyte(u3, u2, n), __builtin_amdgcn_alignbyte(0, u3, n)};
-}
-
-// The scale bytes of a row of fewer than 16 blocks.
-__device__ __forceinline__ u32x4 short_scales(const uint8_t *row, int blocks)
-{
-    uint64_t w[2] = {0, 0};
-    for (int i = 0; i < blocks; ++i)
-        w[i / 8] |= static_cast<uint64_t>(row[i]) << (8 * (i % 8));
-    return u32x4{static_cast<uint32_t>(w[0]), static_cast<uint32_t>(w[0] >> 32), static_cast<uint32_t>(w[1]),
-                 static_cast<uint32_t>(w[1] >> 32)};
-}
 
 // 16 bytes a lane into LDS, lane l's to address `to` + 16 l (one for the wavefront). Past the resource's end: zeros.
 __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t from, uint32_t offset, uint32_t to)
@@ -410,20 +539,28 @@ __device__ __forceinline__ void tile_product(const ProductArgs &a, const Tile &t
                 ws[n] = next_ws[n];
         }
     };
+    issue(0, none, all);
     if (blocks >= 16) {
         load_sc(false, 0);
-        store_sc(false, 0);
+        const u32x4 x = sc;
         load_sc(true, 0);
-        store_sc(true, 0);
+        const u32x4 w = sc;
+        load_sc(true, 1);
+#pragma unroll
+        for (int s = 1; s < kStages - 1; ++s)
+            issue(s, none, all);
+        issue(kStages - 1, none, early);
+        put_sc(false, 0, x);
+        put_sc(true, 0, w);
     } else {
+        load_sc(true, 1);
+#pragma unroll
+        for (int s = 1; s < kStages - 1; ++s)
+            issue(s, none, all);
+        issue(kStages - 1, none, early);
         put_sc(false, 0, short_scales(xsp, blocks));
         put_sc(true, 0, short_scales(wsp, blocks));
     }
-    load_sc(true, 1);
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s)
-        issue(s, none, all);
-    issue(kStages - 1, none, early);
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * kLoads + kEarly) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -514,6 +651,8 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
 // Tiles of BM rows that R rows in E segments can need.
 int64_t max_tiles(int64_t R, int64_t E, int64_t BM) { return R / BM + std::min(R, E); }
 
+constexpr int64_t kFewUnits = 4096;
+
 template <typename O, bool GATED>
 moe_status launch_product(ProductArgs a, hipStream_t stream)
 {
@@ -526,11 +665,16 @@ moe_status launch_product(ProductArgs a, hipStream_t stream)
         hipLaunchKernelGGL((grouped_tile_kernel<O, GATED>), dim3(static_cast<unsigned>(grid)), dim3(kPlanThreads), 0, stream, a);
         return launch_status();
     }
-    a.col_tiles = static_cast<uint32_t>(ceil_div(a.N, 16 * (kPlanThreads / kWave)));
-    const int64_t grid = max_tiles(a.R, a.E, 16) * a.col_tiles;
-    if (grid > 0x7fffffff)
+    const int64_t tiles = max_tiles(a.R, a.E, 16), units = tiles * ceil_div(a.N, GATED ? 16 : 32);
+    const int split = units < kFewUnits && a.H >= 4 * 512 ? 4 : 1;
+    a.col_tiles = static_cast<uint32_t>(ceil_div(a.N, (GATED ? 16 : 32) * (kPlanThreads / kWave / split)));
+    if (tiles * a.col_tiles > 0x7fffffff)
         return MOE_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((grouped_product_kernel<O, GATED>), dim3(static_cast<unsigned>(grid)), dim3(kPlanThreads), 0, stream, a);
+    const dim3 grid(static_cast<unsigned>(tiles * a.col_tiles));
+    if (split == 4)
+        hipLaunchKernelGGL((grouped_rows_kernel<O, GATED, 4>), grid, dim3(kPlanThreads), 0, stream, a);
+    else
+        hipLaunchKernelGGL((grouped_rows_kernel<O, GATED, 1>), grid, dim3(kPlanThreads), 0, stream, a);
     return launch_status();
 }
 
