@@ -354,9 +354,12 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t from, uint32_t off
                                              static_cast<int>(offset), 0, 0, 0);
 }
 
+// Buffer resources end before this offset, which asks for nothing.
+constexpr uint32_t kNowhere = 0xfffffff0u;
+
 __device__ __forceinline__ uint32_t capped(int64_t bytes)
 {
-    return static_cast<uint32_t>(min(bytes, static_cast<int64_t>(0xffffffffu)));
+    return static_cast<uint32_t>(min(bytes, static_cast<int64_t>(kNowhere)));
 }
 
 template <int MS, int NS>
@@ -364,135 +367,144 @@ struct Frags {
     i32x8 x[MS], w[NS];
 };
 
-// A tile of up to 32 MS WM rows by 256 weight rows (gated: 128 of the gate and 128 of the up), four wavefronts, WM beside each
-// other along the rows: a wavefront has 32 MS rows by 32 NS weight rows.
-template <typename O, bool GATED, int MS, int NS, int WM>
-__device__ __forceinline__ void tile_product(const ProductArgs &a, const Tile &tile, Buffers &sh)
+// Workgroup b of nb, dealt to the XCDs in turn, takes the place that keeps runs of kRun neighbours on one XCD.
+constexpr uint32_t kRun = 16;
+__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t nb)
 {
-    constexpr int kRows = 32 * MS * WM, kWN = 4 / WM;  // wavefronts along the columns
-    static_assert(32 * NS * kWN == kTileCols, "");
-    constexpr int kWaveCols = 32 * NS, kHalf = kWaveCols / 2;
+    const uint32_t round = b / (kXcds * kRun), in = b % (kXcds * kRun);
+    return (round + 1) * kXcds * kRun > nb ? b : round * kXcds * kRun + in % kXcds * kRun + in / kXcds;
+}
+
+// A tile of up to 256 rows by 256 weight rows (gated: 128 of the gate and the 128 of the up of the same columns), four wavefronts.
+// Of more than 128 rows a wavefront has 128 by 128 weight rows, two wavefronts beside each other each way; of fewer all of them by
+// 64 weight rows. Gated, a wavefront's first half are gates, its second the ups of the same columns.
+template <typename O, bool GATED>
+__global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs a)
+{
+    __shared__ __attribute__((aligned(128))) Buffers sh;
+    const Tile tile = find_tile<kTileRows>(a, xcd_run(blockIdx.x, gridDim.x));
+    if (tile.e < 0)
+        return;
     constexpr int kOutCols = GATED ? kTileCols / 2 : kTileCols;
-    constexpr int kXLoads = kRows < 64 ? 1 : kRows / 64, kWLoads = kTileCols / 64;  // 16-byte loads a thread and stage
-    constexpr int kLoads = kXLoads + kWLoads, kEarly = kLoads / 2;
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / kWave));
     const int blocks = static_cast<int>(a.H / kMxBlock), stages = (blocks + kStageBlocks - 1) / kStageBlocks;
     const int64_t row_bytes = a.H / 2, n0 = static_cast<int64_t>(tile.col) * kOutCols;
-
-    // the row of x behind row r of the tile (any one where there is none: the epilogue drops it)
-    auto x_row = [&](int r) -> int64_t {
-        int64_t row = tile.first + min(r, tile.rows - 1);
-        if (a.src_row) {
-            row = a.src_row[row];
-            row = row >= 0 && row < a.x_rows ? row : 0;
-        }
-        return row;
-    };
-    // the weight row, from n0 on, behind row b of the tile's weights: gated, a wavefront's first half are gates, its second the ups
-    // of the same columns (is_up)
-    auto w_row = [&](int b) -> int64_t {
-        const int64_t n = GATED ? b / kWaveCols * kHalf + b % kHalf : b;
-        return min(n, a.N - 1 - n0);
-    };
-    auto is_up = [&](int b) { return GATED && b % kWaveCols >= kHalf; };
+    const bool big = tile.rows > 128;
+    const int wave_cols = big ? 128 : 64, wave_half = wave_cols / 2;
 
     // A load takes 16 rows a wavefront, 4 lanes a row: thread t chunk slot t % 4 of rows 64 j + t / 4. Loads go by buffer resources,
-    // whose bounds keep what lies past the last row's end unread. x is from its tile's first row on, or whole with a map.
+    // whose bounds keep what lies past the last row's end unread. x is from its tile's first row on, or whole with a map; rows that
+    // are not there load zeros. The weight row, from n0 on, behind row b of the tile's weights is w_row(b), of the up if is_up(b).
     const int chunk = (lane & 3) ^ swizzle(lane >> 2);
     const int64_t x_at = a.src_row ? 0 : tile.first;
-    const uint8_t *xbase = a.x + x_at * row_bytes;
+    const uint8_t *const xbase = a.x + x_at * row_bytes;
     const uint32_t xbytes = capped((a.x_rows - x_at) * row_bytes);
     const int64_t wrows = a.N * (GATED ? 2 : 1), w_at = tile.e * wrows + n0;
-    uint32_t xo[kXLoads], wo[kWLoads];
+    auto x_row = [&](int r) -> int64_t {
+        if (r >= tile.rows)
+            return -1;
+        const int64_t row = a.src_row ? a.src_row[tile.first + r] : tile.first + r;
+        return row < a.x_rows ? row : -1;
+    };
+    auto w_row = [&](int b) -> int64_t {
+        const int64_t n = GATED ? b / wave_cols * wave_half + b % wave_half : b;
+        return min(n, a.N - 1 - n0);
+    };
+    auto is_up = [&](int b) { return GATED && b % wave_cols >= wave_half; };
+    uint32_t xo[4], wo[4];
 #pragma unroll
-    for (int j = 0; j < kXLoads; ++j)
-        xo[j] = static_cast<uint32_t>((x_row(64 * j + threadIdx.x / 4) - x_at) * row_bytes) + chunk * 16;
-#pragma unroll
-    for (int j = 0; j < kWLoads; ++j)
+    for (int j = 0; j < 4; ++j) {
+        const int64_t row = x_row(64 * j + threadIdx.x / 4);
+        xo[j] = row >= 0 ? static_cast<uint32_t>((row - x_at) * row_bytes) + chunk * 16 : kNowhere;
         wo[j] = static_cast<uint32_t>(w_row(64 * j + threadIdx.x / 4) * row_bytes) + chunk * 16;
-    const uint8_t *xsp = a.x_rows > 0 ? a.xs + x_row(threadIdx.x) * blocks : a.ws;  // (any, where x has no rows)
-    const uint8_t *wsp = a.ws + (w_at + w_row(threadIdx.x) + (is_up(threadIdx.x) ? a.N : 0)) * blocks;
+    }
+    const uint8_t *const wsp = a.ws + (w_at + w_row(threadIdx.x) + (is_up(threadIdx.x) ? a.N : 0)) * blocks;
+    const int64_t xs_row = x_row(threadIdx.x);
+    const uint8_t *const xsp = xs_row >= 0 ? a.xs + xs_row * blocks : wsp;
+    const uint32_t keep = xs_row >= 0 ? 0xffffffffu : 0;  // beside zeros the scale is any but NaN
+    const uint8_t *const gate = a.w + w_at * row_bytes, *const up = gate + (GATED ? a.N * row_bytes : 0);
+    const uint32_t gate_bytes = capped((a.E * wrows - w_at) * row_bytes);
+    const uint32_t up_bytes = GATED ? capped((a.E * wrows - w_at - a.N) * row_bytes) : gate_bytes;
 
     // The stages' addresses as plain numbers: of what it sees to lie in the array the compiler would wait for every load under
     // way into it, those of later stages included, before each read. What a read needs has come by `meet`.
     uint32_t codes = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)&sh.codes[0][0]));
     asm volatile("" : "+s"(codes));
-    // Loads FROM to TO of stage s. x's chunks past the end of the rows are zeros (beside them the weights' are some codes, and zero
-    // times them is zero); past the last stage nothing is read, but the number of loads is the same in every stage.
-    auto issue = [&](int s, auto from, auto to) {
-        const uint32_t at = codes + (s % kStages) * sizeof(sh.codes[0]) + wave * 16 * kStageBytes, k = s * kStageBytes;
-        const bool there = s < stages, in_row = s * kStageBlocks + chunk < blocks;
-#pragma unroll
-        for (int j = from; j < to; ++j) {
-            if (j < kXLoads) {
-                to_lds(make_rsrc(xbase, xbytes), in_row ? xo[j] + k : 0xfffffff0u, at + 64 * j * kStageBytes);
-            } else {
-                const int i = j - kXLoads;
-                const int64_t row = w_at + (is_up(64 * i + 16 * wave) ? a.N : 0);
-                to_lds(make_rsrc(a.w + row * row_bytes, there ? capped((a.E * wrows - row) * row_bytes) : 0), wo[i] + k,
-                       at + (kTileRows + 64 * i) * kStageBytes);
-            }
-        }
+    auto slot = [&](int s) -> uint32_t {
+        return codes + (s % kStages) * static_cast<uint32_t>(sizeof(sh.codes[0])) + wave * 16 * kStageBytes;
     };
-    const auto none = std::integral_constant<int, 0>{};
-    const auto early = std::integral_constant<int, kEarly>{};
-    const auto all = std::integral_constant<int, kLoads>{};
-
+    // x's chunks past the end of the rows are zeros (beside them the weights' are some codes, and zero times them is zero); past the
+    // last stage nothing is read, but the number of loads is the same in every stage.
+    auto load_x = [&](int s, int j) {
+        to_lds(make_rsrc(xbase, xbytes), s * kStageBlocks + chunk < blocks && xo[j] != kNowhere ? xo[j] + s * kStageBytes : kNowhere,
+               slot(s) + 64 * j * kStageBytes);
+    };
+    auto load_w = [&](int s, int j) {
+        const bool u = is_up(64 * j + 16 * wave);
+        const uint32_t bytes = u ? up_bytes : gate_bytes;
+        to_lds(make_rsrc(u ? up : gate, s < stages ? bytes : 0), wo[j] + s * kStageBytes, slot(s) + (kTileRows + 64 * j) * kStageBytes);
+    };
     // Scales come for kScaleStages stages (a group) at a time, x's and the weights' in turns: thread t has row t's. A row's 16 bytes
     // are put down as what each half of a wavefront needs of them: blocks 0, 1 of each stage's four, then blocks 2, 3.
-    const uint8_t *const xsl = blocks >= 16 ? xsp : a.w, *const wsl = blocks >= 16 ? wsp : a.w;  // (rows of 16 bytes to read)
+    const uint8_t *const xsl = blocks >= 16 ? xsp : a.w;  // (16 bytes to read, where the rows are shorter)
+    const int64_t to_wsl = blocks >= 16 ? wsp - xsp : 0;
     u32x4 sc;
-    auto load_sc = [&](bool w, int g) {  // past the end: what nothing uses
-        __builtin_memcpy(&sc, (w ? wsl : xsl) + max(min(16 * g, blocks - 16), 0), sizeof(sc));
-    };
+    auto scale_at = [&](int g) { return max(min(16 * g, blocks - 16), 0); };  // past the end: what nothing uses
+    auto load_sc = [&](bool w, int g) { __builtin_memcpy(&sc, xsl + (w ? to_wsl : 0) + scale_at(g), sizeof(sc)); };
     auto put_sc = [&](bool w, int g, const u32x4 &v) {
+        const uint32_t k = w ? 0xffffffffu : keep;
         st16(sh.scales[g & 1][(w ? kTileRows : 0) + threadIdx.x],
-             u32x4{__builtin_amdgcn_perm(v.y, v.x, 0x05040100u), __builtin_amdgcn_perm(v.w, v.z, 0x05040100u),
-                   __builtin_amdgcn_perm(v.y, v.x, 0x07060302u), __builtin_amdgcn_perm(v.w, v.z, 0x07060302u)});
+             u32x4{__builtin_amdgcn_perm(v.y, v.x, 0x05040100u) & k, __builtin_amdgcn_perm(v.w, v.z, 0x05040100u) & k,
+                   __builtin_amdgcn_perm(v.y, v.x, 0x07060302u) & k, __builtin_amdgcn_perm(v.w, v.z, 0x07060302u) & k});
     };
-    auto store_sc = [&](bool w, int g) { put_sc(w, g, shifted(sc, min(16 * g - max(min(16 * g, blocks - 16), 0), 15))); };
+    auto store_sc = [&](bool w, int g) { put_sc(w, g, shifted(sc, min(16 * g - scale_at(g), 15))); };
 
-    const int half = lane >> 5, r32 = lane & 31;
-    const int x0 = (wave % WM) * 32 * MS + r32, w0 = kTileRows + (wave / WM) * kWaveCols + r32;
-    // a lane's 16 bytes in steps 0 and 1 of a stage: chunks 2 half and 2 half + 1
-    const uint32_t lane_at[2] = {codes + x0 * kStageBytes + ((2 * half) ^ swizzle(r32)) * 16,
-                                 codes + x0 * kStageBytes + ((2 * half + 1) ^ swizzle(r32)) * 16};
-    auto frag = [&](int s, int row, int ks) -> i32x8 {
-        const uint32_t at = lane_at[ks] + (s % kStages) * sizeof(sh.codes[0]) + row * kStageBytes;
-        const i32x4 v = *reinterpret_cast<const __attribute__((address_space(3))) i32x4 *>(at);
-        return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
-    };
-    Frags<MS, NS> f[2];
-    auto read = [&](int s, int ks, Frags<MS, NS> &to) {
+    const int half = lane >> 5, r32 = lane & 31, swz = swizzle(r32);
+    f32x16 acc[4][4];
+    // The products, for tiles of up to 32 MS WM rows, WM wavefronts beside each other along the rows: a wavefront has 32 MS rows by
+    // 32 NS weight rows, in acc[0 .. NS - 1], or of two, gated, in acc[0] and acc[2].
+    auto products = [&](auto ms, auto ns, auto wm) {
+        constexpr int MS = ms, NS = ns, WM = wm;
+        static_assert(32 * NS * (4 / WM) == kTileCols, "");
+        constexpr int kXLoads = MS * WM < 2 ? 1 : MS * WM / 2, kLoads = kXLoads + 4, kStep = GATED ? 4 / NS : 1;
+        const int x0 = (wave % WM) * 32 * MS + r32, w0 = kTileRows + (wave / WM) * 32 * NS + r32;
+        // a lane's 16 bytes in steps 0 and 1 of a stage: chunks 2 half and 2 half + 1
+        const uint32_t lane_at[2] = {codes + x0 * kStageBytes + ((2 * half) ^ swz) * 16,
+                                     codes + x0 * kStageBytes + ((2 * half + 1) ^ swz) * 16};
+        auto frag = [&](int s, int row, int ks) -> i32x8 {
+            const uint32_t at = lane_at[ks] + (s % kStages) * static_cast<uint32_t>(sizeof(sh.codes[0])) + row * kStageBytes;
+            const i32x4 v = *reinterpret_cast<const __attribute__((address_space(3))) i32x4 *>(at);
+            return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
+        };
+        Frags<MS, NS> f[2];
+        auto read = [&](int s, int ks, Frags<MS, NS> &to) {
 #pragma unroll
-        for (int m = 0; m < MS; ++m)
-            to.x[m] = frag(s, 32 * m, ks);
+            for (int m = 0; m < MS; ++m)
+                to.x[m] = frag(s, 32 * m, ks);
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+                to.w[n] = frag(s, w0 - x0 + 32 * n, ks);
+        };
+        // Scales of stages s and s + 1, s even: steps 0 to 3 have bytes 0 to 3.
+        int xs[MS], ws[NS], next_xs[MS], next_ws[NS];
+        auto read_scales = [&](int s, int (&x)[MS], int (&w)[NS]) {
+            const int word = 2 * half + (s / 2) % 2, g = s / kScaleStages & 1;
+#pragma unroll
+            for (int m = 0; m < MS; ++m)
+                x[m] = static_cast<int>(sh.scales[g][x0 + 32 * m][word]);
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+                w[n] = static_cast<int>(sh.scales[g][w0 + 32 * n][word]);
+        };
 #pragma unroll
         for (int n = 0; n < NS; ++n)
-            to.w[n] = frag(s, w0 - x0 + 32 * n, ks);
-    };
-    // Scales of stages s and s + 1, s even: steps 0 to 3 have bytes 0 to 3.
-    int xs[MS], ws[NS], next_xs[MS], next_ws[NS];
-    auto read_scales = [&](int s, int (&x)[MS], int (&w)[NS]) {
-        const int word = 2 * half + (s / 2) % 2, g = s / kScaleStages & 1;
 #pragma unroll
-        for (int m = 0; m < MS; ++m)
-            x[m] = static_cast<int>(sh.scales[g][x0 + 32 * m][word]);
-#pragma unroll
-        for (int n = 0; n < NS; ++n)
-            w[n] = static_cast<int>(sh.scales[g][w0 + 32 * n][word]);
-    };
-
-    f32x16 acc[NS][MS];
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-        for (int m = 0; m < MS; ++m)
-            acc[n][m] = f32x16{};
+            for (int m = 0; m < MS; ++m)
+                acc[n * kStep][m] = f32x16{};
 #define MOE_PRODUCTS(STEP, F)                                                                                         \
-    _Pragma("unroll") for (int n = 0; n < NS; ++n) _Pragma("unroll") for (int m = 0; m < MS; ++m) acc[n][m] =         \
-        __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(F.w[n], F.x[m], acc[n][m], kFp4, kFp4, STEP, ws[n], STEP, xs[m])
-    // the next step's reads, then loads, each before a product of this step
+    _Pragma("unroll") for (int n = 0; n < NS; ++n) _Pragma("unroll") for (int m = 0; m < MS; ++m) acc[n * kStep][m] = \
+        __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(F.w[n], F.x[m], acc[n * kStep][m], kFp4, kFp4, STEP, ws[n], STEP, xs[m])
+        // the next step's reads, then loads, each before a product of this step
 #define MOE_INTERLEAVE(READS, LOADS)                                                                           \
     _Pragma("unroll") for (int i = 0; i < (READS); ++i)                                                        \
     {                                                                                                          \
@@ -504,148 +516,145 @@ __device__ __forceinline__ void tile_product(const ProductArgs &a, const Tile &t
         __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);                                                     \
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                                     \
     }
-    // Stage s, whose number is J more than an even one: two steps of 64 elements, with the operands of the next step on their way.
-    // Between the steps the next stage has come, and as every wavefront has read all of this one, loads of the stage kStages on go
-    // where it was.
-    auto stage = [&](int s, auto J) {
-        read(s, 1, f[1]);
-        issue(s + kStages - 1, early, all);
-        MOE_PRODUCTS(2 * J, f[0]);
-        MOE_INTERLEAVE(MS + NS, kLoads - kEarly);
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * kLoads) : "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (J == 0) {
-            const bool odd = s & 2;
-            asm volatile("" : "+v"(sc.x), "+v"(sc.y), "+v"(sc.z), "+v"(sc.w));  // used from here on: before, it would be waited for
-            store_sc(!odd, s / kScaleStages + 1);
-            load_sc(odd, s / kScaleStages + (odd ? 2 : 1));
+        // Every wavefront's loads have come but the LEFT newest of each, and every wavefront has read what it asked for.
+        auto meet = [&](auto left) {
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(static_cast<int>(left)) : "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // Stage s, whose number is J more than an even one: two steps of 64 elements, with the operands of the next step on their
+        // way. Between the steps the next stage has come (newer are the loads of two stages), and as every wavefront has read all of
+        // this one, loads of the stage kStages on go where it was.
+        auto stage = [&](int s, auto J) {
+            read(s, 1, f[1]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                load_w(s + kStages - 1, j);
+            MOE_PRODUCTS(2 * J, f[0]);
+            MOE_INTERLEAVE(MS + NS, 4);
+            meet(std::integral_constant<int, 2 * kLoads>{});
+            if constexpr (J == 0) {
+                const bool odd = s & 2;
+                asm volatile("" : "+v"(sc.x), "+v"(sc.y), "+v"(sc.z), "+v"(sc.w));  // used from here on: before, it would be waited for
+                store_sc(!odd, s / kScaleStages + 1);
+                load_sc(odd, s / kScaleStages + (odd ? 2 : 1));
+            }
+            read(s + 1, 0, f[0]);
+#pragma unroll
+            for (int j = 0; j < kXLoads; ++j)
+                load_x(s + kStages, j);
+            if constexpr (J == 1)
+                read_scales(s + 1, next_xs, next_ws);
+            MOE_PRODUCTS(2 * J + 1, f[1]);
+            MOE_INTERLEAVE(MS + NS, kXLoads);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (J == 1) {
+#pragma unroll
+                for (int m = 0; m < MS; ++m)
+                    xs[m] = next_xs[m];
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+                    ws[n] = next_ws[n];
+            }
+        };
+        meet(std::integral_constant<int, 2 * kLoads + kXLoads>{});
+        read(0, 0, f[0]);
+        read_scales(0, xs, ws);
+        for (int s = 0; s < stages; s += 2) {  // after an odd number one of zeros
+            stage(s, std::integral_constant<int, 0>{});
+            stage(s + 1, std::integral_constant<int, 1>{});
         }
-        read(s + 1, 0, f[0]);
-        issue(s + kStages, none, early);
-        if constexpr (J == 1)
-            read_scales(s + 1, next_xs, next_ws);
-        MOE_PRODUCTS(2 * J + 1, f[1]);
-        MOE_INTERLEAVE(MS + NS, kEarly);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (J == 1) {
-#pragma unroll
-            for (int m = 0; m < MS; ++m)
-                xs[m] = next_xs[m];
-#pragma unroll
-            for (int n = 0; n < NS; ++n)
-                ws[n] = next_ws[n];
-        }
-    };
-    issue(0, none, all);
-    if (blocks >= 16) {
-        load_sc(false, 0);
-        const u32x4 x = sc;
-        load_sc(true, 0);
-        const u32x4 w = sc;
-        load_sc(true, 1);
-#pragma unroll
-        for (int s = 1; s < kStages - 1; ++s)
-            issue(s, none, all);
-        issue(kStages - 1, none, early);
-        put_sc(false, 0, x);
-        put_sc(true, 0, w);
-    } else {
-        load_sc(true, 1);
-#pragma unroll
-        for (int s = 1; s < kStages - 1; ++s)
-            issue(s, none, all);
-        issue(kStages - 1, none, early);
-        put_sc(false, 0, short_scales(xsp, blocks));
-        put_sc(true, 0, short_scales(wsp, blocks));
-    }
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * kLoads + kEarly) : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    read(0, 0, f[0]);
-    read_scales(0, xs, ws);
-    for (int s = 0; s < stages; s += 2) {  // after an odd number one of zeros
-        stage(s, std::integral_constant<int, 0>{});
-        stage(s + 1, std::integral_constant<int, 1>{});
-    }
 #undef MOE_INTERLEAVE
 #undef MOE_PRODUCTS
+    };
+
+    // stages 0 to 2, x's of stage 3, the scales of group 0 and the weights' of group 1
+    const int x_loads = big ? 4 : tile.rows > 64 ? 2 : 1;
+    u32x4 xsc, wsc;
+    if (blocks >= 16) {
+        load_sc(false, 0);
+        xsc = sc;
+        load_sc(true, 0);
+        wsc = sc;
+    } else {
+        xsc = short_scales(xsp, blocks);
+        wsc = short_scales(wsp, blocks);
+    }
+    load_sc(true, 1);
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) {
+        load_x(s, 0);
+        if (x_loads > 1)
+            load_x(s, 1);
+        if (x_loads > 2) {
+            load_x(s, 2);
+            load_x(s, 3);
+        }
+        if (s < kStages - 1)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                load_w(s, j);
+    }
+    put_sc(false, 0, xsc);
+    put_sc(true, 0, wsc);
+    const auto i1 = std::integral_constant<int, 1>{};
+    const auto i2 = std::integral_constant<int, 2>{};
+    const auto i4 = std::integral_constant<int, 4>{};
+    if (big)
+        products(i4, i4, i2);
+    else if (tile.rows > 64)
+        products(i4, i2, i1);
+    else if (tile.rows > 32)
+        products(i2, i2, i1);
+    else
+        products(i1, i2, i1);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads past the last stage still write zeros
-    // Lane l holds row l % 32 of x and, in each four registers, four consecutive weight rows. 32 rows at a time go through LDS, a
-    // wavefront's own part of it, and out in whole vectors of a row.
-    constexpr int kOut = GATED ? kHalf : kWaveCols, kPad = 16 / sizeof(O), kPitch = kOut + kPad, kVec = 16 / sizeof(O);
-    static_assert(4 * 32 * kPitch * sizeof(O) <= sizeof(sh.codes), "");
     __syncthreads();
-    O *part = reinterpret_cast<O *>(&sh.codes[0][0]) + wave * 32 * kPitch;
-    const int64_t c0 = n0 + (wave / WM) * kOut;
-    const int cols = static_cast<int>(min(static_cast<int64_t>(kOut), a.N - c0));
+
+    // Lane l holds row l % 32 of x and, in each four registers, four consecutive weight rows. 32 rows at a time go through LDS, a
+    // wavefront's own part of it, and out in vectors of a row.
+    constexpr int kMost = GATED ? 64 : 128, kVec = 16 / sizeof(O), kPitch = kMost + kVec, kLanes = kMost / kVec;
+    static_assert(4 * 32 * kPitch * sizeof(O) <= sizeof(sh.codes), "");
+    const int row0 = big ? wave % 2 * 128 : 0, width = GATED ? wave_half : wave_cols;
+    const int64_t c0 = n0 + (big ? wave / 2 : wave) * width;
+    const int cols = static_cast<int>(min(static_cast<int64_t>(width), a.N - c0));
+    O *const part = reinterpret_cast<O *>(&sh.codes[0][0]) + wave * 32 * kPitch;
     const bool vectors = a.N % kVec == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
 #pragma unroll
-    for (int m = 0; m < MS; ++m) {
-        const int r0 = (wave % WM) * 32 * MS + 32 * m, rows = min(32, tile.rows - r0);
+    for (int m = 0; m < 4; ++m) {
+        const int rows = min(32, tile.rows - row0 - 32 * m);
         if (rows <= 0)
             break;
-        bool there = true;
-        if (a.src_row && r32 < rows) {
-            const int64_t from = a.src_row[tile.first + r0 + r32];
-            there = from >= 0 && from < a.x_rows;
-        }
 #pragma unroll
-        for (int n = 0; n < (GATED ? NS / 2 : NS); ++n)
+        for (int n = 0; n < kMost / 32; ++n)
 #pragma unroll
             for (int q = 0; q < 16; q += 4) {
                 float v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[i] = GATED ? silu(acc[n][m][q + i]) * acc[n + NS / 2][m][q + i] : acc[n][m][q + i];
-                    v[i] = there ? v[i] : 0.0f;
-                }
+                for (int i = 0; i < 4; ++i)
+                    v[i] = GATED ? silu(acc[n][m][q + i]) * acc[n + (GATED ? 2 : 0)][m][q + i] : acc[n][m][q + i];
                 put4(part + r32 * kPitch + 32 * n + 2 * q + 4 * half, v);
             }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        O *out = static_cast<O *>(a.out) + (tile.first + r0) * a.N + c0;
+        O *const out = static_cast<O *>(a.out) + (tile.first + row0 + 32 * m) * a.N + c0;
         if (vectors) {
-            constexpr int kLanes = kOut / kVec;  // lanes a row
+            const int r0 = lane / kLanes, c = lane % kLanes * kVec;
+            O *to = out + r0 * a.N + c;
 #pragma unroll
-            for (int i = 0; i < 32 * kLanes / kWave; ++i) {
-                const int r = i * (kWave / kLanes) + lane / kLanes, c = lane % kLanes * kVec;
-                if (r < rows && c < cols)
-                    st16(out + r * a.N + c, ld16(part + r * kPitch + c));
-            }
+            for (int i = 0; i < 32 * kLanes / kWave; ++i, to += kWave / kLanes * a.N)
+                if (r0 + i * (kWave / kLanes) < rows && c < cols)
+                    st16(to, ld16(part + (r0 + i * (kWave / kLanes)) * kPitch + c));
         } else {
+#pragma unroll 1
             for (int r = 0; r < rows; ++r)
+#pragma unroll 1
                 for (int c = lane; c < cols; c += kWave)
                     out[r * a.N + c] = part[r * kPitch + c];
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-}
-
-// Workgroup b of nb, dealt to the XCDs in turn, takes the place that keeps runs of kRun neighbours on one XCD.
-constexpr uint32_t kRun = 16;
-__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t nb)
-{
-    const uint32_t round = b / (kXcds * kRun), in = b % (kXcds * kRun);
-    return (round + 1) * kXcds * kRun > nb ? b : round * kXcds * kRun + in % kXcds * kRun + in / kXcds;
-}
-
-template <typename O, bool GATED>
-__global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs a)
-{
-    __shared__ __attribute__((aligned(128))) Buffers sh;
-    const Tile tile = find_tile<kTileRows>(a, xcd_run(blockIdx.x, gridDim.x));
-    if (tile.e < 0)
-        return;
-    if (tile.rows > 128)
-        tile_product<O, GATED, 4, 4, 2>(a, tile, sh);
-    else if (tile.rows > 64)
-        tile_product<O, GATED, 4, 2, 1>(a, tile, sh);
-    else if (tile.rows > 32)
-        tile_product<O, GATED, 2, 2, 1>(a, tile, sh);
-    else
-        tile_product<O, GATED, 1, 2, 1>(a, tile, sh);
 }
 
 // Tiles of BM rows that R rows in E segments can need.
@@ -657,7 +666,7 @@ template <typename O, bool GATED>
 moe_status launch_product(ProductArgs a, hipStream_t stream)
 {
     // (rows through a map are addressed in 32 bits there)
-    if (a.R > 16 * static_cast<int64_t>(a.E) && (!a.src_row || a.x_rows * (a.H / 2) <= 0xffffffff)) {
+    if (a.R > 16 * static_cast<int64_t>(a.E) && (!a.src_row || a.x_rows * (a.H / 2) <= kNowhere)) {
         a.col_tiles = static_cast<uint32_t>(ceil_div(a.N, GATED ? kTileCols / 2 : kTileCols));
         const int64_t grid = max_tiles(a.R, a.E, kTileRows) * a.col_tiles;
         if (grid > 0x7fffffff)
