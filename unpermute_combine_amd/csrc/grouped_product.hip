@@ -173,18 +173,21 @@ __device__ __forceinline__ i32x8 operand(const u32x4 &v)
     return i32x8{static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w), 0, 0, 0, 0};
 }
 
-// A wavefront's share of 512 elements: 32 weight rows, 16 rows of x, and their scales.
-struct Run {
-    u32x4 w[2][4], x[4], ws[2], xs;
+// A wavefront's share of 512 elements: 32 weight rows and 16 rows of x, with their scales.
+struct Weights {
+    u32x4 v[2][4], scales[2];
+};
+struct Rows {
+    u32x4 v[4], scales;
 };
 
 // Up to 16 rows of an expert by 32 weight rows (gated: 16 of the gate and the 16 of the up of the same columns) a wavefront. The
 // weights go from memory into the matrix instructions' operand registers, the next 512 elements on their way while these are
 // multiplied. SPLIT wavefronts share the columns and take parts of the sum, put together in LDS.
 template <typename O, bool GATED, int SPLIT>
-__global__ __launch_bounds__(kPlanThreads) void grouped_rows_kernel(ProductArgs a)
+__global__ __launch_bounds__(kPlanThreads, 3) void grouped_rows_kernel(ProductArgs a)
 {
-    constexpr int kWaves = kPlanThreads / kWave, kCols = GATED ? 16 : 32;  // columns a wavefront
+    constexpr int kWaves = kPlanThreads / kWave, kCols = GATED ? 16 : 32;  // columns of a wavefront
     __shared__ f32x4 sums[SPLIT > 1 ? kWaves : 1][2][kWave];
     const Tile tile = find_tile<16>(a, blockIdx.x);
     if (tile.e < 0)
@@ -193,11 +196,38 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_rows_kernel(ProductArgs 
     const int r = lane & 15, g = lane >> 4, part = wave % SPLIT;
     const int64_t n0 = (static_cast<int64_t>(tile.col) * (kWaves / SPLIT) + wave / SPLIT) * kCols;
     const int blocks = static_cast<int>(a.H / kMxBlock), runs = (blocks + kRunBlocks - 1) / kRunBlocks;
-    const int64_t row_bytes = a.H / 2, wrows = a.N * (GATED ? 2 : 1);
+    const int64_t wrows = a.N * (GATED ? 2 : 1);
+    const uint32_t row_bytes = static_cast<uint32_t>(a.H / 2);
+    const int cols = static_cast<int>(min(a.N - n0, static_cast<int64_t>(kCols)));  // this wavefront's, if any
     f32x4 acc[2] = {};
-    if (n0 < a.N) {
-        // x's row r, and the scales' row r of each 16 weight rows
-        int64_t row = tile.first + min(r, tile.rows - 1);
+
+    // lane l holds row l % 16 and four consecutive columns of each 16
+    O *const out = static_cast<O *>(a.out) + (tile.first + r) * a.N + n0;
+    const bool vectors = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & (4 * sizeof(O) - 1)) == 0;
+    auto store = [&]() {
+        if (r < tile.rows) {
+#pragma unroll
+            for (int i = 0; i < (GATED ? 1 : 2); ++i) {
+                const int c = 16 * i + 4 * g;
+                float v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    v[q] = GATED ? silu(acc[0][q]) * acc[1][q] : acc[i][q];
+                if (vectors) {
+                    if (c < cols)
+                        put4(out + c, v);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (c + q < cols)
+                            store_out(out + c + q, v[q]);
+                }
+            }
+        }
+    };
+
+    if (cols > 0) {
+        int64_t row = tile.first + min(r, tile.rows - 1);  // x's row r
         bool there = r < tile.rows;
         if (a.src_row) {
             row = a.src_row[row];
@@ -205,21 +235,16 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_rows_kernel(ProductArgs 
             row = there ? row : 0;
         }
         const uint8_t *const x = a.x + row * row_bytes, *const xs = there ? a.xs + row * blocks : a.ws;
-        // the weight rows from w_at(i) on; of the last columns' those past the end are the last one
-        auto w_at = [&](int i) { return tile.e * wrows + n0 + (GATED ? i * a.N : 16 * i); };
-        auto last = [&](int i) { return static_cast<int>(min(a.N - n0 - (GATED ? 0 : 16 * i), int64_t{16})) - 1; };
-        uint32_t wo[2][2];
+        // weights from this wavefront's first column on (gated: of the gate and of the up)
+        const int64_t at = tile.e * wrows + n0;
         const uint8_t *ws[2];
         __amdgpu_buffer_rsrc_t wr[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int end = max(last(i), 0);
-            const int64_t at = min(w_at(i), a.E * wrows - 1);
-            wr[i] = make_rsrc(a.w + at * row_bytes, static_cast<uint32_t>(min((a.E * wrows - at) * row_bytes, int64_t{0xfffffff0})));
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                wo[i][j] = static_cast<uint32_t>(min(8 * j + (r & 7), end) * row_bytes) + (g + (r & 8) / 2) * 16;
-            ws[i] = a.ws + (at + min(r, end)) * blocks;
+            const int64_t first = at + (GATED ? i * a.N : 0);
+            wr[i] = make_rsrc(a.w + first * row_bytes,
+                              static_cast<uint32_t>(min((a.E * wrows - first) * row_bytes, static_cast<int64_t>(0xfffffff0))));
+            ws[i] = a.ws + first * blocks;
         }
         auto scales = [&](const uint8_t *from, int run) -> u32x4 {
             if (blocks < kRunBlocks)
@@ -228,35 +253,41 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_rows_kernel(ProductArgs 
             __builtin_memcpy(&v, from + min(run * kRunBlocks, blocks - kRunBlocks), sizeof(v));
             return v;
         };
-        auto load = [&](int run, Run &to) {
+        auto load_w = [&](int run, Weights &to) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i) {
+                const int n = GATED ? 0 : 16 * i;  // past the last column that column's weights
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    to.w[i][j] = ld16_buf<0>(wr[i], wo[i][j & 1] + run * kRunBytes + (j >> 1) * 128);
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t o = min(n + 8 * j + (r & 7), cols - 1) * row_bytes + (g + (r & 8) / 2) * 16 + run * kRunBytes;
+                    to.v[i][j] = ld16_buf<kPolicyStreamLoad>(wr[i], o);
+                    to.v[i][2 + j] = ld16_buf<kPolicyStreamLoad>(wr[i], o + 128);
+                }
+                to.scales[i] = scales(ws[i] + min(n + r, cols - 1) * blocks, run);
+            }
+        };
+        auto load_x = [&](int run, Rows &to) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int b = run * kRunBlocks + 4 * j + g;
-                to.x[j] = u32x4{0, 0, 0, 0};
+                to.v[j] = u32x4{0, 0, 0, 0};
                 if (there && b < blocks)
-                    to.x[j] = ld16(x + b * 16);
+                    to.v[j] = ld16(x + b * 16);
             }
-            to.ws[0] = scales(ws[0], run);
-            to.ws[1] = scales(ws[1], run);
-            to.xs = scales(xs, run);
+            to.scales = scales(xs, run);
         };
-        auto multiply = [&](int run, Run &f) {
+        const uint32_t keep = there ? 0xffffffffu : 0;  // beside zeros the scale is any but NaN
+        auto multiply = [&](int run, Weights &w, const Rows &x) {
             const int past = blocks < kRunBlocks ? 0 : run * kRunBlocks - min(run * kRunBlocks, blocks - kRunBlocks);
-            const u32x4 sx = shifted(f.xs, past);
-            const uint32_t keep = there ? 0xffffffffu : 0;
+            const u32x4 sx = shifted(x.scales, past);
             const uint32_t s[4] = {sx.x & keep, sx.y & keep, sx.z & keep, sx.w & keep};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const u32x4 sw = shifted(f.ws[i], past);
+                const u32x4 sw = shifted(w.scales[i], past);
                 const uint32_t t[4] = {sw.x, sw.y, sw.z, sw.w};
 #pragma unroll
                 for (int j = 0; j < 4; j += 2) {
-                    u32x4 &p = f.w[i][j], &q = f.w[i][j + 1];
+                    u32x4 &p = w.v[i][j], &q = w.v[i][j + 1];
                     swap_eights(p.x, q.x);
                     swap_eights(p.y, q.y);
                     swap_eights(p.z, q.z);
@@ -265,27 +296,32 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_rows_kernel(ProductArgs 
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        operand(f.w[i][j]), operand(f.x[j]), acc[i], kFp4, kFp4, 0, static_cast<int>(t[j] >> (8 * g)), 0,
+                        operand(w.v[i][j]), operand(x.v[j]), acc[i], kFp4, kFp4, 0, static_cast<int>(t[j] >> (8 * g)), 0,
                         static_cast<int>(s[j] >> (8 * g)));
             }
         };
         const int from = runs * part / SPLIT, to = runs * (part + 1) / SPLIT;
         if (from < to) {
-            Run f[2];
-            load(from, f[0]);
+            Weights f[2];
+            Rows rows;
+            load_w(from, f[0]);
+            load_x(from, rows);
             int run = from;
             for (; run + 2 < to; run += 2) {
-                load(run + 1, f[1]);
-                multiply(run, f[0]);
-                load(run + 2, f[0]);
-                multiply(run + 1, f[1]);
+                load_w(run + 1, f[1]);
+                multiply(run, f[0], rows);
+                load_x(run + 1, rows);
+                load_w(run + 2, f[0]);
+                multiply(run + 1, f[1], rows);
+                load_x(run + 2, rows);
             }
             if (run + 1 < to) {
-                load(run + 1, f[1]);
-                multiply(run, f[0]);
-                multiply(run + 1, f[1]);
+                load_w(run + 1, f[1]);
+                multiply(run, f[0], rows);
+                load_x(run + 1, rows);
+                multiply(run + 1, f[1], rows);
             } else {
-                multiply(run, f[0]);
+                multiply(run, f[0], rows);
             }
         }
     }
@@ -303,28 +339,8 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_rows_kernel(ProductArgs 
             acc[1] += sums[wave + p][1][lane];
         }
     }
-    // lane l holds row l % 16 and four consecutive columns of each 16
-    if (r >= tile.rows)
-        return;
-    O *const out = static_cast<O *>(a.out) + (tile.first + r) * a.N;
-    const bool vectors = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & (4 * sizeof(O) - 1)) == 0;
-#pragma unroll
-    for (int i = 0; i < (GATED ? 1 : 2); ++i) {
-        const int64_t c = n0 + 16 * i + 4 * g;
-        float v[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            v[q] = GATED ? silu(acc[0][q]) * acc[1][q] : acc[i][q];
-        if (vectors) {
-            if (c < a.N)
-                put4(out + c, v);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (c + q < a.N)
-                    store_out(out + c + q, v[q]);
-        }
-    }
+    if (cols > 0)
+        store();
 }
 
 // ---------------------------------------------------------------- tiles through LDS
@@ -332,7 +348,6 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_rows_kernel(ProductArgs 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kTileRows = 256, kTileCols = 256;  // rows and weight rows of the largest tile
 constexpr int kStageBytes = 64;                  // of each row a stage: 128 elements
 constexpr int kStageBlocks = kStageBytes / 16;
 constexpr int kStages = 4;                       // of which LDS has room
@@ -342,9 +357,10 @@ constexpr int kScaleStages = 4;                  // stages whose scales come at 
 // different banks.
 __device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
 
+template <int ROWS, int COLS>
 struct Buffers {
-    uint8_t codes[kStages][(kTileRows + kTileCols) * kStageBytes];
-    uint32_t scales[2][kTileRows + kTileCols][4];
+    uint8_t codes[kStages][(ROWS + COLS) * kStageBytes];
+    uint32_t scales[2][2][kPlanThreads][4];  // x's and the weights'
 };
 
 // 16 bytes a lane into LDS, lane l's to address `to` + 16 l (one for the wavefront). Past the resource's end: zeros.
@@ -375,21 +391,25 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t nb)
     return (round + 1) * kXcds * kRun > nb ? b : round * kXcds * kRun + in % kXcds * kRun + in / kXcds;
 }
 
-// A tile of up to 256 rows by 256 weight rows (gated: 128 of the gate and the 128 of the up of the same columns), four wavefronts.
-// Of more than 128 rows a wavefront has 128 by 128 weight rows, two wavefronts beside each other each way; of fewer all of them by
-// 64 weight rows. Gated, a wavefront's first half are gates, its second the ups of the same columns.
-template <typename O, bool GATED>
+// A tile of up to ROWS rows by COLS weight rows (gated: half of the gate and the half of the up of the same columns), four
+// wavefronts. Wide tiles are 256 by 256: of more than 128 rows a wavefront has 128 by 128 weight rows, two wavefronts beside each
+// other each way; of fewer all of them by 64 weight rows. Narrow ones, 128 by 64, are for products of which the wide ones would
+// leave CUs without one: a wavefront has 32 rows by all weight rows. Gated, a wavefront's first half are gates, its second the ups
+// of the same columns.
+template <typename O, bool GATED, int ROWS, int COLS>
 __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs a)
 {
-    __shared__ __attribute__((aligned(128))) Buffers sh;
-    const Tile tile = find_tile<kTileRows>(a, xcd_run(blockIdx.x, gridDim.x));
+    constexpr bool kWide = COLS == 256;
+    static_assert(kWide ? ROWS == 256 : ROWS == 128 && COLS == 64, "");
+    __shared__ __attribute__((aligned(128))) Buffers<ROWS, COLS> sh;
+    const Tile tile = find_tile<ROWS>(a, xcd_run(blockIdx.x, gridDim.x));
     if (tile.e < 0)
         return;
-    constexpr int kOutCols = GATED ? kTileCols / 2 : kTileCols;
+    constexpr int kOutCols = GATED ? COLS / 2 : COLS, kXMost = ROWS / 64, kWLoads = COLS / 64;  // 16-byte loads a thread and stage
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / kWave));
     const int blocks = static_cast<int>(a.H / kMxBlock), stages = (blocks + kStageBlocks - 1) / kStageBlocks;
     const int64_t row_bytes = a.H / 2, n0 = static_cast<int64_t>(tile.col) * kOutCols;
-    const bool big = tile.rows > 128;
+    const bool big = kWide && tile.rows > 128;
     const int wave_cols = big ? 128 : 64, wave_half = wave_cols / 2;
 
     // A load takes 16 rows a wavefront, 4 lanes a row: thread t chunk slot t % 4 of rows 64 j + t / 4. Loads go by buffer resources,
@@ -411,13 +431,15 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
         return min(n, a.N - 1 - n0);
     };
     auto is_up = [&](int b) { return GATED && b % wave_cols >= wave_half; };
-    uint32_t xo[4], wo[4];
+    uint32_t xo[kXMost], wo[kWLoads];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kXMost; ++j) {
         const int64_t row = x_row(64 * j + threadIdx.x / 4);
         xo[j] = row >= 0 ? static_cast<uint32_t>((row - x_at) * row_bytes) + chunk * 16 : kNowhere;
-        wo[j] = static_cast<uint32_t>(w_row(64 * j + threadIdx.x / 4) * row_bytes) + chunk * 16;
     }
+#pragma unroll
+    for (int j = 0; j < kWLoads; ++j)
+        wo[j] = static_cast<uint32_t>(w_row(64 * j + threadIdx.x / 4) * row_bytes) + chunk * 16;
     const uint8_t *const wsp = a.ws + (w_at + w_row(threadIdx.x) + (is_up(threadIdx.x) ? a.N : 0)) * blocks;
     const int64_t xs_row = x_row(threadIdx.x);
     const uint8_t *const xsp = xs_row >= 0 ? a.xs + xs_row * blocks : wsp;
@@ -442,7 +464,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     auto load_w = [&](int s, int j) {
         const bool u = is_up(64 * j + 16 * wave);
         const uint32_t bytes = u ? up_bytes : gate_bytes;
-        to_lds(make_rsrc(u ? up : gate, s < stages ? bytes : 0), wo[j] + s * kStageBytes, slot(s) + (kTileRows + 64 * j) * kStageBytes);
+        to_lds(make_rsrc(u ? up : gate, s < stages ? bytes : 0), wo[j] + s * kStageBytes, slot(s) + (ROWS + 64 * j) * kStageBytes);
     };
     // Scales come for kScaleStages stages (a group) at a time, x's and the weights' in turns: thread t has row t's. A row's 16 bytes
     // are put down as what each half of a wavefront needs of them: blocks 0, 1 of each stage's four, then blocks 2, 3.
@@ -453,7 +475,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     auto load_sc = [&](bool w, int g) { __builtin_memcpy(&sc, xsl + (w ? to_wsl : 0) + scale_at(g), sizeof(sc)); };
     auto put_sc = [&](bool w, int g, const u32x4 &v) {
         const uint32_t k = w ? 0xffffffffu : keep;
-        st16(sh.scales[g & 1][(w ? kTileRows : 0) + threadIdx.x],
+        st16(sh.scales[g & 1][w ? 1 : 0][threadIdx.x],
              u32x4{__builtin_amdgcn_perm(v.y, v.x, 0x05040100u) & k, __builtin_amdgcn_perm(v.w, v.z, 0x05040100u) & k,
                    __builtin_amdgcn_perm(v.y, v.x, 0x07060302u) & k, __builtin_amdgcn_perm(v.w, v.z, 0x07060302u) & k});
     };
@@ -465,9 +487,9 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     // 32 NS weight rows, in acc[0 .. NS - 1], or of two, gated, in acc[0] and acc[2].
     auto products = [&](auto ms, auto ns, auto wm) {
         constexpr int MS = ms, NS = ns, WM = wm;
-        static_assert(32 * NS * (4 / WM) == kTileCols, "");
-        constexpr int kXLoads = MS * WM < 2 ? 1 : MS * WM / 2, kLoads = kXLoads + 4, kStep = GATED ? 4 / NS : 1;
-        const int x0 = (wave % WM) * 32 * MS + r32, w0 = kTileRows + (wave / WM) * 32 * NS + r32;
+        static_assert(32 * NS * (4 / WM) == COLS, "");
+        constexpr int kXLoads = MS * WM < 2 ? 1 : MS * WM / 2, kLoads = kXLoads + kWLoads, kStep = GATED ? 4 / NS : 1;
+        const int x0 = (wave % WM) * 32 * MS + r32, w0 = ROWS + (wave / WM) * 32 * NS + r32;
         // a lane's 16 bytes in steps 0 and 1 of a stage: chunks 2 half and 2 half + 1
         const uint32_t lane_at[2] = {codes + x0 * kStageBytes + ((2 * half) ^ swz) * 16,
                                      codes + x0 * kStageBytes + ((2 * half + 1) ^ swz) * 16};
@@ -491,10 +513,10 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
             const int word = 2 * half + (s / 2) % 2, g = s / kScaleStages & 1;
 #pragma unroll
             for (int m = 0; m < MS; ++m)
-                x[m] = static_cast<int>(sh.scales[g][x0 + 32 * m][word]);
+                x[m] = static_cast<int>(sh.scales[g][0][x0 + 32 * m][word]);
 #pragma unroll
             for (int n = 0; n < NS; ++n)
-                w[n] = static_cast<int>(sh.scales[g][w0 + 32 * n][word]);
+                w[n] = static_cast<int>(sh.scales[g][1][w0 - ROWS + 32 * n][word]);
         };
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -530,10 +552,10 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
         auto stage = [&](int s, auto J) {
             read(s, 1, f[1]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < kWLoads; ++j)
                 load_w(s + kStages - 1, j);
             MOE_PRODUCTS(2 * J, f[0]);
-            MOE_INTERLEAVE(MS + NS, 4);
+            MOE_INTERLEAVE(MS + NS, kWLoads);
             meet(std::integral_constant<int, 2 * kLoads>{});
             if constexpr (J == 0) {
                 const bool odd = s & 2;
@@ -571,7 +593,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     };
 
     // stages 0 to 2, x's of stage 3, the scales of group 0 and the weights' of group 1
-    const int x_loads = big ? 4 : tile.rows > 64 ? 2 : 1;
+    const int x_loads = !kWide ? 2 : big ? 4 : tile.rows > 64 ? 2 : 1;
     u32x4 xsc, wsc;
     if (blocks >= 16) {
         load_sc(false, 0);
@@ -585,16 +607,13 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     load_sc(true, 1);
 #pragma unroll
     for (int s = 0; s < kStages; ++s) {
-        load_x(s, 0);
-        if (x_loads > 1)
-            load_x(s, 1);
-        if (x_loads > 2) {
-            load_x(s, 2);
-            load_x(s, 3);
-        }
+#pragma unroll
+        for (int j = 0; j < kXMost; ++j)
+            if (j < x_loads)
+                load_x(s, j);
         if (s < kStages - 1)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < kWLoads; ++j)
                 load_w(s, j);
     }
     put_sc(false, 0, xsc);
@@ -602,7 +621,9 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     const auto i1 = std::integral_constant<int, 1>{};
     const auto i2 = std::integral_constant<int, 2>{};
     const auto i4 = std::integral_constant<int, 4>{};
-    if (big)
+    if constexpr (!kWide)
+        products(i1, i2, i4);
+    else if (big)
         products(i4, i4, i2);
     else if (tile.rows > 64)
         products(i4, i2, i1);
@@ -615,15 +636,15 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
 
     // Lane l holds row l % 32 of x and, in each four registers, four consecutive weight rows. 32 rows at a time go through LDS, a
     // wavefront's own part of it, and out in vectors of a row.
-    constexpr int kMost = GATED ? 64 : 128, kVec = 16 / sizeof(O), kPitch = kMost + kVec, kLanes = kMost / kVec;
+    constexpr int kMost = (kWide ? 128 : 64) / (GATED ? 2 : 1), kVec = 16 / sizeof(O), kPitch = kMost + kVec, kLanes = kMost / kVec;
     static_assert(4 * 32 * kPitch * sizeof(O) <= sizeof(sh.codes), "");
-    const int row0 = big ? wave % 2 * 128 : 0, width = GATED ? wave_half : wave_cols;
-    const int64_t c0 = n0 + (big ? wave / 2 : wave) * width;
+    const int row0 = !kWide ? wave * 32 : big ? wave % 2 * 128 : 0, width = GATED ? wave_half : wave_cols;
+    const int64_t c0 = n0 + (!kWide ? 0 : big ? wave / 2 : wave) * width;
     const int cols = static_cast<int>(min(static_cast<int64_t>(width), a.N - c0));
     O *const part = reinterpret_cast<O *>(&sh.codes[0][0]) + wave * 32 * kPitch;
     const bool vectors = a.N % kVec == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
+    for (int m = 0; m < (kWide ? 4 : 1); ++m) {
         const int rows = min(32, tile.rows - row0 - 32 * m);
         if (rows <= 0)
             break;
@@ -660,18 +681,27 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
 // Tiles of BM rows that R rows in E segments can need.
 int64_t max_tiles(int64_t R, int64_t E, int64_t BM) { return R / BM + std::min(R, E); }
 
+constexpr int64_t kWorkgroups = 256;  // of the wide tiles at a time: one a CU
 constexpr int64_t kFewUnits = 4096;
 
 template <typename O, bool GATED>
 moe_status launch_product(ProductArgs a, hipStream_t stream)
 {
-    // (rows through a map are addressed in 32 bits there)
-    if (a.R > 16 * static_cast<int64_t>(a.E) && (!a.src_row || a.x_rows * (a.H / 2) <= kNowhere)) {
-        a.col_tiles = static_cast<uint32_t>(ceil_div(a.N, GATED ? kTileCols / 2 : kTileCols));
-        const int64_t grid = max_tiles(a.R, a.E, kTileRows) * a.col_tiles;
-        if (grid > 0x7fffffff)
+    const int64_t experts = std::min(a.R, static_cast<int64_t>(a.E));  // with rows, at most
+    const int64_t wide = std::max(experts, a.R / 256) * ceil_div(a.N, GATED ? 128 : 256);  // tiles, about
+    const bool few_rows = a.R <= (wide < kWorkgroups ? 24 : 8) * static_cast<int64_t>(a.E);
+    // (rows through a map are addressed in 32 bits by the tiles)
+    if (!few_rows && (!a.src_row || a.x_rows * (a.H / 2) <= kNowhere)) {
+        const bool narrow = wide < kWorkgroups;
+        a.col_tiles = static_cast<uint32_t>(ceil_div(a.N, (narrow ? 64 : 256) / (GATED ? 2 : 1)));
+        const int64_t tiles = max_tiles(a.R, a.E, narrow ? 128 : 256) * a.col_tiles;
+        if (tiles > 0x7fffffff)
             return MOE_ERR_UNSUPPORTED;
-        hipLaunchKernelGGL((grouped_tile_kernel<O, GATED>), dim3(static_cast<unsigned>(grid)), dim3(kPlanThreads), 0, stream, a);
+        const dim3 grid(static_cast<unsigned>(tiles));
+        if (narrow)
+            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 128, 64>), grid, dim3(kPlanThreads), 0, stream, a);
+        else
+            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 256, 256>), grid, dim3(kPlanThreads), 0, stream, a);
         return launch_status();
     }
     const int64_t tiles = max_tiles(a.R, a.E, 16), units = tiles * ceil_div(a.N, GATED ? 16 : 32);
