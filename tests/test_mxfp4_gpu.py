@@ -212,6 +212,10 @@ SIZES = [  # lengths of the segments, H, N
     ([1], 32, 1), ([1], 7168, 48), ([2, 0, 1], 64, 17), ([0, 0, 5], 96, 16), ([16, 17, 1, 0, 33], 160, 33), ([3] * 20, 512, 100),
     ([40, 64, 65], 544, 130), ([127, 128, 129, 1], 1056, 257), ([300, 7, 0, 255], 2080, 1399), ([513], 256, 512), ([1] * 70, 1024, 64),
     ([0, 700, 2], 4096, 300), ([64, 32, 16, 8], 288, 256), ([260, 511], 480, 768),
+    # many columns: the largest tiles, all of their heights
+    ([300, 7, 0, 255], 96, 22000), ([130, 260, 40, 70, 1], 1056, 14001), ([33, 64, 100, 520], 2080, 17000), ([600], 544, 66000),
+    # few rows each of many columns: whole sums, and parts of them
+    ([1] * 70, 2080, 2048), ([17, 1, 0, 3], 4128, 96),
 ]
 
 

@@ -360,7 +360,7 @@ __device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 3) ^ ((r >> 3
 template <int ROWS, int COLS>
 struct Buffers {
     uint8_t codes[kStages][(ROWS + COLS) * kStageBytes];
-    uint32_t scales[2][2][kPlanThreads][4];  // x's and the weights'
+    uint32_t scales[2][ROWS + COLS][4];
 };
 
 // 16 bytes a lane into LDS, lane l's to address `to` + 16 l (one for the wavefront). Past the resource's end: zeros.
@@ -393,14 +393,14 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t nb)
 
 // A tile of up to ROWS rows by COLS weight rows (gated: half of the gate and the half of the up of the same columns), four
 // wavefronts. Wide tiles are 256 by 256: of more than 128 rows a wavefront has 128 by 128 weight rows, two wavefronts beside each
-// other each way; of fewer all of them by 64 weight rows. Narrow ones, 128 by 64, are for products of which the wide ones would
-// leave CUs without one: a wavefront has 32 rows by all weight rows. Gated, a wavefront's first half are gates, its second the ups
-// of the same columns.
+// other each way; of fewer all of them by 64 weight rows. Tiles of 128 by 128, a wavefront with 64 by 64 or, of up to 64 rows, 32
+// by 64, two to a CU, are for products of which the wide ones would leave CUs without one. Gated, a wavefront's first half are
+// gates, its second the ups of the same columns.
 template <typename O, bool GATED, int ROWS, int COLS>
 __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs a)
 {
     constexpr bool kWide = COLS == 256;
-    static_assert(kWide ? ROWS == 256 : ROWS == 128 && COLS == 64, "");
+    static_assert(ROWS == COLS && (kWide || COLS == 128), "");
     __shared__ __attribute__((aligned(128))) Buffers<ROWS, COLS> sh;
     const Tile tile = find_tile<ROWS>(a, xcd_run(blockIdx.x, gridDim.x));
     if (tile.e < 0)
@@ -440,8 +440,9 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
 #pragma unroll
     for (int j = 0; j < kWLoads; ++j)
         wo[j] = static_cast<uint32_t>(w_row(64 * j + threadIdx.x / 4) * row_bytes) + chunk * 16;
-    const uint8_t *const wsp = a.ws + (w_at + w_row(threadIdx.x) + (is_up(threadIdx.x) ? a.N : 0)) * blocks;
-    const int64_t xs_row = x_row(threadIdx.x);
+    const int x_mine = threadIdx.x % ROWS, w_mine = threadIdx.x % COLS;  // rows whose scales a thread takes (some twice)
+    const uint8_t *const wsp = a.ws + (w_at + w_row(w_mine) + (is_up(w_mine) ? a.N : 0)) * blocks;
+    const int64_t xs_row = x_row(x_mine);
     const uint8_t *const xsp = xs_row >= 0 ? a.xs + xs_row * blocks : wsp;
     const uint32_t keep = xs_row >= 0 ? 0xffffffffu : 0;  // beside zeros the scale is any but NaN
     const uint8_t *const gate = a.w + w_at * row_bytes, *const up = gate + (GATED ? a.N * row_bytes : 0);
@@ -466,7 +467,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
         const uint32_t bytes = u ? up_bytes : gate_bytes;
         to_lds(make_rsrc(u ? up : gate, s < stages ? bytes : 0), wo[j] + s * kStageBytes, slot(s) + (ROWS + 64 * j) * kStageBytes);
     };
-    // Scales come for kScaleStages stages (a group) at a time, x's and the weights' in turns: thread t has row t's. A row's 16 bytes
+    // Scales come for kScaleStages stages (a group) at a time, x's and the weights' in turns. A row's 16 bytes
     // are put down as what each half of a wavefront needs of them: blocks 0, 1 of each stage's four, then blocks 2, 3.
     const uint8_t *const xsl = blocks >= 16 ? xsp : a.w;  // (16 bytes to read, where the rows are shorter)
     const int64_t to_wsl = blocks >= 16 ? wsp - xsp : 0;
@@ -475,7 +476,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     auto load_sc = [&](bool w, int g) { __builtin_memcpy(&sc, xsl + (w ? to_wsl : 0) + scale_at(g), sizeof(sc)); };
     auto put_sc = [&](bool w, int g, const u32x4 &v) {
         const uint32_t k = w ? 0xffffffffu : keep;
-        st16(sh.scales[g & 1][w ? 1 : 0][threadIdx.x],
+        st16(sh.scales[g & 1][w ? ROWS + w_mine : x_mine],
              u32x4{__builtin_amdgcn_perm(v.y, v.x, 0x05040100u) & k, __builtin_amdgcn_perm(v.w, v.z, 0x05040100u) & k,
                    __builtin_amdgcn_perm(v.y, v.x, 0x07060302u) & k, __builtin_amdgcn_perm(v.w, v.z, 0x07060302u) & k});
     };
@@ -513,10 +514,10 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
             const int word = 2 * half + (s / 2) % 2, g = s / kScaleStages & 1;
 #pragma unroll
             for (int m = 0; m < MS; ++m)
-                x[m] = static_cast<int>(sh.scales[g][0][x0 + 32 * m][word]);
+                x[m] = static_cast<int>(sh.scales[g][x0 + 32 * m][word]);
 #pragma unroll
             for (int n = 0; n < NS; ++n)
-                w[n] = static_cast<int>(sh.scales[g][1][w0 - ROWS + 32 * n][word]);
+                w[n] = static_cast<int>(sh.scales[g][w0 + 32 * n][word]);
         };
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -593,7 +594,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     };
 
     // stages 0 to 2, x's of stage 3, the scales of group 0 and the weights' of group 1
-    const int x_loads = !kWide ? 2 : big ? 4 : tile.rows > 64 ? 2 : 1;
+    const int x_loads = big ? 4 : tile.rows > 64 ? 2 : 1;
     u32x4 xsc, wsc;
     if (blocks >= 16) {
         load_sc(false, 0);
@@ -622,7 +623,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     const auto i2 = std::integral_constant<int, 2>{};
     const auto i4 = std::integral_constant<int, 4>{};
     if constexpr (!kWide)
-        products(i1, i2, i4);
+        tile.rows > 64 ? products(i2, i2, i2) : products(i1, i2, i2);
     else if (big)
         products(i4, i4, i2);
     else if (tile.rows > 64)
@@ -638,14 +639,15 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     // wavefront's own part of it, and out in vectors of a row.
     constexpr int kMost = (kWide ? 128 : 64) / (GATED ? 2 : 1), kVec = 16 / sizeof(O), kPitch = kMost + kVec, kLanes = kMost / kVec;
     static_assert(4 * 32 * kPitch * sizeof(O) <= sizeof(sh.codes), "");
-    const int row0 = !kWide ? wave * 32 : big ? wave % 2 * 128 : 0, width = GATED ? wave_half : wave_cols;
-    const int64_t c0 = n0 + (!kWide ? 0 : big ? wave / 2 : wave) * width;
+    const int row0 = !kWide ? wave % 2 * (tile.rows > 64 ? 64 : 32) : big ? wave % 2 * 128 : 0;
+    const int width = GATED ? wave_half : wave_cols;
+    const int64_t c0 = n0 + (!kWide || big ? wave / 2 : wave) * width;
     const int cols = static_cast<int>(min(static_cast<int64_t>(width), a.N - c0));
     O *const part = reinterpret_cast<O *>(&sh.codes[0][0]) + wave * 32 * kPitch;
     const bool vectors = a.N % kVec == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
 #pragma unroll
-    for (int m = 0; m < (kWide ? 4 : 1); ++m) {
-        const int rows = min(32, tile.rows - row0 - 32 * m);
+    for (int m = 0; m < (kWide ? 4 : 2); ++m) {
+        const int rows = min(!kWide && tile.rows <= 64 && m > 0 ? 0 : 32, tile.rows - row0 - 32 * m);
         if (rows <= 0)
             break;
 #pragma unroll
@@ -689,17 +691,17 @@ moe_status launch_product(ProductArgs a, hipStream_t stream)
 {
     const int64_t experts = std::min(a.R, static_cast<int64_t>(a.E));  // with rows, at most
     const int64_t wide = std::max(experts, a.R / 256) * ceil_div(a.N, GATED ? 128 : 256);  // tiles, about
-    const bool few_rows = a.R <= (wide < kWorkgroups ? 24 : 8) * static_cast<int64_t>(a.E);
+    const bool few_rows = a.R <= (wide < kWorkgroups ? 16 : 8) * static_cast<int64_t>(a.E);
     // (rows through a map are addressed in 32 bits by the tiles)
     if (!few_rows && (!a.src_row || a.x_rows * (a.H / 2) <= kNowhere)) {
-        const bool narrow = wide < kWorkgroups;
-        a.col_tiles = static_cast<uint32_t>(ceil_div(a.N, (narrow ? 64 : 256) / (GATED ? 2 : 1)));
-        const int64_t tiles = max_tiles(a.R, a.E, narrow ? 128 : 256) * a.col_tiles;
+        const int size = wide < kWorkgroups ? 128 : 256;
+        a.col_tiles = static_cast<uint32_t>(ceil_div(a.N, GATED ? size / 2 : size));
+        const int64_t tiles = max_tiles(a.R, a.E, size) * a.col_tiles;
         if (tiles > 0x7fffffff)
             return MOE_ERR_UNSUPPORTED;
         const dim3 grid(static_cast<unsigned>(tiles));
-        if (narrow)
-            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 128, 64>), grid, dim3(kPlanThreads), 0, stream, a);
+        if (size == 128)
+            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 128, 128>), grid, dim3(kPlanThreads), 0, stream, a);
         else
             hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 256, 256>), grid, dim3(kPlanThreads), 0, stream, a);
         return launch_status();
