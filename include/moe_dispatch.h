@@ -390,7 +390,8 @@ moe_status moe_route_topk_backward(const int32_t *topk_idx, const float *topk_w,
  *   [0, E) count nowhere; token_mask [T] bytes or NULL: tokens with 0 (padding) count nowhere, whatever their logits hold.
  *   loss [1] float32; counts [E] int32: slots of each expert; prob_sum [E] float32: sum_t p[t,e]; tokens [1] int32: n. With
  *   tokens on several ranks counts, prob_sum and tokens are what is summed over the ranks (the loss follows from them).
- * p is float32, its sums and the loss are double, rounded once; no result depends on timing. coef must be finite.
+ * p is float32; its sums are double (eight tokens at a time, and a workgroup's, float32), the loss double, rounded once; no
+ * result depends on timing. coef must be finite.
  * T * K <= 2^31 - 1 (else MOE_ERR_UNSUPPORTED). T = 0 writes zeros. The workspace (16-byte aligned, contents need no
  * initialisation and mean nothing after the call) must hold moe_balance_loss_workspace_size bytes; calls that may overlap
  * need one each. */
@@ -402,8 +403,8 @@ moe_status moe_balance_loss(const float *logits, const int32_t *topk_idx, const 
 /* Backward of moe_balance_loss, from its counts and tokens (or their sums over ranks: the gradient is then that of the loss
  * of all ranks' tokens):
  *   d_logits[t,e] = d_loss * coef * (E/n) * p[t,e] * (f_e - sum_j f_j p[t,j])  (+ d_logits_in[t,e])
- * and 0 (+ d_logits_in) for tokens that do not count, and where n <= 0; the counts, piecewise constant, have no gradient. The
- * sum over j and the difference are double, the rest float32.
+ * and 0 (+ d_logits_in) for tokens that do not count, and where n <= 0; the counts, piecewise constant, have no gradient. In
+ * float32.
  *   d_loss [1] float32 (NULL: 1); d_logits_in [T, E] or NULL: the gradient that reaches the logits by other ways
  *   (moe_route_topk_backward's); d_logits [T, E], which may be d_logits_in. */
 moe_status moe_balance_loss_backward(const float *logits, const uint8_t *token_mask, const int32_t *counts,

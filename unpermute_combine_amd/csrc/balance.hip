@@ -10,9 +10,11 @@
 namespace moe {
 namespace {
 
-constexpr int kStatThreads = 1024;
+constexpr int kStatThreads = 512;
+constexpr int kJoinThreads = 256, kJoinCols = 32, kMaxJoinBlocks = MOE_MAX_EXPERTS / kJoinCols;
 constexpr int kBackThreads = 256;
-constexpr int kMaxStatBlocks = 128;
+constexpr int kMaxStatBlocks = 256;  // one a CU
+constexpr int kFlush = 8;            // tokens of a lane summed in float32 before they join its double sums
 
 constexpr int kDppRowMirror = 0x140;
 constexpr int kDppRowHalfMirror = 0x141;
@@ -54,11 +56,10 @@ __device__ __forceinline__ float token_sum(float v)
     return v;
 }
 
-template <int L>
-__device__ __forceinline__ double token_sum(double v)
+__device__ __forceinline__ double wave_sum(double v)
 {
 #pragma unroll
-    for (int d = 1; d < L; d *= 2)
+    for (int d = 1; d < kWave; d *= 2)
         v += __shfl_xor(v, d);
     return v;
 }
@@ -70,49 +71,68 @@ __device__ __forceinline__ int column(int sub, int q, int i)
     return V4 ? 4 * (sub + L * q) + i : sub + L * (4 * q + i);
 }
 
-// p of token t, 4 Q elements a lane (zeros past E). A row whose logits are all -inf has p = 0.
+// A token's row, 4 Q elements a lane (-inf past E).
 template <int L, bool V4, int Q>
-__device__ __forceinline__ void probs(const float *__restrict__ row, int E, int sub, float (&p)[4 * Q])
+__device__ __forceinline__ void load_row(const float *__restrict__ row, int E, int sub, float (&v)[4 * Q])
 {
     const float none = -__builtin_inff();
     if constexpr (V4) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const int c = column<L, V4>(sub, q, 0);
-            const u32x4 v = ld16(row + (c < E ? c : 0));
-            p[4 * q] = c < E ? __uint_as_float(v.x) : none;
-            p[4 * q + 1] = c < E ? __uint_as_float(v.y) : none;
-            p[4 * q + 2] = c < E ? __uint_as_float(v.z) : none;
-            p[4 * q + 3] = c < E ? __uint_as_float(v.w) : none;
+            const u32x4 w = ld16(row + (c < E ? c : 0));
+            v[4 * q] = c < E ? __uint_as_float(w.x) : none;
+            v[4 * q + 1] = c < E ? __uint_as_float(w.y) : none;
+            v[4 * q + 2] = c < E ? __uint_as_float(w.z) : none;
+            v[4 * q + 3] = c < E ? __uint_as_float(w.w) : none;
         }
     } else {
 #pragma unroll
         for (int j = 0; j < 4 * Q; ++j) {
             const int c = sub + L * j;
-            const float v = row[c < E ? c : E - 1];
-            p[j] = c < E ? v : none;
+            const float w = row[c < E ? c : E - 1];
+            v[j] = c < E ? w : none;
         }
     }
+}
+
+// The row's softmax in its place. A row whose logits are all -inf has p = 0. 2^x and 1/x by their instructions, right to an ulp:
+// the exponent's rounding, u (top - x), is what counts.
+template <int L, int N>
+__device__ __forceinline__ void softmax(float (&p)[N])
+{
+    constexpr float kLog2e = 1.44269504088896340736f;
+    const float none = -__builtin_inff();
     float top = p[0];
 #pragma unroll
-    for (int j = 1; j < 4 * Q; ++j)
+    for (int j = 1; j < N; ++j)
         top = fmaxf(top, p[j]);
     top = token_max<L>(top);
     top = top == none ? 0.0f : top;  // exp(-inf - 0) = 0
     float sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4 * Q; ++j) {
-        p[j] = expf(p[j] - top);  // NaN, and +inf - +inf, stay NaN
+    for (int j = 0; j < N; ++j) {
+        p[j] = __builtin_amdgcn_exp2f((p[j] - top) * kLog2e);  // NaN, and +inf - +inf, stay NaN
         sum += p[j];
     }
     sum = token_sum<L>(sum);
-    const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float r = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
 #pragma unroll
-    for (int j = 0; j < 4 * Q; ++j)
+    for (int j = 0; j < N; ++j)
         p[j] *= r;
 }
 
 // ---------------------------------------------------------------- forward
+
+struct Share {  // of an expert in a range of tokens
+    float prob;
+    int32_t count;
+};
+
+struct Joined {  // behind the workgroups' shares: workgroups of the join that are done, and each one's share of the loss
+    int32_t done, pad;
+    double dot[kMaxJoinBlocks];
+};
 
 struct StatArgs {
     const float *logits;
@@ -121,79 +141,91 @@ struct StatArgs {
     int64_t T, tokens_per_block;
     int32_t E, K;
     float coef;
-    double *psum;     // [blocks][E]: a block's sums of p
-    int32_t *pcount;  // [blocks][E + 1]: its counts, and its tokens that count
+    Joined *joined;
+    Share *shares;  // [blocks][E + 1]: a workgroup's, and its tokens that count
     float *loss, *prob_sum;
     int32_t *counts, *tokens;
 };
 
 // Sum over the workgroup, in every thread; the same order for the same sizes.
+template <int THREADS>
 __device__ __forceinline__ double block_sum(double v, double *sh)
 {
-    v = token_sum<kWave>(v);
+    v = wave_sum(v);
     __syncthreads();
     if ((threadIdx.x & (kWave - 1)) == 0)
         sh[threadIdx.x / kWave] = v;
     __syncthreads();
     double s = 0.0;
-    for (int w = 0; w < kStatThreads / kWave; ++w)
+#pragma unroll
+    for (int w = 0; w < THREADS / kWave; ++w)
         s += sh[w];
     return s;
 }
 
-// The results from the sums of one column a thread (threads past E: zeros).
-__device__ __forceinline__ void write_results(const StatArgs &a, int c, double sum, int32_t count, int32_t n, double *sh)
+__device__ __forceinline__ void write_loss(const StatArgs &a, double dot, int32_t n)
 {
-    if (c < a.E) {
-        a.prob_sum[c] = static_cast<float>(sum);
-        a.counts[c] = count;
-    }
-    const double dot = block_sum(c < a.E ? count * sum : 0.0, sh);
-    if (threadIdx.x == 0) {
-        a.tokens[0] = n;
-        const double nd = n;
-        a.loss[0] = n == 0 ? 0.0f : static_cast<float>(static_cast<double>(a.coef) * a.E * dot / (nd * nd * a.K));
-    }
+    a.tokens[0] = n;
+    const double nd = n;
+    a.loss[0] = n == 0 ? 0.0f : static_cast<float>(static_cast<double>(a.coef) * a.E * dot / (nd * nd * a.K));
 }
 
-// Each workgroup takes a range of tokens, L lanes a token. A lane keeps the sums of its columns in double, the workgroup's
-// lanes are put together in a fixed order, and the counts are integers: the results do not depend on timing.
+// Each workgroup takes a range of tokens, L lanes a token, two tokens at a time. A lane keeps the sums of its columns, the
+// workgroup's lanes are put together in a fixed order, and the counts are integers: the results do not depend on timing.
 template <int L, bool V4, int Q>
 __global__ __launch_bounds__(kStatThreads) void balance_stat_kernel(StatArgs a)
 {
-    constexpr int kGroups = kStatThreads / L, kWaves = kStatThreads / kWave, kCols = 4 * L;
+    constexpr int kGroups = kStatThreads / L, kWaves = kStatThreads / kWave, kCols = 4 * L, N = 4 * Q;
     __shared__ double part[kWaves][kCols];
-    __shared__ int32_t hist[4 * L * Q];
+    __shared__ int32_t hist[kCols * Q];
     __shared__ int32_t ntok;
     const int sub = threadIdx.x % L, group = threadIdx.x / L, wave = threadIdx.x / kWave;
-    for (int i = threadIdx.x; i < 4 * L * Q; i += kStatThreads)
+    const int64_t t0 = blockIdx.x * a.tokens_per_block, t1 = min(a.T, t0 + a.tokens_per_block);
+    double acc[N] = {};
+    int32_t mine = 0;
+    if (t0 < t1) {
+        float few[N] = {};
+        int n = 0;
+        for (int64_t t = t0 + group; t < t1; t += 2 * kGroups) {
+            const int64_t u = t + kGroups;
+            float p[N], q[N];
+            load_row<L, V4, Q>(a.logits + t * a.E, a.E, sub, p);
+            load_row<L, V4, Q>(a.logits + min(u, t1 - 1) * a.E, a.E, sub, q);
+            const bool first = !a.mask || a.mask[t], second = u < t1 && (!a.mask || a.mask[min(u, t1 - 1)]);
+            softmax<L>(p);
+            softmax<L>(q);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                few[j] += (first ? p[j] : 0.0f) + (second ? q[j] : 0.0f);
+            mine += first + second;
+            if ((n += 2) == kFlush) {
+                n = 0;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    acc[j] += static_cast<double>(few[j]);
+                    few[j] = 0.0f;
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            acc[j] += static_cast<double>(few[j]);
+    }
+    for (int i = threadIdx.x; i < kCols * Q; i += kStatThreads)
         hist[i] = 0;
     if (threadIdx.x == 0)
         ntok = 0;
     __syncthreads();
-    const int64_t t0 = blockIdx.x * a.tokens_per_block, t1 = min(a.T, t0 + a.tokens_per_block);
-    double acc[4 * Q] = {};
-    for (int64_t t = t0 + group; t < t1; t += kGroups) {
-        if (a.mask && !a.mask[t])
-            continue;
-        float p[4 * Q];
-        probs<L, V4, Q>(a.logits + t * a.E, a.E, sub, p);
-#pragma unroll
-        for (int j = 0; j < 4 * Q; ++j)
-            acc[j] += static_cast<double>(p[j]);
-        if (sub == 0)
-            atomicAdd(&ntok, 1);
-    }
+    if (sub == 0)
+        atomicAdd(&ntok, mine);
     for (int64_t i = t0 * a.K + threadIdx.x; i < t1 * a.K; i += kStatThreads) {
         const int32_t e = a.topk_idx[i];
         if (e >= 0 && e < a.E && (!a.mask || a.mask[i / a.K]))
             atomicAdd(&hist[e], 1);
     }
-    const int chunk_of = threadIdx.x;  // the thread that ends up with column threadIdx.x
-    double total = 0.0;
+    double share = 0.0;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        __syncthreads();
+    for (int q = 0; q < Q; ++q) {  // kCols columns at a time, whose threads are as many or fewer than the workgroup's
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             double v = acc[4 * q + i];
@@ -205,60 +237,92 @@ __global__ __launch_bounds__(kStatThreads) void balance_stat_kernel(StatArgs a)
                 part[wave][column<L, V4>(sub, 0, i)] = v;
         }
         __syncthreads();
-        if (chunk_of >= q * kCols && chunk_of < (q + 1) * kCols) {
+        const int c = q * kCols + threadIdx.x;
+        if (threadIdx.x < kCols && c < a.E) {
+            double total = 0.0;
+#pragma unroll
             for (int w = 0; w < kWaves; ++w)
-                total += part[w][chunk_of - q * kCols];
+                total += part[w][threadIdx.x];
+            if (gridDim.x == 1) {
+                a.prob_sum[c] = static_cast<float>(total);
+                a.counts[c] = hist[c];
+                share += hist[c] * total;
+            } else {
+                a.shares[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + c] = Share{static_cast<float>(total), hist[c]};
+            }
         }
+        __syncthreads();
     }
-    const int32_t count = threadIdx.x < 4 * L * Q ? hist[threadIdx.x] : 0;
-    const int c = threadIdx.x;
     if (gridDim.x == 1) {
-        write_results(a, c, total, count, ntok, &part[0][0]);
-        return;
+        const double dot = block_sum<kStatThreads>(share, &part[0][0]);
+        if (threadIdx.x == 0)
+            write_loss(a, dot, ntok);
+    } else if (threadIdx.x == 0) {
+        a.shares[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + a.E] = Share{0.0f, ntok};
+        if (blockIdx.x == 0)
+            a.joined->done = 0;  // for the join, the next launch
     }
-    if (c < a.E) {
-        a.psum[static_cast<int64_t>(blockIdx.x) * a.E + c] = total;
-        a.pcount[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + c] = count;
-    }
-    if (threadIdx.x == 0)
-        a.pcount[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + a.E] = ntok;
 }
 
-// The workgroups' sums, added in their order, and the results.
-__global__ __launch_bounds__(kStatThreads) void balance_join_kernel(StatArgs a, int blocks)
+// The workgroups' sums, added in their order, kJoinCols columns a workgroup; the last one to be done has the loss. (One workgroup
+// for all columns has its CU's bandwidth alone: 10 us of 20 at T16384 E256.)
+__global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(StatArgs a, int blocks)
 {
-    __shared__ double sh[kStatThreads];
-    __shared__ int32_t cnt[kStatThreads];
-    __shared__ int32_t ntok;
-    int width = kWave;  // threads a row of sums; the rows are dealt to kStatThreads / width of them
-    while (width < a.E)
-        width *= 2;
-    const int c = threadIdx.x % width, part = threadIdx.x / width, parts = kStatThreads / width;
+    constexpr int kParts = kJoinThreads / kJoinCols, kAhead = 16;  // rows whose loads are under way together
+    __shared__ double sh[kJoinThreads];
+    __shared__ int32_t cnt[kJoinThreads];
+    __shared__ int32_t ntok, last;
+    const int col = threadIdx.x % kJoinCols, part = threadIdx.x / kJoinCols, c = blockIdx.x * kJoinCols + col;
+    static_assert(kMaxStatBlocks <= kJoinThreads, "");
+    const int32_t here =
+        static_cast<int>(threadIdx.x) < blocks ? a.shares[static_cast<int64_t>(threadIdx.x) * (a.E + 1) + a.E].count : 0;
     if (threadIdx.x == 0)
         ntok = 0;
     double sum = 0.0;
     int32_t count = 0;
     if (c < a.E) {
-#pragma unroll 8
-        for (int b = part; b < blocks; b += parts) {
-            sum += a.psum[static_cast<int64_t>(b) * a.E + c];
-            count += a.pcount[static_cast<int64_t>(b) * (a.E + 1) + c];
+        for (int b = part; b < blocks; b += kAhead * kParts) {
+            Share v[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                v[i] = a.shares[static_cast<int64_t>(min(b + i * kParts, blocks - 1)) * (a.E + 1) + c];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const bool there = b + i * kParts < blocks;
+                sum += there ? static_cast<double>(v[i].prob) : 0.0;
+                count += there ? v[i].count : 0;
+            }
         }
     }
     sh[threadIdx.x] = sum;
     cnt[threadIdx.x] = count;
     __syncthreads();
-    if (threadIdx.x < blocks)
-        atomicAdd(&ntok, a.pcount[static_cast<int64_t>(threadIdx.x) * (a.E + 1) + a.E]);
-    sum = 0.0;
-    count = 0;
-    if (threadIdx.x < width)
-        for (int p = 0; p < parts; ++p) {
-            sum += sh[p * width + threadIdx.x];
-            count += cnt[p * width + threadIdx.x];
+    if (here)
+        atomicAdd(&ntok, here);
+    double share = 0.0;
+    if (threadIdx.x < kJoinCols && c < a.E) {
+#pragma unroll
+        for (int p = 1; p < kParts; ++p) {
+            sum += sh[p * kJoinCols + col];
+            count += cnt[p * kJoinCols + col];
         }
+        a.prob_sum[c] = static_cast<float>(sum);
+        a.counts[c] = count;
+        share = count * sum;
+    }
     __syncthreads();
-    write_results(a, threadIdx.x, sum, count, ntok, sh);
+    const double dot = block_sum<kJoinThreads>(share, sh);
+    if (threadIdx.x == 0) {
+        __hip_atomic_store(&a.joined->dot[blockIdx.x], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        last = __hip_atomic_fetch_add(&a.joined->done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == static_cast<int>(gridDim.x) - 1;
+    }
+    __syncthreads();
+    if (last && threadIdx.x == 0) {
+        double total = 0.0;
+        for (unsigned b = 0; b < gridDim.x; ++b)
+            total += __hip_atomic_load(&a.joined->dot[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        write_loss(a, total, ntok);
+    }
 }
 
 // ---------------------------------------------------------------- backward
@@ -274,40 +338,67 @@ struct BackArgs {
     float coef;
 };
 
+// A gradient row out, the one that is added read in its place.
+template <int L, bool V4, int Q>
+__device__ __forceinline__ void store_row(const float (&d)[4 * Q], const float *__restrict__ add, float *__restrict__ out, int E, int sub)
+{
+    if constexpr (V4) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int c = column<L, V4>(sub, q, 0);
+            if (c >= E)
+                continue;
+            u32x4 b{0, 0, 0, 0};
+            if (add)
+                b = ld16(add + c);
+            const float v[4] = {d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+            const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] = __float_as_uint(add ? v[i] + __uint_as_float(w[i]) : v[i]);
+            st16(out + c, u32x4{o[0], o[1], o[2], o[3]});
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4 * Q; ++j) {
+            const int c = sub + L * j;
+            if (c < E)
+                out[c] = add ? d[j] + add[c] : d[j];
+        }
+    }
+}
+
+// L lanes a token, as above; f, the same for all tokens, stays in registers.
 template <int L, bool V4, int Q>
 __global__ __launch_bounds__(kBackThreads) void balance_backward_kernel(BackArgs a)
 {
-    constexpr int kGroups = kBackThreads / L;
+    constexpr int kGroups = kBackThreads / L, N = 4 * Q;
     const int sub = threadIdx.x % L;
     const int32_t n = a.tokens[0];
-    const double share = n > 0 ? 1.0 / (static_cast<double>(n) * a.K) : 0.0;
+    const float share = n > 0 ? static_cast<float>(1.0 / (static_cast<double>(n) * a.K)) : 0.0f;
     const float scale = n > 0 ? static_cast<float>(static_cast<double>(a.d_loss ? a.d_loss[0] : 1.0f) * a.coef * a.E / n) : 0.0f;
-    double f[4 * Q];
+    float f[N];
 #pragma unroll
-    for (int j = 0; j < 4 * Q; ++j) {
+    for (int j = 0; j < N; ++j) {
         const int c = column<L, V4>(sub, j / 4, j % 4);
-        f[j] = c < a.E ? a.counts[c] * share : 0.0;
+        f[j] = c < a.E ? static_cast<float>(a.counts[c]) * share : 0.0f;
     }
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / L; t < a.T;
          t += static_cast<int64_t>(gridDim.x) * kGroups) {
-        float d[4 * Q] = {};
-        if (n > 0 && (!a.mask || a.mask[t])) {
-            probs<L, V4, Q>(a.logits + t * a.E, a.E, sub, d);
-            double s = 0.0;
+        float d[N];
+        load_row<L, V4, Q>(a.logits + t * a.E, a.E, sub, d);
+        softmax<L>(d);
+        float s = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4 * Q; ++j)
-                s = fma(f[j], static_cast<double>(d[j]), s);
-            s = token_sum<L>(s);
+        for (int j = 0; j < N; ++j)
+            s = fmaf(f[j], d[j], s);
+        s = token_sum<L>(s);
+        const bool counts = n > 0 && (!a.mask || a.mask[t]);
 #pragma unroll
-            for (int j = 0; j < 4 * Q; ++j)
-                d[j] = scale * d[j] * static_cast<float>(f[j] - s);
-        }
-#pragma unroll
-        for (int j = 0; j < 4 * Q; ++j) {
-            const int c = column<L, V4>(sub, j / 4, j % 4);
-            if (c < a.E)
-                a.out[t * a.E + c] = a.add ? d[j] + a.add[t * a.E + c] : d[j];
-        }
+        for (int j = 0; j < N; ++j)
+            d[j] = counts ? scale * d[j] * (f[j] - s) : 0.0f;
+        store_row<L, V4, Q>(d, a.add ? a.add + t * a.E : nullptr, a.out + t * a.E, a.E, sub);
     }
 }
 
@@ -315,16 +406,16 @@ __global__ __launch_bounds__(kBackThreads) void balance_backward_kernel(BackArgs
 
 int stat_lanes(int32_t E) { return E <= 256 ? 16 : kWave; }
 
-// Workgroups of the forward: each has one pass over its tokens at least.
+// Workgroups of the forward: each has one pass over two tokens a group of lanes at least.
 int stat_blocks(int64_t T, int32_t E)
 {
-    return static_cast<int>(std::min<int64_t>(kMaxStatBlocks, std::max<int64_t>(1, ceil_div(T, kStatThreads / stat_lanes(E)))));
+    return static_cast<int>(std::min<int64_t>(kMaxStatBlocks, std::max<int64_t>(1, ceil_div(T, 2 * (kStatThreads / stat_lanes(E))))));
 }
 
 size_t stat_bytes(int64_t T, int32_t E)
 {
     const size_t blocks = static_cast<size_t>(stat_blocks(T, E));
-    return blocks == 1 ? 0 : blocks * (sizeof(double) * E + sizeof(int32_t) * (E + 1));
+    return blocks == 1 ? 0 : sizeof(Joined) + blocks * sizeof(Share) * (E + 1);
 }
 
 moe_status check_sizes(int64_t T, int32_t E, int32_t K, float coef)
@@ -393,16 +484,16 @@ extern "C" moe_status moe_balance_loss(const float *logits, const int32_t *topk_
     if (workspace_bytes < need || (need > 0 && (!workspace || !aligned16(workspace))))
         return MOE_ERR_INVALID;
     const int blocks = stat_blocks(T, E);
-    double *psum = static_cast<double *>(workspace);
-    const StatArgs a{logits, topk_idx, token_mask, T, ceil_div(T, blocks), E, K, coef, psum,
-                     need > 0 ? reinterpret_cast<int32_t *>(psum + static_cast<size_t>(blocks) * E) : nullptr,
-                     loss, prob_sum, counts, tokens};
+    Joined *joined = static_cast<Joined *>(workspace);
+    const StatArgs a{logits, topk_idx, token_mask, T, ceil_div(T, blocks), E, K, coef, joined,
+                     need > 0 ? reinterpret_cast<Share *>(joined + 1) : nullptr, loss, prob_sum, counts, tokens};
     if (E % 4 == 0 && aligned16(logits))
         MOE_BALANCE_DISPATCH(launch_stat, true, E, a, blocks, stream);
     else
         MOE_BALANCE_DISPATCH(launch_stat, false, E, a, blocks, stream);
     if (blocks > 1)
-        hipLaunchKernelGGL(balance_join_kernel, dim3(1), dim3(kStatThreads), 0, stream, a, blocks);
+        hipLaunchKernelGGL(balance_join_kernel, dim3(static_cast<unsigned>(ceil_div(E, kJoinCols))), dim3(kJoinThreads), 0, stream, a,
+                           blocks);
     return launch_status();
 }
 
