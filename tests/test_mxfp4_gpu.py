@@ -290,6 +290,15 @@ def test_bad_segments_stay_inside(m):
         m.grouped_product_mxfp4(*x, *w, torch.tensor(ends, dtype=I32, device=DEV), out=out)
         torch.cuda.synchronize()
         assert bool((guard[:32] == 7).all()) and bool((guard[32 + R:] == 7).all()), ends
+    # as many overlapping experts as there may be, whose tiles together are more than 32 bits count
+    E, R2, N2 = 1024, 8192, 1 << 16
+    xq, wq = rows4(60, R2, 32), (torch.zeros(E, N2, 16, dtype=U8, device=DEV), torch.full((E, N2, 1), 127, dtype=U8, device=DEV))
+    guard = torch.full((R2 + 64, N2), 7.0, dtype=BF16, device=DEV)
+    ends = torch.tensor([0, R2], dtype=I32, device=DEV).repeat(E // 2)
+    m.grouped_product_mxfp4(*xq, *wq, ends, out=guard[32:32 + R2])
+    torch.cuda.synchronize()
+    assert bool((guard[:32] == 7).all()) and bool((guard[32 + R2:] == 7).all())
+    del wq, guard
     # ends past R, cut
     check(m, x, w, [(0, 0), (0, 30), (30, 30), (30, R)], torch.tensor([-5, 30, 30, 1 << 30], dtype=I32, device=DEV))
     # counts longer than their segments, or negative

@@ -220,7 +220,7 @@ __global__ __launch_bounds__(kStatThreads) void balance_stat_kernel(StatArgs a)
         atomicAdd(&ntok, mine);
     for (int64_t i = t0 * a.K + threadIdx.x; i < t1 * a.K; i += kStatThreads) {
         const int32_t e = a.topk_idx[i];
-        if (e >= 0 && e < a.E && (!a.mask || a.mask[i / a.K]))
+        if (e >= 0 && e < a.E && (!a.mask || a.mask[static_cast<uint32_t>(i) / static_cast<uint32_t>(a.K)]))
             atomicAdd(&hist[e], 1);
     }
     double share = 0.0;

@@ -57,9 +57,11 @@ struct Tile {
 
 // The i-th of the (rows, columns) tiles of BM rows: experts in order, of an expert kGroup tiles of the same columns beside each
 // other. (Those that run at the same time on an XCD then share both their weights and their rows in its L2: one expert of 8192
-// cubed 334 -> 298 us against all the rows' tiles first.)
+// cubed 334 -> 298 us against all the rows' tiles first.) Every thread of a workgroup of kPlanThreads calls it and gets the same.
+// Sums of tiles stop at 2^32 - 1, which only segments that overlap reach: no two experts then claim the i-th, i < 2^31.
 constexpr uint32_t kGroup = 8;
-// Every thread of a workgroup of kPlanThreads calls it and gets the same.
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
+
 template <int BM>
 __device__ __forceinline__ Tile find_tile(const ProductArgs &a, uint32_t i)
 {
@@ -77,30 +79,33 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs &a, uint32_t i)
             start[j] = static_cast<uint32_t>(s);
             len[j] = static_cast<uint32_t>(l);
             tiles[j] = (len[j] + BM - 1) / BM * a.col_tiles;
-            mine += tiles[j];
+            mine = add_sat(mine, tiles[j]);
         }
     }
-    // (the launch has made sure that their number fits)
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     uint32_t upto = mine;
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) {
         const uint32_t o = __shfl_up(upto, d);
-        upto += lane >= d ? o : 0;
+        upto = add_sat(upto, lane >= d ? o : 0);
     }
     if (lane == kWave - 1)
         wave_tiles[wave] = upto;
     if (threadIdx.x == 0)
         found = Tile{-1, 0, 0, 0};
+    uint32_t before = __shfl_up(upto, 1);
+    before = lane == 0 ? 0 : before;
     __syncthreads();
-    uint32_t k = i - (upto - mine);
 #pragma unroll
     for (int v = 0; v < kPlanThreads / kWave - 1; ++v)
-        k -= v < wave ? wave_tiles[v] : 0;
-    if (k < mine) {  // (before this thread's tiles k is negative, as a large number)
+        before = add_sat(before, v < wave ? wave_tiles[v] : 0);
+    if (i >= before && i - before < mine) {
+        uint32_t k = i - before;
+        bool left = true;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            if (k < tiles[j]) {
+            if (left && k < tiles[j]) {
+                left = false;
                 const uint32_t n = (len[j] + BM - 1) / BM, g = k / (kGroup * a.col_tiles), in = k % (kGroup * a.col_tiles);
                 const uint32_t high = min(kGroup, n - kGroup * g), m = kGroup * g + in % high;
                 found = Tile{e0 + j, static_cast<int32_t>(min(len[j] - m * BM, static_cast<uint32_t>(BM))),
