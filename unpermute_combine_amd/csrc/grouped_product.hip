@@ -58,6 +58,9 @@ struct Tile {
 // The i-th of the (rows, columns) tiles of BM rows: experts in order, of an expert kGroup tiles of the same columns beside each
 // other. (Those that run at the same time on an XCD then share both their weights and their rows in its L2: one expert of 8192
 // cubed 334 -> 298 us against all the rows' tiles first.) Every thread of a workgroup of kPlanThreads calls it and gets the same.
+// Of up to four tiles of 256 the rows are dealt out evenly, by 32, where rows are long: two of 150 take less than one of 256 and
+// one of 44 (R131072 E256 H7168 N1024 gated 1363 -> 1315 us; where they are short each tile's begin and end count more: H1024
+// N7168 1077 -> 1134).
 // Sums of tiles stop at 2^32 - 1, which only segments that overlap reach: no two experts then claim the i-th, i < 2^31.
 constexpr uint32_t kGroup = 8;
 __device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
@@ -69,16 +72,18 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs &a, uint32_t i)
     __shared__ Tile found;
     constexpr int kPer = MOE_MAX_EXPERTS / kPlanThreads;
     const int per = static_cast<int>((a.E + kPlanThreads - 1) / kPlanThreads), e0 = threadIdx.x * per;
-    uint32_t tiles[kPer], start[kPer], len[kPer], mine = 0;
+    uint32_t tiles[kPer], start[kPer], len[kPer], height[kPer], mine = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        tiles[j] = start[j] = len[j] = 0;
+        tiles[j] = start[j] = len[j] = height[j] = 0;
         if (j < per && e0 + j < a.E) {
             int64_t s, l;
             segment(a, e0 + j, s, l);
             start[j] = static_cast<uint32_t>(s);
             len[j] = static_cast<uint32_t>(l);
-            tiles[j] = (len[j] + BM - 1) / BM * a.col_tiles;
+            const uint32_t n = (len[j] + BM - 1) / BM;
+            height[j] = BM == 256 && a.H >= 2048 && n > 1 && n <= 4 ? ((len[j] + n - 1) / n + 31) / 32 * 32 : BM;
+            tiles[j] = n * a.col_tiles;
             mine = add_sat(mine, tiles[j]);
         }
     }
@@ -108,8 +113,8 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs &a, uint32_t i)
                 left = false;
                 const uint32_t n = (len[j] + BM - 1) / BM, g = k / (kGroup * a.col_tiles), in = k % (kGroup * a.col_tiles);
                 const uint32_t high = min(kGroup, n - kGroup * g), m = kGroup * g + in % high;
-                found = Tile{e0 + j, static_cast<int32_t>(min(len[j] - m * BM, static_cast<uint32_t>(BM))),
-                             static_cast<int64_t>(start[j]) + m * BM, static_cast<int32_t>(in / high)};
+                found = Tile{e0 + j, static_cast<int32_t>(min(len[j] - m * height[j], height[j])),
+                             static_cast<int64_t>(start[j]) + m * height[j], static_cast<int32_t>(in / high)};
             }
             k -= tiles[j];
         }
@@ -599,7 +604,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     };
 
     // stages 0 to 2, x's of stage 3, the scales of group 0 and the weights' of group 1
-    const int x_loads = big ? 4 : tile.rows > 64 ? 2 : 1;
+    const int x_loads = big ? (tile.rows > 192 ? 4 : 3) : tile.rows > 64 ? 2 : 1;
     u32x4 xsc, wsc;
     if (blocks >= 16) {
         load_sc(false, 0);
@@ -626,11 +631,14 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     put_sc(true, 0, wsc);
     const auto i1 = std::integral_constant<int, 1>{};
     const auto i2 = std::integral_constant<int, 2>{};
+    const auto i3 = std::integral_constant<int, 3>{};
     const auto i4 = std::integral_constant<int, 4>{};
     if constexpr (!kWide)
         tile.rows > 64 ? products(i2, i2, i2) : products(i1, i2, i2);
-    else if (big)
+    else if (tile.rows > 192)
         products(i4, i4, i2);
+    else if (big)
+        products(i3, i4, i2);
     else if (tile.rows > 64)
         products(i4, i2, i1);
     else if (tile.rows > 32)
@@ -644,7 +652,9 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     // wavefront's own part of it, and out in vectors of a row.
     constexpr int kMost = (kWide ? 128 : 64) / (GATED ? 2 : 1), kVec = 16 / sizeof(O), kPitch = kMost + kVec, kLanes = kMost / kVec;
     static_assert(4 * 32 * kPitch * sizeof(O) <= sizeof(sh.codes), "");
-    const int row0 = !kWide ? wave % 2 * (tile.rows > 64 ? 64 : 32) : big ? wave % 2 * 128 : 0;
+    // a wavefront's rows and columns
+    const int height = !kWide ? (tile.rows > 64 ? 64 : 32) : big && tile.rows <= 192 ? 96 : 128;
+    const int row0 = !kWide || big ? wave % 2 * height : 0;
     const int width = GATED ? wave_half : wave_cols;
     const int64_t c0 = n0 + (!kWide || big ? wave / 2 : wave) * width;
     const int cols = static_cast<int>(min(static_cast<int64_t>(width), a.N - c0));
@@ -652,7 +662,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     const bool vectors = a.N % kVec == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
 #pragma unroll
     for (int m = 0; m < (kWide ? 4 : 2); ++m) {
-        const int rows = min(!kWide && tile.rows <= 64 && m > 0 ? 0 : 32, tile.rows - row0 - 32 * m);
+        const int rows = min(32, min(height, tile.rows - row0) - 32 * m);
         if (rows <= 0)
             break;
 #pragma unroll
