@@ -65,11 +65,16 @@ struct Tile {
 constexpr uint32_t kGroup = 8;
 __device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
 
+struct Search {
+    Tile found;
+    uint32_t wave_tiles[kPlanThreads / kWave];
+};
+
 template <int BM>
-__device__ __forceinline__ Tile find_tile(const ProductArgs &a, uint32_t i)
+__device__ __forceinline__ Tile find_tile(const ProductArgs &a, uint32_t i, Search &sh)
 {
-    __shared__ uint32_t wave_tiles[kPlanThreads / kWave];
-    __shared__ Tile found;
+    uint32_t *const wave_tiles = sh.wave_tiles;
+    Tile &found = sh.found;
     constexpr int kPer = MOE_MAX_EXPERTS / kPlanThreads;
     const int per = static_cast<int>((a.E + kPlanThreads - 1) / kPlanThreads), e0 = threadIdx.x * per;
     uint32_t tiles[kPer], start[kPer], len[kPer], height[kPer], mine = 0;
@@ -199,7 +204,8 @@ __global__ __launch_bounds__(kPlanThreads, 3) void grouped_rows_kernel(ProductAr
 {
     constexpr int kWaves = kPlanThreads / kWave, kCols = GATED ? 16 : 32;  // columns of a wavefront
     __shared__ f32x4 sums[SPLIT > 1 ? kWaves : 1][2][kWave];
-    const Tile tile = find_tile<16>(a, blockIdx.x);
+    __shared__ Search search;
+    const Tile tile = find_tile<16>(a, blockIdx.x, search);
     if (tile.e < 0)
         return;
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / kWave));
@@ -362,15 +368,16 @@ constexpr int kStageBytes = 64;                  // of each row a stage: 128 ele
 constexpr int kStageBlocks = kStageBytes / 16;
 constexpr int kStages = 4;                       // of which LDS has room
 constexpr int kScaleStages = 4;                  // stages whose scales come at a time: 16 bytes of a row
+constexpr int kLineStages = 8;                   // or 32 bytes, where rows of scales begin at multiples of 16 bytes
 
 // The 16-byte chunk c of row r lies in slot c ^ swizzle(r) of its 64 bytes: 8 and 16 consecutive rows' same chunk fall into
 // different banks.
 __device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
 
-template <int ROWS, int COLS>
+template <int ROWS, int COLS, bool LINES>
 struct Buffers {
     uint8_t codes[kStages][(ROWS + COLS) * kStageBytes];
-    uint32_t scales[2][ROWS + COLS][4];
+    uint32_t scales[2][ROWS + COLS][LINES ? kLineStages : kScaleStages];
 };
 
 // 16 bytes a lane into LDS, lane l's to address `to` + 16 l (one for the wavefront). Past the resource's end: zeros.
@@ -406,13 +413,13 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t nb)
 // other each way; of fewer all of them by 64 weight rows. Tiles of 128 by 128, a wavefront with 64 by 64 or, of up to 64 rows, 32
 // by 64, two to a CU, are for products of which the wide ones would leave CUs without one. Gated, a wavefront's first half are
 // gates, its second the ups of the same columns.
-template <typename O, bool GATED, int ROWS, int COLS>
+template <typename O, bool GATED, int ROWS, int COLS, bool LINES>
 __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs a)
 {
     constexpr bool kWide = COLS == 256;
     static_assert(ROWS == COLS && (kWide || COLS == 128), "");
-    __shared__ __attribute__((aligned(128))) Buffers<ROWS, COLS> sh;
-    const Tile tile = find_tile<ROWS>(a, xcd_run(blockIdx.x, gridDim.x));
+    __shared__ __attribute__((aligned(128))) Buffers<ROWS, COLS, LINES> sh;  // wide, with lines: all of a CU's LDS
+    const Tile tile = find_tile<ROWS>(a, xcd_run(blockIdx.x, gridDim.x), *reinterpret_cast<Search *>(sh.scales[1]));
     if (tile.e < 0)
         return;
     constexpr int kOutCols = GATED ? COLS / 2 : COLS, kXMost = ROWS / 64, kWLoads = COLS / 64;  // 16-byte loads a thread and stage
@@ -477,8 +484,8 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
         const uint32_t bytes = u ? up_bytes : gate_bytes;
         to_lds(make_rsrc(u ? up : gate, s < stages ? bytes : 0), wo[j] + s * kStageBytes, slot(s) + (ROWS + 64 * j) * kStageBytes);
     };
-    // Scales come for kScaleStages stages (a group) at a time, x's and the weights' in turns. A row's 16 bytes
-    // are put down as what each half of a wavefront needs of them: blocks 0, 1 of each stage's four, then blocks 2, 3.
+    // Scales come for kScaleStages stages (a group) at a time, x's and the weights' in turns. A row's 16 bytes are put down as what
+    // each half of a wavefront needs of them: blocks 0, 1 of each stage's four, then blocks 2, 3.
     const uint8_t *const xsl = blocks >= 16 ? xsp : a.w;  // (16 bytes to read, where the rows are shorter)
     const int64_t to_wsl = blocks >= 16 ? wsp - xsp : 0;
     u32x4 sc;
@@ -491,6 +498,38 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
                    __builtin_amdgcn_perm(v.y, v.x, 0x07060302u) & k, __builtin_amdgcn_perm(v.w, v.z, 0x07060302u) & k});
     };
     auto store_sc = [&](bool w, int g) { put_sc(w, g, shifted(sc, min(16 * g - scale_at(g), 15))); };
+    // With lines they come for kLineStages stages, straight into LDS as they lie, two lanes a row: half the requests of the way above,
+    // and nothing to move (R131072 E256 H7168 N1024 gated 1342 -> 1218 us, R12288 E128 251 -> 236; short of rows, H4096 E64, 32 rows an
+    // expert, 117 -> 123). The loads of a group are four quarters, each 32 rows a wavefront, of which lane l has row l / 2: rows
+    // 32 (4 q + wavefront) on of x's and the weights'.
+    uint32_t so[4];
+    uint32_t scales_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint32_t *)&sh.scales[0][0][0]));
+    const bool line_up = is_up(32 * wave);
+    const uint8_t *const x_lines = a.xs + x_at * blocks, *const w_lines = a.ws + (w_at + (line_up ? a.N : 0)) * blocks;
+    const uint32_t x_line_bytes = capped((a.x_rows - x_at) * blocks);
+    const uint32_t w_line_bytes = capped((a.E * wrows - w_at - (line_up ? a.N : 0)) * blocks);
+    if constexpr (LINES) {
+        asm volatile("" : "+s"(scales_at));  // (as for codes)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int b = 32 * (4 * q + wave) + lane / 2;
+            const int64_t row = q < 2 ? x_row(b) - x_at : w_row(b - ROWS);
+            so[q] = row >= 0 ? static_cast<uint32_t>(row * blocks) + lane % 2 * 16 : kNowhere;
+        }
+    }
+    auto load_line = [&](int g, int q) {
+        uint32_t from = 0;  // so[q], without a branch
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            from |= so[i] & (q == i ? 0xffffffffu : 0);
+        to_lds(make_rsrc(q < 2 ? x_lines : w_lines, q < 2 ? x_line_bytes : w_line_bytes),
+               from == kNowhere ? kNowhere : from + g * 4 * kLineStages,
+               scales_at + (g & 1) * static_cast<uint32_t>(sizeof(sh.scales[0])) + (4 * q + wave) * 32 * 4 * kLineStages);
+    };
+    const auto i1 = std::integral_constant<int, 1>{};
+    const auto i2 = std::integral_constant<int, 2>{};
+    const auto i3 = std::integral_constant<int, 3>{};
+    const auto i4 = std::integral_constant<int, 4>{};
 
     const int half = lane >> 5, r32 = lane & 31, swz = swizzle(r32);
     f32x16 acc[4][4];
@@ -520,14 +559,24 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
         };
         // Scales of stages s and s + 1, s even: steps 0 to 3 have bytes 0 to 3.
         int xs[MS], ws[NS], next_xs[MS], next_ws[NS];
+        auto read_scale = [&](int s, int row) -> int {
+            if constexpr (LINES) {
+                const uint32_t at = scales_at + (s / kLineStages & 1) * static_cast<uint32_t>(sizeof(sh.scales[0])) +
+                                    row * 4 * kLineStages + s % kLineStages * 4;
+                const uint64_t v = *reinterpret_cast<const __attribute__((address_space(3))) uint64_t *>(at);
+                return static_cast<int>(__builtin_amdgcn_perm(static_cast<uint32_t>(v >> 32), static_cast<uint32_t>(v),
+                                                              half ? 0x07060302u : 0x05040100u));
+            } else {
+                return static_cast<int>(sh.scales[s / kScaleStages & 1][row][2 * half + (s / 2) % 2]);
+            }
+        };
         auto read_scales = [&](int s, int (&x)[MS], int (&w)[NS]) {
-            const int word = 2 * half + (s / 2) % 2, g = s / kScaleStages & 1;
 #pragma unroll
             for (int m = 0; m < MS; ++m)
-                x[m] = static_cast<int>(sh.scales[g][x0 + 32 * m][word]);
+                x[m] = read_scale(s, x0 + 32 * m);
 #pragma unroll
             for (int n = 0; n < NS; ++n)
-                w[n] = static_cast<int>(sh.scales[g][w0 + 32 * n][word]);
+                w[n] = read_scale(s, w0 + 32 * n);
         };
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -568,7 +617,10 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
             MOE_PRODUCTS(2 * J, f[0]);
             MOE_INTERLEAVE(MS + NS, kWLoads);
             meet(std::integral_constant<int, 2 * kLoads>{});
-            if constexpr (J == 0) {
+            if constexpr (J == 0 && LINES) {
+                const int t = s / 2 + 1;  // the last quarter of a group comes a pair of stages before its first scales are read
+                load_line(t / 4 + 1, t % 4);
+            } else if constexpr (J == 0) {
                 const bool odd = s & 2;
                 asm volatile("" : "+v"(sc.x), "+v"(sc.y), "+v"(sc.z), "+v"(sc.w));  // used from here on: before, it would be waited for
                 store_sc(!odd, s / kScaleStages + 1);
@@ -603,19 +655,26 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
 #undef MOE_PRODUCTS
     };
 
-    // stages 0 to 2, x's of stage 3, the scales of group 0 and the weights' of group 1
+    // stages 0 to 2, x's of stage 3, the scales of group 0 and the first of group 1
     const int x_loads = big ? (tile.rows > 192 ? 4 : 3) : tile.rows > 64 ? 2 : 1;
     u32x4 xsc, wsc;
-    if (blocks >= 16) {
-        load_sc(false, 0);
-        xsc = sc;
-        load_sc(true, 0);
-        wsc = sc;
+    if constexpr (LINES) {
+        __syncthreads();  // the search is done with its place
+#pragma unroll
+        for (int t = 0; t < 5; ++t)
+            load_line(t / 4, t % 4);
     } else {
-        xsc = short_scales(xsp, blocks);
-        wsc = short_scales(wsp, blocks);
+        if (blocks >= 16) {
+            load_sc(false, 0);
+            xsc = sc;
+            load_sc(true, 0);
+            wsc = sc;
+        } else {
+            xsc = short_scales(xsp, blocks);
+            wsc = short_scales(wsp, blocks);
+        }
+        load_sc(true, 1);
     }
-    load_sc(true, 1);
 #pragma unroll
     for (int s = 0; s < kStages; ++s) {
 #pragma unroll
@@ -627,12 +686,10 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
             for (int j = 0; j < kWLoads; ++j)
                 load_w(s, j);
     }
-    put_sc(false, 0, xsc);
-    put_sc(true, 0, wsc);
-    const auto i1 = std::integral_constant<int, 1>{};
-    const auto i2 = std::integral_constant<int, 2>{};
-    const auto i3 = std::integral_constant<int, 3>{};
-    const auto i4 = std::integral_constant<int, 4>{};
+    if constexpr (!LINES) {
+        put_sc(false, 0, xsc);
+        put_sc(true, 0, wsc);
+    }
     if constexpr (!kWide)
         tile.rows > 64 ? products(i2, i2, i2) : products(i1, i2, i2);
     else if (tile.rows > 192)
@@ -716,9 +773,11 @@ moe_status launch_product(ProductArgs a, hipStream_t stream)
             return MOE_ERR_UNSUPPORTED;
         const dim3 grid(static_cast<unsigned>(tiles));
         if (size == 128)
-            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 128, 128>), grid, dim3(kPlanThreads), 0, stream, a);
+            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 128, 128, false>), grid, dim3(kPlanThreads), 0, stream, a);
+        else if (a.H % 512 == 0 && aligned16(a.xs) && aligned16(a.ws))
+            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 256, 256, true>), grid, dim3(kPlanThreads), 0, stream, a);
         else
-            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 256, 256>), grid, dim3(kPlanThreads), 0, stream, a);
+            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 256, 256, false>), grid, dim3(kPlanThreads), 0, stream, a);
         return launch_status();
     }
     const int64_t tiles = max_tiles(a.R, a.E, 16), units = tiles * ceil_div(a.N, GATED ? 16 : 32);
