@@ -511,7 +511,8 @@ moe_status moe_few_token_experts(const void *x, moe_dtype dt, int64_t T, int64_t
  * power of two, and an element is one of +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} times it:
  *   amax = max |x|, scale = 2^(floor(log2 amax) - 2), but at least 2^-127; 1 when amax is 0
  *   code = the nearest of those values to x / scale (a tie goes to the even code, what is above 6 to 6; the sign is kept)
- *   x [T, H] (x_dt float32 or bf16); H a multiple of 32 (else MOE_ERR_INVALID), at most 2^26.
+ *   x [T, H] (x_dt float32 or bf16); H a multiple of 32 (else MOE_ERR_INVALID), at most 2^26;
+ *   T * H / 8 <= 2^32 - 2^8 for float32, T * H / 32 for bf16 (else MOE_ERR_UNSUPPORTED).
  *   q [T, H/2] bytes: two codes each, the even element's in the low half. scales [T, H/32] bytes: the exponent + 127; 255
  *   (which stands for NaN) for a block that holds a NaN or an infinity, whose codes are 0.
  * Both are byte rows that the permutes move as MOE_FP8_E4M3 rows of H/2 and H/32 elements. */
@@ -533,7 +534,8 @@ moe_status moe_quantize_mxfp4(const void *x, moe_dtype x_dt, int64_t T, int64_t 
  *   out [R, N] (float32 or bf16), which overlaps no input. Rows in no segment are left untouched. Segments are cut to [0, R);
  *   ones that overlap give unspecified rows.
  * Rows are independent: a NaN scale makes NaN of its own row or column alone. H a multiple of 32 (else MOE_ERR_INVALID);
- * H, N <= 2^20, x and w 16-byte aligned (else MOE_ERR_UNSUPPORTED). */
+ * H, N <= 2^20, x and w 16-byte aligned (else MOE_ERR_UNSUPPORTED, as for a launch that would pass 2^32 threads: few rows of each of
+ * very many experts, short, with some 2^20 columns). */
 moe_status moe_grouped_product_mxfp4(const uint8_t *x, const uint8_t *x_scales, int64_t x_rows, const int32_t *src_row,
                                      int64_t R, int64_t H, const uint8_t *w, const uint8_t *w_scales, int32_t E, int64_t N,
                                      int32_t gated, const int32_t *group_list, const int32_t *counts, int32_t capacity,

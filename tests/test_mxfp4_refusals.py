@@ -19,7 +19,7 @@ def test_quantize_refusals(capi):
     assert call(T=0) == call(T=0, x=None, q=None, s=None) == capi.MOE_OK
     for bad in (dict(T=-1), dict(H=0), dict(H=-32), dict(H=33), dict(H=16), dict(x=None), dict(q=None), dict(s=None), dict(dt=7)):
         assert call(**bad) == capi.MOE_ERR_INVALID, bad
-    for bad in (dict(dt=Q), dict(T=1 << 31), dict(H=1 << 27)):
+    for bad in (dict(dt=Q), dict(T=1 << 31), dict(H=1 << 27), dict(dt=capi.MOE_F32, T=1 << 30, H=32), dict(T=1 << 30, H=128)):
         assert call(**bad) == capi.MOE_ERR_UNSUPPORTED, bad
 
 
@@ -34,7 +34,8 @@ def test_product_refusals(capi):
                 dict(cap=2, ct=None), dict(cap=3, ct=P)):  # no counts; 4 experts of 3 rows do not fit into 8
         assert call(**bad) == capi.MOE_ERR_INVALID, bad
     for bad in (dict(od=Q), dict(E=1025), dict(R=1 << 31, xr=1 << 31), dict(H=(1 << 20) + 32), dict(N=(1 << 20) + 1),
-                dict(x=ctypes.c_void_p(4104)), dict(w=ctypes.c_void_p(4097)), dict(R=1 << 30, sr=P, N=1 << 20)):
+                dict(x=ctypes.c_void_p(4104)), dict(w=ctypes.c_void_p(4097)), dict(R=1 << 30, sr=P, N=1 << 20),
+                dict(R=8192, xr=8192, E=1024, N=1 << 20, H=32, gated=1)):  # rows of 16 by 64 columns: 1536 * 2^14 workgroups
         assert call(**bad) == capi.MOE_ERR_UNSUPPORTED, bad
 
 

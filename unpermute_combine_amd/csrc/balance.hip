@@ -172,6 +172,8 @@ __device__ __forceinline__ void write_loss(const StatArgs &a, double dot, int32_
 
 // Each workgroup takes a range of tokens, L lanes a token, two tokens at a time. A lane keeps the sums of its columns, the
 // workgroup's lanes are put together in a fixed order, and the counts are integers: the results do not depend on timing.
+// T16384 E256 K8 8.4 us, of which its 17 MB are 2.6: one workgroup a CU, whose two wavefronts a SIMD go through two passes of
+// loads, softmax and sums one after the other, and through 16 KB of LDS into the workgroup's shares. T64 E8, one launch, 3.7 us.
 template <int L, bool V4, int Q>
 __global__ __launch_bounds__(kStatThreads) void balance_stat_kernel(StatArgs a)
 {
@@ -265,7 +267,8 @@ __global__ __launch_bounds__(kStatThreads) void balance_stat_kernel(StatArgs a)
 }
 
 // The workgroups' sums, added in their order, kJoinCols columns a workgroup; the last one to be done has the loss. (One workgroup
-// for all columns has its CU's bandwidth alone: 10 us of 20 at T16384 E256.)
+// for all columns has its CU's bandwidth alone: 10 us against 7.3 at T16384 E256, whose shares are 0.5 MB. Both launches are bound by
+// a chain of latencies.)
 __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(StatArgs a, int blocks)
 {
     constexpr int kParts = kJoinThreads / kJoinCols, kAhead = 16;  // rows whose loads are under way together
@@ -369,7 +372,8 @@ __device__ __forceinline__ void store_row(const float (&d)[4 * Q], const float *
     }
 }
 
-// L lanes a token, as above; f, the same for all tokens, stays in registers.
+// L lanes a token, as above; f, the same for all tokens, stays in registers. Memory and one row's latency: T16384 E256 with a
+// gradient to add, 50 MB in 12-13 us; T2999 E61 3.7 us.
 template <int L, bool V4, int Q>
 __global__ __launch_bounds__(kBackThreads) void balance_backward_kernel(BackArgs a)
 {

@@ -1,8 +1,11 @@
 // The products of the experts' rows with their weights, both in microscaled 4-bit floating point:
 //   y[r, n] = sum_h X[r, h] W_e[n, h]        for the rows r of expert e's segment, float32 sums
 //   out = y, or gated (W_e's first N rows the gate, the next N the up): out[r, n] = silu(y[r, n]) * y[r, N + n]
-// A matrix instruction (v_mfma_scale_f32_16x16x128) takes 16 rows of each operand by 128 elements: lane l holds the 32
-// elements of block l / 16 of row l % 16, and the block's scale.
+// The matrix instructions take both operands' codes with their scales: of 16x16x128 lane l holds the 32 elements of block l / 16 of
+// row l % 16, of 32x32x64 those of block l / 32 of row l % 32, and the block's scale byte. The weights are the first operand, so
+// that a lane's sums are of consecutive columns. An expert with few rows is bound by reading its weights, one with many by the
+// matrix instructions (5.65 PFLOP/s is what they reach by themselves here, at the clock that the power leaves them); there is a
+// kernel for each. Both sum over h in the order of the elements, or in four parts of it.
 #include <algorithm>
 #include <type_traits>
 
@@ -173,6 +176,7 @@ __device__ __forceinline__ u32x4 short_scales(const uint8_t *row, int blocks)
 
 constexpr int kRunBytes = 256, kRunBlocks = kRunBytes / 16;  // of each row at a time: 512 elements, 16 scale bytes
 constexpr int kDppRowRor8 = 0x128;
+constexpr int kRowsWorkgroups = 3;  // a CU: their registers are 168 a thread
 
 // Weights come in whole cache lines: an instruction reads 128 bytes of 8 rows, rows 0..7 into a and 8..15 into b, lanes 8..15 of
 // each 16 the second 64 bytes. Swapping lanes 8..15 of a with 0..7 of b leaves the two 64-byte halves of all 16 rows.
@@ -199,8 +203,12 @@ struct Rows {
 // Up to 16 rows of an expert by 32 weight rows (gated: 16 of the gate and the 16 of the up of the same columns) a wavefront. The
 // weights go from memory into the matrix instructions' operand registers, the next 512 elements on their way while these are
 // multiplied. SPLIT wavefronts share the columns and take parts of the sum, put together in LDS.
+// Bound by reading the weights: 512 rows of E128 H2048 N4096, 570 MB in 92 us (6.2 TB/s; a large read reaches 6.7); one token's 8
+// experts of E256 H7168 N1024 gated, 62 MB in 12.7 (4.9), of which the search of the segment, the first loads and the last are 4.
+// The weights through the caches' streaming policy and in whole lines; x's rows are single buffered, so that three workgroups fit a
+// CU (double buffered, two of them: 110 us).
 template <typename O, bool GATED, int SPLIT>
-__global__ __launch_bounds__(kPlanThreads, 3) void grouped_rows_kernel(ProductArgs a)
+__global__ __launch_bounds__(kPlanThreads, kRowsWorkgroups) void grouped_rows_kernel(ProductArgs a)
 {
     constexpr int kWaves = kPlanThreads / kWave, kCols = GATED ? 16 : 32;  // columns of a wavefront
     __shared__ f32x4 sums[SPLIT > 1 ? kWaves : 1][2][kWave];
@@ -413,6 +421,11 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t nb)
 // other each way; of fewer all of them by 64 weight rows. Tiles of 128 by 128, a wavefront with 64 by 64 or, of up to 64 rows, 32
 // by 64, two to a CU, are for products of which the wide ones would leave CUs without one. Gated, a wavefront's first half are
 // gates, its second the ups of the same columns.
+// A product's operands are read from LDS a step ahead, and stages of 128 elements come three ahead by loads that write LDS
+// themselves; what is issued between two products is spread out by the scheduling barriers. R131072 E256 H7168 N1024 gated with
+// a map 1.18-1.22 ms (3.2 PFLOP/s of 3.85e12), 8192 cubed 288 us (3.8). Bound by the matrix instructions and what
+// feeds them, and by each tile's begin and end, some 13 us of a workgroup that has its CU to itself: R131072 E256 H1024 N7168
+// 1.02-1.07 ms (1.8 PFLOP/s; its outputs alone are 1.9 GB).
 template <typename O, bool GATED, int ROWS, int COLS, bool LINES>
 __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs a)
 {
@@ -755,21 +768,27 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
 // Tiles of BM rows that R rows in E segments can need.
 int64_t max_tiles(int64_t R, int64_t E, int64_t BM) { return R / BM + std::min(R, E); }
 
-constexpr int64_t kWorkgroups = 256;  // of the wide tiles at a time: one a CU
-constexpr int64_t kFewUnits = 4096;
+constexpr int64_t kCus = 256;
+constexpr int64_t kMaxGrid = 0xffffffff / kPlanThreads;  // a grid's threads are a 32-bit number
 
 template <typename O, bool GATED>
 moe_status launch_product(ProductArgs a, hipStream_t stream)
 {
+    // Wide tiles, about: with fewer than CUs the tiles of 128 (E8 H4096 N2048, 128 rows an expert 17.6 against 30.4 us; one expert
+    // of 2048 rows 19.0 against 31.3; E8 N4096 27.0 against 31.3), otherwise the wide ones (4096 cubed, 256 of them, 44 against 56;
+    // R131072 E256 H1024 N7168 1070 against 1271; where experts have few rows and H is short the small ones would win, H1024, 32
+    // rows of each of 64: 46 against 41).
     const int64_t experts = std::min(a.R, static_cast<int64_t>(a.E));  // with rows, at most
-    const int64_t wide = std::max(experts, a.R / 256) * ceil_div(a.N, GATED ? 128 : 256);  // tiles, about
-    const bool few_rows = a.R <= (wide < kWorkgroups ? 16 : 8) * static_cast<int64_t>(a.E);
+    const int64_t wide = std::max(experts, a.R / 256) * ceil_div(a.N, GATED ? 128 : 256);
+    // Up to 8 rows an expert without tiles (E128 H4096 N2048 gated, 8 rows: 204 against 213 us; E64, 12 rows: 126 against 110), or 16
+    // where tiles are few (E8 H4096 N2048, 12 rows: 12.7 against 14.2; 16: 14.3 against 14.2).
+    const bool few_rows = a.R <= (wide < kCus ? 16 : 8) * static_cast<int64_t>(a.E);
     // (rows through a map are addressed in 32 bits by the tiles)
     if (!few_rows && (!a.src_row || a.x_rows * (a.H / 2) <= kNowhere)) {
-        const int size = wide < kWorkgroups ? 128 : 256;
+        const int size = wide < kCus ? 128 : 256;
         a.col_tiles = static_cast<uint32_t>(ceil_div(a.N, GATED ? size / 2 : size));
         const int64_t tiles = max_tiles(a.R, a.E, size) * a.col_tiles;
-        if (tiles > 0x7fffffff)
+        if (tiles > kMaxGrid)
             return MOE_ERR_UNSUPPORTED;
         const dim3 grid(static_cast<unsigned>(tiles));
         if (size == 128)
@@ -780,12 +799,16 @@ moe_status launch_product(ProductArgs a, hipStream_t stream)
             hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 256, 256, false>), grid, dim3(kPlanThreads), 0, stream, a);
         return launch_status();
     }
-    const int64_t tiles = max_tiles(a.R, a.E, 16), units = tiles * ceil_div(a.N, GATED ? 16 : 32);
-    const int split = units < kFewUnits && a.H >= 4 * 512 ? 4 : 1;
+    // Four wavefronts a unit (32 weight rows of an expert's 16 rows) where they all run at once: 512 units of H7168 12.7 against
+    // 20.2 us by one, 768 of H4096 12.9 against 15.3, 256 of H1024 4.4 against 5.6; 992 of H4096 18.3 against 14.4, 16384 of H2048
+    // 137 against 93. Of H512 there is one run of elements to share.
+    const int64_t units = std::max(experts, a.R / 16) * ceil_div(a.N, GATED ? 16 : 32);
+    const int split = units <= kRowsWorkgroups * kCus && a.H >= 2 * 2 * kRunBytes ? 4 : 1;
     a.col_tiles = static_cast<uint32_t>(ceil_div(a.N, (GATED ? 16 : 32) * (kPlanThreads / kWave / split)));
-    if (tiles * a.col_tiles > 0x7fffffff)
+    const int64_t tiles = max_tiles(a.R, a.E, 16) * a.col_tiles;
+    if (tiles > kMaxGrid)
         return MOE_ERR_UNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>(tiles * a.col_tiles));
+    const dim3 grid(static_cast<unsigned>(tiles));
     if (split == 4)
         hipLaunchKernelGGL((grouped_rows_kernel<O, GATED, 4>), grid, dim3(kPlanThreads), 0, stream, a);
     else
