@@ -11,7 +11,7 @@ namespace moe {
 namespace {
 
 constexpr int kStatThreads = 512;
-constexpr int kJoinThreads = 256, kJoinCols = 32, kMaxJoinBlocks = MOE_MAX_EXPERTS / kJoinCols;
+constexpr int kJoinThreads = 256, kJoinCols = 16, kMaxJoinBlocks = MOE_MAX_EXPERTS / kJoinCols;
 constexpr int kBackThreads = 256;
 constexpr int kMaxStatBlocks = 256;  // one a CU
 constexpr int kFlush = 8;            // tokens of a lane summed in float32 before they join its double sums
@@ -54,6 +54,22 @@ __device__ __forceinline__ float token_sum(float v)
         v += __shfl_xor(v, 32);
     }
     return v;
+}
+
+// The sum over lanes l, l ^ 16, l ^ 32 and l ^ 48: an exchange of two registers' rows gives
+// both operands.
+__device__ __forceinline__ double row_sum(double v)
+{
+    const uint64_t w = __double_as_longlong(v);
+    const uint32_t lo = static_cast<uint32_t>(w), hi = static_cast<uint32_t>(w >> 32);
+    const auto a = __builtin_amdgcn_permlane16_swap(lo, lo, false, false), b = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+    const double s = __longlong_as_double(static_cast<uint64_t>(b[0]) << 32 | a[0]) +
+                     __longlong_as_double(static_cast<uint64_t>(b[1]) << 32 | a[1]);
+    const uint64_t x = __double_as_longlong(s);
+    const uint32_t xl = static_cast<uint32_t>(x), xh = static_cast<uint32_t>(x >> 32);
+    const auto c = __builtin_amdgcn_permlane32_swap(xl, xl, false, false), d = __builtin_amdgcn_permlane32_swap(xh, xh, false, false);
+    return __longlong_as_double(static_cast<uint64_t>(d[0]) << 32 | c[0]) +
+           __longlong_as_double(static_cast<uint64_t>(d[1]) << 32 | c[1]);
 }
 
 __device__ __forceinline__ double wave_sum(double v)
@@ -172,17 +188,26 @@ __device__ __forceinline__ void write_loss(const StatArgs &a, double dot, int32_
 
 // Each workgroup takes a range of tokens, L lanes a token, two tokens at a time. A lane keeps the sums of its columns, the
 // workgroup's lanes are put together in a fixed order, and the counts are integers: the results do not depend on timing.
-// T16384 E256 K8 8.4 us, of which its 17 MB are 2.6: one workgroup a CU, whose two wavefronts a SIMD go through two passes of
-// loads, softmax and sums one after the other, and through 16 KB of LDS into the workgroup's shares. T64 E8, one launch, 3.7 us.
+// T16384 E256 K8 7.1 us, of which its 17 MB are 2.6: one workgroup a CU, whose wavefronts load two tokens a group of lanes, take
+// their softmax and go through LDS into the workgroup's shares, one latency after the other (the slots, on their way beside the
+// logits, and all columns through LDS at a time 1.9 us less). T64 E8, one launch, 3.4 us.
 template <int L, bool V4, int Q>
 __global__ __launch_bounds__(kStatThreads) void balance_stat_kernel(StatArgs a)
 {
     constexpr int kGroups = kStatThreads / L, kWaves = kStatThreads / kWave, kCols = 4 * L, N = 4 * Q;
-    __shared__ double part[kWaves][kCols];
+    __shared__ double part[kWaves][kCols * Q];
     __shared__ int32_t hist[kCols * Q];
     __shared__ int32_t ntok;
     const int sub = threadIdx.x % L, group = threadIdx.x / L, wave = threadIdx.x / kWave;
     const int64_t t0 = blockIdx.x * a.tokens_per_block, t1 = min(a.T, t0 + a.tokens_per_block);
+    for (int i = threadIdx.x; i < kCols * Q; i += kStatThreads)
+        hist[i] = 0;
+    if (threadIdx.x == 0)
+        ntok = 0;
+    // a slot of this workgroup's, on its way beside the logits
+    const int64_t slot = t0 * a.K + threadIdx.x, slots = t1 * a.K;
+    auto counted = [&](int64_t i) { return !a.mask || a.mask[static_cast<uint32_t>(i) / static_cast<uint32_t>(a.K)]; };
+    const int32_t e0 = slot < slots && counted(slot) ? a.topk_idx[slot] : -1;
     double acc[N] = {};
     int32_t mine = 0;
     if (t0 < t1) {
@@ -213,47 +238,36 @@ __global__ __launch_bounds__(kStatThreads) void balance_stat_kernel(StatArgs a)
         for (int j = 0; j < N; ++j)
             acc[j] += static_cast<double>(few[j]);
     }
-    for (int i = threadIdx.x; i < kCols * Q; i += kStatThreads)
-        hist[i] = 0;
-    if (threadIdx.x == 0)
-        ntok = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const double v = L == 16 ? row_sum(acc[j]) : acc[j];
+        if ((threadIdx.x & (kWave - 1)) < L)
+            part[wave][column<L, V4>(sub, j / 4, j % 4)] = v;
+    }
     __syncthreads();
     if (sub == 0)
         atomicAdd(&ntok, mine);
-    for (int64_t i = t0 * a.K + threadIdx.x; i < t1 * a.K; i += kStatThreads) {
+    if (e0 >= 0 && e0 < a.E)
+        atomicAdd(&hist[e0], 1);
+    for (int64_t i = slot + kStatThreads; i < slots; i += kStatThreads) {
         const int32_t e = a.topk_idx[i];
-        if (e >= 0 && e < a.E && (!a.mask || a.mask[static_cast<uint32_t>(i) / static_cast<uint32_t>(a.K)]))
+        if (e >= 0 && e < a.E && counted(i))
             atomicAdd(&hist[e], 1);
     }
+    __syncthreads();
     double share = 0.0;
+    for (int c = threadIdx.x; c < a.E; c += kStatThreads) {
+        double total = 0.0;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {  // kCols columns at a time, whose threads are as many or fewer than the workgroup's
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            double v = acc[4 * q + i];
-            if constexpr (L == 16) {
-                v += __shfl_xor(v, 16);
-                v += __shfl_xor(v, 32);
-            }
-            if ((threadIdx.x & (kWave - 1)) < L)
-                part[wave][column<L, V4>(sub, 0, i)] = v;
+        for (int w = 0; w < kWaves; ++w)
+            total += part[w][c];
+        if (gridDim.x == 1) {
+            a.prob_sum[c] = static_cast<float>(total);
+            a.counts[c] = hist[c];
+            share += hist[c] * total;
+        } else {
+            a.shares[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + c] = Share{static_cast<float>(total), hist[c]};
         }
-        __syncthreads();
-        const int c = q * kCols + threadIdx.x;
-        if (threadIdx.x < kCols && c < a.E) {
-            double total = 0.0;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                total += part[w][threadIdx.x];
-            if (gridDim.x == 1) {
-                a.prob_sum[c] = static_cast<float>(total);
-                a.counts[c] = hist[c];
-                share += hist[c] * total;
-            } else {
-                a.shares[static_cast<int64_t>(blockIdx.x) * (a.E + 1) + c] = Share{static_cast<float>(total), hist[c]};
-            }
-        }
-        __syncthreads();
     }
     if (gridDim.x == 1) {
         const double dot = block_sum<kStatThreads>(share, &part[0][0]);
@@ -267,8 +281,8 @@ __global__ __launch_bounds__(kStatThreads) void balance_stat_kernel(StatArgs a)
 }
 
 // The workgroups' sums, added in their order, kJoinCols columns a workgroup; the last one to be done has the loss. (One workgroup
-// for all columns has its CU's bandwidth alone: 10 us against 7.3 at T16384 E256, whose shares are 0.5 MB. Both launches are bound by
-// a chain of latencies.)
+// for all columns has its CU's bandwidth alone. Both launches at T16384 E256, whose shares are 0.5 MB: 16.5 us with 8 columns, 13.1
+// with 16, 13.7 with 32; E1024 21.4 with 16 or 32; T4096 E128 10.0 and 9.8.) Bound by a chain of latencies.
 __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(StatArgs a, int blocks)
 {
     constexpr int kParts = kJoinThreads / kJoinCols, kAhead = 16;  // rows whose loads are under way together
@@ -320,11 +334,14 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(StatArgs a, 
         last = __hip_atomic_fetch_add(&a.joined->done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == static_cast<int>(gridDim.x) - 1;
     }
     __syncthreads();
-    if (last && threadIdx.x == 0) {
+    if (last && threadIdx.x < kWave) {
+        static_assert(kMaxJoinBlocks <= kWave, "");
         double total = 0.0;
-        for (unsigned b = 0; b < gridDim.x; ++b)
-            total += __hip_atomic_load(&a.joined->dot[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        write_loss(a, total, ntok);
+        if (threadIdx.x < gridDim.x)
+            total = __hip_atomic_load(&a.joined->dot[threadIdx.x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        total = wave_sum(total);
+        if (threadIdx.x == 0)
+            write_loss(a, total, ntok);
     }
 }
 
