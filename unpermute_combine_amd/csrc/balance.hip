@@ -281,8 +281,8 @@ __global__ __launch_bounds__(kStatThreads) void balance_stat_kernel(StatArgs a)
 }
 
 // The workgroups' sums, added in their order, kJoinCols columns a workgroup; the last one to be done has the loss. (One workgroup
-// for all columns has its CU's bandwidth alone. Both launches at T16384 E256, whose shares are 0.5 MB: 16.5 us with 8 columns, 13.1
-// with 16, 13.7 with 32; E1024 21.4 with 16 or 32; T4096 E128 10.0 and 9.8.) Bound by a chain of latencies.
+// for all columns has its CU's bandwidth alone. Both launches at T16384 E256, whose shares are 0.5 MB: 13.1 us, 13.7 with 32
+// columns; E1024 21.4 with 16 or 32; T4096 E128 10.0 and 9.8.) Bound by a chain of latencies.
 __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(StatArgs a, int blocks)
 {
     constexpr int kParts = kJoinThreads / kJoinCols, kAhead = 16;  // rows whose loads are under way together
