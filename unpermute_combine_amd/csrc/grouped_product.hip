@@ -423,9 +423,9 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t nb)
 // gates, its second the ups of the same columns.
 // A product's operands are read from LDS a step ahead, and stages of 128 elements come three ahead by loads that write LDS
 // themselves; what is issued between two products is spread out by the scheduling barriers. R131072 E256 H7168 N1024 gated with
-// a map 1.18-1.22 ms (3.2 PFLOP/s of 3.85e12), 8192 cubed 288 us (3.8). Bound by the matrix instructions and what
-// feeds them, and by each tile's begin and end, some 13 us of a workgroup that has its CU to itself: R131072 E256 H1024 N7168
-// 1.02-1.07 ms (1.8 PFLOP/s; its outputs alone are 1.9 GB).
+// a map 1.15-1.20 ms (3.85e12 operations, 3.2-3.3 PFLOP/s), 8192 cubed 290 us (3.8). Bound by the matrix instructions and what
+// feeds them, and by each tile's begin and end (search 1-2 us, first stages 2-4, outputs 4), when its CU has
+// nothing else to do: R131072 E256 H1024 N7168 1.02 ms (1.9 PFLOP/s; its outputs alone are 1.9 GB).
 template <typename O, bool GATED, int ROWS, int COLS, bool LINES>
 __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs a)
 {
@@ -435,6 +435,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     const Tile tile = find_tile<ROWS>(a, xcd_run(blockIdx.x, gridDim.x), *reinterpret_cast<Search *>(sh.scales[1]));
     if (tile.e < 0)
         return;
+    __syncthreads();  // the search is done with its place
     constexpr int kOutCols = GATED ? COLS / 2 : COLS, kXMost = ROWS / 64, kWLoads = COLS / 64;  // 16-byte loads a thread and stage
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / kWave));
     const int blocks = static_cast<int>(a.H / kMxBlock), stages = (blocks + kStageBlocks - 1) / kStageBlocks;
@@ -450,31 +451,39 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     const uint8_t *const xbase = a.x + x_at * row_bytes;
     const uint32_t xbytes = capped((a.x_rows - x_at) * row_bytes);
     const int64_t wrows = a.N * (GATED ? 2 : 1), w_at = tile.e * wrows + n0;
-    auto x_row = [&](int r) -> int64_t {
-        if (r >= tile.rows)
-            return -1;
-        const int64_t row = a.src_row ? a.src_row[tile.first + r] : tile.first + r;
-        return row < a.x_rows ? row : -1;
+    // (without a map some number that is there, and not used: the loads need no branch and come together)
+    const int32_t *const map = a.src_row ? a.src_row + tile.first : a.capacity > 0 ? a.counts : a.group_list;
+    const int map_last = a.src_row ? tile.rows - 1 : 0;
+    auto mapped = [&](int r) -> int32_t { return map[min(r, map_last)]; };
+    // x's row r of the tile, behind the base above; -1 if there is none
+    auto x_row = [&](int r, int32_t from) -> int32_t {
+        const int32_t row = a.src_row ? from : r;
+        return r < tile.rows && row < a.x_rows - x_at ? row : -1;
     };
-    auto w_row = [&](int b) -> int64_t {
-        const int64_t n = GATED ? b / wave_cols * wave_half + b % wave_half : b;
-        return min(n, a.N - 1 - n0);
+    auto w_row = [&](int b) -> int32_t {
+        const int n = GATED ? b / wave_cols * wave_half + b % wave_half : b;
+        return min(n, static_cast<int>(a.N - 1 - n0));
     };
     auto is_up = [&](int b) { return GATED && b % wave_cols >= wave_half; };
+    const int x_mine = threadIdx.x % ROWS, w_mine = threadIdx.x % COLS;  // rows whose scales a thread takes (some twice)
+    // The map's entries on their way first, behind them the weights of stages 0 and 1 (R131072 E256 H7168 N1024 gated 1231 -> 1190 us,
+    // H1024 N7168 1062 -> 1025, against the map's entries one by one and then all loads).
+    int32_t from[kXMost], from_mine = 0, from_lines[2];
+#pragma unroll
+    for (int j = 0; j < kXMost; ++j)
+        from[j] = mapped(64 * j + threadIdx.x / 4);
+    if constexpr (LINES) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            from_lines[q] = mapped(32 * (4 * q + wave) + lane / 2);
+    } else {
+        from_mine = mapped(x_mine);
+    }
     uint32_t xo[kXMost], wo[kWLoads];
 #pragma unroll
-    for (int j = 0; j < kXMost; ++j) {
-        const int64_t row = x_row(64 * j + threadIdx.x / 4);
-        xo[j] = row >= 0 ? static_cast<uint32_t>((row - x_at) * row_bytes) + chunk * 16 : kNowhere;
-    }
-#pragma unroll
     for (int j = 0; j < kWLoads; ++j)
-        wo[j] = static_cast<uint32_t>(w_row(64 * j + threadIdx.x / 4) * row_bytes) + chunk * 16;
-    const int x_mine = threadIdx.x % ROWS, w_mine = threadIdx.x % COLS;  // rows whose scales a thread takes (some twice)
+        wo[j] = static_cast<uint32_t>(w_row(64 * j + threadIdx.x / 4)) * static_cast<uint32_t>(row_bytes) + chunk * 16;
     const uint8_t *const wsp = a.ws + (w_at + w_row(w_mine) + (is_up(w_mine) ? a.N : 0)) * blocks;
-    const int64_t xs_row = x_row(x_mine);
-    const uint8_t *const xsp = xs_row >= 0 ? a.xs + xs_row * blocks : wsp;
-    const uint32_t keep = xs_row >= 0 ? 0xffffffffu : 0;  // beside zeros the scale is any but NaN
     const uint8_t *const gate = a.w + w_at * row_bytes, *const up = gate + (GATED ? a.N * row_bytes : 0);
     const uint32_t gate_bytes = capped((a.E * wrows - w_at) * row_bytes);
     const uint32_t up_bytes = GATED ? capped((a.E * wrows - w_at - a.N) * row_bytes) : gate_bytes;
@@ -497,6 +506,21 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
         const uint32_t bytes = u ? up_bytes : gate_bytes;
         to_lds(make_rsrc(u ? up : gate, s < stages ? bytes : 0), wo[j] + s * kStageBytes, slot(s) + (ROWS + 64 * j) * kStageBytes);
     };
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < kWLoads; ++j)
+            load_w(s, j);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < kXMost; ++j) {
+        const int32_t row = x_row(64 * j + threadIdx.x / 4, from[j]);
+        xo[j] = row >= 0 ? static_cast<uint32_t>(row) * static_cast<uint32_t>(row_bytes) + chunk * 16 : kNowhere;
+    }
+    const int32_t xs_row = x_row(x_mine, from_mine);
+    const uint8_t *const xsp = xs_row >= 0 ? a.xs + (x_at + xs_row) * blocks : wsp;
+    const uint32_t keep = xs_row >= 0 ? 0xffffffffu : 0;  // beside zeros the scale is any but NaN
     // Scales come for kScaleStages stages (a group) at a time, x's and the weights' in turns. A row's 16 bytes are put down as what
     // each half of a wavefront needs of them: blocks 0, 1 of each stage's four, then blocks 2, 3.
     const uint8_t *const xsl = blocks >= 16 ? xsp : a.w;  // (16 bytes to read, where the rows are shorter)
@@ -526,8 +550,8 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int b = 32 * (4 * q + wave) + lane / 2;
-            const int64_t row = q < 2 ? x_row(b) - x_at : w_row(b - ROWS);
-            so[q] = row >= 0 ? static_cast<uint32_t>(row * blocks) + lane % 2 * 16 : kNowhere;
+            const int32_t row = q < 2 ? x_row(b, from_lines[q & 1]) : w_row(b - ROWS);
+            so[q] = row >= 0 ? static_cast<uint32_t>(row) * static_cast<uint32_t>(blocks) + lane % 2 * 16 : kNowhere;
         }
     }
     auto load_line = [&](int g, int q) {
@@ -657,7 +681,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
                     ws[n] = next_ws[n];
             }
         };
-        meet(std::integral_constant<int, 2 * kLoads + kXLoads>{});
+        meet(std::integral_constant<int, 3 * kXLoads + kWLoads>{});  // x's of stages 1 to 3, the weights' of stage 2
         read(0, 0, f[0]);
         read_scales(0, xs, ws);
         for (int s = 0; s < stages; s += 2) {  // after an odd number one of zeros
@@ -668,11 +692,10 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
 #undef MOE_PRODUCTS
     };
 
-    // stages 0 to 2, x's of stage 3, the scales of group 0 and the first of group 1
+    // what is left of stages 0 to 2, x's of stage 3, the scales of group 0 and the first of group 1
     const int x_loads = big ? (tile.rows > 192 ? 4 : 3) : tile.rows > 64 ? 2 : 1;
     u32x4 xsc, wsc;
     if constexpr (LINES) {
-        __syncthreads();  // the search is done with its place
 #pragma unroll
         for (int t = 0; t < 5; ++t)
             load_line(t / 4, t % 4);
@@ -694,10 +717,10 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
         for (int j = 0; j < kXMost; ++j)
             if (j < x_loads)
                 load_x(s, j);
-        if (s < kStages - 1)
+        if (s == 1)
 #pragma unroll
             for (int j = 0; j < kWLoads; ++j)
-                load_w(s, j);
+                load_w(2, j);
     }
     if constexpr (!LINES) {
         put_sc(false, 0, xsc);
