@@ -406,7 +406,8 @@ moe_status moe_balance_loss(const float *logits, const int32_t *topk_idx, const 
  * and 0 (+ d_logits_in) for tokens that do not count, and where n <= 0; the counts, piecewise constant, have no gradient. In
  * float32.
  *   d_loss [1] float32 (NULL: 1); d_logits_in [T, E] or NULL: the gradient that reaches the logits by other ways
- *   (moe_route_topk_backward's); d_logits [T, E], which may be d_logits_in. */
+ *   (moe_route_topk_backward's); d_logits [T, E], which may be d_logits_in and overlaps no other
+ *   input. */
 moe_status moe_balance_loss_backward(const float *logits, const uint8_t *token_mask, const int32_t *counts,
                                      const int32_t *tokens, const float *d_loss, int64_t T, int32_t E, int32_t K,
                                      float coef, const float *d_logits_in, float *d_logits, hipStream_t stream);
@@ -515,7 +516,7 @@ moe_status moe_few_token_experts(const void *x, moe_dtype dt, int64_t T, int64_t
  *   T * H / 8 <= 2^32 - 2^8 for float32, T * H / 32 for bf16 (else MOE_ERR_UNSUPPORTED).
  *   q [T, H/2] bytes: two codes each, the even element's in the low half. scales [T, H/32] bytes: the exponent + 127; 255
  *   (which stands for NaN) for a block that holds a NaN or an infinity, whose codes are 0.
- * Both are byte rows that the permutes move as MOE_FP8_E4M3 rows of H/2 and H/32 elements. */
+ * Both are byte rows that the permutes move as MOE_FP8_E4M3 rows of H/2 and H/32 elements; they overlap neither x nor each other. */
 moe_status moe_quantize_mxfp4(const void *x, moe_dtype x_dt, int64_t T, int64_t H, uint8_t *q, uint8_t *scales,
                               hipStream_t stream);
 
