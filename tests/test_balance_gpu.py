@@ -71,7 +71,7 @@ def tokens_of(n):
 
 SHAPES = [(1, 1, 1), (1, 8, 2), (3, 7, 7), (64, 8, 2), (65, 16, 3), (63, 60, 4), (130, 61, 4), (1000, 64, 8), (257, 100, 6),
           (500, 128, 1), (333, 130, 8), (2049, 256, 8), (3000, 255, 32), (700, 260, 5), (401, 384, 8), (515, 513, 2), (290, 1000, 32),
-          (1025, 1024, 8), (16384, 256, 8), (20001, 33, 2)]
+          (1025, 1024, 8), (16384, 256, 8), (20001, 33, 2), (256, 256, 32), (255, 12, 3), (64, 600, 3), (65, 512, 4), (257, 8, 2)]
 
 
 @pytest.mark.parametrize("T,E,K", SHAPES)
