@@ -3,7 +3,8 @@
 A float32 g is a sum of 24 powers of two or less; each is a block of a row of x (code +-1, the power its scale) against a code 1 of
 the weights, so that the sum is g whatever its order, and a block of its own gives the up. With u = 2^-24, -log2(e) g rounds once
 (the constant in two parts), u |g| in e^-g; the instructions for 2^x and 1 / x are right to 2 u each, the sum and the product round
-once: (|g| + 6) u of silu. Past g = -88.72 e^-g passes float32 and silu is 0."""
+once: (|g| + 6) u of silu. Where 1 / (1 + e^-g) is below the normal float32 (g < -87.3) it has 21 bits or more, 4 u besides; past
+g = -88.72 e^-g passes float32 and silu is 0."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -62,6 +63,15 @@ def test_silu_to_its_bound(m, experts):
     g[2048], g[2049] = -44.37, -22.24
     got, want = gates(m, g, 0, experts), g.double() * torch.sigmoid(g.double())
     off = (got - want).abs() / (want.abs() * (g.double().abs() + 6) * U)
+    assert float(off.max()) <= 1, f"g = {float(g[off.argmax()])}: {float(off.max()):.3g} of the bound"
+
+
+@pytest.mark.parametrize("experts", [1, 512])
+def test_silu_before_its_exponential_overflows(m, experts):
+    """g in (-88.72, -87.3) beside an up of 2^60: outputs that float32 holds well."""
+    g = torch.linspace(-88.72, -87.3, 8 * 512)
+    got, want = gates(m, g, 60, experts), g.double() * torch.sigmoid(g.double()) * 2.0 ** 60
+    off = (got - want).abs() / (want.abs() * (g.double().abs() + 10) * U)
     assert float(off.max()) <= 1, f"g = {float(g[off.argmax()])}: {float(off.max()):.3g} of the bound"
 
 

@@ -138,10 +138,14 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs &a, uint32_t i, Sear
 
 // g / (1 + exp(-g)) by the instructions for 2^x and 1 / x, right to an ulp each: with the argument's rounding (|g| + 6) u in all.
 // (log2 e alone is off by 0.23 u of itself, which would be |g| 0.23 u more: its low part goes into the same rounding.)
+// 1 / x gives 0 for results below the normal numbers, as 1 / (1 + exp(-g)) is from g = -87.3 on: it is taken of a sixteenth, and
+// the product with 1/16 keeps 21 bits or more there (4 u besides). Past g = -88.72 exp(-g) passes float32: 0.
 __device__ __forceinline__ float silu(float g)
 {
     constexpr float kLog2e = 1.44269504088896340736f, kLow = 1.925963033500e-8f;  // their sum is log2 e
-    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(fmaf(-kLog2e, g, -kLow * g)));
+    constexpr float kPart = 1.0f / 16;
+    const float e = __builtin_amdgcn_exp2f(fmaf(-kLog2e, g, -kLow * g));
+    return g * (__builtin_amdgcn_rcpf(fmaf(e, kPart, kPart)) * kPart);
 }
 
 __device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
