@@ -535,8 +535,8 @@ moe_status moe_quantize_mxfp4(const void *x, moe_dtype x_dt, int64_t T, int64_t 
  *   out [R, N] (float32 or bf16), which overlaps no input. Rows in no segment are left untouched. Segments are cut to [0, R);
  *   ones that overlap give unspecified rows.
  * Rows are independent: a NaN scale makes NaN of its own row or column alone. H a multiple of 32 (else MOE_ERR_INVALID);
- * H, N <= 2^20, x and w 16-byte aligned (else MOE_ERR_UNSUPPORTED, as for a launch that would pass 2^32 threads: few rows of each of
- * very many experts, short, with some 2^20 columns). */
+ * H, N <= 2^20, x and w 16-byte aligned (else MOE_ERR_UNSUPPORTED, as for a launch that would pass 2^32 threads: R * N from 2^38
+ * on, or up to 8 rows of each of more than 680 experts with some 2^20 columns). */
 moe_status moe_grouped_product_mxfp4(const uint8_t *x, const uint8_t *x_scales, int64_t x_rows, const int32_t *src_row,
                                      int64_t R, int64_t H, const uint8_t *w, const uint8_t *w_scales, int32_t E, int64_t N,
                                      int32_t gated, const int32_t *group_list, const int32_t *counts, int32_t capacity,

@@ -400,6 +400,15 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t from, uint32_t off
                                              static_cast<int>(offset), 0, 0, 0);
 }
 
+// The same by an address of each lane's.
+__device__ __forceinline__ void to_lds(const uint8_t *from, uint32_t to)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                     reinterpret_cast<__attribute__((address_space(3))) void *>(to), 16, 0, 0);
+}
+
+__device__ const u32x4 kZeros = {0, 0, 0, 0};  // what such a load reads of a row that is not there
+
 // Buffer resources end before this offset, which asks for nothing.
 constexpr uint32_t kNowhere = 0xfffffff0u;
 
@@ -431,7 +440,9 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t nb)
 // a map 1.15-1.20 ms (3.85e12 operations, 3.2-3.3 PFLOP/s), 8192 cubed 290 us (3.8). Bound by the matrix instructions and what
 // feeds them, and by each tile's begin and end (search 1-2 us, first stages 2-4, outputs 4), when its CU has
 // nothing else to do: R131072 E256 H1024 N7168 1.02 ms (1.9 PFLOP/s; its outputs alone are 1.9 GB).
-template <typename O, bool GATED, int ROWS, int COLS, bool LINES>
+// FAR is for a map onto more codes than a buffer resource's 32-bit offsets reach: x comes by 64-bit addresses (R131072 E256 H7168
+// N1024 gated of 1.2 M rows 1.53 ms, of 1.19 M by offsets 1.30; 16 rows a workgroup without tiles took 12.4).
+template <typename O, bool GATED, int ROWS, int COLS, bool LINES, bool FAR>
 __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs a)
 {
     constexpr bool kWide = COLS == 256;
@@ -485,6 +496,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
         from_mine = mapped(x_mine);
     }
     uint32_t xo[kXMost], wo[kWLoads];
+    const uint8_t *xp[kXMost];
 #pragma unroll
     for (int j = 0; j < kWLoads; ++j)
         wo[j] = static_cast<uint32_t>(w_row(64 * j + threadIdx.x / 4)) * static_cast<uint32_t>(row_bytes) + chunk * 16;
@@ -503,6 +515,11 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     // x's chunks past the end of the rows are zeros (beside them the weights' are some codes, and zero times them is zero); past the
     // last stage nothing is read, but the number of loads is the same in every stage.
     auto load_x = [&](int s, int j) {
+        if constexpr (FAR) {
+            const uint8_t *const zeros = reinterpret_cast<const uint8_t *>(&kZeros);
+            to_lds(s * kStageBlocks + chunk < blocks && xp[j] ? xp[j] + s * kStageBytes : zeros, slot(s) + 64 * j * kStageBytes);
+            return;
+        }
         to_lds(make_rsrc(xbase, xbytes), s * kStageBlocks + chunk < blocks && xo[j] != kNowhere ? xo[j] + s * kStageBytes : kNowhere,
                slot(s) + 64 * j * kStageBytes);
     };
@@ -522,6 +539,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     for (int j = 0; j < kXMost; ++j) {
         const int32_t row = x_row(64 * j + threadIdx.x / 4, from[j]);
         xo[j] = row >= 0 ? static_cast<uint32_t>(row) * static_cast<uint32_t>(row_bytes) + chunk * 16 : kNowhere;
+        xp[j] = row >= 0 ? xbase + row * row_bytes + chunk * 16 : nullptr;
     }
     const int32_t xs_row = x_row(x_mine, from_mine);
     const uint8_t *const xsp = xs_row >= 0 ? a.xs + (x_at + xs_row) * blocks : wsp;
@@ -813,20 +831,24 @@ moe_status launch_product(ProductArgs a, hipStream_t stream)
     // segments: all rows on one expert, each 16 of which read its weights again, take less than rows on all (2048 rows of E256 H7168
     // N1024 gated 185 against 356).
     const bool few_rows = a.R <= (wide < kCus ? 16 : 8) * static_cast<int64_t>(a.E);
-    // (rows through a map are addressed in 32 bits by the tiles)
-    if (!few_rows && (!a.src_row || a.x_rows * (a.H / 2) <= kNowhere)) {
+    if (!few_rows) {
         const int size = wide < kCus ? 128 : 256;
         a.col_tiles = static_cast<uint32_t>(ceil_div(a.N, GATED ? size / 2 : size));
         const int64_t tiles = max_tiles(a.R, a.E, size) * a.col_tiles;
         if (tiles > kMaxGrid)
             return MOE_ERR_UNSUPPORTED;
         const dim3 grid(static_cast<unsigned>(tiles));
-        if (size == 128)
-            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 128, 128, false>), grid, dim3(kPlanThreads), 0, stream, a);
+        const bool far = a.src_row && a.x_rows * (a.H / 2) > kNowhere;
+        if (size == 128 && far)
+            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 128, 128, false, true>), grid, dim3(kPlanThreads), 0, stream, a);
+        else if (size == 128)
+            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 128, 128, false, false>), grid, dim3(kPlanThreads), 0, stream, a);
+        else if (far)
+            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 256, 256, false, true>), grid, dim3(kPlanThreads), 0, stream, a);
         else if (a.H % 512 == 0 && aligned16(a.xs) && aligned16(a.ws))
-            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 256, 256, true>), grid, dim3(kPlanThreads), 0, stream, a);
+            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 256, 256, true, false>), grid, dim3(kPlanThreads), 0, stream, a);
         else
-            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 256, 256, false>), grid, dim3(kPlanThreads), 0, stream, a);
+            hipLaunchKernelGGL((grouped_tile_kernel<O, GATED, 256, 256, false, false>), grid, dim3(kPlanThreads), 0, stream, a);
         return launch_status();
     }
     // Four wavefronts a unit (32 weight rows of an expert's 16 rows) where they all run at once: 512 units of H7168 12.7 against
