@@ -358,9 +358,9 @@ struct BackArgs {
     float coef;
 };
 
-// A gradient row out, the one that is added read in its place.
+// A gradient row out, with another added, which may be the row itself: each element is read before it is written, by the same lane.
 template <int L, bool V4, int Q>
-__device__ __forceinline__ void store_row(const float (&d)[4 * Q], const float *__restrict__ add, float *__restrict__ out, int E, int sub)
+__device__ __forceinline__ void store_row(const float (&d)[4 * Q], const float *add, float *out, int E, int sub)
 {
     if constexpr (V4) {
 #pragma unroll
