@@ -638,8 +638,10 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
             for (int n = 0; n < NS; ++n)
                 w[n] = read_scale(s, w0 + 32 * n);
         };
+        // (ungated, those of columns that only wider wavefronts have too: the outputs read them. A branch there pays where it spares
+        // gates, R12288 E128 H4096 N2048 285 -> 277 us, and costs elsewhere, R131072 E256 H1024 N7168 1020 -> 1030 against 1015.)
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
+        for (int n = 0; n < (GATED ? NS : COLS / 64); ++n)
 #pragma unroll
             for (int m = 0; m < MS; ++m)
                 acc[n * kStep][m] = f32x16{};
@@ -782,7 +784,9 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
         if (rows <= 0)
             break;
 #pragma unroll
-        for (int n = 0; n < kMost / 32; ++n)
+        for (int n = 0; n < kMost / 32; ++n) {
+            if (GATED && n == kMost / 64 && width < kMost)  // a wavefront of half as many columns has no more sums
+                break;
 #pragma unroll
             for (int q = 0; q < 16; q += 4) {
                 float v[4];
@@ -791,6 +795,7 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
                     v[i] = GATED ? silu(acc[n][m][q + i]) * acc[n + (GATED ? 2 : 0)][m][q + i] : acc[n][m][q + i];
                 put4(part + r32 * kPitch + 32 * n + 2 * q + 4 * half, v);
             }
+        }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         O *const out = static_cast<O *>(a.out) + (tile.first + row0 + 32 * m) * a.N + c0;
         if (vectors) {
