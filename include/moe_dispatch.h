@@ -534,6 +534,8 @@ moe_status moe_quantize_mxfp4(const void *x, moe_dtype x_dt, int64_t T, int64_t 
  *   (moe_index.kept_counts) rows from e * capacity, group_list is not read, R >= E * capacity.
  *   out [R, N] (float32 or bf16), which overlaps no input. Rows in no segment are left untouched. Segments are cut to [0, R);
  *   ones that overlap give unspecified rows.
+ * R and E choose the kernel, and R counts rows that take no part too: segments aligned to 8 and more, or of a capacity past 8, take
+ * calls with few tokens off the kernel for few rows (one token twice the time, 64 tokens a fifth more).
  * Rows are independent: a NaN scale makes NaN of its own row or column alone. H a multiple of 32 (else MOE_ERR_INVALID);
  * H, N <= 2^20, x and w 16-byte aligned (else MOE_ERR_UNSUPPORTED, as for a launch that would pass 2^32 threads: R * N from 2^38
  * on, or up to 8 rows of each of more than 680 experts with some 2^20 columns). */

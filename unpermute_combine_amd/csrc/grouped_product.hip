@@ -4,8 +4,8 @@
 // The matrix instructions take both operands' codes with their scales: of 16x16x128 lane l holds the 32 elements of block l / 16 of
 // row l % 16, of 32x32x64 those of block l / 32 of row l % 32, and the block's scale byte. The weights are the first operand, so
 // that a lane's sums are of consecutive columns. An expert with few rows is bound by reading its weights, one with many by the
-// matrix instructions (5.65 PFLOP/s is what they reach by themselves here, at the clock that the power leaves them); there is a
-// kernel for each. Both sum over h in the order of the elements, or in four parts of it.
+// matrix instructions (6.7 PFLOP/s is what they reach by themselves here with random codes, at 1.66 GHz; with zeros, whose products
+// take less power, 9.8 at 2.39 GHz); there is a kernel for each. Both sum over h in the order of the elements, or in four parts of it.
 #include <algorithm>
 #include <type_traits>
 
@@ -437,9 +437,10 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t nb)
 // gates, its second the ups of the same columns.
 // A product's operands are read from LDS a step ahead, and stages of 128 elements come three ahead by loads that write LDS
 // themselves; what is issued between two products is spread out by the scheduling barriers. R131072 E256 H7168 N1024 gated with
-// a map 1.15-1.20 ms (3.85e12 operations, 3.2-3.3 PFLOP/s), 8192 cubed 290 us (3.8). Bound by the matrix instructions and what
-// feeds them, and by each tile's begin and end (search 1-2 us, first stages 2-4, outputs 4), when its CU has
-// nothing else to do: R131072 E256 H1024 N7168 1.02 ms (1.9 PFLOP/s; its outputs alone are 1.9 GB).
+// a map 1.17-1.24 ms (3.85e12 operations, 3.1-3.3 PFLOP/s), 8192 cubed 265 us (4.1). There a stage takes 1466 cycles (at 1.67 GHz, the
+// power's limit), 1295 without its loads (at 1.91), of which the matrix instructions by themselves are 1036: bound by them, by
+// what feeds them and by the power, and by each tile's begin and end (search and first stages 4-5 us, outputs 3-4), when its CU has
+// nothing else to do: R131072 E256 H1024 N7168 1.00-1.05 ms (1.9 PFLOP/s; its outputs alone are 1.9 GB).
 // FAR is for a map onto more codes than a buffer resource's 32-bit offsets reach: x comes by 64-bit addresses (R131072 E256 H7168
 // N1024 gated of 1.2 M rows 1.53 ms, of 1.19 M by offsets 1.30; 16 rows a workgroup without tiles took 12.4).
 template <typename O, bool GATED, int ROWS, int COLS, bool LINES, bool FAR>
@@ -834,7 +835,8 @@ moe_status launch_product(ProductArgs a, hipStream_t stream)
     // Up to 8 rows an expert without tiles (E128 H4096 N2048 gated, 8 rows: 204 against 213 us; E64, 12 rows: 126 against 110), or 16
     // where tiles are few (E8 H4096 N2048, 12 rows: 12.7 against 14.2; 16: 14.3 against 14.2). The host does not know the
     // segments: all rows on one expert, each 16 of which read its weights again, take less than rows on all (2048 rows of E256 H7168
-    // N1024 gated 185 against 356).
+    // N1024 gated 185 against 356). Nor does it know the rows that take part of aligned and drop-and-pad segments, and goes by all: one
+    // token of E256 H7168 N1024 gated with segments of multiples of 16 27 us, of 8 20, without alignment 12; 64 tokens 320 and 270.
     const bool few_rows = a.R <= (wide < kCus ? 16 : 8) * static_cast<int64_t>(a.E);
     if (!few_rows) {
         const int size = wide < kCus ? 128 : 256;
