@@ -496,8 +496,9 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     } else {
         from_mine = mapped(x_mine);
     }
-    uint32_t xo[kXMost], wo[kWLoads];
-    const uint8_t *xp[kXMost];
+    // where x's chunks are: by offsets, or by addresses
+    std::conditional_t<FAR, const uint8_t *, uint32_t> xo[kXMost];
+    uint32_t wo[kWLoads];
 #pragma unroll
     for (int j = 0; j < kWLoads; ++j)
         wo[j] = static_cast<uint32_t>(w_row(64 * j + threadIdx.x / 4)) * static_cast<uint32_t>(row_bytes) + chunk * 16;
@@ -516,13 +517,12 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
     // x's chunks past the end of the rows are zeros (beside them the weights' are some codes, and zero times them is zero); past the
     // last stage nothing is read, but the number of loads is the same in every stage.
     auto load_x = [&](int s, int j) {
-        if constexpr (FAR) {
-            const uint8_t *const zeros = reinterpret_cast<const uint8_t *>(&kZeros);
-            to_lds(s * kStageBlocks + chunk < blocks && xp[j] ? xp[j] + s * kStageBytes : zeros, slot(s) + 64 * j * kStageBytes);
-            return;
-        }
-        to_lds(make_rsrc(xbase, xbytes), s * kStageBlocks + chunk < blocks && xo[j] != kNowhere ? xo[j] + s * kStageBytes : kNowhere,
-               slot(s) + 64 * j * kStageBytes);
+        if constexpr (FAR)
+            to_lds(s * kStageBlocks + chunk < blocks && xo[j] ? xo[j] + s * kStageBytes : reinterpret_cast<const uint8_t *>(&kZeros),
+                   slot(s) + 64 * j * kStageBytes);
+        else
+            to_lds(make_rsrc(xbase, xbytes), s * kStageBlocks + chunk < blocks && xo[j] != kNowhere ? xo[j] + s * kStageBytes : kNowhere,
+                   slot(s) + 64 * j * kStageBytes);
     };
     auto load_w = [&](int s, int j) {
         const bool u = is_up(64 * j + 16 * wave);
@@ -539,8 +539,10 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
 #pragma unroll
     for (int j = 0; j < kXMost; ++j) {
         const int32_t row = x_row(64 * j + threadIdx.x / 4, from[j]);
-        xo[j] = row >= 0 ? static_cast<uint32_t>(row) * static_cast<uint32_t>(row_bytes) + chunk * 16 : kNowhere;
-        xp[j] = row >= 0 ? xbase + row * row_bytes + chunk * 16 : nullptr;
+        if constexpr (FAR)
+            xo[j] = row >= 0 ? xbase + row * row_bytes + chunk * 16 : nullptr;
+        else
+            xo[j] = row >= 0 ? static_cast<uint32_t>(row) * static_cast<uint32_t>(row_bytes) + chunk * 16 : kNowhere;
     }
     const int32_t xs_row = x_row(x_mine, from_mine);
     const uint8_t *const xsp = xs_row >= 0 ? a.xs + (x_at + xs_row) * blocks : wsp;
@@ -639,13 +641,19 @@ __global__ __launch_bounds__(kPlanThreads) void grouped_tile_kernel(ProductArgs 
             for (int n = 0; n < NS; ++n)
                 w[n] = read_scale(s, w0 + 32 * n);
         };
-        // (ungated, those of columns that only wider wavefronts have too: the outputs read them. A branch there pays where it spares
-        // gates, R12288 E128 H4096 N2048 285 -> 277 us, and costs elsewhere, R131072 E256 H1024 N7168 1020 -> 1030 against 1015.)
 #pragma unroll
-        for (int n = 0; n < (GATED ? NS : COLS / 64); ++n)
+        for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int m = 0; m < MS; ++m)
                 acc[n * kStep][m] = f32x16{};
+        // Ungated, the outputs also read sums of columns that only wider wavefronts have, and drop them: any number will do. (Zeros,
+        // or a branch at the outputs, cost all tiles more, R131072 E256 H1024 N7168 1033 against 1028 us; gated the branch spares gates,
+        // R12288 E128 H4096 N2048 283 -> 278.)
+#pragma unroll
+        for (int n = NS; n < (GATED ? NS : COLS / 64); ++n)
+#pragma unroll
+            for (int m = 0; m < MS; ++m)
+                asm("" : "=a"(acc[n][m]));
 #define MOE_PRODUCTS(STEP, F)                                                                                         \
     _Pragma("unroll") for (int n = 0; n < NS; ++n) _Pragma("unroll") for (int m = 0; m < MS; ++m) acc[n * kStep][m] = \
         __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(F.w[n], F.x[m], acc[n * kStep][m], kFp4, kFp4, STEP, ws[n], STEP, xs[m])
